@@ -20,6 +20,15 @@ namespace {
 
 thread_local int g_last_hip_error = 0;
 
+}  // namespace
+
+// the launches of linear_ops.hip report through the same gemm_epi_last_hip_error
+namespace gemm_epi {
+void set_last_hip_error(int e) { g_last_hip_error = e; }
+}  // namespace gemm_epi
+
+namespace {
+
 // Relative MFMA efficiency of a tile (bigger tiles reuse each LDS operand
 // read over more MFMAs and amortise the epilogue better).  128 x 128 is a
 // little above 3/4 so that 3 waves of it beat 1 of 256 x 256 (and 6 beat 2,

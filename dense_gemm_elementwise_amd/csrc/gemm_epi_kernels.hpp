@@ -457,7 +457,7 @@ __device__ __forceinline__ void dma16(const i32x4 &rsrc, uint32_t lds_addr, int 
 template <uint32_t OFF>
 __device__ __forceinline__ void m0_set(uint32_t base)
 {
-    asm volatile("s_add_u32 m0, %0, %1" : : "s"(base), "i"(OFF) : "memory", "m0");
+    asm volatile("s_add_u32 m0, %0, %1" : : "s"(base), "i"(OFF) : "memory", "m0", "scc");
 }
 __device__ __forceinline__ void dma16_issue(const i32x4 &rsrc, int voffset)
 {

@@ -1,0 +1,698 @@
+// linear_gemm.hpp -- gfx950 matrix products of the training and serving
+// operators (include/linear_ops.h) and the epilogues fused into them.
+//
+// One workgroup of four waves computes one BM x BN tile of
+//   C[m][n] = sum_k A(m, k) B(n, k),      16-bit operands, fp32 accumulation,
+// in three layouts of the same product, by how each operand lies in memory:
+//   NT  A rows and B rows are both K-contiguous   (D = X W^T: the forward)
+//   NN  A K-contiguous, B k-major (k rows of n)   (dX = dZ W)
+//   TN  both k-major                              (dW = dZ^T X)
+// so that a gradient needs no transposed copy of anything.
+//
+// Layout in LDS and schedule.  Like the 4-wave tiles of gemm_epi_kernels.hpp,
+// each wave owns a (BM/2) x (BN/2) block of 16x16x32 MFMAs held in AGPRs, K
+// is walked in steps of 32, and every step's instruction order is fixed by
+// hand: the next step's operand reads and the DMAs of a later step sit in
+// the gaps between the MFMAs.  Both kinds of operand fill exactly one LDS
+// slot of 64 R bytes per step (R = BM or BN):
+//   k-major       32 k-rows of R columns, a ring of 4 slots, filled 4 steps
+//                 ahead, read with the transposing ds_read_b64_tr_b16;
+//   K-contiguous  half the rows (of each wave's share) of a 64-deep chunk, so
+//                 that a DMA moves full 128-byte lines, read with
+//                 ds_read_b128.  A ring of NH halves, filled NH - 1 steps
+//                 ahead: NH = 6 beside a k-major operand (160 KB of LDS in
+//                 all at 256 x 256); beside another K-contiguous one 5 each
+//                 (160 KB again).
+// Chunk c is read in steps 2c-1 and 2c (fragments are read one step early),
+// so its halves are free after the barrier at the start of step 2c+1, and
+// step t may refill the slot of half t-1 for either ring.  With NH = 5 a
+// chunk lands at least two steps before its first read, and NT needs a
+// barrier (and a wait) on odd steps only.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_epi_kernels.hpp"
+
+namespace gemm_epi {
+
+enum LinAct : int { ACT_IDENTITY = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3 };
+
+// What the epilogue does with the fp32 tile.
+enum LinEpi : int {
+    LE_LINEAR = 0,  // Z = acc + bias, D = act(Z) + residual
+    LE_OUT = 1,     // [C32 +] acc, into C32 or, times *alpha, into D
+    LE_XFWD = 2,    // per row: maximum and sum of exponentials over the tile's columns; the target's logit
+    LE_XP = 3,      // P = (exp(acc - lse) - [column == target]) * scale, 16-bit
+};
+
+// One row of the cross entropy's gradient: scale is the incoming gradient
+// times a power of two (see xent_rows_kernel), 0 with target -1 in ignored rows.
+struct XentRow {
+    float lse, scale;
+    int target, ignored;
+};
+
+struct LinParams {
+    const _Float16 *A, *B;
+    int64_t lda, ldb;    // elements between rows (K-contiguous) or k-rows (k-major)
+    int M, N, K;         // output rows and columns; contraction length (K-contiguous operands: a multiple of 8)
+    int m_read, n_read;  // columns a k-major A / B may read: M / N rounded up to 8
+    int k_rows;          // k-rows a k-major operand has (<= K; the ones past it read as zeros)
+    int tiles_m, tiles_n, num_tiles, group_m;
+    int k_split;         // contraction length of one split, a multiple of 64 (K rounded up when there is one)
+    const _Float16 *bias, *R;
+    _Float16 *D, *Z;
+    int64_t ldr, ldd, ldz;
+    float *C32;            // fp32 output or accumulator, rows of ldc floats (a multiple of 8); split s adds s * c_split
+    int64_t ldc, c_split;
+    int acc_in, acc_out;   // add C32's values; write to C32 instead of D
+    const float *alpha;    // device scalar that D is multiplied by, or NULL
+    int vec;               // D, Z and R take 16-byte vectors (host rule: alignment, leading dimensions and N)
+    const XentRow *rows;   // LE_XP
+    const int64_t *target; // LE_XFWD
+    int v0;                // vocabulary index of column 0
+    float *part_max, *part_sum;  // LE_XFWD: [M][nparts]
+    int nparts;
+    float *tlogit;         // LE_XFWD: the target's logit of each row
+    int n_store;           // LE_XP: columns written (N rounded up to 8, zeros past N)
+};
+
+// phi(z) parts shared by the activation and its gradient (see act_gelu for the
+// polynomial): the upper tail Q(|x|) = erfc(|x| / sqrt 2) / 2 of the normal
+// distribution as q * h * h with h = e^(-x^2/4)
+__device__ __forceinline__ void act_normal_tail(float x, float &q, float &h)
+{
+#pragma clang fp contract(off)
+    constexpr float c[9] = {-2.037919330e-04f, 2.859725058e-01f, 2.504409850e-01f, 3.914754093e-01f,
+                            -2.268847674e-01f, 7.775521874e-01f, -6.962806582e-01f, 2.504747510e-01f,
+                            -3.254655749e-02f};
+    const float z = __builtin_fabsf(x) * 0.707106781186547524f;
+    const float t = 2.0f * act_rcp(2.0f + z);
+    float p = c[8];
+#pragma unroll
+    for (int k = 7; k >= 0; k--) p = __builtin_fmaf(p, t, c[k]);
+    h = act_exp(-0.5f * (z * z));
+    q = 0.5f * p;
+}
+
+template <int ACT>
+__device__ __forceinline__ float lin_act(float z)
+{
+    if constexpr (ACT == ACT_RELU)
+        return z > 0.0f ? z : (z != z ? z : 0.0f);
+    else if constexpr (ACT == ACT_GELU)
+        return act_gelu(z);
+    else if constexpr (ACT == ACT_SILU)
+        return act_silu(z);
+    else
+        return z;
+}
+
+// act'(z).  The clamps only replace values where the derivative has long
+// reached 0 or 1 (they keep infinity times zero out); a NaN passes through.
+template <int ACT>
+__device__ __forceinline__ float lin_act_grad(float z)
+{
+#pragma clang fp contract(off)
+    if constexpr (ACT == ACT_RELU) {
+        return z > 0.0f ? 1.0f : 0.0f;
+    } else if constexpr (ACT == ACT_GELU) {
+        // Phi(z) + z phi(z), phi(z) = e^(-z^2/2) / sqrt(2 pi)
+        z = z < -40.0f ? -40.0f : (z > 40.0f ? 40.0f : z);
+        float q, h;
+        act_normal_tail(z, q, h);
+        const float e = h * h;
+        const float cdf = z < 0.0f ? q * e : 1.0f - q * e;
+        return cdf + z * (0.398942280401432678f * e);
+    } else if constexpr (ACT == ACT_SILU) {
+        // s (1 + z (1 - s)), s = sigmoid(z), 1 - s = sigmoid(-z)
+        z = z < -200.0f ? -200.0f : (z > 200.0f ? 200.0f : z);
+        return act_sigmoid(z) * __builtin_fmaf(z, act_sigmoid(-z), 1.0f);
+    } else {
+        return z != z ? z : 1.0f;
+    }
+}
+
+// 2^x on the hardware exponential; logits are turned to base 2 with one fma
+constexpr float kLog2e = 1.44269504088896341f;
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_row(float x)
+{
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+// over the 16 lanes of a DPP row (rotations by 8, 4, 2, 1), every lane gets the result
+__device__ __forceinline__ float row16_max(float v)
+{
+    v = __builtin_fmaxf(v, dpp_row<0x128>(v));
+    v = __builtin_fmaxf(v, dpp_row<0x124>(v));
+    v = __builtin_fmaxf(v, dpp_row<0x122>(v));
+    return __builtin_fmaxf(v, dpp_row<0x121>(v));
+}
+__device__ __forceinline__ float row16_sum(float v)
+{
+    v += dpp_row<0x128>(v);
+    v += dpp_row<0x124>(v);
+    v += dpp_row<0x122>(v);
+    return v + dpp_row<0x121>(v);
+}
+
+// Joins two (maximum, sum of exponentials) pairs.  A maximum of -infinity
+// (nothing, or nothing but -infinity, so far) counts as 0 in the exponent, so
+// that no infinity is subtracted from itself.
+__device__ __forceinline__ void softmax_join(float &m, float &s, float m2, float s2)
+{
+    const float top = __builtin_fmaxf(m, m2);
+    const float ref = top == -__builtin_inff() ? 0.0f : top;
+    s = s * exp2_hw((m - ref) * kLog2e) + s2 * exp2_hw((m2 - ref) * kLog2e);
+    m = top;
+}
+
+// ---------------------------------------------------------------------------
+// One operand of the main loop (R: BM or BN; KM: k-major; NH: ring halves of a
+// K-contiguous one).
+// ---------------------------------------------------------------------------
+template <int R, bool KM, int NH>
+struct LinOperand {
+    static constexpr int TB = R / 32;            // 16-wide blocks per wave
+    static constexpr int ND = R / 64;            // DMA instructions per wave and step
+    static constexpr int SLOT = 64 * R;          // bytes
+    static constexpr int NSLOT = KM ? 4 : NH;
+    static constexpr int LEAD = KM ? 4 : NH - 1;  // steps between a fill and the step that it feeds (KM) / half index
+    static constexpr int BYTES = SLOT * NSLOT;
+    static constexpr int NR = KM ? 2 * TB : TB;  // LDS reads per wave and step
+    static constexpr int CH = R / 8;             // 16-byte chunks per k-row (KM)
+    static constexpr uint32_t kParked = 0x7FFFFFF0u;
+
+    // DMA q of a fill moves the same lane's chunk by whole rows (or k-rows), so
+    // only the lane's own offset stays in registers: one, or two for the
+    // 256-wide k-major operand, whose swizzle alternates with q.
+    static constexpr int NV = KM && R == 256 ? 2 : 1;
+
+    const _Float16 *base;  // first element of the tile's rows / columns at k = 0
+    int64_t ld;
+    int ld2;               // bytes between rows or k-rows
+    int64_t row_bytes;     // K-contiguous: bytes of the tile's rows
+    int k_rows, kb, k_end, nk;
+    int kcol;              // K-contiguous: this lane's column inside a chunk
+    uint32_t voff[NV];
+    const char *rd[KM ? TB : 2];
+
+    // r0: first row / column of the tile, count: how many exist past it
+    // (readable ones); w: this wave's index along the operand
+    __device__ __forceinline__ void init(const _Float16 *ptr, int64_t ld_, int r0, int count, int k_rows_, int kb_,
+                                         int k_end_, int nk_, const char *lds, int lane, int wave, int w)
+    {
+        ld = ld_;
+        ld2 = (int)ld * 2;
+        k_rows = k_rows_;
+        kb = kb_;
+        k_end = k_end_;
+        nk = nk_;
+        const int li = lane & 15, lg = lane >> 4;
+        if constexpr (KM) {
+            base = ptr + r0;
+            row_bytes = 0;
+            kcol = 0;
+#pragma unroll
+            for (int q = 0; q < NV; q++) {
+                const int lin = (q * 4 + wave) * 64 + lane;
+                const int krow = lin / CH;
+                const int c = (lin % CH) ^ swz_b<CH, 16>(krow);
+                voff[q] = c * 8 < count ? (uint32_t)(krow * ld2 + c * 16) : kParked;
+            }
+#pragma unroll
+            for (int j = 0; j < TB; j++) {
+                const int n = w * (R / 2) + j * 16 + 4 * (li & 3);
+                const int krow = 8 * lg + (li >> 2);
+                rd[j] = lds + krow * (R * 2) + (((n >> 3) ^ swz_b<CH, 16>(krow)) * 16) + (n & 7) * 2;
+            }
+        } else {
+            base = ptr + (int64_t)r0 * ld;
+            row_bytes = (int64_t)min(count, R) * ld * 2;
+            // half h of a chunk holds rows w (R/2) + h (R/4) .. + R/4 - 1 of each
+            // wave's share w; its local row is w (R/4) + x, and DMA q covers
+            // local rows 32 q + 8 wave .. + 7.  The swizzle (bits 1-3 of the
+            // local row) is the same for every q and h.
+            const int lr0 = 8 * wave + (lane >> 3);
+            const int c = (lane & 7) ^ swz_a<8>(lr0);
+            kcol = c * 8;
+            voff[0] = (uint32_t)(lr0 * ld2 + c * 16);
+            const int lr = w * (R / 4) + li;
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) rd[kk] = lds + lr * 128 + (((kk * 4 + lg) ^ swz_a<8>(lr)) * 16);
+        }
+    }
+
+    // The buffer descriptor of the fill that step t makes (t < 0: the
+    // prologue); zero records past the segment's end.  Rows past the tile's
+    // last one, and k-rows past k_rows, lie past the record count.
+    __device__ __forceinline__ i32x4 rsrc(int t) const
+    {
+        if constexpr (KM) {
+            const int s = t + LEAD, k0 = kb + s * 32;
+            const int n = s < nk ? min(32, k_rows - k0) : 0;
+            // a k-row's columns end ld - r0 elements past the base at most: the
+            // record count may reach into the following columns of the last
+            // row, which the parked lanes never touch
+            return make_rsrc(base + (int64_t)k0 * ld, n > 0 ? (uint32_t)((int64_t)n * ld * 2) : 0u);
+        } else {
+            const int c = (t + LEAD) >> 1, k0 = kb + c * 64;
+            return make_rsrc(base + k0, k0 < k_end ? (uint32_t)(row_bytes - (int64_t)k0 * 2) : 0u);
+        }
+    }
+    // byte offset of DMA q of the fill that step t makes, half h.  A parked
+    // lane's offset plus the row steps stays between 2^31 - 16 and 2^32, past
+    // every record count.
+    __device__ __forceinline__ int off(int t, int h, int q) const
+    {
+        if constexpr (KM) {
+            return (int)(voff[q % NV] + (uint32_t)(q / NV * 16 * ld2));
+        } else {
+            const int row = (32 * q) / (R / 4) * (R / 2) + h * (R / 4) + (32 * q) % (R / 4);
+            const uint32_t v = kb + ((t + LEAD) >> 1) * 64 + kcol < k_end ? voff[0] : kParked;
+            return (int)(v + (uint32_t)(row * ld2));
+        }
+    }
+};
+
+template <int BM, int BN, bool AKM, bool BKM>
+struct LinCfg {
+    static constexpr int NH = (AKM || BKM) ? 6 : 5;
+    using OA = LinOperand<BM, AKM, NH>;
+    using OB = LinOperand<BN, BKM, NH>;
+    static constexpr int MAIN = OA::BYTES + OB::BYTES;
+    static constexpr int WN = BN / 2;
+    static constexpr int LDW = WN + 4;  // slab pitch in floats
+    static constexpr int EPI = 4 * 64 * LDW * 4 + BM * 16;
+    static constexpr int LDS = MAIN > EPI ? MAIN : EPI;
+    static_assert(LDS <= 160 * 1024, "LDS budget");
+};
+
+template <int BM, int BN, bool AKM, bool BKM, bool BF>
+__device__ __forceinline__ void mainloop_lin(f32x4 (&acc)[BM / 32][BN / 32], const LinParams &p, int m0, int n0,
+                                             int kb, int k_end, char *smem)
+{
+    using C = LinCfg<BM, BN, AKM, BKM>;
+    using OA = typename C::OA;
+    using OB = typename C::OB;
+    constexpr int TM = BM / 32, TN = BN / 32;
+    constexpr int NMF = TM * TN, NDA = OA::ND, ND = OA::ND + OB::ND, NRA = OA::NR, NR = OA::NR + OB::NR;
+    constexpr bool BOTH_KC = !AKM && !BKM;
+    constexpr int PERIOD = BOTH_KC ? 10 : (AKM && BKM ? 4 : 12);
+    static_assert(NMF >= 3 * ND && NMF >= NR, "the gap schedule needs room");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int nk = (k_end - kb + 31) >> 5;
+    const uint32_t lds_w = (uint32_t)__builtin_amdgcn_readfirstlane((int)(lds_addr_of(smem) + wave * 1024));
+
+    OA oa;
+    OB ob;
+    oa.init(p.A, p.lda, m0, (AKM ? p.m_read : p.M) - m0, p.k_rows, kb, k_end, nk, smem, lane, wave, wave >> 1);
+    ob.init(p.B, p.ldb, n0, (BKM ? p.n_read : p.N) - n0, p.k_rows, kb, k_end, nk, smem + OA::BYTES, lane, wave,
+            wave & 1);
+
+    half8 fa[2][TM], fb[2][TN];
+    fp16x4_t lo_a, lo_b;  // first half of a transposed read pair
+    auto join = [](fp16x4_t lo, fp16x4_t hi) {
+        const half4 l = __builtin_bit_cast(half4, lo), h = __builtin_bit_cast(half4, hi);
+        return half8{l[0], l[1], l[2], l[3], h[0], h[1], h[2], h[3]};
+    };
+    // read r of operand o for the step d (its index modulo the period)
+    auto read_op = [&](auto &o, auto R_, auto D_, half8 *dst, fp16x4_t &lo) {
+        using O = typename std::remove_reference<decltype(o)>::type;
+        constexpr int r = decltype(R_)::value, d = decltype(D_)::value;
+        if constexpr (O::NSLOT == 4 && O::LEAD == 4) {  // k-major
+            constexpr int rowb = O::CH * 16;
+            const fp16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+                (GE_LDS(fp16x4_t) *)(o.rd[r / 2] + (d % 4) * O::SLOT + (r & 1) * 4 * rowb));
+            if constexpr ((r & 1) == 0)
+                lo = v;
+            else
+                dst[r / 2] = join(lo, v);
+        } else {
+            constexpr int half = (d >> 1) * 2 + (r >= O::TB / 2 ? 1 : 0);
+            constexpr int x = r % (O::TB / 2);
+            dst[r] = *(const half8 *)(o.rd[d & 1] + (half % O::NSLOT) * O::SLOT + x * 2048);
+        }
+    };
+    // read r of a step: A block 0 (both halves of it when k-major), every B block, the other A blocks
+    constexpr int A0 = AKM ? 2 : 1;
+    auto do_read = [&](auto R_, auto D_, auto P_) {
+        constexpr int r = decltype(R_)::value, P = decltype(P_)::value;
+        if constexpr (r < A0)
+            read_op(oa, R_, D_, fa[P], lo_a);
+        else if constexpr (r < A0 + OB::NR)
+            read_op(ob, std::integral_constant<int, r - A0>{}, D_, fb[P], lo_b);
+        else
+            read_op(oa, std::integral_constant<int, r - OB::NR>{}, D_, fa[P], lo_a);
+    };
+
+    // prologue: the fills of the virtual steps before 0, in their order
+    constexpr int FIRST = OA::LEAD > OB::LEAD ? OA::LEAD : OB::LEAD;
+    static_for<FIRST>([&](auto V_) {
+        constexpr int v = decltype(V_)::value - FIRST;
+        if constexpr (v + OA::LEAD >= 0) {
+            constexpr int f = v + OA::LEAD;
+            const i32x4 r = oa.rsrc(v);
+#pragma unroll
+            for (int q = 0; q < OA::ND; q++)
+                dma16(r, lds_w + (f % OA::NSLOT) * OA::SLOT + q * 4096, oa.off(v, f & 1, q));
+        }
+        if constexpr (v + OB::LEAD >= 0) {
+            constexpr int f = v + OB::LEAD;
+            const i32x4 r = ob.rsrc(v);
+#pragma unroll
+            for (int q = 0; q < OB::ND; q++)
+                dma16(r, lds_w + OA::BYTES + (f % OB::NSLOT) * OB::SLOT + q * 4096, ob.off(v, f & 1, q));
+        }
+    });
+    // step 0 reads the first k-major stage and chunk 0 (two halves): all but
+    // the newest two (both K-contiguous) or three virtual steps
+    wait_vmcnt<(BOTH_KC ? 2 : 3) * ND>();
+    barrier_lds();
+    static_for<NR>([&](auto R_) {
+        do_read(R_, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
+    });
+    agpr_fence(acc);  // the accumulators' zeroing (VALU) before the first MFMA reads them
+
+    auto kstep = [&](auto D_, int t) {
+        constexpr int D = decltype(D_)::value;
+        constexpr int P = D & 1;
+        constexpr int FA = D + OA::LEAD, FB = D + OB::LEAD;  // the fills this step makes
+        using DN = std::integral_constant<int, (D + 1) % PERIOD>;
+        i32x4 ra, rb;
+        static_for<NMF>([&](auto M_) {
+            constexpr int m = decltype(M_)::value;
+            mfma16_agpr<BF>(acc[m / TN][m % TN], fa[P][m / TN], fb[P][m % TN]);
+            static_for<NR>([&](auto R_) {
+                constexpr int r = decltype(R_)::value;
+                if constexpr (r * NMF / NR == m) do_read(R_, DN{}, std::integral_constant<int, P ^ 1>{});
+            });
+            static_for<ND>([&](auto G_) {
+                constexpr int g = decltype(G_)::value;
+                constexpr int g0 = g * NMF / ND;
+                if constexpr (m == g0) {
+                    if constexpr (g == 0) ra = oa.rsrc(t);
+                    if constexpr (g == NDA) rb = ob.rsrc(t);
+                } else if constexpr (m == g0 + 1) {
+                    constexpr uint32_t OFF =
+                        g < NDA ? (uint32_t)((FA % OA::NSLOT) * OA::SLOT + g * 4096)
+                                : (uint32_t)(OA::BYTES + (FB % OB::NSLOT) * OB::SLOT + (g - NDA) * 4096);
+                    m0_set<OFF>(lds_w);
+                } else if constexpr (m == g0 + 2) {
+                    if constexpr (g < NDA)
+                        dma16_issue(ra, oa.off(t, FA & 1, g));
+                    else
+                        dma16_issue(rb, ob.off(t, FB & 1, g - NDA));
+                }
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // Step t publishes what it reads for step t+1: the k-major stage t+1
+    // (filled in step t-3) and, for odd t, chunk (t+1)/2 (its last half filled
+    // in step t-3 for NH = 6, t-2 for NH = 5).  The barrier also frees the
+    // slots that this step's fills overwrite, the last step's included (its
+    // fills write zeros).
+    auto step = [&](auto D_, int t) {
+        constexpr int D = decltype(D_)::value;
+        if constexpr (!BOTH_KC) {
+            wait_vmcnt<2 * ND>();
+            barrier_lds();
+        } else if constexpr (D & 1) {
+            wait_vmcnt<ND>();
+            barrier_lds();
+        }
+        kstep(D_, t);
+    };
+#pragma unroll 1
+    for (int t = 0; t < nk; t += PERIOD) {
+        step(std::integral_constant<int, 0>{}, t);
+        static_for<PERIOD - 1>([&](auto D_) {
+            constexpr int d = decltype(D_)::value + 1;
+            if (t + d < nk) step(std::integral_constant<int, d>{}, t + d);
+        });
+    }
+    // the last fills (zero records) still write their slots, which the epilogue reuses
+    wait_vmcnt<0>();
+    agpr_fence(acc);
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues.  The tile goes through LDS one 16-row slab per wave at a time, so
+// that a lane owns 8 consecutive columns (16-byte accesses).  With p.vec the
+// outputs and the residual go through range-checked buffer accesses (rows
+// past M and, parked, columns past N are dropped; an absent tensor is a
+// descriptor of zero records, which reads as zeros); otherwise one element
+// per lane, adjacent lanes on adjacent columns, so that an access still
+// covers 128 contiguous bytes whatever the row's alignment.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int EPI, int ACT, bool BF>
+__device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], const LinParams &p, int m0, int n0,
+                                             int tile_n, int split, char *smem)
+{
+    constexpr int TM = BM / 32, TN = BN / 32, WN = BN / 2;
+    constexpr int LDW = WN + 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int li = lane & 15, lg = lane >> 4;
+    const int rows_here = min(p.M - m0, BM);
+    barrier_lds();  // every wave is done with the main loop's LDS
+
+    if constexpr (EPI == LE_XFWD) {
+        // Softmax statistics of the tile's columns, in the accumulator layout:
+        // lane (li, lg) of wave (wm, wn) holds rows wm BM/2 + 16 i + 4 lg + r,
+        // columns wn WN + 16 j + li.
+        int *tcol = (int *)smem;                    // the target's column in this tile, or -1
+        float *red = (float *)(smem + BM * 4);      // [2][BM][2]: the two column halves' (max, sum)
+        if (tid < BM) {
+            int64_t c = -1;
+            if (tid < rows_here) {
+                c = p.target[m0 + tid] - n0;
+                if (c < 0 || c >= min(p.N - n0, BN)) c = -1;
+            }
+            tcol[tid] = (int)c;
+        }
+        barrier_lds();
+        const bool edge = n0 + BN > p.N;
+#pragma unroll
+        for (int i = 0; i < TM; i++) {
+            float x[TN][4];
+#pragma unroll
+            for (int j = 0; j < TN; j++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    x[j][r] = acc[i][j][r];
+                    if (edge && n0 + wn * WN + j * 16 + li >= p.N) x[j][r] = -__builtin_inff();
+                }
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int row = wm * (BM / 2) + i * 16 + 4 * lg + r;
+                float m = x[0][r];
+#pragma unroll
+                for (int j = 1; j < TN; j++) m = __builtin_fmaxf(m, x[j][r]);
+                m = row16_max(m);
+                const float ref = m == -__builtin_inff() ? 0.0f : m;
+                float s = 0.0f;
+#pragma unroll
+                for (int j = 0; j < TN; j++) s += exp2_hw((x[j][r] - ref) * kLog2e);
+                s = row16_sum(s);
+                if (li == 0) {
+                    red[(wn * BM + row) * 2] = m;
+                    red[(wn * BM + row) * 2 + 1] = s;
+                }
+                const int t = tcol[row] - wn * WN;
+                if (t >= 0 && t < WN && (t & 15) == li) {
+                    float v = x[0][r];
+#pragma unroll
+                    for (int j = 1; j < TN; j++)
+                        if ((t >> 4) == j) v = x[j][r];
+                    p.tlogit[m0 + row] = v;
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        barrier_lds();
+        if (tid < rows_here) {
+            float m = red[tid * 2], s = red[tid * 2 + 1];
+            softmax_join(m, s, red[(BM + tid) * 2], red[(BM + tid) * 2 + 1]);
+            const int64_t o = (int64_t)(m0 + tid) * p.nparts + tile_n;
+            p.part_max[o] = m;
+            p.part_sum[o] = s;
+        }
+        return;
+    }
+
+    constexpr int LPR = WN / 8, RPP = 64 / LPR, PASSES = 16 / RPP;
+    float *slab = (float *)(smem + wave * (64 * LDW * 4));
+    int32_t *xrow = (int32_t *)(smem + 4 * 64 * LDW * 4);  // LE_XP: the tile's XentRow entries
+    if constexpr (EPI == LE_XP) {
+        if (tid < BM) {
+            i32x4 r = {0, 0, -1, 1};
+            if (tid < rows_here) r = *(const i32x4 *)(p.rows + m0 + tid);
+            *(i32x4 *)(xrow + 4 * tid) = r;
+        }
+        barrier_lds();
+    }
+    const int ncols = EPI == LE_XP ? p.n_store : p.N;
+    const int scol = 8 * (lane % LPR);
+    const int gcol = n0 + wn * WN + scol;
+    const bool col_in = gcol < ncols;
+    const int64_t m0l = m0;
+    auto res_of = [&](const void *ptr, int64_t ld, int es) {
+        return epi_rsrc((const char *)ptr + m0l * ld * es, ptr ? (uint32_t)((int64_t)rows_here * ld * es) : 0u);
+    };
+    // byte offset of local row `row` in a tensor of `es`-byte elements, or parked
+    auto off_of = [&](int row, int64_t ld, int es) {
+        return col_in ? (row * (int)ld + gcol) * es : (int)0x7FFFFFE0;
+    };
+    float alpha = 1.0f;
+    if constexpr (EPI == LE_OUT)
+        if (p.alpha) alpha = *p.alpha;
+
+    const bool vec = EPI == LE_XP || p.vec || (EPI == LE_OUT && p.acc_out);
+    const __amdgpu_buffer_rsrc_t rD = res_of(p.D, p.ldd, 2);
+    const __amdgpu_buffer_rsrc_t rR = res_of(EPI == LE_LINEAR ? p.R : nullptr, p.ldr, 2);
+    const __amdgpu_buffer_rsrc_t rZ = res_of(EPI == LE_LINEAR ? p.Z : nullptr, p.ldz, 2);
+    const __amdgpu_buffer_rsrc_t rC =
+        res_of(EPI == LE_OUT && p.C32 ? p.C32 + (int64_t)split * p.c_split : nullptr, p.ldc, 4);
+    float bias[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        bias[e] = EPI == LE_LINEAR && vec && p.bias && col_in ? ld16<BF>(p.bias[gcol + e]) : 0.0f;
+
+    // 64 rows of the wave's block at a time: the accumulators' part is unrolled
+    // (registers cannot be indexed at run time), the rest is a loop over 16-row
+    // slabs, with the next slab's residual (or accumulator) loads in flight
+#pragma unroll
+    for (int ph = 0; ph < TM / 4; ph++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+#pragma unroll
+            for (int j = 0; j < TN; j++)
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    slab[(i * 16 + 4 * lg + r) * LDW + j * 16 + li] = acc[ph * 4 + i][j][r];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        wave_lds_sync();
+        const int row0 = wm * (BM / 2) + ph * 64;
+        if (vec) {
+            half8 rbuf[PASSES] = {};
+            auto fetch = [&](int s) {
+                if constexpr (EPI == LE_LINEAR) {
+#pragma unroll
+                    for (int q = 0; q < PASSES; q++)
+                        rbuf[q] = buf_load<half8, 0>(rR, off_of(row0 + s * 16 + q * RPP + lane / LPR, p.ldr, 2));
+                }
+            };
+            fetch(0);
+#pragma unroll 1
+            for (int s = 0; s < 4; s++) {
+                half8 rcur[PASSES];
+#pragma unroll
+                for (int q = 0; q < PASSES; q++) rcur[q] = rbuf[q];
+                if (s < 3) fetch(s + 1);
+#pragma unroll
+                for (int q = 0; q < PASSES; q++) {
+                    const int srow = s * 16 + q * RPP + lane / LPR, row = row0 + srow;
+                    const float *src = slab + srow * LDW + scol;
+                    const f32x4 v0 = *(const f32x4 *)src, v1 = *(const f32x4 *)(src + 4);
+                    float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+                    half8 d;
+                    if constexpr (EPI == LE_LINEAR) {
+                        half8 z;
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const float t = v[e] + bias[e];
+                            z[e] = st16<BF>(t);
+                            d[e] = st16<BF>(lin_act<ACT>(t) + ld16<BF>(rcur[q][e]));
+                        }
+                        buf_store<half8, 2>(d, rD, off_of(row, p.ldd, 2));
+                        buf_store<half8, 2>(z, rZ, off_of(row, p.ldz, 2));
+                    } else if constexpr (EPI == LE_OUT) {
+                        const int oc = off_of(row, p.ldc, 4);
+                        if (p.acc_in) {
+                            const f32x4 c0 = buf_load<f32x4, 0>(rC, oc), c1 = buf_load<f32x4, 0>(rC, oc + 16);
+#pragma unroll
+                            for (int e = 0; e < 8; e++) v[e] += e < 4 ? c0[e & 3] : c1[e & 3];
+                        }
+                        if (p.acc_out) {
+                            buf_store<f32x4, 0>(f32x4{v[0], v[1], v[2], v[3]}, rC, oc);
+                            buf_store<f32x4, 0>(f32x4{v[4], v[5], v[6], v[7]}, rC, oc + 16);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; e++) d[e] = st16<BF>(v[e] * alpha);
+                            buf_store<half8, 2>(d, rD, off_of(row, p.ldd, 2));
+                        }
+                    } else {  // LE_XP; P is read again soon, so it is stored plainly
+                        const f32x4 xf = *(const f32x4 *)(xrow + 4 * row);
+                        const float lse = xf[0], scale = xf[1];
+                        const i32x4 x = __builtin_bit_cast(i32x4, xf);
+                        const int tc = x[2] - p.v0 - gcol;
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            // the difference first: where the probability is large, logit and lse are close
+                            float pr = exp2_hw((v[e] - lse) * kLog2e);
+                            pr = (pr - (tc == e ? 1.0f : 0.0f)) * scale;
+                            if (x[3] || gcol + e >= p.N) pr = 0.0f;
+                            d[e] = st16<BF>(pr);
+                        }
+                        buf_store<half8, 0>(d, rD, off_of(row, p.ldd, 2));
+                    }
+                }
+            }
+        } else if constexpr (EPI != LE_XP) {
+#pragma unroll 1
+            for (int x = 0; x < 64; x++) {
+                const int row = row0 + x;
+                if (row >= rows_here) break;
+#pragma unroll
+                for (int c = 0; c < WN; c += 64) {
+                    const int gn = n0 + wn * WN + c + lane;
+                    if (gn >= p.N) continue;
+                    float v = slab[x * LDW + c + lane];
+                    if constexpr (EPI == LE_LINEAR) {
+                        v += p.bias ? ld16<BF>(p.bias[gn]) : 0.0f;
+                        const float r = p.R ? ld16<BF>(p.R[(m0l + row) * p.ldr + gn]) : 0.0f;
+                        if (p.Z) p.Z[(m0l + row) * p.ldz + gn] = st16<BF>(v);
+                        p.D[(m0l + row) * p.ldd + gn] = st16<BF>(lin_act<ACT>(v) + r);
+                    } else {
+                        if (p.acc_in) v += p.C32[(m0l + row) * p.ldc + gn];
+                        p.D[(m0l + row) * p.ldd + gn] = st16<BF>(v * alpha);
+                    }
+                }
+            }
+        }
+        wave_lds_sync();  // this wave's reads are done before the next 64 rows overwrite its slabs
+    }
+}
+
+template <int BM, int BN, bool AKM, bool BKM, int EPI, int ACT, bool BF>
+__global__ __launch_bounds__(256) void lin_gemm_kernel(LinParams p)
+{
+    using C = LinCfg<BM, BN, AKM, BKM>;
+    __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
+    const int lid = xcd_logical_id((int)gridDim.x, (int)blockIdx.x);
+    const int split = lid / p.num_tiles, t = lid - split * p.num_tiles;
+    // tiles in groups of group_m tile rows, column-major inside a group
+    const int full = p.group_m * p.tiles_n, g = t / full, first = g * p.group_m;
+    const int gm = min(p.tiles_m - first, p.group_m), rr = t - g * full;
+    const int tm = first + rr % gm, tn = rr / gm;
+    const int m0 = tm * BM, n0 = tn * BN;
+    const int kb = split * p.k_split, k_end = min(p.K, kb + p.k_split);
+
+    f32x4 acc[BM / 32][BN / 32];
+#pragma unroll
+    for (int i = 0; i < BM / 32; i++)
+#pragma unroll
+        for (int j = 0; j < BN / 32; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    mainloop_lin<BM, BN, AKM, BKM, BF>(acc, p, m0, n0, kb, k_end, smem);
+    lin_epilogue<BM, BN, EPI, ACT, BF>(acc, p, m0, n0, tn, split, smem);
+}
+
+}  // namespace gemm_epi

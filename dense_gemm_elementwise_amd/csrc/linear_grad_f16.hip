@@ -1,0 +1,17 @@
+// linear_grad_f16.hip -- the gradients' products, fp16: NN (dX = dZ W) and TN
+// (dW = dZ^T X).
+#include "linear_launch.hpp"
+
+namespace gemm_epi {
+
+hipError_t lin_launch_nn_f16(int tile, const LinParams &p, int groups, hipStream_t s)
+{
+    return lin_launch_out<false, true, false>(tile, p, groups, s);
+}
+
+hipError_t lin_launch_tn_f16(int tile, const LinParams &p, int groups, hipStream_t s)
+{
+    return lin_launch_out<true, true, false>(tile, p, groups, s);
+}
+
+}  // namespace gemm_epi

@@ -1,0 +1,1057 @@
+// linear_ops.hip -- the C ABI of include/linear_ops.h: argument checks, plans
+// (tiles, splits, pieces of the vocabulary, workspace layout) and launches.
+//
+// Every check runs on the host before any HIP call.  A plan depends on the
+// arguments alone, so the workspace query and the call lay the workspace out
+// alike.
+#include <hip/hip_runtime.h>
+#include <algorithm>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "linear_launch.hpp"
+#include "linear_ops.h"
+#include "linear_small.hpp"
+#include "norm_residual.hpp"
+
+namespace gemm_epi {
+void set_last_hip_error(int e);  // gemm_epi.hip
+}
+
+using namespace gemm_epi;
+
+namespace {
+
+constexpr int kCUs = 256;
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
+
+int hip_status(hipError_t e)
+{
+    if (e == hipSuccess) return GEMM_EPI_OK;
+    set_last_hip_error((int)e);
+    return GEMM_EPI_ERR_HIP;
+}
+
+#define GE_TRY(call)                                  \
+    do {                                              \
+        const int ge_rc = hip_status(call);           \
+        if (ge_rc != GEMM_EPI_OK) return ge_rc;       \
+    } while (0)
+
+// (arguments convert to the kernel's own parameter types)
+template <typename T>
+struct Same {
+    using type = T;
+};
+template <typename... P>
+hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, typename Same<P>::type... a)
+{
+    void *args[] = {(void *)&a...};
+    return hipLaunchKernel((const void *)kernel, grid, block, args, 0, s);
+}
+
+// a matrix operand: NULL, alignment and row stride
+int check_matrix(const void *p, int64_t ld, int64_t cols, uintptr_t es, int null_status)
+{
+    if (!p) return null_status;
+    if (!aligned(p, es)) return GEMM_EPI_ERR_ALIGN;
+    if (ld < cols || ld > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
+    return GEMM_EPI_OK;
+}
+#define GE_CHECK(call)                          \
+    do {                                        \
+        const int ge_rc = (call);               \
+        if (ge_rc != GEMM_EPI_OK) return ge_rc; \
+    } while (0)
+
+int check_dims(int64_t rows, int64_t rows2, int64_t cols)
+{
+    if (rows < 0 || rows > INT32_MAX - 256 || rows2 < 1 || rows2 > INT32_MAX - 256 || cols < 1 || cols > GE_MAX_COLS)
+        return GEMM_EPI_ERR_SHAPE;
+    return GEMM_EPI_OK;
+}
+int check_dtype(int64_t dtype) { return dtype == GEMM_EPI_F16 || dtype == GEMM_EPI_BF16 ? GEMM_EPI_OK : GEMM_EPI_ERR_DTYPE; }
+
+// A region of the workspace.
+struct Layout {
+    int64_t bytes = 0;
+    int64_t take(int64_t n)
+    {
+        const int64_t at = bytes;
+        bytes = round_up(bytes + n, 256);
+        return at;
+    }
+};
+
+int check_workspace(const void *ws, int64_t have, int64_t need)
+{
+    if (need == 0) return GEMM_EPI_OK;
+    if (!ws || have < need) return GEMM_EPI_ERR_WORKSPACE;
+    return aligned(ws, 16) ? GEMM_EPI_OK : GEMM_EPI_ERR_ALIGN;
+}
+
+// ---- tiles and splits ---------------------------------------------------------
+// One product M x N x K on `tile`, its contraction cut into `splits` pieces of
+// k_split (a multiple of 64).
+struct ProductPlan {
+    int tile = kLinSmall, splits = 1;
+    int tiles_m = 0, tiles_n = 0;
+    int64_t k_split = 0;
+    int64_t part_bytes = 0;  // fp32 partial sums of the splits
+};
+
+// Estimated microseconds of a plan: rounds of workgroups on 256 CUs at the rate
+// a CU reaches on the tile, a fixed cost per round (prologue, epilogue, fill),
+// and the partial sums' round trip and launch.  Rates per CU in TFLOP/s: 256 x
+// 256 5.5, the 128 x 256 ones 4.9, 128 x 128 4.2 with two workgroups on a
+// CU and 2.6 with one.
+double product_cost(int64_t M, int64_t N, int64_t K, int tile, int splits)
+{
+    const LinTile t = kLinTiles[tile];
+    const int64_t groups = ceil_div(M, t.bm) * ceil_div(N, t.bn) * splits;
+    const double work = 2.0 * t.bm * t.bn * (double)round_up(ceil_div(K, splits), 32);
+    double us;
+    if (tile == kLinSmall) {
+        const int64_t pairs = groups / (2 * kCUs), rest = groups % (2 * kCUs);
+        us = pairs * (2 * work / 4.2e6 + 3.0);
+        if (rest > kCUs)
+            us += 2 * work / 4.2e6 + 3.0;
+        else if (rest > 0)
+            us += work / 2.6e6 + 3.0;
+    } else {
+        us = (double)ceil_div(groups, kCUs) * (work / (tile == kLinBig ? 5.5e6 : 4.9e6) + 4.0);
+    }
+    if (splits > 1) us += 4.0 + (double)splits * M * N * 8 / 4.0e6;
+    return us;
+}
+
+// tiles: bit mask of the tiles that exist for this product, split_tiles: of
+// those whose split form exists
+ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsigned split_tiles)
+{
+    ProductPlan best;
+    double best_cost = 1e300;
+    for (int i = 0; i < 4; i++) {
+        if (!(tiles >> i & 1)) continue;
+        const LinTile t = kLinTiles[i];
+        const int64_t grid = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+        for (int want = 1; want <= 64; want *= 2) {
+            if (want > 1 && (!(split_tiles >> i & 1) || K < want * 256 || grid * want > 4 * kCUs)) break;
+            const int64_t k_split = round_up(ceil_div(K, want), 64);
+            const int splits = (int)ceil_div(K, k_split);
+            const double c = product_cost(M, N, K, i, splits);
+            if (c < best_cost) {
+                best_cost = c;
+                best.tile = i;
+                best.splits = splits;
+                best.k_split = k_split;
+            }
+        }
+    }
+    const LinTile t = kLinTiles[best.tile];
+    best.tiles_m = (int)ceil_div(M, t.bm);
+    best.tiles_n = (int)ceil_div(N, t.bn);
+    best.part_bytes = best.splits > 1 ? best.splits * M * round_up(N, 8) * 4 : 0;
+    return best;
+}
+
+bool product_fits(const ProductPlan &pl)
+{
+    return (int64_t)pl.tiles_m * pl.tiles_n <= INT32_MAX / 64 / pl.splits;
+}
+
+void set_product(LinParams &p, const ProductPlan &pl, int64_t M, int64_t N, int64_t K)
+{
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.tiles_m = pl.tiles_m;
+    p.tiles_n = pl.tiles_n;
+    p.num_tiles = pl.tiles_m * pl.tiles_n;
+    p.group_m = 8;
+    p.k_split = (int)pl.k_split;
+}
+
+// rows that the 16-byte DMA of the products can read
+bool dma_rows(const void *p, int64_t ld, int64_t cols) { return cols % 8 == 0 && ld % 8 == 0 && aligned(p, 16); }
+
+// An operand as the products read it: in place, or a padded copy.
+struct Operand16 {
+    const _Float16 *p;
+    int64_t ld;
+};
+struct StagePlan2 {
+    bool on[2] = {false, false};
+    int64_t off[2] = {0, 0};
+    int64_t ldo = 0;
+};
+// stages up to two operands with `cols` columns
+hipError_t run_staging(const StagePlan2 &st, char *ws, int64_t cols, Operand16 &a, int64_t a_rows, Operand16 &b,
+                       int64_t b_rows, hipStream_t s)
+{
+    PadParams q = {};
+    int n = 0;
+    Operand16 *op[2] = {&a, &b};
+    const int64_t rows[2] = {a_rows, b_rows};
+    for (int i = 0; i < 2; i++) {
+        if (!st.on[i]) continue;
+        q.src[n] = op[i]->p;
+        q.lds[n] = op[i]->ld;
+        q.rows[n] = rows[i];
+        q.dst[n] = (_Float16 *)(ws + st.off[i]);
+        op[i]->p = q.dst[n];
+        op[i]->ld = st.ldo;
+        n++;
+    }
+    if (n == 0) return hipSuccess;
+    q.cols = (int)cols;
+    q.ldo = (int)st.ldo;
+    const int64_t blocks = std::min<int64_t>(ceil_div(std::max(q.rows[0], q.rows[1]) * (st.ldo / 8), 256), 4096);
+    return launch(pad_rows_kernel, dim3((unsigned)blocks, n), dim3(256), s, q);
+}
+StagePlan2 plan_staging2(const void *a, int64_t lda, int64_t a_rows, const void *b, int64_t ldb, int64_t b_rows,
+                         int64_t cols, Layout &lay)
+{
+    StagePlan2 st;
+    st.ldo = round_up(cols, 8);
+    st.on[0] = !dma_rows(a, lda, cols);
+    st.on[1] = !dma_rows(b, ldb, cols);
+    if (st.on[0]) st.off[0] = lay.take(a_rows * st.ldo * 2);
+    if (st.on[1]) st.off[1] = lay.take(b_rows * st.ldo * 2);
+    return st;
+}
+
+template <bool BF, int EPI>
+hipError_t launch_split_sum(int act, const SplitSumParams &q, hipStream_t s)
+{
+    const int64_t blocks = std::min<int64_t>(ceil_div((int64_t)q.M * ((q.N + 7) / 8), 256), 4096);
+    const dim3 g((unsigned)blocks), b(256);
+    if constexpr (EPI == LE_LINEAR) {
+        switch (act) {
+        case ACT_RELU: return launch(split_sum_kernel<BF, EPI, ACT_RELU>, g, b, s, q);
+        case ACT_GELU: return launch(split_sum_kernel<BF, EPI, ACT_GELU>, g, b, s, q);
+        case ACT_SILU: return launch(split_sum_kernel<BF, EPI, ACT_SILU>, g, b, s, q);
+        default: break;
+        }
+    }
+    return launch(split_sum_kernel<BF, EPI, ACT_IDENTITY>, g, b, s, q);
+}
+
+// A gradient product (NN or TN) into D (16-bit), or into / onto the fp32
+// accumulator acc, through partial sums where the plan splits it.  p holds the
+// operands.
+template <bool BF>
+hipError_t run_grad_product(bool tn, LinParams p, const ProductPlan &pl, int64_t M, int64_t N, int64_t K, void *D,
+                            int64_t ldd, float *acc, bool acc_in, bool acc_out, const float *alpha, float *part,
+                            hipStream_t s)
+{
+    set_product(p, pl, M, N, K);
+    const int64_t ldc = round_up(N, 8);
+    p.ldc = ldc;
+    p.ldd = ldd;
+    if (pl.splits > 1) {
+        p.C32 = part;
+        p.c_split = M * ldc;
+        p.acc_out = 1;
+    } else {
+        p.C32 = acc;
+        p.acc_in = acc_in;
+        p.acc_out = acc_out;
+        p.alpha = alpha;
+        p.D = (_Float16 *)D;
+        p.vec = dma_rows(D, ldd, N);
+    }
+    const int groups = p.num_tiles * pl.splits;
+    hipError_t e;
+    if (tn)
+        e = BF ? lin_launch_tn_bf16(pl.tile, p, groups, s) : lin_launch_tn_f16(pl.tile, p, groups, s);
+    else
+        e = BF ? lin_launch_nn_bf16(pl.tile, p, groups, s) : lin_launch_nn_f16(pl.tile, p, groups, s);
+    if (e != hipSuccess || pl.splits == 1) return e;
+    SplitSumParams q = {};
+    q.part = part;
+    q.splits = pl.splits;
+    q.M = (int)M;
+    q.N = (int)N;
+    q.ldc = ldc;
+    q.c_split = M * ldc;
+    q.D = (_Float16 *)D;
+    q.ldd = ldd;
+    q.C32 = acc;
+    q.acc_in = acc_in;
+    q.acc_out = acc_out;
+    q.alpha = alpha;
+    return launch_split_sum<BF, LE_OUT>(0, q, s);
+}
+
+hipError_t run_zero(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes, hipStream_t s)
+{
+    const int64_t blocks = std::min<int64_t>(ceil_div(rows * (bytes / 2), 256), 4096);
+    return launch(zero_rows_kernel, dim3((unsigned)blocks), dim3(256), s, (char *)p, ld_bytes, rows, bytes / 2);
+}
+
+// ---- linear -------------------------------------------------------------------
+constexpr int64_t kSkinnyRows = 16;  // one MFMA block of X rows
+
+struct LinearPlan {
+    bool skinny = false;
+    StagePlan2 st;  // X, W
+    ProductPlan pl;
+    int64_t off_part = 0, bytes = 0;
+};
+
+int check_linear(const ge_linear_args *a)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_dims(a->M, a->N, a->K));
+    if (a->N > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
+    if (!a->W || (a->M > 0 && !a->X)) return GEMM_EPI_ERR_NULL_INPUT;
+    if (a->M > 0 && !a->D) return GEMM_EPI_ERR_NULL_OUTPUT;
+    if (a->act < GE_ACT_IDENTITY || a->act > GE_ACT_SILU) return GEMM_EPI_ERR_KIND;
+    GE_CHECK(check_dtype(a->dtype));
+    GE_CHECK(check_matrix(a->W, a->ldw, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+    if (a->X) GE_CHECK(check_matrix(a->X, a->ldx, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+    if (a->D) GE_CHECK(check_matrix(a->D, a->ldd, a->N, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->residual) GE_CHECK(check_matrix(a->residual, a->ldr, a->N, 2, GEMM_EPI_ERR_NULL_INPUT));
+    if (a->Z) GE_CHECK(check_matrix(a->Z, a->ldz, a->N, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->bias && !aligned(a->bias, 2)) return GEMM_EPI_ERR_ALIGN;
+    return GEMM_EPI_OK;
+}
+
+int plan_linear(const ge_linear_args *a, LinearPlan &pl)
+{
+    GE_CHECK(check_linear(a));
+    if (a->M == 0) return GEMM_EPI_OK;
+    pl.skinny = a->M <= kSkinnyRows;
+    if (pl.skinny) return GEMM_EPI_OK;
+    Layout lay;
+    pl.st = plan_staging2(a->X, a->ldx, a->M, a->W, a->ldw, a->N, a->K, lay);
+    pl.pl = plan_product(a->M, a->N, a->K, 0xF, 1u << kLinSmall);
+    if (!product_fits(pl.pl)) return GEMM_EPI_ERR_SHAPE;
+    pl.off_part = lay.take(pl.pl.part_bytes);
+    pl.bytes = lay.bytes;
+    return GEMM_EPI_OK;
+}
+
+template <bool BF>
+int run_linear(const ge_linear_args *a, const LinearPlan &pl)
+{
+    hipStream_t s = (hipStream_t)a->stream;
+    char *ws = (char *)a->workspace;
+    const int act = (int)a->act;
+    if (pl.skinny) {
+        SkinnyParams q = {};
+        q.X = (const _Float16 *)a->X;
+        q.W = (const _Float16 *)a->W;
+        q.ldx = a->ldx;
+        q.ldw = a->ldw;
+        q.M = (int)a->M;
+        q.N = (int)a->N;
+        q.K = (int)a->K;
+        q.bias = (const _Float16 *)a->bias;
+        q.R = (const _Float16 *)a->residual;
+        q.D = (_Float16 *)a->D;
+        q.Z = (_Float16 *)a->Z;
+        q.ldr = a->ldr;
+        q.ldd = a->ldd;
+        q.ldz = a->ldz;
+        const dim3 g((unsigned)ceil_div(a->N, 16)), b(256);
+        switch (act) {
+        case ACT_RELU: return hip_status(launch(skinny_kernel<BF, false, ACT_RELU>, g, b, s, q));
+        case ACT_GELU: return hip_status(launch(skinny_kernel<BF, false, ACT_GELU>, g, b, s, q));
+        case ACT_SILU: return hip_status(launch(skinny_kernel<BF, false, ACT_SILU>, g, b, s, q));
+        default: return hip_status(launch(skinny_kernel<BF, false, ACT_IDENTITY>, g, b, s, q));
+        }
+    }
+    Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
+    GE_TRY(run_staging(pl.st, ws, a->K, x, a->M, w, a->N, s));
+    LinParams p = {};
+    set_product(p, pl.pl, a->M, a->N, round_up(a->K, 8));
+    p.A = x.p;
+    p.lda = x.ld;
+    p.B = w.p;
+    p.ldb = w.ld;
+    const int groups = p.num_tiles * pl.pl.splits;
+    if (pl.pl.splits > 1) {
+        const int64_t ldc = round_up(a->N, 8);
+        p.C32 = (float *)(ws + pl.off_part);
+        p.ldc = ldc;
+        p.c_split = a->M * ldc;
+        p.acc_out = 1;
+        GE_TRY(BF ? lin_launch_fwd_split_bf16(p, groups, s) : lin_launch_fwd_split_f16(p, groups, s));
+        SplitSumParams q = {};
+        q.part = p.C32;
+        q.splits = pl.pl.splits;
+        q.M = (int)a->M;
+        q.N = (int)a->N;
+        q.ldc = ldc;
+        q.c_split = p.c_split;
+        q.bias = (const _Float16 *)a->bias;
+        q.R = (const _Float16 *)a->residual;
+        q.D = (_Float16 *)a->D;
+        q.Z = (_Float16 *)a->Z;
+        q.ldr = a->ldr;
+        q.ldd = a->ldd;
+        q.ldz = a->ldz;
+        return hip_status(launch_split_sum<BF, LE_LINEAR>(act, q, s));
+    }
+    p.bias = (const _Float16 *)a->bias;
+    p.R = (const _Float16 *)a->residual;
+    p.D = (_Float16 *)a->D;
+    p.Z = (_Float16 *)a->Z;
+    p.ldr = a->ldr;
+    p.ldd = a->ldd;
+    p.ldz = a->ldz;
+    p.vec = dma_rows(a->D, a->ldd, a->N) && (!a->Z || dma_rows(a->Z, a->ldz, a->N)) &&
+            (!a->residual || dma_rows(a->residual, a->ldr, a->N));
+    if (pl.pl.tile == kLinBig)
+        return hip_status(BF ? lin_launch_fwd_big_bf16(act, p, groups, s) : lin_launch_fwd_big_f16(act, p, groups, s));
+    return hip_status(BF ? lin_launch_fwd_bf16(act, pl.pl.tile, p, groups, s)
+                         : lin_launch_fwd_f16(act, pl.pl.tile, p, groups, s));
+}
+
+// ---- linear, backward -----------------------------------------------------------
+struct LinearGradPlan {
+    bool direct = false;  // dD itself is dZ
+    int64_t N8 = 0;
+    int strips = 0, rows_per_strip = 0;
+    StagePlan2 st;  // X, W
+    ProductPlan dx, dw;
+    int64_t off_dz = 0, off_bias = 0, off_part = 0, bytes = 0;
+};
+
+int check_linear_grad(const ge_linear_backward_args *a)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_dims(a->M, a->N, a->K));
+    if (a->N > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
+    if (!a->dX && !a->dW && !a->dbias) return GEMM_EPI_ERR_NULL_OUTPUT;
+    if (a->act < GE_ACT_IDENTITY || a->act > GE_ACT_SILU) return GEMM_EPI_ERR_KIND;
+    GE_CHECK(check_dtype(a->dtype));
+    if (a->M > 0) {
+        GE_CHECK(check_matrix(a->dD, a->lddd, a->N, 2, GEMM_EPI_ERR_NULL_INPUT));
+        if (a->act != GE_ACT_IDENTITY) GE_CHECK(check_matrix(a->Z, a->ldz, a->N, 2, GEMM_EPI_ERR_NULL_INPUT));
+        if (a->dW) GE_CHECK(check_matrix(a->X, a->ldx, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+        if (a->dX) GE_CHECK(check_matrix(a->W, a->ldw, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+    }
+    if (a->dX) GE_CHECK(check_matrix(a->dX, a->lddx, a->K, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->dW) GE_CHECK(check_matrix(a->dW, a->lddw, a->K, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->dbias && !aligned(a->dbias, 4)) return GEMM_EPI_ERR_ALIGN;
+    return GEMM_EPI_OK;
+}
+
+int plan_linear_grad(const ge_linear_backward_args *a, LinearGradPlan &pl)
+{
+    GE_CHECK(check_linear_grad(a));
+    if (a->M == 0) return GEMM_EPI_OK;
+    pl.N8 = round_up(a->N, 8);
+    Layout lay;
+    pl.direct = a->act == GE_ACT_IDENTITY && dma_rows(a->dD, a->lddd, a->N);
+    if (!pl.direct) pl.off_dz = lay.take(a->M * pl.N8 * 2);
+    // strips of rows: about 2048 blocks of 256 columns, at least 32 rows each
+    const int64_t cols = ceil_div(a->N, 256);
+    pl.rows_per_strip = (int)round_up(std::max<int64_t>(32, ceil_div(a->M, std::max<int64_t>(1, 2048 / cols))), 8);
+    pl.strips = (int)ceil_div(a->M, pl.rows_per_strip);
+    if (a->dbias) pl.off_bias = lay.take((int64_t)pl.strips * pl.N8 * 4);
+    // an unwanted product's operand is not staged (the other operand stands in)
+    const void *x = a->dW ? a->X : a->W, *w = a->dX ? a->W : a->X;
+    const int64_t ldx = a->dW ? a->ldx : a->ldw, ldw = a->dX ? a->ldw : a->ldx;
+    if (a->dX || a->dW) {
+        pl.st = plan_staging2(x, ldx, a->dW ? a->M : 0, w, ldw, a->dX ? a->N : 0, a->K, lay);
+        pl.st.on[0] &= a->dW != nullptr;
+        pl.st.on[1] &= a->dX != nullptr;
+    }
+    int64_t part = 0;
+    if (a->dX) {
+        pl.dx = plan_product(a->M, a->K, pl.N8, 0xF, 0xF);
+        if (!product_fits(pl.dx)) return GEMM_EPI_ERR_SHAPE;
+        part = std::max(part, pl.dx.part_bytes);
+    }
+    if (a->dW) {
+        pl.dw = plan_product(a->N, a->K, a->M, 0xF, 0xF);
+        if (!product_fits(pl.dw)) return GEMM_EPI_ERR_SHAPE;
+        part = std::max(part, pl.dw.part_bytes);
+    }
+    pl.off_part = lay.take(part);
+    pl.bytes = lay.bytes;
+    return GEMM_EPI_OK;
+}
+
+template <bool BF>
+hipError_t launch_dz(int act, const DzParams &q, dim3 g, hipStream_t s)
+{
+    switch (act) {
+    case ACT_RELU: return launch(dz_kernel<BF, ACT_RELU>, g, dim3(256), s, q);
+    case ACT_GELU: return launch(dz_kernel<BF, ACT_GELU>, g, dim3(256), s, q);
+    case ACT_SILU: return launch(dz_kernel<BF, ACT_SILU>, g, dim3(256), s, q);
+    default: return launch(dz_kernel<BF, ACT_IDENTITY>, g, dim3(256), s, q);
+    }
+}
+
+template <bool BF>
+int run_linear_grad(const ge_linear_backward_args *a, const LinearGradPlan &pl)
+{
+    hipStream_t s = (hipStream_t)a->stream;
+    char *ws = (char *)a->workspace;
+    if (a->M == 0) {
+        if (a->dW) GE_TRY(run_zero(a->dW, a->lddw * 2, a->N, a->K * 2, s));
+        if (a->dbias) GE_TRY(run_zero(a->dbias, a->N * 4, 1, a->N * 4, s));
+        return GEMM_EPI_OK;
+    }
+    Operand16 dz = {(const _Float16 *)a->dD, a->lddd};
+    if (!pl.direct || a->dbias) {
+        DzParams q = {};
+        q.dD = (const _Float16 *)a->dD;
+        q.Z = (const _Float16 *)a->Z;
+        q.ldd = a->lddd;
+        q.ldz = a->ldz;
+        q.ldo = pl.N8;
+        q.out = pl.direct ? nullptr : (_Float16 *)(ws + pl.off_dz);
+        q.partial = a->dbias ? (float *)(ws + pl.off_bias) : nullptr;
+        q.M = (int)a->M;
+        q.N = (int)a->N;
+        q.N8 = (int)pl.N8;
+        q.rows_per_strip = pl.rows_per_strip;
+        GE_TRY(launch_dz<BF>((int)a->act, q, dim3((unsigned)ceil_div(a->N, 256), pl.strips), s));
+        if (!pl.direct) dz = {q.out, pl.N8};
+        if (a->dbias) {
+            ColSumParams c = {};
+            c.partial[0] = q.partial;
+            c.out[0] = a->dbias;
+            c.parts[0] = pl.strips;
+            c.ld = (int)pl.N8;
+            c.cols = (int)a->N;
+            GE_TRY(launch(colsum_kernel, dim3((unsigned)ceil_div(a->N, 64)), dim3(1024), s, c));
+        }
+    }
+    Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
+    GE_TRY(run_staging(pl.st, ws, a->K, x, a->M, w, a->N, s));
+    float *part = (float *)(ws + pl.off_part);
+    if (a->dX) {
+        LinParams p = {};
+        p.A = dz.p;
+        p.lda = dz.ld;
+        p.B = w.p;
+        p.ldb = w.ld;
+        p.n_read = (int)round_up(a->K, 8);
+        p.k_rows = (int)a->N;
+        GE_TRY(run_grad_product<BF>(false, p, pl.dx, a->M, a->K, pl.N8, a->dX, a->lddx, nullptr, false, false, nullptr,
+                                    part, s));
+    }
+    if (a->dW) {
+        LinParams p = {};
+        p.A = dz.p;
+        p.lda = dz.ld;
+        p.m_read = (int)pl.N8;
+        p.B = x.p;
+        p.ldb = x.ld;
+        p.n_read = (int)round_up(a->K, 8);
+        p.k_rows = (int)a->M;
+        GE_TRY(run_grad_product<BF>(true, p, pl.dw, a->N, a->K, a->M, a->dW, a->lddw, nullptr, false, false, nullptr,
+                                    part, s));
+    }
+    return GEMM_EPI_OK;
+}
+
+// ---- cross entropy ---------------------------------------------------------------
+constexpr unsigned kSquareTiles = 1u << kLinBig | 1u << kLinSmall;
+
+struct XentPlan {
+    bool skinny = false;
+    StagePlan2 st;
+    ProductPlan pl;
+    int nparts = 0;
+    int64_t off_max = 0, off_sum = 0, off_tlogit = 0, bytes = 0;
+};
+
+int check_xent(const ge_linear_xent_args *a)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_dims(a->T, a->V, a->K));
+    if (!a->W || (a->T > 0 && (!a->X || !a->target))) return GEMM_EPI_ERR_NULL_INPUT;
+    if (a->T > 0 && (!a->loss || !a->lse)) return GEMM_EPI_ERR_NULL_OUTPUT;
+    GE_CHECK(check_dtype(a->dtype));
+    GE_CHECK(check_matrix(a->W, a->ldw, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+    if (a->X) GE_CHECK(check_matrix(a->X, a->ldx, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+    if (!aligned(a->target, 8) || !aligned(a->loss, 4) || !aligned(a->lse, 4)) return GEMM_EPI_ERR_ALIGN;
+    return GEMM_EPI_OK;
+}
+
+int plan_xent(const ge_linear_xent_args *a, XentPlan &pl)
+{
+    GE_CHECK(check_xent(a));
+    if (a->T == 0) return GEMM_EPI_OK;
+    Layout lay;
+    pl.skinny = a->T <= kSkinnyRows;
+    if (pl.skinny) {
+        pl.nparts = (int)ceil_div(a->V, 64);
+    } else {
+        pl.st = plan_staging2(a->X, a->ldx, a->T, a->W, a->ldw, a->V, a->K, lay);
+        pl.pl = plan_product(a->T, a->V, a->K, kSquareTiles, 0);
+        if (!product_fits(pl.pl)) return GEMM_EPI_ERR_SHAPE;
+        pl.nparts = pl.pl.tiles_n;
+    }
+    pl.off_max = lay.take(a->T * pl.nparts * 4);
+    pl.off_sum = lay.take(a->T * pl.nparts * 4);
+    pl.off_tlogit = lay.take(a->T * 4);
+    pl.bytes = lay.bytes;
+    return GEMM_EPI_OK;
+}
+
+template <bool BF>
+int run_xent(const ge_linear_xent_args *a, const XentPlan &pl)
+{
+    hipStream_t s = (hipStream_t)a->stream;
+    char *ws = (char *)a->workspace;
+    float *pmax = (float *)(ws + pl.off_max), *psum = (float *)(ws + pl.off_sum),
+          *tlogit = (float *)(ws + pl.off_tlogit);
+    if (pl.skinny) {
+        SkinnyParams q = {};
+        q.X = (const _Float16 *)a->X;
+        q.W = (const _Float16 *)a->W;
+        q.ldx = a->ldx;
+        q.ldw = a->ldw;
+        q.M = (int)a->T;
+        q.N = (int)a->V;
+        q.K = (int)a->K;
+        q.target = a->target;
+        q.part_max = pmax;
+        q.part_sum = psum;
+        q.tlogit = tlogit;
+        q.nparts = pl.nparts;
+        GE_TRY(launch(skinny_kernel<BF, true, ACT_IDENTITY>, dim3(pl.nparts), dim3(256), s, q));
+    } else {
+        Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
+        GE_TRY(run_staging(pl.st, ws, a->K, x, a->T, w, a->V, s));
+        LinParams p = {};
+        set_product(p, pl.pl, a->T, a->V, round_up(a->K, 8));
+        p.A = x.p;
+        p.lda = x.ld;
+        p.B = w.p;
+        p.ldb = w.ld;
+        p.target = a->target;
+        p.part_max = pmax;
+        p.part_sum = psum;
+        p.nparts = pl.nparts;
+        p.tlogit = tlogit;
+        GE_TRY(BF ? lin_launch_xent_bf16(LE_XFWD, pl.pl.tile, p, p.num_tiles, s)
+                  : lin_launch_xent_f16(LE_XFWD, pl.pl.tile, p, p.num_tiles, s));
+    }
+    return hip_status(launch(xent_loss_kernel, dim3((unsigned)a->T), dim3(pl.nparts > 128 ? 256 : 64), s,
+                             (const float *)pmax, (const float *)psum, pl.nparts, (const float *)tlogit, a->target,
+                             a->V, a->ignore_index, a->loss, a->lse));
+}
+
+// The vocabulary goes in pieces of `piece` columns: P of one piece is written
+// by one product and read by two.  A piece as large as 128 MiB of P (half the
+// last-level cache) keeps those reads off HBM; more pieces cost a round trip of
+// dX's fp32 accumulator each, T K 8 bytes against 2 T K piece operations, so a
+// piece is not made shorter than 8192 columns.
+constexpr int64_t kPieceBytes = 128 << 20, kPieceMin = 8192;
+
+struct XentGradPlan {
+    StagePlan2 st;
+    int64_t piece = 0, pld = 0;
+    int pieces = 0;
+    ProductPlan p, dx, dw;            // of a full piece
+    ProductPlan p_last, dx_last, dw_last;
+    int64_t off_rows = 0, off_alpha = 0, off_p = 0, off_acc = 0, off_part = 0, bytes = 0;
+};
+
+int check_xent_grad(const ge_linear_xent_backward_args *a)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_dims(a->T, a->V, a->K));
+    if (!a->dX && !a->dW) return GEMM_EPI_ERR_NULL_OUTPUT;
+    if (!a->W || (a->T > 0 && (!a->X || !a->target || !a->lse || !a->dloss))) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_dtype(a->dtype));
+    GE_CHECK(check_matrix(a->W, a->ldw, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+    if (a->X) GE_CHECK(check_matrix(a->X, a->ldx, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+    if (a->dX) GE_CHECK(check_matrix(a->dX, a->lddx, a->K, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->dW) GE_CHECK(check_matrix(a->dW, a->lddw, a->K, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (!aligned(a->target, 8) || !aligned(a->dloss, 4) || !aligned(a->lse, 4)) return GEMM_EPI_ERR_ALIGN;
+    return GEMM_EPI_OK;
+}
+
+int plan_xent_grad(const ge_linear_xent_backward_args *a, XentGradPlan &pl)
+{
+    GE_CHECK(check_xent_grad(a));
+    if (a->T == 0) return GEMM_EPI_OK;
+    Layout lay;
+    pl.st = plan_staging2(a->X, a->ldx, a->T, a->W, a->ldw, a->V, a->K, lay);
+    int64_t piece = std::max(kPieceMin, kPieceBytes / (a->T * 2) / 256 * 256);
+    pl.pieces = (int)ceil_div(a->V, piece);
+    piece = round_up(ceil_div(a->V, pl.pieces), 256);  // even pieces
+    pl.pieces = (int)ceil_div(a->V, piece);
+    pl.piece = pl.pieces == 1 ? a->V : piece;
+    pl.pld = round_up(pl.piece, 8);
+    if (pl.pld > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
+    int64_t part = 0;
+    auto plan = [&](int64_t n, ProductPlan &p, ProductPlan &dx, ProductPlan &dw) {
+        p = plan_product(a->T, n, a->K, kSquareTiles, 0);
+        dx = plan_product(a->T, a->K, round_up(n, 8), 0xF, 0xF);
+        dw = plan_product(n, a->K, a->T, 0xF, 0xF);
+        if (a->dX) part = std::max(part, dx.part_bytes);
+        if (a->dW) part = std::max(part, dw.part_bytes);
+        return product_fits(p) && product_fits(dx) && product_fits(dw);
+    };
+    const int64_t last = a->V - (pl.pieces - 1) * pl.piece;
+    if (!plan(pl.piece, pl.p, pl.dx, pl.dw) || !plan(last, pl.p_last, pl.dx_last, pl.dw_last))
+        return GEMM_EPI_ERR_SHAPE;
+    pl.off_rows = lay.take(a->T * (int64_t)sizeof(XentRow));
+    pl.off_alpha = lay.take(4);
+    pl.off_p = lay.take(a->T * pl.pld * 2);
+    if (a->dX && pl.pieces > 1) pl.off_acc = lay.take(a->T * round_up(a->K, 8) * 4);
+    pl.off_part = lay.take(part);
+    pl.bytes = lay.bytes;
+    return GEMM_EPI_OK;
+}
+
+template <bool BF>
+int run_xent_grad(const ge_linear_xent_backward_args *a, const XentGradPlan &pl)
+{
+    hipStream_t s = (hipStream_t)a->stream;
+    char *ws = (char *)a->workspace;
+    if (a->T == 0) return a->dW ? hip_status(run_zero(a->dW, a->lddw * 2, a->V, a->K * 2, s)) : GEMM_EPI_OK;
+    XentRow *rows = (XentRow *)(ws + pl.off_rows);
+    float *alpha = (float *)(ws + pl.off_alpha);
+    GE_TRY(launch(xent_rows_kernel, dim3(1), dim3(1024), s, (int)a->T, a->V, a->ignore_index, a->dloss, a->lse,
+                  a->target, rows, alpha));
+    Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
+    GE_TRY(run_staging(pl.st, ws, a->K, x, a->T, w, a->V, s));
+    _Float16 *P = (_Float16 *)(ws + pl.off_p);
+    float *acc = pl.pieces > 1 ? (float *)(ws + pl.off_acc) : nullptr;
+    float *part = (float *)(ws + pl.off_part);
+    for (int c = 0; c < pl.pieces; c++) {
+        const bool last = c == pl.pieces - 1;
+        const int64_t v0 = c * pl.piece, n = last ? a->V - v0 : pl.piece;
+        LinParams p = {};
+        set_product(p, last ? pl.p_last : pl.p, a->T, n, round_up(a->K, 8));
+        p.A = x.p;
+        p.lda = x.ld;
+        p.B = w.p + v0 * w.ld;
+        p.ldb = w.ld;
+        p.rows = rows;
+        p.v0 = (int)v0;
+        p.D = P;
+        p.ldd = pl.pld;
+        p.n_store = (int)round_up(n, 8);
+        const int tile = last ? pl.p_last.tile : pl.p.tile;
+        GE_TRY(BF ? lin_launch_xent_bf16(LE_XP, tile, p, p.num_tiles, s)
+                  : lin_launch_xent_f16(LE_XP, tile, p, p.num_tiles, s));
+        if (a->dX) {
+            LinParams q = {};
+            q.A = P;
+            q.lda = pl.pld;
+            q.B = p.B;
+            q.ldb = w.ld;
+            q.n_read = (int)round_up(a->K, 8);
+            q.k_rows = (int)n;
+            GE_TRY(run_grad_product<BF>(false, q, last ? pl.dx_last : pl.dx, a->T, a->K, round_up(n, 8), a->dX, a->lddx,
+                                        acc, c > 0, !last, alpha, part, s));
+        }
+        if (a->dW) {
+            LinParams q = {};
+            q.A = P;
+            q.lda = pl.pld;
+            q.m_read = (int)round_up(n, 8);
+            q.B = x.p;
+            q.ldb = x.ld;
+            q.n_read = (int)round_up(a->K, 8);
+            q.k_rows = (int)a->T;
+            GE_TRY(run_grad_product<BF>(true, q, last ? pl.dw_last : pl.dw, n, a->K, a->T,
+                                        (char *)a->dW + v0 * a->lddw * 2, a->lddw, nullptr, false, false, alpha, part,
+                                        s));
+        }
+    }
+    return GEMM_EPI_OK;
+}
+
+// ---- norms and the residual step ----------------------------------------------
+int check_norm(int64_t T, int64_t H, int64_t G, int64_t post, int64_t pre, const void *gate, double scale, double eps,
+               int64_t dtype, int64_t sdtype)
+{
+    if (T < 0 || T > INT32_MAX || H < 1 || H > GE_MAX_HIDDEN || G < 1 || T % G != 0) return GEMM_EPI_ERR_SHAPE;
+    if (!gate && G != 1) return GEMM_EPI_ERR_SHAPE;
+    if (post < GE_NORM_NONE || post > GE_NORM_LAYER || (pre != GE_NORM_RMS && pre != GE_NORM_LAYER))
+        return GEMM_EPI_ERR_KIND;
+    GE_CHECK(check_dtype(dtype));
+    if (sdtype != dtype && sdtype != GEMM_EPI_F32) return GEMM_EPI_ERR_DTYPE;
+    if (!(eps >= 0.0) || scale != scale) return GEMM_EPI_ERR_SHAPE;
+    return GEMM_EPI_OK;
+}
+
+int check_norm_args(const ge_norm_residual_args *a)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_norm(a->T, a->hidden, a->G, a->post, a->pre, a->gate, a->scale, a->eps, a->dtype, a->stream_dtype));
+    const uintptr_t es = a->stream_dtype == GEMM_EPI_F32 ? 4 : 2;
+    for (const void *v : {a->w_post, a->w_pre, a->gate})
+        if (!aligned(v, 2)) return GEMM_EPI_ERR_ALIGN;
+    if (a->T == 0) return GEMM_EPI_OK;
+    GE_CHECK(check_matrix(a->H, a->ldh, a->hidden, es, GEMM_EPI_ERR_NULL_INPUT));
+    GE_CHECK(check_matrix(a->Y, a->ldy, a->hidden, 2, GEMM_EPI_ERR_NULL_INPUT));
+    GE_CHECK(check_matrix(a->H_out, a->ldho, a->hidden, es, GEMM_EPI_ERR_NULL_OUTPUT));
+    return check_matrix(a->X, a->ldx, a->hidden, 2, GEMM_EPI_ERR_NULL_OUTPUT);
+}
+
+// Calls f(threads per row, vectors per thread) for a row length.
+template <typename F>
+hipError_t dispatch_row(int64_t H, F &&f)
+{
+    if (H <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    if (H <= 1024) return f(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
+    if (H <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+    if (H <= 4096) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 1>{});
+    if (H <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+}
+
+template <bool BF, bool S32>
+hipError_t run_norm(const ge_norm_residual_args *a)
+{
+    NormParams p = {};
+    p.H = a->H;
+    p.Y = (const _Float16 *)a->Y;
+    p.w_post = (const _Float16 *)a->w_post;
+    p.w_pre = (const _Float16 *)a->w_pre;
+    p.gate = (const _Float16 *)a->gate;
+    p.H_out = a->H_out;
+    p.X = (_Float16 *)a->X;
+    p.ldh = a->ldh;
+    p.ldy = a->ldy;
+    p.ldho = a->ldho;
+    p.ldx = a->ldx;
+    p.hidden = (int)a->hidden;
+    p.rows_per_gate = (int)(a->T / a->G);
+    p.post = (int)a->post;
+    p.pre = (int)a->pre;
+    p.scale = (float)a->scale;
+    p.eps = (float)a->eps;
+    return dispatch_row(a->hidden, [&](auto tpr, auto nv) {
+        constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+        return launch(norm_residual_kernel<BF, S32, TPR, NV>, dim3((unsigned)a->T), dim3(TPR),
+                      (hipStream_t)a->stream, p);
+    });
+}
+
+// Runs of rows that share a gate row, and workgroups.  About 512 workgroups
+// walk the rows (two per CU), each at least 4 rows, so that the partial column
+// sums stay small beside the rows themselves.
+struct NormGradPlan {
+    int64_t rows_per_gate = 0, rows_per_run = 0, runs = 0, runs_per_block = 1, blocks = 0;
+    int runs_per_gate = 1;
+    int64_t off_post = 0, off_pre = 0, off_gate = 0, bytes = 0;
+};
+constexpr int64_t kNormBlocks = 512, kNormMinRows = 4;
+
+int plan_norm_grad(const ge_norm_residual_backward_args *a, NormGradPlan &pl)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_norm(a->T, a->hidden, a->G, a->post, a->pre, a->gate, a->scale, a->eps, a->dtype, a->stream_dtype));
+    if (a->hidden > GE_MAX_HIDDEN_GRAD) return GEMM_EPI_ERR_SHAPE;
+    const uintptr_t es = a->stream_dtype == GEMM_EPI_F32 ? 4 : 2;
+    for (const void *v : {a->w_post, a->w_pre, a->gate})
+        if (!aligned(v, 2)) return GEMM_EPI_ERR_ALIGN;
+    for (const void *v : {a->dw_post, a->dw_pre, a->dgate})
+        if (!aligned(v, 4)) return GEMM_EPI_ERR_ALIGN;
+    if (a->T == 0) return GEMM_EPI_OK;
+    GE_CHECK(check_matrix(a->dX, a->lddx, a->hidden, 2, GEMM_EPI_ERR_NULL_INPUT));
+    GE_CHECK(check_matrix(a->dH_out, a->lddho, a->hidden, es, GEMM_EPI_ERR_NULL_INPUT));
+    GE_CHECK(check_matrix(a->H_out, a->ldho, a->hidden, es, GEMM_EPI_ERR_NULL_INPUT));
+    GE_CHECK(check_matrix(a->Y, a->ldy, a->hidden, 2, GEMM_EPI_ERR_NULL_INPUT));
+    GE_CHECK(check_matrix(a->dH, a->lddh, a->hidden, es, GEMM_EPI_ERR_NULL_OUTPUT));
+    GE_CHECK(check_matrix(a->dY, a->lddy, a->hidden, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    pl.rows_per_gate = a->T / a->G;
+    const int64_t blocks = std::min(kNormBlocks, ceil_div(a->T, kNormMinRows));
+    pl.rows_per_run = std::min(pl.rows_per_gate, ceil_div(a->T, blocks));
+    pl.runs_per_gate = (int)ceil_div(pl.rows_per_gate, pl.rows_per_run);
+    pl.runs = a->G * pl.runs_per_gate;
+    pl.runs_per_block = pl.runs_per_gate > 1 ? 1 : ceil_div(pl.runs, blocks);
+    pl.blocks = ceil_div(pl.runs, pl.runs_per_block);
+    Layout lay;
+    if (a->dw_post && a->post != GE_NORM_NONE) pl.off_post = lay.take(pl.blocks * a->hidden * 4);
+    if (a->dw_pre) pl.off_pre = lay.take(pl.blocks * a->hidden * 4);
+    if (a->dgate && pl.runs_per_gate > 1) pl.off_gate = lay.take(pl.runs * a->hidden * 4);
+    pl.bytes = lay.bytes;
+    return GEMM_EPI_OK;
+}
+
+template <bool BF, bool S32>
+int run_norm_grad(const ge_norm_residual_backward_args *a, const NormGradPlan &pl)
+{
+    hipStream_t s = (hipStream_t)a->stream;
+    char *ws = (char *)a->workspace;
+    const int64_t H = a->hidden;
+    const bool post = a->dw_post && a->post != GE_NORM_NONE;
+    if (a->dw_post && !post) GE_TRY(run_zero(a->dw_post, H * 4, 1, H * 4, s));
+    if (a->T == 0) {
+        if (post) GE_TRY(run_zero(a->dw_post, H * 4, 1, H * 4, s));
+        if (a->dw_pre) GE_TRY(run_zero(a->dw_pre, H * 4, 1, H * 4, s));
+        if (a->dgate) GE_TRY(run_zero(a->dgate, H * 4, a->G, H * 4, s));
+        return GEMM_EPI_OK;
+    }
+    NormGradParams p = {};
+    p.dX = (const _Float16 *)a->dX;
+    p.Y = (const _Float16 *)a->Y;
+    p.w_post = a->post != GE_NORM_NONE ? (const _Float16 *)a->w_post : nullptr;
+    p.w_pre = (const _Float16 *)a->w_pre;
+    p.gate = (const _Float16 *)a->gate;
+    p.dH_out = a->dH_out;
+    p.H_out = a->H_out;
+    p.dH = a->dH;
+    p.dY = (_Float16 *)a->dY;
+    p.lddx = (int)a->lddx;
+    p.lddho = (int)a->lddho;
+    p.ldho = (int)a->ldho;
+    p.ldy = (int)a->ldy;
+    p.lddh = (int)a->lddh;
+    p.lddy = (int)a->lddy;
+    p.hidden = (int)H;
+    p.post = (int)a->post;
+    p.pre = (int)a->pre;
+    p.scale = (float)a->scale;
+    p.eps = (float)a->eps;
+    p.rows_per_gate = (int)pl.rows_per_gate;
+    p.rows_per_run = (int)pl.rows_per_run;
+    p.runs_per_gate = pl.runs_per_gate;
+    p.runs = (int)pl.runs;
+    p.runs_per_block = (int)pl.runs_per_block;
+    p.gate_direct = pl.runs_per_gate == 1;
+    p.p_post = post ? (float *)(ws + pl.off_post) : nullptr;
+    p.p_pre = a->dw_pre ? (float *)(ws + pl.off_pre) : nullptr;
+    p.dgate = !a->dgate || p.gate_direct ? a->dgate : (float *)(ws + pl.off_gate);
+    // 8 elements per thread, in whole waves; two workgroups of up to 640 fit on
+    // a compute unit (rows of single elements take more registers: not there)
+    const dim3 g((unsigned)pl.blocks), b((unsigned)round_up(ceil_div(H, 8), 64));
+    const bool quads = H % 4 == 0;
+    if (H <= 4096)
+        GE_TRY(launch(quads ? norm_residual_grad_kernel<BF, S32, 512, 4> : norm_residual_grad_kernel<BF, S32, 512, 1>,
+                      g, b, s, p));
+    else if (H <= 5120 && quads)
+        GE_TRY(launch(norm_residual_grad_kernel<BF, S32, 640, 4>, g, b, s, p));
+    else
+        GE_TRY(launch(quads ? norm_residual_grad_kernel<BF, S32, 1024, 4> : norm_residual_grad_kernel<BF, S32, 1024, 1>,
+                      g, b, s, p));
+    ColSumParams c = {};
+    c.partial[0] = p.p_post;
+    c.out[0] = post ? a->dw_post : nullptr;
+    c.partial[1] = p.p_pre;
+    c.out[1] = a->dw_pre;
+    c.parts[0] = c.parts[1] = (int)pl.blocks;
+    c.partial[2] = p.dgate;
+    const bool gates = a->dgate && !p.gate_direct;
+    c.out[2] = gates ? a->dgate : nullptr;
+    c.parts[2] = pl.runs_per_gate;
+    c.ld = c.cols = (int)H;
+    if (!c.out[0] && !c.out[1] && !gates) return GEMM_EPI_OK;
+    return hip_status(launch(colsum_kernel, dim3((unsigned)ceil_div(H, 64), 2 + (gates ? (unsigned)a->G : 0u)),
+                             dim3(1024), s, c));
+}
+
+}  // namespace
+
+extern "C" {
+
+int ge_linear_workspace(const ge_linear_args *a, int64_t *bytes)
+{
+    LinearPlan pl;
+    GE_CHECK(plan_linear(a, pl));
+    if (!bytes) return GEMM_EPI_ERR_NULL_OUTPUT;
+    *bytes = pl.bytes;
+    return GEMM_EPI_OK;
+}
+
+int ge_linear(const ge_linear_args *a)
+{
+    LinearPlan pl;
+    GE_CHECK(plan_linear(a, pl));
+    GE_CHECK(check_workspace(a->workspace, a->workspace_bytes, pl.bytes));
+    if (a->M == 0) return GEMM_EPI_OK;
+    return a->dtype == GEMM_EPI_BF16 ? run_linear<true>(a, pl) : run_linear<false>(a, pl);
+}
+
+int ge_linear_backward_workspace(const ge_linear_backward_args *a, int64_t *bytes)
+{
+    LinearGradPlan pl;
+    GE_CHECK(plan_linear_grad(a, pl));
+    if (!bytes) return GEMM_EPI_ERR_NULL_OUTPUT;
+    *bytes = pl.bytes;
+    return GEMM_EPI_OK;
+}
+
+int ge_linear_backward(const ge_linear_backward_args *a)
+{
+    LinearGradPlan pl;
+    GE_CHECK(plan_linear_grad(a, pl));
+    GE_CHECK(check_workspace(a->workspace, a->workspace_bytes, pl.bytes));
+    return a->dtype == GEMM_EPI_BF16 ? run_linear_grad<true>(a, pl) : run_linear_grad<false>(a, pl);
+}
+
+int ge_linear_xent_workspace(const ge_linear_xent_args *a, int64_t *bytes)
+{
+    XentPlan pl;
+    GE_CHECK(plan_xent(a, pl));
+    if (!bytes) return GEMM_EPI_ERR_NULL_OUTPUT;
+    *bytes = pl.bytes;
+    return GEMM_EPI_OK;
+}
+
+int ge_linear_xent(const ge_linear_xent_args *a)
+{
+    XentPlan pl;
+    GE_CHECK(plan_xent(a, pl));
+    GE_CHECK(check_workspace(a->workspace, a->workspace_bytes, pl.bytes));
+    if (a->T == 0) return GEMM_EPI_OK;
+    return a->dtype == GEMM_EPI_BF16 ? run_xent<true>(a, pl) : run_xent<false>(a, pl);
+}
+
+int ge_linear_xent_backward_workspace(const ge_linear_xent_backward_args *a, int64_t *bytes)
+{
+    XentGradPlan pl;
+    GE_CHECK(plan_xent_grad(a, pl));
+    if (!bytes) return GEMM_EPI_ERR_NULL_OUTPUT;
+    *bytes = pl.bytes;
+    return GEMM_EPI_OK;
+}
+
+int ge_linear_xent_backward(const ge_linear_xent_backward_args *a)
+{
+    XentGradPlan pl;
+    GE_CHECK(plan_xent_grad(a, pl));
+    GE_CHECK(check_workspace(a->workspace, a->workspace_bytes, pl.bytes));
+    return a->dtype == GEMM_EPI_BF16 ? run_xent_grad<true>(a, pl) : run_xent_grad<false>(a, pl);
+}
+
+int ge_norm_residual(const ge_norm_residual_args *a)
+{
+    GE_CHECK(check_norm_args(a));
+    if (a->T == 0) return GEMM_EPI_OK;
+    if (a->stream_dtype == GEMM_EPI_F32)
+        return hip_status(a->dtype == GEMM_EPI_BF16 ? run_norm<true, true>(a) : run_norm<false, true>(a));
+    return hip_status(a->dtype == GEMM_EPI_BF16 ? run_norm<true, false>(a) : run_norm<false, false>(a));
+}
+
+int ge_norm_residual_backward_workspace(const ge_norm_residual_backward_args *a, int64_t *bytes)
+{
+    NormGradPlan pl;
+    GE_CHECK(plan_norm_grad(a, pl));
+    if (!bytes) return GEMM_EPI_ERR_NULL_OUTPUT;
+    *bytes = pl.bytes;
+    return GEMM_EPI_OK;
+}
+
+int ge_norm_residual_backward(const ge_norm_residual_backward_args *a)
+{
+    NormGradPlan pl;
+    GE_CHECK(plan_norm_grad(a, pl));
+    GE_CHECK(check_workspace(a->workspace, a->workspace_bytes, pl.bytes));
+    if (a->stream_dtype == GEMM_EPI_F32)
+        return a->dtype == GEMM_EPI_BF16 ? run_norm_grad<true, true>(a, pl) : run_norm_grad<false, true>(a, pl);
+    return a->dtype == GEMM_EPI_BF16 ? run_norm_grad<true, false>(a, pl) : run_norm_grad<false, false>(a, pl);
+}
+
+}  // extern "C"

@@ -1,0 +1,441 @@
+// linear_small.hpp -- the kernels around the matrix products of
+// linear_gemm.hpp: products with few rows, dZ and the bias gradient, the sum
+// over splits of the contraction, operand staging, and the row passes of the
+// cross entropy.  All are bound by memory or by latency.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "linear_gemm.hpp"
+
+namespace gemm_epi {
+
+// 16-byte access at any element alignment (global memory takes it at the
+// rate of the cache lines it touches)
+typedef half8 half8u __attribute__((aligned(2)));
+typedef f32x4 f32x4u __attribute__((aligned(4)));
+
+// 8 consecutive elements, the first n of which exist (the rest read as zeros)
+__device__ __forceinline__ half8 load8(const _Float16 *p, int n)
+{
+    if (n >= 8) return *(const half8u *)p;
+    half8 v = {};
+#pragma unroll
+    for (int e = 0; e < 7; e++)
+        if (e < n) v[e] = p[e];
+    return v;
+}
+__device__ __forceinline__ void store8(_Float16 *p, half8 v, int n)
+{
+    if (n >= 8) {
+        *(half8u *)p = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; e++)
+        if (e < n) p[e] = v[e];
+}
+
+// ---------------------------------------------------------------------------
+// Products with at most 16 rows of X (single tokens): bound by reading W
+// once.  A wave holds 16 rows of W against all rows of X in one 16x16x32
+// MFMA block; each lane reads 16 bytes of a W row per MFMA, straight into the
+// operand layout, 8 MFMAs (512 contiguous bytes a row) per group of loads and
+// the next group's loads in flight.  No LDS on the way in, so any alignment
+// and any K run the same code.  Rows past N or M repeat the last one and are
+// never stored.
+//   linear: the workgroup's four waves take turns over K for the same 16
+//     rows (N / 16 workgroups fill the chip from N = 4096 on), their sums meet
+//     in LDS, 256 threads apply the epilogue.
+//   cross entropy: every wave has 16 rows of its own (the vocabulary fills the
+//     chip) and all of K; the workgroup leaves the softmax statistics of its 64
+//     columns.
+// ---------------------------------------------------------------------------
+struct SkinnyParams {
+    const _Float16 *X, *W;
+    int64_t ldx, ldw;
+    int M, N, K;
+    const _Float16 *bias, *R;
+    _Float16 *D, *Z;
+    int64_t ldr, ldd, ldz;
+    const int64_t *target;
+    float *part_max, *part_sum, *tlogit;
+    int nparts;
+};
+
+template <bool BF, bool XENT, int ACT>
+__global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
+{
+    constexpr int U = 8, SPAN = 32 * U;
+    __shared__ float red[XENT ? 2 * 4 * 16 : 4 * 256];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int li = lane & 15, lg = lane >> 4;
+    const int n0 = XENT ? blockIdx.x * 64 + wave * 16 : blockIdx.x * 16;
+    const _Float16 *w = p.W + (int64_t)min(n0 + li, p.N - 1) * p.ldw + lg * 8;
+    const _Float16 *x = p.X + (int64_t)min(li, p.M - 1) * p.ldx + lg * 8;
+    const int step = XENT ? SPAN : 4 * SPAN;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    half8 wv[U], xv[U];
+    auto fetch = [&](int k0) {
+        if (k0 + SPAN <= p.K) {
+#pragma unroll
+            for (int u = 0; u < U; u++) wv[u] = __builtin_nontemporal_load((const half8u *)(w + k0 + u * 32));
+#pragma unroll
+            for (int u = 0; u < U; u++) xv[u] = *(const half8u *)(x + k0 + u * 32);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int n = p.K - (k0 + u * 32 + lg * 8);
+                wv[u] = load8(w + k0 + u * 32, n);
+                xv[u] = load8(x + k0 + u * 32, n);
+            }
+        }
+    };
+    int k0 = XENT ? 0 : wave * SPAN;
+    if (k0 < p.K) fetch(k0);
+    while (k0 < p.K) {
+        half8 wc[U], xc[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            wc[u] = wv[u];
+            xc[u] = xv[u];
+        }
+        k0 += step;
+        if (k0 < p.K) fetch(k0);
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if constexpr (BF)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wc[u]),
+                                                              __builtin_bit_cast(bf16x8, xc[u]), acc, 0, 0, 0);
+            else
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(wc[u], xc[u], acc, 0, 0, 0);
+        }
+    }
+    // lane (li, lg), register r: row li of X, row 4 lg + r of W
+    if constexpr (!XENT) {
+        *(f32x4 *)(red + (wave * 64 + lane) * 4) = acc;
+        __syncthreads();
+        const int wr = tid & 15, xr = tid >> 4;  // adjacent threads on adjacent columns of D
+        const int at = ((wr >> 2) * 16 + xr) * 4 + (wr & 3);
+        const int n = n0 + wr;
+        if (xr < p.M && n < p.N) {
+            const float s = (red[at] + red[256 + at]) + (red[512 + at] + red[768 + at]);
+            const float z = s + (p.bias ? ld16<BF>(p.bias[n]) : 0.0f);
+            const float r = p.R ? ld16<BF>(p.R[xr * p.ldr + n]) : 0.0f;
+            if (p.Z) p.Z[xr * p.ldz + n] = st16<BF>(z);
+            p.D[xr * p.ldd + n] = st16<BF>(lin_act<ACT>(z) + r);
+        }
+    } else {
+        float m = -__builtin_inff();
+        const int64_t t = li < p.M ? p.target[li] : -1;
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int v = n0 + 4 * lg + r;
+            if (v >= p.N) acc[r] = -__builtin_inff();
+            if (li < p.M && v < p.N && v == t) p.tlogit[li] = acc[r];
+            m = __builtin_fmaxf(m, acc[r]);
+        }
+        m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+        m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+        float s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; r++) s += exp2_hw((acc[r] - ref) * kLog2e);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (lg == 0) {
+            red[wave * 16 + li] = m;
+            red[64 + wave * 16 + li] = s;
+        }
+        __syncthreads();
+        if (tid < p.M) {
+            m = red[tid];
+            s = red[64 + tid];
+#pragma unroll
+            for (int u = 1; u < 4; u++) softmax_join(m, s, red[u * 16 + tid], red[64 + u * 16 + tid]);
+            const int64_t o = (int64_t)tid * p.nparts + blockIdx.x;
+            p.part_max[o] = m;
+            p.part_sum[o] = s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dZ = dD act'(Z), rounded once to the element type (it is an MFMA operand),
+// in rows of ldo elements zero-padded to a multiple of 8 columns, and the
+// column sums of the unrounded dZ over each strip of rows.  A block covers 256
+// columns x a strip: 32 lanes of 8 columns by 8 rows at a time; one pass over
+// dD and Z, bound by their bytes.
+// ---------------------------------------------------------------------------
+struct DzParams {
+    const _Float16 *dD, *Z;
+    int64_t ldd, ldz, ldo;
+    _Float16 *out;  // NULL: only the sums (identity, dD usable as it is)
+    float *partial;  // [strips][N8], or NULL
+    int M, N, N8, rows_per_strip;
+};
+
+template <bool BF, int ACT>
+__global__ __launch_bounds__(256) void dz_kernel(DzParams p)
+{
+    __shared__ float red[8][256 + 8];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int c = blockIdx.x * 256 + tx * 8;
+    const int n = p.N - c;  // columns that exist from c on
+    const int r0 = blockIdx.y * p.rows_per_strip, r1 = min(p.M, r0 + p.rows_per_strip);
+    float sum[8] = {};
+    if (c < p.N8) {
+        auto one = [&](int m, half8 d, half8 z) {
+            half8 o;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                float v = ld16<BF>(d[e]);
+                if constexpr (ACT != ACT_IDENTITY) v *= lin_act_grad<ACT>(ld16<BF>(z[e]));
+                if (e >= n) v = 0.0f;
+                sum[e] += v;
+                o[e] = st16<BF>(v);
+            }
+            if (p.out) *(half8 *)(p.out + (int64_t)m * p.ldo + c) = o;
+        };
+        int m = r0 + ty;
+        for (; m + 24 < r1; m += 32) {  // four rows' loads in flight
+            half8 d[4], z[4] = {};
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                d[u] = load8(p.dD + (int64_t)(m + 8 * u) * p.ldd + c, n);
+                if constexpr (ACT != ACT_IDENTITY) z[u] = load8(p.Z + (int64_t)(m + 8 * u) * p.ldz + c, n);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; u++) one(m + 8 * u, d[u], z[u]);
+        }
+        for (; m < r1; m += 8) {
+            const half8 d = load8(p.dD + (int64_t)m * p.ldd + c, n);
+            half8 z = {};
+            if constexpr (ACT != ACT_IDENTITY) z = load8(p.Z + (int64_t)m * p.ldz + c, n);
+            one(m, d, z);
+        }
+    }
+    if (!p.partial) return;
+#pragma unroll
+    for (int e = 0; e < 8; e++) red[ty][tx * 8 + e] = sum[e];
+    __syncthreads();
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    float s = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 8; y++) s += red[y][threadIdx.x];
+    if (col < p.N8) p.partial[(int64_t)blockIdx.y * p.N8 + col] = s;
+}
+
+// The last step of every column sum: out[c] = sum over parts, in a fixed order,
+// of partial[part][c].  Grid row 0 and 1 are two sums over all parts; grid rows
+// from 2 on are the groups of a third, each over parts of its own.  64 columns
+// per block; 16 groups of threads take every 16th part, 8 loads in flight.
+struct ColSumParams {
+    const float *partial[3];
+    float *out[3];  // NULL: not wanted
+    int parts[3];
+    int ld, cols;
+};
+__global__ __launch_bounds__(1024) void colsum_kernel(ColSumParams p)
+{
+    __shared__ float red[16][64];
+    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + tx, v = min((int)blockIdx.y, 2), g = (int)blockIdx.y - v;
+    if (!p.out[v]) return;
+    const int parts = p.parts[v];
+    const float *src = p.partial[v] + (int64_t)g * parts * p.ld + c;
+    float s = 0.0f;
+    if (c < p.cols) {
+        int i = ty;
+        for (; i + 112 < parts; i += 128) {
+            float x[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++) x[u] = src[(int64_t)(i + 16 * u) * p.ld];
+            s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        }
+        for (; i < parts; i += 16) s += src[(int64_t)i * p.ld];
+    }
+    red[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && c < p.cols) {
+        s = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 16; u++) s += red[u][tx];
+        p.out[v][(int64_t)g * p.cols + c] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The sum over the splits of a product's contraction, in split order, and the
+// epilogue the product would have had: 8 columns per thread.
+// ---------------------------------------------------------------------------
+struct SplitSumParams {
+    const float *part;  // [splits][M][ldc]
+    int splits, M, N;
+    int64_t ldc, c_split;
+    const _Float16 *bias, *R;
+    _Float16 *D, *Z;
+    int64_t ldr, ldd, ldz;
+    float *C32;  // LE_OUT: accumulator, rows of ldc
+    int acc_in, acc_out;
+    const float *alpha;
+};
+
+template <bool BF, int EPI, int ACT>
+__global__ __launch_bounds__(256) void split_sum_kernel(SplitSumParams p)
+{
+    const int groups = (p.N + 7) / 8;
+    const int64_t total = (int64_t)p.M * groups;
+    float alpha = 1.0f;
+    if constexpr (EPI == LE_OUT)
+        if (p.alpha) alpha = *p.alpha;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int m = (int)(i / groups), c = (int)(i - (int64_t)m * groups) * 8, n = p.N - c;
+        const float *src = p.part + (int64_t)m * p.ldc + c;
+        float v[8] = {};
+        if (EPI == LE_OUT && p.acc_in) {
+            const float *a = p.C32 + (int64_t)m * p.ldc + c;
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[e] = a[e];
+        }
+        for (int s = 0; s < p.splits; s++, src += p.c_split) {
+            const f32x4 a = *(const f32x4 *)src, b = *(const f32x4 *)(src + 4);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                v[e] += a[e];
+                v[4 + e] += b[e];
+            }
+        }
+        half8 d, z;
+        if constexpr (EPI == LE_LINEAR) {
+            half8 bias = {}, r = {};
+            if (p.bias) bias = load8(p.bias + c, n);
+            if (p.R) r = load8(p.R + (int64_t)m * p.ldr + c, n);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float t = v[e] + ld16<BF>(bias[e]);
+                z[e] = st16<BF>(t);
+                d[e] = st16<BF>(lin_act<ACT>(t) + ld16<BF>(r[e]));
+            }
+            if (p.Z) store8(p.Z + (int64_t)m * p.ldz + c, z, n);
+            store8(p.D + (int64_t)m * p.ldd + c, d, n);
+        } else if (p.acc_out) {
+            float *a = p.C32 + (int64_t)m * p.ldc + c;
+            *(f32x4 *)a = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4 *)(a + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) d[e] = st16<BF>(v[e] * alpha);
+            store8(p.D + (int64_t)m * p.ldd + c, d, n);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Staging: operands whose rows are not 16-byte aligned, or not a multiple of
+// 8 elements long, are copied to rows of ldo elements (a multiple of 8), zeros
+// past the row's end.  One grid row per tensor.
+// ---------------------------------------------------------------------------
+struct PadParams {
+    const _Float16 *src[2];
+    _Float16 *dst[2];
+    int64_t lds[2], rows[2];
+    int cols, ldo;
+};
+__global__ __launch_bounds__(256) void pad_rows_kernel(PadParams p)
+{
+    const int v = blockIdx.y, groups = p.ldo / 8;
+    const int64_t total = p.rows[v] * groups;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / groups;
+        const int c = (int)(i - r * groups) * 8;
+        *(half8 *)(p.dst[v] + r * p.ldo + c) = load8(p.src[v] + r * p.lds[v] + c, p.cols - c);
+    }
+}
+
+// Zeros (gradients of an empty batch): a kernel, so that the call records into a HIP graph.
+__global__ __launch_bounds__(256) void zero_rows_kernel(char *dst, int64_t ld_bytes, int64_t rows, int64_t halves)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * halves; i += (int64_t)gridDim.x * 256)
+        *(uint16_t *)(dst + i / halves * ld_bytes + i % halves * 2) = 0;
+}
+
+// ---------------------------------------------------------------------------
+// Cross entropy, the row passes.
+// ---------------------------------------------------------------------------
+// Joins the column tiles' (maximum, sum) pairs of one row per block.
+__global__ __launch_bounds__(256) void xent_loss_kernel(const float *part_max, const float *part_sum, int nparts,
+                                                        const float *tlogit, const int64_t *target, int64_t V,
+                                                        int64_t ignore, float *loss, float *lse)
+{
+    __shared__ float rm[4], rs[4];
+    const int64_t row = blockIdx.x;
+    const float *pm = part_max + row * nparts, *ps = part_sum + row * nparts;
+    float m = -__builtin_inff(), s = 0.0f;
+    for (int i = threadIdx.x; i < nparts; i += blockDim.x) softmax_join(m, s, pm[i], ps[i]);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
+        softmax_join(m, s, m2, s2);
+    }
+    if ((threadIdx.x & 63) == 0) {
+        rm[threadIdx.x >> 6] = m;
+        rs[threadIdx.x >> 6] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int u = 1; u < (int)blockDim.x / 64; u++) softmax_join(m, s, rm[u], rs[u]);
+        const float l = m + logf(s);
+        const int64_t t = target[row];
+        lse[row] = l;
+        if (t == ignore)
+            loss[row] = 0.0f;
+        else if (t < 0 || t >= V)
+            loss[row] = __builtin_nanf("");
+        else
+            loss[row] = l - tlogit[row];
+    }
+}
+
+// The gradient's row data.  P is stored in 16 bits, and fp16 has no room for
+// a probability of 1e-6 times a loss of 1/T.  So the incoming gradients are
+// divided by the power of two s at or below their largest magnitude and
+// multiplied by 2^14: |P| stays below 2^15 + 1 < 65504 and a probability
+// down to 2^-28 is still a normal number.  Powers of two, so nothing is
+// rounded; the products' fp32 sums are multiplied by s 2^-14 (`alpha`) before
+// their one rounding.  One block; T values are read twice.
+__global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, int64_t ignore, const float *dloss,
+                                                         const float *lse, const int64_t *target, XentRow *rows,
+                                                         float *alpha)
+{
+    __shared__ float red[16];
+    float top = 0.0f;
+    for (int t = threadIdx.x; t < T; t += 1024) {
+        const float a = __builtin_fabsf(dloss[t]);
+        if (target[t] != ignore && a < __builtin_inff()) top = __builtin_fmaxf(top, a);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o));
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 16; u++) top = __builtin_fmaxf(top, red[u]);
+    // the exponent of top, kept where both 2^(14-e) and 2^(e-14) are normal
+    int e = (int)((__builtin_bit_cast(uint32_t, top) >> 23) & 255) - 127;
+    e = e < -100 ? -100 : (e > 126 ? 126 : e);
+    const float up = __builtin_bit_cast(float, (uint32_t)(14 - e + 127) << 23);
+    if (threadIdx.x == 0) *alpha = __builtin_bit_cast(float, (uint32_t)(e - 14 + 127) << 23);
+    for (int t = threadIdx.x; t < T; t += 1024) {
+        const int64_t c = target[t];
+        XentRow r;
+        r.lse = lse[t];
+        r.ignored = c == ignore;
+        r.target = c >= 0 && c < V ? (int)c : -1;
+        r.scale = dloss[t] * up;
+        if (!r.ignored && r.target < 0) r.scale = __builtin_nanf("");
+        rows[t] = r;
+    }
+}
+
+}  // namespace gemm_epi

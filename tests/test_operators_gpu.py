@@ -1,0 +1,690 @@
+"""The training and serving operators on the GPU against their definitions in
+64 bits, with elementwise bounds that are derived from the roundings each
+operator makes:
+
+ * u(t) = eps(t) / 2 relative for the one rounding of an output (plus half the
+   smallest subnormal for fp16);
+ * fp32 sums of n products: at most (n + 2) 2^-24 of the sum of magnitudes;
+ * an activation or its derivative: 4e-6 of its magnitude, and 1.13 times the
+   error of its argument (the largest slope of gelu);
+ * an intermediate that is an MFMA operand (dZ, P): u(t) of its magnitude,
+   summed with the magnitudes of the other operand.
+"""
+import math
+
+import pytest
+import torch
+
+import dense_gemm_elementwise_amd as ge
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+E24 = 2.0 ** -24
+IGNORE = -100
+
+
+def log(*a):
+    print(*a, flush=True)
+
+
+def u(t):
+    return torch.finfo(t).eps / 2
+
+
+def floor_of(t):
+    return {F16: 2.0 ** -25, BF16: 2.0 ** -134, F32: 2.0 ** -150}[t]
+
+
+def rnd(g, *shape, std=1.0, mean=0.0, t=BF16):
+    return (torch.randn(shape, generator=g, dtype=torch.float32) * std + mean).to(t).to(DEV)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def close(name, got, want, bound):
+    """|got - want| <= bound everywhere, `bound` a float64 tensor without the output's own rounding."""
+    got64 = got.double().cpu()
+    want, bound = want.cpu(), bound.cpu() if isinstance(bound, torch.Tensor) else bound
+    assert got64.shape == want.shape, name
+    assert not got64.isnan().any(), f"{name}: NaN"
+    lim = u(got.dtype) * want.abs() + floor_of(got.dtype) + bound * (1 + u(got.dtype))
+    bad = (got64 - want).abs() > lim
+    if bad.any():
+        i = int(bad.flatten().nonzero()[0])
+        raise AssertionError(f"{name}: {int(bad.sum())} of {bad.numel()} off, first at {i}: "
+                             f"{got64.flatten()[i]} want {want.flatten()[i]} bound {lim.flatten()[i]}")
+
+
+def act64(z, act):
+    if act == "relu":
+        return z.clamp(min=0)
+    if act == "silu":
+        return z * torch.sigmoid(z)
+    if act == "gelu":
+        return 0.5 * z * torch.erfc(-z * 0.5 ** 0.5)
+    return z
+
+
+def act_grad64(z, act):
+    if act == "relu":
+        return (z > 0).double()
+    if act == "silu":
+        return torch.sigmoid(z) * (1 + z * torch.sigmoid(-z))
+    if act == "gelu":
+        return 0.5 * torch.erfc(-z * 0.5 ** 0.5) + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    return torch.ones_like(z)
+
+
+def linear_ref(x, w, bias, residual, act):
+    """(D, Z) in 64 bits and the bounds of their errors before the last rounding."""
+    x, w = x.double().cpu(), w.double().cpu()
+    z = x @ w.t()
+    mag = x.abs() @ w.abs().t()
+    if bias is not None:
+        z = z + bias.double().cpu()
+        mag = mag + bias.double().cpu().abs()
+    bz = (x.shape[1] + 3) * E24 * mag
+    a = act64(z, act)
+    d, bd = a, 1.13 * bz + 4e-6 * a.abs()
+    if residual is not None:
+        d = d + residual.double().cpu()
+        bd = bd + E24 * d.abs()
+    return d, bd, z, bz
+
+
+SHAPES = [(1, 64, 64), (1, 1, 1), (1, 1003, 999), (3, 40, 8), (16, 520, 300), (17, 64, 64), (17, 1, 1), (33, 7, 5),
+          (64, 129, 72), (128, 128, 32), (129, 257, 33), (200, 264, 520), (257, 255, 264), (300, 1000, 1001)]
+
+
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_linear(shape, t):
+    M, N, K = shape
+    for n, act in enumerate(("identity", "relu", "gelu", "silu")):
+        log(f"[linear] {shape} {t} {act}")
+        g = gen(M * 31 + N + K + n)
+        x, w = rnd(g, M, K, t=t), rnd(g, N, K, std=K ** -0.5, t=t)
+        bias = rnd(g, N, std=0.5, t=t) if n != 1 else None
+        residual = rnd(g, M, N, t=t) if n != 2 else None
+        d, bd, z, bz = linear_ref(x, w, bias, residual, act)
+        got = ge.linear(x, w, bias, residual, act=act, save_z=True)
+        close("D", got[0], d, bd)
+        close("Z", got[1], z, bz)
+        assert torch.equal(ge.linear(x, w, bias, residual, act=act), got[0])
+
+
+# every tile and the split form: grids and depths that the plan gives them
+@pytest.mark.parametrize("shape", [(2048, 2048, 96), (2304, 3232, 128), (1280, 4400, 64), (4400, 1290, 72),
+                                   (512, 768, 4096), (40, 128, 8192), (130, 136, 2056)], ids=str)
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+def test_linear_tiles(shape, t):
+    M, N, K = shape
+    log(f"[linear tiles] {shape} {t}")
+    g = gen(M + N + K)
+    x, w = rnd(g, M, K, t=t), rnd(g, N, K, std=K ** -0.5, t=t)
+    bias, residual = rnd(g, N, t=t), rnd(g, M, N, t=t)
+    got = ge.linear(x, w, bias, residual, act="silu", save_z=True)
+    d, bd, z, bz = linear_ref(x, w, bias, residual, "silu")
+    close("D", got[0], d, bd)
+    close("Z", got[1], z, bz)
+
+
+@pytest.mark.parametrize("M", [2, 70])
+def test_linear_strides(M):
+    """Column slices of wider tensors at odd offsets, read in place."""
+    g = gen(5)
+    N, K = 72, 48
+    for off in (0, 1, 8):
+        log(f"[linear strides] M={M} off={off}")
+        x = rnd(g, M, K + 24)[:, off:off + K]
+        w = rnd(g, N, K + 16, std=K ** -0.5)[:, off:off + K]
+        residual = rnd(g, M, N + 9)[:, off:off + N]
+        d, bd, z, bz = linear_ref(x, w, None, residual, "gelu")
+        got = ge.linear(x, w, None, residual, act="gelu", save_z=True)
+        close("D", got[0], d, bd)
+        close("Z", got[1], z, bz)
+        dd = rnd(g, M, N + 9)[:, off:off + N]
+        a, b = (ge.linear_backward(dd.contiguous(), x.contiguous(), w.contiguous(), got[1], act="gelu"),
+                ge.linear_backward(dd, x, w, got[1], act="gelu"))
+        for p, q in zip(a, b):
+            assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+def test_linear_special_values(t):
+    """Infinities and NaN stay in their own row or column; the tiles' padding stays out."""
+    g = gen(9)
+    for M in (3, 40):
+        x, w = rnd(g, M, 72, t=t), rnd(g, 24, 72, t=t)
+        clean = ge.linear(x, w, act="silu")
+        x[1, 3], x[2, 5], w[7, 0] = float("nan"), float("inf"), float("-inf")
+        got = ge.linear(x, w, act="silu")
+        assert got[1].isnan().all()
+        keep = [i for i in range(M) if i not in (1, 2)]
+        cols = [i for i in range(24) if i != 7]
+        assert torch.equal(got[keep][:, cols], clean[keep][:, cols])
+        # relu keeps a NaN, and clears negatives to +0
+        z = ge.linear(x, w, act="relu")
+        assert z[1].isnan().all() and (z[keep][:, cols] >= 0).all()
+
+
+def linear_grad_ref(dd, x, w, z, act):
+    dd, x, w, z = (v.double().cpu() for v in (dd, x, w, z))
+    dz = dd * act_grad64(z, act)
+    e = 4e-6 * (dd.abs() * (1 + z.abs()) if act in ("gelu", "silu") else dz.abs())  # of the factor, fp32
+    t = dz, e
+    return t, x, w
+
+
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(1, 64, 64), (1, 1, 1), (5, 9, 3), (64, 64, 64), (65, 130, 72), (31, 257, 33),
+                                   (300, 70, 1000), (1001, 203, 99), (128, 2048, 136), (2100, 1100, 264),
+                                   (8, 4096, 96), (4096, 40, 48)], ids=str)
+def test_linear_backward(shape, t):
+    M, N, K = shape
+    for n, act in enumerate(("identity", "relu", "gelu", "silu")):
+        log(f"[linear_backward] {shape} {t} {act}")
+        g = gen(M + 7 * N + K + n)
+        x, w = rnd(g, M, K, t=t), rnd(g, N, K, std=K ** -0.5, t=t)
+        z, dd = rnd(g, M, N, std=2.0, t=t), rnd(g, M, N, t=t)
+        (dz, e), x64, w64 = linear_grad_ref(dd, x, w, z, act)
+        dx, dw, db = ge.linear_backward(dd, x, w, z, act=act)
+        ez = e + (u(t) * dz.abs() + floor_of(t) if act != "identity" else 0)
+        close("dX", dx, dz @ w64, ez @ w64.abs() + (N + 2) * E24 * (dz.abs() @ w64.abs()))
+        close("dW", dw, dz.t() @ x64, ez.t() @ x64.abs() + (M + 2) * E24 * (dz.abs().t() @ x64.abs()))
+        close("dbias", db, dz.sum(0), e.sum(0) + (M + 2) * E24 * dz.abs().sum(0))
+        # each alone gives the same bits
+        one = ge.linear_backward(dd, x, w, z, act=act, need_dx=False, need_dbias=False)
+        assert one[0] is None and one[2] is None and torch.equal(one[1], dw)
+        one = ge.linear_backward(dd, x, w, z, act=act, need_dw=False, need_dbias=False)
+        assert one[1] is None and torch.equal(one[0], dx)
+        one = ge.linear_backward(dd, x, w, z, act=act, need_dw=False, need_dx=False)
+        assert torch.equal(one[2], db)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "relu"])
+def test_act_gradient_everywhere(act):
+    """act'(z) at every finite bf16 z and at the infinities, through an identity product."""
+    log(f"[act'] {act}")
+    z = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF16)
+    z = z[~z.isnan()][:65024].reshape(-1, 64).to(DEV)
+    eye = torch.eye(64, dtype=BF16, device=DEV)
+    dx, _, _ = ge.linear_backward(torch.ones_like(z), torch.zeros_like(z), eye, z, act=act, need_dw=False)
+    z64 = z.double().cpu().clamp(-300, 300)
+    want = act_grad64(z64, act)
+    close("act'", dx, want, 4e-6 * (1 + z64.abs()) * torch.sigmoid(z64 + 3))
+
+
+def test_linear_gradient_against_differences():
+    """The gradient of sum(D * c) by central differences of the 64-bit forward."""
+    g = gen(3)
+    M, N, K = 4, 6, 8
+    for act in ("gelu", "silu"):
+        x, w, c = rnd(g, M, K, t=F16), rnd(g, N, K, std=0.3, t=F16), rnd(g, M, N, t=F16)
+        _, z = ge.linear(x, w, act=act, save_z=True)
+        dx, dw, db = ge.linear_backward(c, x, w, z, act=act)
+        x64, w64, c64 = x.double().cpu(), w.double().cpu(), c.double().cpu()
+
+        def f(xv, wv, bv):
+            return (act64(xv @ wv.t() + bv, act) * c64).sum()
+        zero, h = torch.zeros(N, dtype=torch.float64), 1e-5
+
+        def diff(i, args):
+            out = torch.zeros_like(args[i])
+            for j in range(out.numel()):
+                lo, hi = [a.clone() for a in args], [a.clone() for a in args]
+                lo[i].view(-1)[j] -= h
+                hi[i].view(-1)[j] += h
+                out.view(-1)[j] = (f(*hi) - f(*lo)) / (2 * h)
+            return out
+        args = (x64, w64, zero)
+        # Z's rounding moves act' by at most 1.2 u |z|, dZ's by u: 3 roundings of magnitudes up to 4
+        for got, i, other in ((dx, 0, w64), (dw, 1, x64), (db, 2, torch.ones(N, 1, dtype=torch.float64))):
+            scale = (c64.abs().sum() * other.abs().max()).item()
+            assert (got.double().cpu() - diff(i, args)).abs().max() < 8 * u(F16) * scale, (act, i)
+
+
+# ---- cross entropy ------------------------------------------------------------
+def xent_ref(x, w, target):
+    x, w = x.double().cpu(), w.double().cpu()
+    logits = x @ w.t()
+    be = (x.shape[1] + 2) * E24 * (x.abs() @ w.abs().t())  # of every logit
+    lse = torch.logsumexp(logits, 1)
+    t = target.cpu()
+    live = t != IGNORE
+    at = torch.where(live, t, 0)[:, None]
+    loss = torch.where(live, lse - logits.gather(1, at)[:, 0], 0.0)
+    return logits, be, lse, loss, live, at
+
+
+XSHAPES = [(1, 1000, 64), (1, 1, 1), (1, 5, 3), (7, 129, 33), (16, 2000, 520), (17, 1000, 64), (130, 257, 72),
+           (300, 1003, 99), (256, 4100, 264), (40, 20000, 48), (600, 9000, 40)]
+
+
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("shape", XSHAPES, ids=str)
+def test_linear_xent(shape, t):
+    T, V, K = shape
+    log(f"[xent] {shape} {t}")
+    g = gen(T + V + K)
+    x, w = rnd(g, T, K, t=t), rnd(g, V, K, std=2 * K ** -0.5, t=t)
+    target = torch.randint(0, V, (T,), generator=g)
+    target[:: 5] = IGNORE if T > 1 else target[0]
+    if T > 4:
+        target[1], target[2] = 0, V - 1
+    dloss = torch.rand(T, generator=g) * (4096.0 if t == F16 else 1.0) / T
+    target, dloss = target.to(DEV), dloss.to(DEV)
+    logits, be, lse, loss, live, at = xent_ref(x, w, target)
+    got_loss, got_lse = ge.linear_xent(x, w, target, ignore_index=IGNORE)
+    # of lse: the largest error of a logit, the sums (a tree under 64 deep), the exponentials and the logarithm
+    bl = be.amax(1) + 1e-5 + lse.abs() * 2.0 ** -23
+    close("lse", got_lse, lse, bl)
+    close("loss", got_loss, loss, torch.where(live, bl + be.gather(1, at)[:, 0] + 2 * E24 * logits.abs().amax(1), 0.0))
+    assert (got_loss[~live.to(DEV)] == 0).all()
+
+    dx, dw = ge.linear_xent_backward(dloss, x, w, target, got_lse, ignore_index=IGNORE)
+    p = torch.exp(logits - lse[:, None])
+    one = torch.zeros_like(p).scatter_(1, at, 1.0)
+    scale = torch.where(live, dloss.double().cpu(), 0.0)[:, None]
+    P = (p - one) * scale
+    eP = p * scale * (be + bl[:, None] + 2e-6 * (1 + (logits - lse[:, None]).abs())) + (u(t) + 4 * E24) * P.abs() \
+        + scale.max() * 2.0 ** -40  # fp16 subnormals of the scaled P
+    x64, w64 = x.double().cpu(), w.double().cpu()
+    close("dX", dx, P @ w64, eP @ w64.abs() + (V + 9) * E24 * (P.abs() @ w64.abs()))
+    close("dW", dw, P.t() @ x64, eP.t() @ x64.abs() + (T + 9) * E24 * (P.abs().t() @ x64.abs()))
+    only = ge.linear_xent_backward(dloss, x, w, target, got_lse, ignore_index=IGNORE, need_dx=False)
+    assert only[0] is None and torch.equal(only[1], dw)
+    only = ge.linear_xent_backward(dloss, x, w, target, got_lse, ignore_index=IGNORE, need_dw=False)
+    assert only[1] is None and torch.equal(only[0], dx)
+
+
+def test_xent_several_pieces():
+    """A batch large enough for several pieces of the vocabulary: the fp32 accumulator between them."""
+    log("[xent pieces]")
+    g = gen(21)
+    T, V, K = 9000, 16500, 24
+    x, w = rnd(g, T, K), rnd(g, V, K, std=2 * K ** -0.5)
+    target = torch.randint(0, V, (T,), generator=g).to(DEV)
+    loss, lse = ge.linear_xent(x, w, target)
+    dloss = torch.full((T,), 1.0 / T, device=DEV)
+    dx, dw = ge.linear_xent_backward(dloss, x, w, target, lse)
+    # the same in fp32 on the GPU; bounds of both: sums in fp32, P in bf16
+    p = x.float() @ w.float().t()
+    ref_lse = torch.logsumexp(p, 1)
+    assert (lse - ref_lse).abs().max() < 1e-4
+    p = (p - ref_lse[:, None]).exp_()
+    p[torch.arange(T, device=DEV), target] -= 1
+    p /= T
+    ref_dx, ref_dw = p @ w.float(), p.t() @ x.float()
+    for name, got, ref, mag in (("dX", dx, ref_dx, p.abs() @ w.float().abs()),
+                                ("dW", dw, ref_dw, p.abs().t() @ x.float().abs())):
+        bad = (got.float() - ref).abs() > u(BF16) * ref.abs() + (u(BF16) + 2e-4) * mag
+        assert not bad.any(), name
+
+
+def test_xent_masks():
+    log("[xent masks]")
+    g = gen(8)
+    for T in (5, 40):
+        V, K = 300, 64
+        x, w = rnd(g, T, K), rnd(g, V, K, std=0.3)
+        none = torch.full((T,), IGNORE, device=DEV)
+        loss, lse = ge.linear_xent(x, w, none)
+        assert (loss == 0).all() and lse.isfinite().all()
+        dl = torch.ones(T, device=DEV)
+        dx, dw = ge.linear_xent_backward(dl, x, w, none, lse)
+        assert (dx == 0).all() and (dw == 0).all()
+        # a zero incoming gradient
+        tgt = torch.randint(0, V, (T,), generator=g).to(DEV)
+        _, lse = ge.linear_xent(x, w, tgt)
+        dx, dw = ge.linear_xent_backward(dl * 0, x, w, tgt, lse)
+        assert (dx == 0).all() and (dw == 0).all()
+        # out of range: NaN, in its own row only; an ignore index inside the range masks too
+        bad = tgt.clone()
+        bad[0], bad[1] = V, -1
+        loss, _ = ge.linear_xent(x, w, bad)
+        good, _ = ge.linear_xent(x, w, tgt)
+        assert loss[:2].isnan().all() and torch.equal(loss[2:], good[2:])
+        loss, lse = ge.linear_xent(x, w, tgt, ignore_index=int(tgt[2]))
+        assert (loss[tgt == tgt[2]] == 0).all()
+        dx, _ = ge.linear_xent_backward(dl, x, w, tgt, lse, ignore_index=int(tgt[2]))
+        assert (dx[tgt == tgt[2]] == 0).all()
+        # an ignored row's NaN stays out of the other rows and of dX
+        x2 = x.clone()
+        x2[3] = float("nan")
+        masked = tgt.clone()
+        masked[3] = IGNORE
+        l2, lse2 = ge.linear_xent(x2, w, masked)
+        assert l2[3] == 0 and torch.equal(l2[4:], good[4:])
+        dx, _ = ge.linear_xent_backward(dl, x2, w, masked, lse2)
+        assert (dx[3] == 0).all() and dx.isfinite().all()
+
+
+def test_xent_extreme_logits():
+    """Logits at 3e4, where exp overflows, and all-equal rows."""
+    log("[xent extremes]")
+    for T in (3, 40):
+        K, V = 16, 700
+        x = torch.full((T, K), 40.0, dtype=F16, device=DEV)
+        w = torch.full((V, K), 47.0, dtype=F16, device=DEV)
+        w[5] = -47.0
+        tgt = torch.full((T,), 5, device=DEV)
+        loss, lse = ge.linear_xent(x, w, tgt)
+        top = 40.0 * 47.0 * K
+        assert (lse.double().cpu() - (top + math.log(V - 1))).abs().max() <= top * 2.0 ** -23 + 1e-5
+        assert (loss.double().cpu() - (2 * top + math.log(V - 1))).abs().max() <= 4 * top * 2.0 ** -23
+        tgt[:] = 6
+        loss, lse = ge.linear_xent(x, w, tgt)
+        dx, dw = ge.linear_xent_backward(torch.ones(T, device=DEV), x, w, tgt, lse)
+        assert dx.isfinite().all() and dw.isfinite().all()
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-6, 1.0, 2.0 ** 20])
+def test_xent_gradient_scales(scale):
+    """P keeps its digits in 16 bits whatever the incoming gradient's size."""
+    log(f"[xent scale] {scale}")
+    g = gen(4)
+    T, V, K = 33, 500, 32
+    t = BF16
+    x, w = rnd(g, T, K, t=t), rnd(g, V, K, t=t, std=0.3)
+    tgt = torch.randint(0, V, (T,), generator=g).to(DEV)
+    _, lse = ge.linear_xent(x, w, tgt)
+    a = ge.linear_xent_backward(torch.full((T,), 1.0, device=DEV), x, w, tgt, lse)
+    s = 2.0 ** round(math.log2(scale))
+    b = ge.linear_xent_backward(torch.full((T,), s, device=DEV), x, w, tgt, lse)
+    for p, q in zip(a, b):
+        assert torch.equal((p.float() * s).to(t), q)
+
+
+# ---- norms ----------------------------------------------------------------------
+def norm64(v, kind, eps):
+    """(normalised rows, reciprocal scale, mean)"""
+    mu = v.mean(1, keepdim=True) if kind == "layer" else torch.zeros(v.shape[0], 1, dtype=torch.float64)
+    c = v - mu
+    r = 1 / torch.sqrt((c * c).mean(1, keepdim=True) + eps)
+    return c * r, r, mu
+
+
+NSHAPES = [(1, 64, 1), (1, 1, 1), (4, 5, 2), (3, 100, 3), (17, 513, 1), (8, 1024, 4), (30, 1030, 30), (12, 2048, 2),
+           (9, 4100, 3), (5, 8192, 1), (6, 8200, 2), (2, 16384, 1), (700, 72, 7), (2050, 40, 1025), (1200, 136, 1)]
+NKINDS = [("rms", "rms"), ("layer", "layer"), ("none", "rms"), ("rms", "layer")]
+
+
+@pytest.mark.parametrize("t,s", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)],
+                         ids=["bf16", "f16", "bf16-f32", "f16-f32"])
+@pytest.mark.parametrize("shape", NSHAPES, ids=str)
+def test_norm_residual(shape, t, s):
+    T, H, G = shape
+    eps = 1e-5
+    for n, (post, pre) in enumerate(NKINDS):
+        log(f"[norm] {shape} {t} {s} {post} {pre}")
+        g = gen(T + H + G + n)
+        h, y = rnd(g, T, H, std=2.0, mean=-0.5, t=s), rnd(g, T, H, std=3.0, mean=0.25, t=t)
+        gate = rnd(g, G, H, std=0.3, mean=0.5, t=t) if n != 3 else None
+        wo = rnd(g, H, std=0.1, mean=1.0, t=t) if post != "none" else None
+        wi = rnd(g, H, std=0.1, mean=1.0, t=t) if n != 2 else None
+        kw = dict(w_post=wo, w_pre=wi, gate=gate, scale=0.7, post=post, pre=pre, eps=eps)
+        ho, x = ge.norm_residual(h, y, **kw)
+        one = torch.ones(H, dtype=torch.float64)
+        y64, h64 = y.double().cpu(), h.double().cpu()
+        g64 = gate.double().cpu().repeat_interleave(T // G, 0) if gate is not None else one
+        wo64 = wo.double().cpu() if wo is not None else one
+        wi64 = wi.double().cpu() if wi is not None else one
+        # of fp32 norms: 4e-6 of the value (sums of squares, rsqrt, three products) and the mean's
+        # rounding, 2^-22 of the largest element
+        if post != "none":
+            yn, ry, _ = norm64(y64, post, eps)
+            eyn = 4e-6 * yn.abs() + ry * y64.abs().amax(1, keepdim=True) * 2.0 ** -22
+        else:
+            yn, eyn = y64, y64.abs() * E24
+        step = 0.7 * g64 * wo64 * yn
+        hh = h64 + step
+        eh = 0.7 * (g64 * wo64).abs() * eyn + 4 * E24 * (step.abs() + hh.abs())
+        close("H'", ho, hh, eh)
+        hn, rh, _ = norm64(hh, pre, eps)
+        # every element of the row enters the scale: the relative error of the largest
+        ehn = rh * eh + hn.abs() * (4e-6 + (eh * rh).amax(1, keepdim=True)) \
+            + rh * hh.abs().amax(1, keepdim=True) * 2.0 ** -22 + (eh * rh).mean(1, keepdim=True)
+        if H == 1 and pre == "layer":  # a single element less its mean: 0 times 1 / sqrt(eps)
+            ehn = ehn + (hh.abs() * 2.0 ** -22 + eh) / math.sqrt(eps)
+        close("X", x, hn * wi64, ehn * wi64.abs())
+
+        if H > 8192:  # the gradient's limit
+            continue
+        # the gradient at the stored H'
+        dx, dho = rnd(g, T, H, t=t), rnd(g, T, H, t=s)
+        got = ge.norm_residual_backward(dx, dho, ho, y, **kw)
+        H64 = ho.double().cpu()
+        hn, rh, _ = norm64(H64, pre, eps)
+        dx64, dho64 = dx.double().cpu(), dho.double().cpu()
+        dn = dx64 * wi64
+        c_h = (dn * hn).mean(1, keepdim=True)
+        dm = dn.mean(1, keepdim=True) if pre == "layer" else 0.0
+        dh = dho64 + (dn - hn * c_h - dm) * rh
+        big = rh * H64.abs().amax(1, keepdim=True) * 2.0 ** -22 + 4e-6 * hn.abs()  # of hn
+        mag = dn.abs() + hn.abs() * (dn * hn).abs().mean(1, keepdim=True) + dn.abs().mean(1, keepdim=True)
+        edh = rh * (1e-5 * mag + big * c_h.abs() + hn.abs() * (dn.abs() * big).mean(1, keepdim=True)) \
+            + 4 * E24 * dh.abs() + E24 * dho64.abs()
+        close("dH", got[0], dh, edh)
+        dyw = 0.7 * g64 * dh
+        edyw = 0.7 * g64.abs() * edh + 3 * E24 * dyw.abs()
+        d = dyw * wo64
+        if post != "none":
+            yn, ry, _ = norm64(y64, post, eps)
+            c_y = (d * yn).mean(1, keepdim=True)
+            m_y = d.mean(1, keepdim=True) if post == "layer" else 0.0
+            dy = (d - yn * c_y - m_y) * ry
+            ed = edyw * wo64.abs()
+            magy = d.abs() + yn.abs() * (d * yn).abs().mean(1, keepdim=True) + d.abs().mean(1, keepdim=True)
+            edy = ry * (1e-5 * magy + ed + yn.abs() * ((ed * yn.abs()).mean(1, keepdim=True)
+                                                       + (d.abs() * eyn).mean(1, keepdim=True))
+                        + eyn * c_y.abs() + ed.mean(1, keepdim=True))
+        else:
+            yn, dy, edy = y64, dyw, edyw
+        close("dY", got[1], dy, edy)
+        rows = (T + 4) * E24
+        if wo is not None:
+            close("dw_post", got[2], (dyw * yn).sum(0),
+                  (edyw * yn.abs() + dyw.abs() * eyn).sum(0) + rows * (dyw * yn).abs().sum(0))
+        else:
+            assert got[2] is None
+        if wi is not None:
+            close("dw_pre", got[3], (dx64 * hn).sum(0), (dx64.abs() * big).sum(0) + rows * (dx64 * hn).abs().sum(0))
+        else:
+            assert got[3] is None
+        if gate is not None:
+            yw = 0.7 * yn * wo64
+            v, e = yw * dh, yw.abs() * edh + 0.7 * wo64.abs() * eyn * dh.abs() + 4 * E24 * (yw * dh).abs()
+            close("dgate", got[4], v.view(G, T // G, H).sum(1),
+                  e.view(G, T // G, H).sum(1) + rows * v.abs().view(G, T // G, H).sum(1))
+        else:
+            assert got[4] is None
+
+
+def test_norm_large_mean():
+    """A mean of 1000 deviations costs the LAYER norm no more than the input's own rounding."""
+    log("[norm mean]")
+    g = gen(6)
+    h = torch.zeros(4, 512, device=DEV)
+    y = rnd(g, 4, 512, t=F16, std=1.0, mean=1000.0)
+    _, x = ge.norm_residual(h, y, post="layer", pre="layer")
+    want = norm64(norm64(y.double().cpu(), "layer", 1e-5)[0], "layer", 1e-5)[0]
+    assert (x.double().cpu() - want).abs().max() < 5 * u(F16) * 4 + 1000 * 2.0 ** -21
+
+
+def test_norm_gradient_against_differences():
+    g = gen(13)
+    T, H, G, eps, h = 4, 6, 2, 1e-3, 1e-5
+    for post, pre in (("rms", "rms"), ("layer", "layer"), ("rms", "layer")):
+        H0, y = rnd(g, T, H, t=F32), rnd(g, T, H, t=F16)
+        gate, wo, wi = rnd(g, G, H, t=F16), rnd(g, H, t=F16), rnd(g, H, t=F16)
+        kw = dict(w_post=wo, w_pre=wi, gate=gate, scale=0.7, post=post, pre=pre, eps=eps)
+        ho, _ = ge.norm_residual(H0, y, **kw)
+        cx, ch = rnd(g, T, H, t=F16), rnd(g, T, H, t=F32)
+        got = ge.norm_residual_backward(cx, ch, ho, y, **kw)
+        leaves = [v.double().cpu() for v in (H0, y, wo, wi, gate)]
+
+        def f(h0, yv, wov, wiv, gv):
+            hh = h0 + 0.7 * gv.repeat_interleave(T // G, 0) * norm64(yv, post, eps)[0] * wov
+            return (hh * ch.double().cpu()).sum() + (norm64(hh, pre, eps)[0] * wiv * cx.double().cpu()).sum()
+        for i, gr in enumerate(got):
+            out = torch.zeros_like(leaves[i])
+            for j in range(out.numel()):
+                lo, hi = [a.clone() for a in leaves], [a.clone() for a in leaves]
+                lo[i].view(-1)[j] -= h
+                hi[i].view(-1)[j] += h
+                out.view(-1)[j] = (f(*hi) - f(*lo)) / (2 * h)
+            # dY is rounded to fp16; the rest fp32 from an fp32 H'
+            lim = (u(F16) if gr.dtype == F16 else 0) * out.abs() + 2e-5 * (1 + out.abs().max())
+            assert ((gr.double().cpu() - out).abs() <= lim).all(), (post, pre, i)
+
+
+# ---- calls ------------------------------------------------------------------------
+def test_empty_batches():
+    log("[empty]")
+    x, w = torch.empty(0, 64, dtype=BF16, device=DEV), torch.ones(48, 64, dtype=BF16, device=DEV)
+    d, z = ge.linear(x, w, act="gelu", save_z=True)
+    assert d.shape == z.shape == (0, 48)
+    dx, dw, db = ge.linear_backward(d, x, w, z, act="gelu")
+    assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all()
+    t = torch.empty(0, dtype=torch.int64, device=DEV)
+    loss, lse = ge.linear_xent(x, w, t)
+    assert loss.shape == lse.shape == (0,)
+    dx, dw = ge.linear_xent_backward(loss, x, w, t, lse)
+    assert dx.shape == (0, 64) and (dw == 0).all()
+    v = torch.ones(64, dtype=BF16, device=DEV)
+    ho, xo = ge.norm_residual(x, x, w_post=v, w_pre=v)
+    assert ho.shape == xo.shape == (0, 64)
+    out = ge.norm_residual_backward(x, x, x, x, w_post=v, w_pre=v)
+    assert (out[2] == 0).all() and (out[3] == 0).all()
+
+
+def test_refusals_on_the_gpu():
+    x = torch.zeros(4, 8, dtype=F16, device=DEV)
+    w = torch.zeros(6, 8, dtype=F16, device=DEV)
+    for bad, err in (((x, w.to(BF16)), TypeError), ((x, w[:, :7]), ValueError), ((x, w.t()), ValueError),
+                     ((x, w.cpu()), ValueError), ((x[None], w), ValueError),
+                     ((x, w, torch.zeros(5, dtype=F16, device=DEV)), ValueError),
+                     ((x, w, None, torch.zeros(6, 4, dtype=F16, device=DEV).t()), ValueError)):
+        with pytest.raises(err):
+            ge.linear(*bad)
+    with pytest.raises(ValueError, match="act"):
+        ge.linear(x, w, act="tanh")
+    with pytest.raises(ValueError, match="needs z"):
+        ge.linear_backward(torch.zeros(4, 6, dtype=F16, device=DEV), x, w, act="gelu")
+    with pytest.raises(ValueError, match="requires grad"):
+        ge.linear(x, w.clone().requires_grad_())
+    with torch.no_grad():
+        ge.linear(x, w.clone().requires_grad_())
+    with pytest.raises(TypeError):
+        ge.linear_xent(x, w, torch.zeros(4, device=DEV))
+    with pytest.raises(ValueError):
+        ge.linear_xent(x, w, torch.zeros(5, dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError, match="divide"):
+        ge.norm_residual(x, x, gate=torch.zeros(3, 8, dtype=F16, device=DEV))
+    with pytest.raises(ValueError, match="overlap"):
+        ge.norm_residual(x, x[:1].expand(4, 8))
+    with pytest.raises(ValueError, match="pre"):
+        ge.norm_residual(x, x, pre="none")
+    with pytest.raises(ValueError, match="w_post"):
+        ge.norm_residual(x, x, post="none", w_post=x[0])
+    wide = torch.zeros(1, 16385, dtype=F16, device=DEV)
+    with pytest.raises(ge.GemmEpiError):
+        ge.norm_residual(wide, wide)
+
+
+def operators_of(M, t=BF16):
+    """A set of calls covering every operator, on fresh inputs: f() -> tuple of outputs."""
+    g = gen(M)
+    N, K, V = 264, 128, 1000
+    x, w, b, r = rnd(g, M, K, t=t), rnd(g, N, K, t=t, std=0.1), rnd(g, N, t=t), rnd(g, M, N, t=t)
+    wv = rnd(g, V, N, t=t, std=0.1)
+    tgt = torch.randint(0, V, (M,), generator=g).to(DEV)
+    v = rnd(g, N, t=t, mean=1.0, std=0.1)
+    dl = torch.full((M,), 1.0 / M, device=DEV)
+    ins = [x, w, b, r, wv, tgt, v, dl]
+
+    def f(stream=None):
+        k = dict(stream=stream)
+        d, z = ge.linear(x, w, b, r, act="gelu", save_z=True, **k)
+        ho, xo = ge.norm_residual(r, d, w_post=v, w_pre=v, **k)
+        loss, lse = ge.linear_xent(xo, wv, tgt, **k)
+        dxo, dwv = ge.linear_xent_backward(dl, xo, wv, tgt, lse, **k)
+        dh, dd, dwo, dwi, _ = ge.norm_residual_backward(dxo, torch.zeros_like(ho) if stream is None else ho, ho, d,
+                                                        w_post=v, w_pre=v, **k)
+        dx, dw, db = ge.linear_backward(dd, x, w, z, act="gelu", **k)
+        return d, z, ho, xo, loss, lse, dxo, dwv, dh, dd, dwo, dwi, dx, dw, db
+    return f, ins
+
+
+@pytest.mark.parametrize("M", [1, 200])
+def test_repeats_and_streams(M):
+    """The same bits every time, on the current stream, on a given one and on a current side stream."""
+    log(f"[streams] M={M}")
+    f, ins = operators_of(M)
+    a, b = f(), f()
+    torch.cuda.synchronize()
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c = f()
+    d1, d2 = f(side), f(side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for p, q in zip(a, c):
+        assert torch.equal(p, q)
+    for p, q in zip(d1, d2):
+        assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("M", [1, 200])
+def test_graph_capture(M):
+    """Recorded into a HIP graph and replayed on changed inputs, with eager work between the replays."""
+    log(f"[graph] M={M}")
+    f, ins = operators_of(M)
+    f()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = f()
+    for rep in range(4):
+        ins[0].mul_(-0.5)
+        ins[3].add_(0.25)
+        for o in out:
+            o.fill_(7)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        want = f()
+        torch.cuda.synchronize()
+        for i, (p, q) in enumerate(zip(got, want)):
+            assert torch.equal(p, q), (rep, i)
+
+
+def test_guards():
+    """Nothing is written outside the outputs (ragged sizes, rows past every tile)."""
+    import struct
+    from dense_gemm_elementwise_amd import operators as o
+    log("[guards]")
+    g = gen(2)
+    M, N, K = 150, 133, 40
+    x, w = rnd(g, M, K), rnd(g, N, K)
+    for ld in (N, N + 3, 136):
+        buf = torch.full((M * ld + 512,), 3.0, dtype=BF16, device=DEV)
+        d = buf[256:256 + M * ld].view(M, ld)
+        args = o._LINEAR.pack(M, N, K, x.data_ptr(), K, w.data_ptr(), K, 0, 0, 0, d.data_ptr(), ld, 0, 0, 0, 1)
+        s = torch.cuda.current_stream().cuda_stream
+        rc, need = o.workspace_bytes("ge_linear", args + struct.pack("@3q", 0, 0, s))
+        assert rc == 0
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+        assert o._functions()["ge_linear"](args + struct.pack("@3q", ws.data_ptr(), need, s)) == 0
+        torch.cuda.synchronize()
+        assert (buf[:256] == 3).all() and (buf[256 + M * ld:] == 3).all()
+        assert (d[:, N:] == 3).all()
+        assert torch.equal(d[:, :N], ge.linear(x, w))
