@@ -79,35 +79,48 @@ struct LinParams {
     int n_store;           // LE_XP: columns written (N rounded up to 8, zeros past N)
 };
 
-// phi(z) parts shared by the activation and its gradient (see act_gelu for the
-// polynomial): the upper tail Q(|x|) = erfc(|x| / sqrt 2) / 2 of the normal
-// distribution as q * h * h with h = e^(-x^2/4)
+// Activations of the linear operator.  An epilogue's arithmetic runs while the
+// matrix units wait, so these are cheaper forms than those of the epilogue
+// kinds (act_gelu, act_silu): at 8192 x 8192 x 2048 they took the gelu call
+// from 301 us to what the comment at lin_epilogue says.  Relative error 3e-6
+// (gelu) and a few fp32 units (silu), down into the subnormals.
+//
+// The upper tail Q(|x|) = erfc(|x| / sqrt 2) / 2 of the normal distribution is
+// q h h, h = e^(-x^2/4), q a polynomial in 1 / (1 + 0.3 |x|) by
+// fit_normal_tail.py.
 __device__ __forceinline__ void act_normal_tail(float x, float &q, float &h)
 {
 #pragma clang fp contract(off)
-    constexpr float c[9] = {-2.037919330e-04f, 2.859725058e-01f, 2.504409850e-01f, 3.914754093e-01f,
-                            -2.268847674e-01f, 7.775521874e-01f, -6.962806582e-01f, 2.504747510e-01f,
-                            -3.254655749e-02f};
-    const float z = __builtin_fabsf(x) * 0.707106781186547524f;
-    const float t = 2.0f * act_rcp(2.0f + z);
-    float p = c[8];
-#pragma unroll
-    for (int k = 7; k >= 0; k--) p = __builtin_fmaf(p, t, c[k]);
-    h = act_exp(-0.5f * (z * z));
-    q = 0.5f * p;
+    const float u = act_rcp(__builtin_fmaf(0.3f, __builtin_fabsf(x), 1.0f));
+    float p = -8.459328115e-02f;
+    p = __builtin_fmaf(p, u, 2.405729890e-01f);
+    p = __builtin_fmaf(p, u, -4.864473268e-02f);
+    p = __builtin_fmaf(p, u, 1.647647172e-01f);
+    p = __builtin_fmaf(p, u, 1.067044288e-01f);
+    p = __builtin_fmaf(p, u, 1.212747246e-01f);
+    q = __builtin_fmaf(p, u, -7.979097427e-05f);
+    h = __builtin_amdgcn_exp2f((x * (-0.25f * 1.44269504088896341f)) * x);
 }
 
 template <int ACT>
 __device__ __forceinline__ float lin_act(float z)
 {
-    if constexpr (ACT == ACT_RELU)
-        return z > 0.0f ? z : (z != z ? z : 0.0f);
-    else if constexpr (ACT == ACT_GELU)
-        return act_gelu(z);
-    else if constexpr (ACT == ACT_SILU)
-        return act_silu(z);
-    else
+#pragma clang fp contract(off)
+    if constexpr (ACT == ACT_RELU) {
+        return z < 0.0f ? 0.0f : z;  // keeps a NaN
+    } else if constexpr (ACT == ACT_GELU) {
+        // z Phi(z) = max(z, 0) - |z| Q(|z|).  The factor |z| is clamped against
+        // infinity times zero; h of a NaN is a NaN.
+        float q, h;
+        act_normal_tail(z, q, h);
+        return __builtin_fmaxf(z, 0.0f) - ((__builtin_fminf(__builtin_fabsf(z), 100.0f) * q) * h) * h;
+    } else if constexpr (ACT == ACT_SILU) {
+        // z / (1 + e^-z), below zero z e^z / (1 + e^z), e^-|z| = v v
+        const float v = __builtin_amdgcn_exp2f(__builtin_fabsf(z) * (-0.5f * 1.44269504088896341f));
+        return (z < 0.0f ? (z * v) * v : z) * act_rcp(__builtin_fmaf(v, v, 1.0f));
+    } else {
         return z;
+    }
 }
 
 // act'(z).  The clamps only replace values where the derivative has long
@@ -442,14 +455,49 @@ __device__ __forceinline__ void mainloop_lin(f32x4 (&acc)[BM / 32][BN / 32], con
     agpr_fence(acc);
 }
 
+// 16-byte access at any element alignment (global memory takes it at the
+// rate of the cache lines it touches)
+typedef half8 half8u __attribute__((aligned(2)));
+typedef f32x4 f32x4u __attribute__((aligned(4)));
+
+// 8 consecutive elements, the first n of which exist (the rest read as zeros)
+__device__ __forceinline__ half8 load8(const _Float16 *p, int n)
+{
+    if (n >= 8) return *(const half8u *)p;
+    half8 v = {};
+#pragma unroll
+    for (int e = 0; e < 7; e++)
+        if (e < n) v[e] = p[e];
+    return v;
+}
+__device__ __forceinline__ void store8(_Float16 *p, half8 v, int n)
+{
+    if (n >= 8) {
+        *(half8u *)p = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; e++)
+        if (e < n) p[e] = v[e];
+}
+
+// Keeps one row of accumulator blocks in AGPRs up to here: without it the
+// compiler copies many rows to VGPRs at the start of the epilogue and runs out.
+template <int TN>
+__device__ __forceinline__ void pin_row(f32x4 (&row)[TN])
+{
+#pragma unroll
+    for (int j = 0; j < TN; j++) asm volatile("" : "+a"(row[j]));
+}
+
 // ---------------------------------------------------------------------------
-// Epilogues.  The tile goes through LDS one 16-row slab per wave at a time, so
+// Epilogues.  The tile goes through LDS 64 rows a wave at a time, so
 // that a lane owns 8 consecutive columns (16-byte accesses).  With p.vec the
 // outputs and the residual go through range-checked buffer accesses (rows
 // past M and, parked, columns past N are dropped; an absent tensor is a
-// descriptor of zero records, which reads as zeros); otherwise one element
-// per lane, adjacent lanes on adjacent columns, so that an access still
-// covers 128 contiguous bytes whatever the row's alignment.
+// descriptor of zero records, which reads as zeros); otherwise through
+// guarded 16-byte accesses at any element alignment, element by element where
+// a row ends inside one.
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int EPI, int ACT, bool BF>
 __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], const LinParams &p, int m0, int n0,
@@ -481,14 +529,19 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
         const bool edge = n0 + BN > p.N;
 #pragma unroll
         for (int i = 0; i < TM; i++) {
+            pin_row<TN>(acc[i]);
             float x[TN][4];
 #pragma unroll
             for (int j = 0; j < TN; j++)
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    x[j][r] = acc[i][j][r];
-                    if (edge && n0 + wn * WN + j * 16 + li >= p.N) x[j][r] = -__builtin_inff();
-                }
+                for (int r = 0; r < 4; r++) x[j][r] = acc[i][j][r];
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < TN; j++)
+                    if (n0 + wn * WN + j * 16 + li >= p.N)
+#pragma unroll
+                        for (int r = 0; r < 4; r++) x[j][r] = -__builtin_inff();
+            }
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const int row = wm * (BM / 2) + i * 16 + 4 * lg + r;
@@ -496,11 +549,14 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
 #pragma unroll
                 for (int j = 1; j < TN; j++) m = __builtin_fmaxf(m, x[j][r]);
                 m = row16_max(m);
-                const float ref = m == -__builtin_inff() ? 0.0f : m;
+                // e^(x - m) as 2^(x log2 e - ref), one fma an element; what the
+                // rounding of ref = m log2 e left out is put back once a row
+                const float mf = m == -__builtin_inff() ? 0.0f : m;
+                const float ref = mf * kLog2e;
                 float s = 0.0f;
 #pragma unroll
-                for (int j = 0; j < TN; j++) s += exp2_hw((x[j][r] - ref) * kLog2e);
-                s = row16_sum(s);
+                for (int j = 0; j < TN; j++) s += exp2_hw(__builtin_fmaf(x[j][r], kLog2e, -ref));
+                s = row16_sum(s) * exp2_hw(-__builtin_fmaf(mf, kLog2e, -ref));
                 if (li == 0) {
                     red[(wn * BM + row) * 2] = m;
                     red[(wn * BM + row) * 2 + 1] = s;
@@ -560,18 +616,22 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
     const __amdgpu_buffer_rsrc_t rZ = res_of(EPI == LE_LINEAR ? p.Z : nullptr, p.ldz, 2);
     const __amdgpu_buffer_rsrc_t rC =
         res_of(EPI == LE_OUT && p.C32 ? p.C32 + (int64_t)split * p.c_split : nullptr, p.ldc, 4);
-    float bias[8];
+    const int ncol = ncols - gcol;  // columns that exist from this lane's first on
+    float bias[8] = {};
+    if (EPI == LE_LINEAR && p.bias) {
+        const half8 b8 = load8(p.bias + gcol, ncol);
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-        bias[e] = EPI == LE_LINEAR && vec && p.bias && col_in ? ld16<BF>(p.bias[gcol + e]) : 0.0f;
+        for (int e = 0; e < 8; e++) bias[e] = ld16<BF>(b8[e]);
+    }
 
     // 64 rows of the wave's block at a time: the accumulators' part is unrolled
     // (registers cannot be indexed at run time), the rest is a loop over 16-row
-    // slabs, with the next slab's residual (or accumulator) loads in flight
+    // slabs, with the next slab's residual loads in flight
 #pragma unroll
     for (int ph = 0; ph < TM / 4; ph++) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
+            pin_row<TN>(acc[ph * 4 + i]);
 #pragma unroll
             for (int j = 0; j < TN; j++)
 #pragma unroll
@@ -581,13 +641,27 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
         }
         wave_lds_sync();
         const int row0 = wm * (BM / 2) + ph * 64;
-        if (vec) {
+        auto slabs = [&](auto VEC_) {
+            constexpr bool VEC = decltype(VEC_)::value;
+            // 8 elements of a 16-bit tensor's row
+            auto get8 = [&](__amdgpu_buffer_rsrc_t r, const _Float16 *t, int64_t ld, int row) {
+                if constexpr (VEC)
+                    return buf_load<half8, 0>(r, off_of(row, ld, 2));
+                else
+                    return t && row < rows_here ? load8(t + (m0l + row) * ld + gcol, ncol) : half8{};
+            };
+            auto put8 = [&](half8 v, __amdgpu_buffer_rsrc_t r, _Float16 *t, int64_t ld, int row) {
+                if constexpr (VEC)
+                    buf_store<half8, EPI == LE_XP ? 0 : 2>(v, r, off_of(row, ld, 2));
+                else if (t && row < rows_here)
+                    store8(t + (m0l + row) * ld + gcol, v, ncol);
+            };
             half8 rbuf[PASSES] = {};
             auto fetch = [&](int s) {
                 if constexpr (EPI == LE_LINEAR) {
 #pragma unroll
                     for (int q = 0; q < PASSES; q++)
-                        rbuf[q] = buf_load<half8, 0>(rR, off_of(row0 + s * 16 + q * RPP + lane / LPR, p.ldr, 2));
+                        rbuf[q] = get8(rR, p.R, p.ldr, row0 + s * 16 + q * RPP + lane / LPR);
                 }
             };
             fetch(0);
@@ -597,6 +671,15 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
 #pragma unroll
                 for (int q = 0; q < PASSES; q++) rcur[q] = rbuf[q];
                 if (s < 3) fetch(s + 1);
+                f32x4 cin[PASSES][2];
+                if (EPI == LE_OUT && p.acc_in) {
+#pragma unroll
+                    for (int q = 0; q < PASSES; q++) {
+                        const int oc = off_of(row0 + s * 16 + q * RPP + lane / LPR, p.ldc, 4);
+                        cin[q][0] = buf_load<f32x4, 0>(rC, oc);
+                        cin[q][1] = buf_load<f32x4, 0>(rC, oc + 16);
+                    }
+                }
 #pragma unroll
                 for (int q = 0; q < PASSES; q++) {
                     const int srow = s * 16 + q * RPP + lane / LPR, row = row0 + srow;
@@ -612,61 +695,58 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
                             z[e] = st16<BF>(t);
                             d[e] = st16<BF>(lin_act<ACT>(t) + ld16<BF>(rcur[q][e]));
                         }
-                        buf_store<half8, 2>(d, rD, off_of(row, p.ldd, 2));
-                        buf_store<half8, 2>(z, rZ, off_of(row, p.ldz, 2));
+                        put8(d, rD, p.D, p.ldd, row);
+                        put8(z, rZ, p.Z, p.ldz, row);
                     } else if constexpr (EPI == LE_OUT) {
-                        const int oc = off_of(row, p.ldc, 4);
                         if (p.acc_in) {
-                            const f32x4 c0 = buf_load<f32x4, 0>(rC, oc), c1 = buf_load<f32x4, 0>(rC, oc + 16);
 #pragma unroll
-                            for (int e = 0; e < 8; e++) v[e] += e < 4 ? c0[e & 3] : c1[e & 3];
+                            for (int e = 0; e < 8; e++) v[e] += cin[q][e >> 2][e & 3];
                         }
                         if (p.acc_out) {
+                            const int oc = off_of(row, p.ldc, 4);
                             buf_store<f32x4, 0>(f32x4{v[0], v[1], v[2], v[3]}, rC, oc);
                             buf_store<f32x4, 0>(f32x4{v[4], v[5], v[6], v[7]}, rC, oc + 16);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 8; e++) d[e] = st16<BF>(v[e] * alpha);
-                            buf_store<half8, 2>(d, rD, off_of(row, p.ldd, 2));
+                            put8(d, rD, p.D, p.ldd, row);
                         }
-                    } else {  // LE_XP; P is read again soon, so it is stored plainly
-                        const f32x4 xf = *(const f32x4 *)(xrow + 4 * row);
-                        const float lse = xf[0], scale = xf[1];
-                        const i32x4 x = __builtin_bit_cast(i32x4, xf);
-                        const int tc = x[2] - p.v0 - gcol;
-#pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            // the difference first: where the probability is large, logit and lse are close
-                            float pr = exp2_hw((v[e] - lse) * kLog2e);
-                            pr = (pr - (tc == e ? 1.0f : 0.0f)) * scale;
-                            if (x[3] || gcol + e >= p.N) pr = 0.0f;
-                            d[e] = st16<BF>(pr);
-                        }
-                        buf_store<half8, 0>(d, rD, off_of(row, p.ldd, 2));
-                    }
-                }
-            }
-        } else if constexpr (EPI != LE_XP) {
-#pragma unroll 1
-            for (int x = 0; x < 64; x++) {
-                const int row = row0 + x;
-                if (row >= rows_here) break;
-#pragma unroll
-                for (int c = 0; c < WN; c += 64) {
-                    const int gn = n0 + wn * WN + c + lane;
-                    if (gn >= p.N) continue;
-                    float v = slab[x * LDW + c + lane];
-                    if constexpr (EPI == LE_LINEAR) {
-                        v += p.bias ? ld16<BF>(p.bias[gn]) : 0.0f;
-                        const float r = p.R ? ld16<BF>(p.R[(m0l + row) * p.ldr + gn]) : 0.0f;
-                        if (p.Z) p.Z[(m0l + row) * p.ldz + gn] = st16<BF>(v);
-                        p.D[(m0l + row) * p.ldd + gn] = st16<BF>(lin_act<ACT>(v) + r);
                     } else {
-                        if (p.acc_in) v += p.C32[(m0l + row) * p.ldc + gn];
-                        p.D[(m0l + row) * p.ldd + gn] = st16<BF>(v * alpha);
+                        // p = 2^(logit log2 e - lse log2 e); the target's 1 is
+                        // taken off in the few lanes that hold one.  An ignored
+                        // row, and columns past the vocabulary, are zeros whatever
+                        // was computed there.
+                        const f32x4 xf = *(const f32x4 *)(xrow + 4 * row);
+                        const float c = xf[0] * kLog2e, scale = xf[1];
+                        const i32x4 xi = __builtin_bit_cast(i32x4, xf);
+                        const int tc = xi[2] - p.v0 - gcol;
+                        float pr[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) pr[e] = exp2_hw(__builtin_fmaf(v[e], kLog2e, -c));
+                        if ((unsigned)tc < 8u) {
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                if (e == tc) pr[e] -= 1.0f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; e++) d[e] = st16<BF>(pr[e] * scale);
+                        if (xi[3] || gcol + 8 > p.N) {
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                if (xi[3] || gcol + e >= p.N) d[e] = (_Float16)0.0f;
+                        }
+                        put8(d, rD, p.D, p.ldd, row);
                     }
                 }
             }
+        };
+        if constexpr (EPI == LE_XP) {
+            slabs(std::true_type{});
+        } else {
+            if (vec)
+                slabs(std::true_type{});
+            else
+                slabs(std::false_type{});
         }
         wave_lds_sync();  // this wave's reads are done before the next 64 rows overwrite its slabs
     }

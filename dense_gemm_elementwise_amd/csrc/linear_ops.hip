@@ -6,6 +6,7 @@
 // alike.
 #include <hip/hip_runtime.h>
 #include <algorithm>
+#include <math.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -103,28 +104,39 @@ struct ProductPlan {
     int64_t part_bytes = 0;  // fp32 partial sums of the splits
 };
 
-// Estimated microseconds of a plan: rounds of workgroups on 256 CUs at the rate
-// a CU reaches on the tile, a fixed cost per round (prologue, epilogue, fill),
-// and the partial sums' round trip and launch.  Rates per CU in TFLOP/s: 256 x
-// 256 5.5, the 128 x 256 ones 4.9, 128 x 128 4.2 with two workgroups on a
-// CU and 2.6 with one.
+// Estimated microseconds of a plan, from timings of every tile and split on 54
+// shapes (64^3 to 8192^2 x 2048, and 1 to 40 rows against 8192 x 4096): each
+// round of workgroups costs a fixed time (first loads, epilogue) and a time
+// per unit of K, which grows with the share of the chip at work (its clock
+// falls under full load).  Measured (fixed us; ns per unit of K, from few
+// workgroups to a full chip):
+//   256 x 256           13;   15.6 .. 22
+//   128 x 256, 256 x 128  9;    8   .. 11.8
+//   128 x 128            5;    7.2 .. 8.6, and 5.5; 13.2 for two on a CU
+// Past two rounds the workgroups drift apart and the last round costs half of
+// one.  A split adds a launch, its workgroups and the partial sums'
+// round trip.  The pick was
+// within 8% of the fastest form on all but 3 of the 54.
 double product_cost(int64_t M, int64_t N, int64_t K, int tile, int splits)
 {
     const LinTile t = kLinTiles[tile];
-    const int64_t groups = ceil_div(M, t.bm) * ceil_div(N, t.bn) * splits;
-    const double work = 2.0 * t.bm * t.bn * (double)round_up(ceil_div(K, splits), 32);
-    double us;
-    if (tile == kLinSmall) {
-        const int64_t pairs = groups / (2 * kCUs), rest = groups % (2 * kCUs);
-        us = pairs * (2 * work / 4.2e6 + 3.0);
-        if (rest > kCUs)
-            us += 2 * work / 4.2e6 + 3.0;
-        else if (rest > 0)
-            us += work / 2.6e6 + 3.0;
+    const double groups = (double)(ceil_div(M, t.bm) * ceil_div(N, t.bn) * splits);
+    const double k = (double)round_up(ceil_div(K, splits), 32) * 1e-3;
+    const double share = std::min(1.0, groups / kCUs);
+    double slots = kCUs, round;
+    if (tile == kLinBig) {
+        round = 13.0 + k * (15.6 + 6.4 * share);
+    } else if (tile != kLinSmall) {
+        round = 9.0 + k * (8.0 + 3.8 * share);
+    } else if (groups <= kCUs) {
+        round = 5.0 + k * (7.2 + 1.4 * share);
     } else {
-        us = (double)ceil_div(groups, kCUs) * (work / (tile == kLinBig ? 5.5e6 : 4.9e6) + 4.0);
+        slots = 2 * kCUs;
+        round = 5.5 + k * 13.2;
     }
-    if (splits > 1) us += 4.0 + (double)splits * M * N * 8 / 4.0e6;
+    const double rounds = groups / slots;
+    double us = round * (rounds <= 2.0 ? ceil(rounds) : rounds + 0.5);
+    if (splits > 1) us += 2.0 + 0.25 * splits + (double)splits * M * N * 8 / 4.0e6;
     return us;
 }
 
@@ -142,7 +154,7 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsign
             if (want > 1 && (!(split_tiles >> i & 1) || K < want * 256 || grid * want > 4 * kCUs)) break;
             const int64_t k_split = round_up(ceil_div(K, want), 64);
             const int splits = (int)ceil_div(K, k_split);
-            const double c = product_cost(M, N, K, i, splits);
+            double c = product_cost(M, N, K, i, splits);
             if (c < best_cost) {
                 best_cost = c;
                 best.tile = i;
@@ -294,7 +306,23 @@ hipError_t run_zero(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes, hipS
 }
 
 // ---- linear -------------------------------------------------------------------
-constexpr int64_t kSkinnyRows = 16;  // one MFMA block of X rows
+// Rows of X up to which a product reads W through row_dot_kernel, and through
+// skinny_kernel (one MFMA block); past them it takes the tiles.
+constexpr int64_t kDotRows = 2, kSkinnyRows = 16;
+// workgroups of row_dot_kernel: eight of four waves on every CU, fewer where
+// there are fewer rows of W
+int row_dot_groups(int64_t N) { return (int)std::min<int64_t>(ceil_div(N, 4), 8 * kCUs); }
+
+template <bool BF, bool XENT, int ACT>
+hipError_t launch_few_rows(const SkinnyParams &q, hipStream_t s)
+{
+    const dim3 b(256);
+    if (q.M > kDotRows)
+        return launch(skinny_kernel<BF, XENT, ACT>, dim3((unsigned)ceil_div(q.N, XENT ? 64 : 16)), b, s, q);
+    const dim3 g((unsigned)row_dot_groups(q.N));
+    if (q.M == 1) return launch(row_dot_kernel<BF, XENT, ACT, 1>, g, b, s, q);
+    return launch(row_dot_kernel<BF, XENT, ACT, 2>, g, b, s, q);
+}
 
 struct LinearPlan {
     bool skinny = false;
@@ -358,12 +386,11 @@ int run_linear(const ge_linear_args *a, const LinearPlan &pl)
         q.ldr = a->ldr;
         q.ldd = a->ldd;
         q.ldz = a->ldz;
-        const dim3 g((unsigned)ceil_div(a->N, 16)), b(256);
         switch (act) {
-        case ACT_RELU: return hip_status(launch(skinny_kernel<BF, false, ACT_RELU>, g, b, s, q));
-        case ACT_GELU: return hip_status(launch(skinny_kernel<BF, false, ACT_GELU>, g, b, s, q));
-        case ACT_SILU: return hip_status(launch(skinny_kernel<BF, false, ACT_SILU>, g, b, s, q));
-        default: return hip_status(launch(skinny_kernel<BF, false, ACT_IDENTITY>, g, b, s, q));
+        case ACT_RELU: return hip_status(launch_few_rows<BF, false, ACT_RELU>(q, s));
+        case ACT_GELU: return hip_status(launch_few_rows<BF, false, ACT_GELU>(q, s));
+        case ACT_SILU: return hip_status(launch_few_rows<BF, false, ACT_SILU>(q, s));
+        default: return hip_status(launch_few_rows<BF, false, ACT_IDENTITY>(q, s));
         }
     }
     Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
@@ -587,7 +614,7 @@ int plan_xent(const ge_linear_xent_args *a, XentPlan &pl)
     Layout lay;
     pl.skinny = a->T <= kSkinnyRows;
     if (pl.skinny) {
-        pl.nparts = (int)ceil_div(a->V, 64);
+        pl.nparts = a->T <= kDotRows ? row_dot_groups(a->V) : (int)ceil_div(a->V, 64);
     } else {
         pl.st = plan_staging2(a->X, a->ldx, a->T, a->W, a->ldw, a->V, a->K, lay);
         pl.pl = plan_product(a->T, a->V, a->K, kSquareTiles, 0);
@@ -622,7 +649,7 @@ int run_xent(const ge_linear_xent_args *a, const XentPlan &pl)
         q.part_sum = psum;
         q.tlogit = tlogit;
         q.nparts = pl.nparts;
-        GE_TRY(launch(skinny_kernel<BF, true, ACT_IDENTITY>, dim3(pl.nparts), dim3(256), s, q));
+        GE_TRY((launch_few_rows<BF, true, ACT_IDENTITY>(q, s)));
     } else {
         Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
         GE_TRY(run_staging(pl.st, ws, a->K, x, a->T, w, a->V, s));

@@ -11,46 +11,17 @@
 
 namespace gemm_epi {
 
-// 16-byte access at any element alignment (global memory takes it at the
-// rate of the cache lines it touches)
-typedef half8 half8u __attribute__((aligned(2)));
-typedef f32x4 f32x4u __attribute__((aligned(4)));
-
-// 8 consecutive elements, the first n of which exist (the rest read as zeros)
-__device__ __forceinline__ half8 load8(const _Float16 *p, int n)
-{
-    if (n >= 8) return *(const half8u *)p;
-    half8 v = {};
-#pragma unroll
-    for (int e = 0; e < 7; e++)
-        if (e < n) v[e] = p[e];
-    return v;
-}
-__device__ __forceinline__ void store8(_Float16 *p, half8 v, int n)
-{
-    if (n >= 8) {
-        *(half8u *)p = v;
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 7; e++)
-        if (e < n) p[e] = v[e];
-}
-
 // ---------------------------------------------------------------------------
-// Products with at most 16 rows of X (single tokens): bound by reading W
-// once.  A wave holds 16 rows of W against all rows of X in one 16x16x32
-// MFMA block; each lane reads 16 bytes of a W row per MFMA, straight into the
-// operand layout, 8 MFMAs (512 contiguous bytes a row) per group of loads and
-// the next group's loads in flight.  No LDS on the way in, so any alignment
-// and any K run the same code.  Rows past N or M repeat the last one and are
-// never stored.
-//   linear: the workgroup's four waves take turns over K for the same 16
-//     rows (N / 16 workgroups fill the chip from N = 4096 on), their sums meet
-//     in LDS, 256 threads apply the epilogue.
-//   cross entropy: every wave has 16 rows of its own (the vocabulary fills the
-//     chip) and all of K; the workgroup leaves the softmax statistics of its 64
-//     columns.
+// Products with at most 16 rows of X (single tokens, small batches of them):
+// bound by reading W once.  No LDS on the way in, 16-byte loads at any
+// alignment, and plain loads: non-temporal ones were 15-18% slower.  V = 100003,
+// K = 4096, one row of X, bf16, W in HBM:
+//   row_dot_kernel (1 or 2 rows): a wave reads one row of W, 1 KB contiguous
+//     per load, against the rows of X in fp32 multiply-adds: 116 us, 7.1 TB/s;
+//   skinny_kernel (3 to 16): a wave reads 16 rows of W, 64 bytes of each per
+//     load, straight into the operand layout of one 16x16x32 MFMA against all
+//     rows of X: 132 us, 6.2 TB/s whatever the rows of X, where the
+//     multiply-adds of the other would take over from the loads.
 // ---------------------------------------------------------------------------
 struct SkinnyParams {
     const _Float16 *X, *W;
@@ -64,6 +35,104 @@ struct SkinnyParams {
     int nparts;
 };
 
+// Joins the four waves' running (maximum, sum) of M rows and leaves them in the
+// workgroup's column of the partial statistics; red: [2][4][MX].
+template <int MX>
+__device__ __forceinline__ void xent_part(float *red, int M, float *part_max, float *part_sum, int nparts)
+{
+    __syncthreads();
+    const int tid = threadIdx.x;
+    if (tid >= M) return;
+    float m = red[tid], s = red[4 * MX + tid];
+#pragma unroll
+    for (int u = 1; u < 4; u++) softmax_join(m, s, red[u * MX + tid], red[4 * MX + u * MX + tid]);
+    const int64_t o = (int64_t)tid * nparts + blockIdx.x;
+    part_max[o] = m;
+    part_sum[o] = s;
+}
+
+// One row of W per wave and turn, rows dealt out over all waves; lane l takes
+// columns 8 l + 512 i.  MX: M, 1 or 2.  In the cross entropy a
+// wave keeps a running maximum and sum over its rows.
+template <bool BF, bool XENT, int ACT, int MX>
+__global__ __launch_bounds__(256, 8) void row_dot_kernel(SkinnyParams p)
+{
+    __shared__ float red[2 * 4 * MX];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    constexpr int U = 4 / MX;  // groups of 512 columns whose loads are in flight together
+    const int mine = lane < p.M ? lane : 0;  // lanes 0 .. M-1 finish one row of X each
+    const int64_t target = XENT ? p.target[mine] : 0;
+    float top = -__builtin_inff(), sum = 0.0f;
+    for (int n = blockIdx.x * 4 + wave; n < p.N; n += gridDim.x * 4) {
+        const _Float16 *w = p.W + (int64_t)n * p.ldw;
+        float bias = 0.0f, res = 0.0f;
+        if constexpr (!XENT) {
+            if (p.bias) bias = ld16<BF>(p.bias[n]);
+            if (p.R) res = ld16<BF>(p.R[mine * p.ldr + n]);
+        }
+        float acc[MX] = {};
+        auto add = [&](const half8 &wv, const half8 &xv, int m) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) acc[m] = __builtin_fmaf(ld16<BF>(wv[e]), ld16<BF>(xv[e]), acc[m]);
+        };
+        int k = 0;
+        for (; k + 512 * U <= p.K; k += 512 * U) {
+            half8 wv[U], xv[U][MX];
+#pragma unroll
+            for (int u = 0; u < U; u++) wv[u] = *(const half8u *)(w + k + u * 512 + lane * 8);
+#pragma unroll
+            for (int u = 0; u < U; u++)
+#pragma unroll
+                for (int m = 0; m < MX; m++)
+                    xv[u][m] = *(const half8u *)(p.X + min(m, p.M - 1) * p.ldx + k + u * 512 + lane * 8);
+#pragma unroll
+            for (int u = 0; u < U; u++)
+#pragma unroll
+                for (int m = 0; m < MX; m++) add(wv[u], xv[u][m], m);
+        }
+        for (k += lane * 8; k < p.K; k += 512) {
+            const half8 wv = load8(w + k, p.K - k);
+#pragma unroll
+            for (int m = 0; m < MX; m++) add(wv, load8(p.X + min(m, p.M - 1) * p.ldx + k, p.K - k), m);
+        }
+        float v = 0.0f;  // lane m: row m's sum
+#pragma unroll
+        for (int m = 0; m < MX; m++) {
+            float a = row16_sum(acc[m]);
+            a += __shfl_xor(a, 16);
+            a += __shfl_xor(a, 32);
+            if (lane == m) v = a;
+        }
+        if constexpr (XENT) {
+            if (lane < p.M) {
+                softmax_join(top, sum, v, 1.0f);
+                if (target == n) p.tlogit[lane] = v;
+            }
+        } else if (lane < p.M) {
+            const float z = v + bias;
+            if (p.Z) p.Z[lane * p.ldz + n] = st16<BF>(z);
+            p.D[lane * p.ldd + n] = st16<BF>(lin_act<ACT>(z) + res);
+        }
+    }
+    if constexpr (XENT) {
+        if (lane < MX) {
+            red[wave * MX + lane] = top;
+            red[4 * MX + wave * MX + lane] = sum;
+        }
+        xent_part<MX>(red, p.M, p.part_max, p.part_sum, p.nparts);
+    }
+}
+
+// A wave holds 16 rows of W against all rows of X in one MFMA block; a lane
+// reads 16 bytes of a W row per MFMA, 8 MFMAs (512 contiguous bytes a row) per
+// group of loads and the next group's loads in flight.  Rows past N or M repeat
+// the last one and are never stored.
+//   linear: the workgroup's four waves take turns over K for the same 16
+//     rows (N / 16 workgroups fill the chip from N = 4096 on), their sums meet
+//     in LDS, 256 threads apply the epilogue.
+//   cross entropy: every wave has 16 rows of its own (the vocabulary fills the
+//     chip) and all of K; the workgroup leaves the softmax statistics of its 64
+//     columns.
 template <bool BF, bool XENT, int ACT>
 __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
 {
@@ -80,7 +149,7 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
     auto fetch = [&](int k0) {
         if (k0 + SPAN <= p.K) {
 #pragma unroll
-            for (int u = 0; u < U; u++) wv[u] = __builtin_nontemporal_load((const half8u *)(w + k0 + u * 32));
+            for (int u = 0; u < U; u++) wv[u] = *(const half8u *)(w + k0 + u * 32);
 #pragma unroll
             for (int u = 0; u < U; u++) xv[u] = *(const half8u *)(x + k0 + u * 32);
         } else {
@@ -148,16 +217,7 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
             red[wave * 16 + li] = m;
             red[64 + wave * 16 + li] = s;
         }
-        __syncthreads();
-        if (tid < p.M) {
-            m = red[tid];
-            s = red[64 + tid];
-#pragma unroll
-            for (int u = 1; u < 4; u++) softmax_join(m, s, red[u * 16 + tid], red[64 + u * 16 + tid]);
-            const int64_t o = (int64_t)tid * p.nparts + blockIdx.x;
-            p.part_max[o] = m;
-            p.part_sum[o] = s;
-        }
+        xent_part<16>(red, p.M, p.part_max, p.part_sum, p.nparts);
     }
 }
 
@@ -400,11 +460,15 @@ __global__ __launch_bounds__(256) void xent_loss_kernel(const float *part_max, c
 
 // The gradient's row data.  P is stored in 16 bits, and fp16 has no room for
 // a probability of 1e-6 times a loss of 1/T.  So the incoming gradients are
-// divided by the power of two s at or below their largest magnitude and
-// multiplied by 2^14: |P| stays below 2^15 + 1 < 65504 and a probability
-// down to 2^-28 is still a normal number.  Powers of two, so nothing is
-// rounded; the products' fp32 sums are multiplied by s 2^-14 (`alpha`) before
-// their one rounding.  One block; T values are read twice.
+// divided by the largest of their magnitudes (fp32) and multiplied by 2^14:
+// |P| stays below 2^14 + 1 < 65504 and a probability down to 2^-28 is still a
+// normal number.  The products' fp32 sums are multiplied by that magnitude
+// times 2^-14 (`alpha`) before their one rounding.  Dividing by the magnitude
+// itself, not by the power of two below it, keeps the entry at the target, near
+// -1 in a row of the largest gradient, where 16 bits hold it best: a mean over
+// the batch has only such rows, and fp16 gradients of a 333 x 9999 batch came
+// out 1.5 times as far from exact with the power of two.  One block; T values
+// are read twice.
 __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, int64_t ignore, const float *dloss,
                                                          const float *lse, const int64_t *target, XentRow *rows,
                                                          float *alpha)
@@ -421,18 +485,15 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, int64
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < 16; u++) top = __builtin_fmaxf(top, red[u]);
-    // the exponent of top, kept where both 2^(14-e) and 2^(e-14) are normal
-    int e = (int)((__builtin_bit_cast(uint32_t, top) >> 23) & 255) - 127;
-    e = e < -100 ? -100 : (e > 126 ? 126 : e);
-    const float up = __builtin_bit_cast(float, (uint32_t)(14 - e + 127) << 23);
-    if (threadIdx.x == 0) *alpha = __builtin_bit_cast(float, (uint32_t)(e - 14 + 127) << 23);
+    if (threadIdx.x == 0) *alpha = top * 0x1p-14f;
+    const float div = top > 0.0f ? top : 1.0f;
     for (int t = threadIdx.x; t < T; t += 1024) {
         const int64_t c = target[t];
         XentRow r;
         r.lse = lse[t];
         r.ignored = c == ignore;
         r.target = c >= 0 && c < V ? (int)c : -1;
-        r.scale = dloss[t] * up;
+        r.scale = dloss[t] / div * 0x1p14f;
         if (!r.ignored && r.target < 0) r.scale = __builtin_nanf("");
         rows[t] = r;
     }

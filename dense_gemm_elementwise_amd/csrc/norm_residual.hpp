@@ -60,6 +60,15 @@ struct StreamVec<BF, true> {
     }
 };
 
+// the last lane of a lower row (0x142: the row below; 0x143: row 1) in the rows
+// of ROWS, zero in the others
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_rows(float x)
+{
+    return __builtin_bit_cast(float,
+                              __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, false));
+}
+
 // Sums of N values over the workgroup of up to 16 waves, in a fixed order; every
 // thread gets them.  The two LDS buffers alternate from call to call: a thread
 // writes a buffer again only past the other one's barrier, which every thread
@@ -73,13 +82,20 @@ struct BlockSum {
     {
 #pragma unroll
         for (int i = 0; i < N; i++) {
+            // rows of 16 lanes, then row 0 onto 1 and 2 onto 3, then the lower
+            // half onto the upper: lane 63 has the wave's sum
             v[i] = row16_sum(v[i]);
-            v[i] += __shfl_xor(v[i], 16);
-            v[i] += __shfl_xor(v[i], 32);
+            v[i] += dpp_rows<0x142, 0xA>(v[i]);
+            v[i] += dpp_rows<0x143, 0xC>(v[i]);
         }
-        if (waves == 1) return;
+        if (waves == 1) {
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                v[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v[i]), 63));
+            return;
+        }
         const int li = threadIdx.x & 15;
-        if ((threadIdx.x & 63) == 0)
+        if ((threadIdx.x & 63) == 63)
 #pragma unroll
             for (int i = 0; i < N; i++) lds[phase][threadIdx.x >> 6][i] = v[i];
         barrier_lds();

@@ -42,8 +42,14 @@ _NORM = struct.Struct("@3q 2q 2q 3q 2q 2d 2q 2q 2q")
 _NORM_GRAD = struct.Struct("@3q 2q 2q 2q 2q 3q 2q 2d 2q 2q 3q 2q")
 _TAIL = struct.Struct("@3q")  # workspace, workspace_bytes, stream
 _STREAM = struct.Struct("@q")
+_NO_TAIL = _TAIL.pack(0, 0, 0)
 
 _fns = None
+
+# the current stream's address by device index; the plain query where torch has
+# it (a torch.cuda.Stream object costs 1.5 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _functions():
@@ -79,15 +85,17 @@ def _raise(rc):
 
 
 def _queue(name, head, dev, raw_stream):
-    """Makes one call; a call that needs a workspace says so first, and gets one
-    from torch's allocator (in the order of the current stream)."""
-    f = _functions()[name]
-    if name not in _WORKSPACE:
+    """Makes one call.  A workspace, where the call needs one, comes from
+    torch's allocator, in the order of the current stream.  ge_linear is tried
+    without one first: the calls where latency counts (few rows) need none."""
+    fns = _fns or _functions()
+    f = fns[name]
+    if name == "ge_norm_residual":
         rc = f(head + _STREAM.pack(raw_stream))
     else:
-        rc = f(head + _TAIL.pack(0, 0, raw_stream))
+        rc = f(head + _TAIL.pack(0, 0, raw_stream)) if name == "ge_linear" else 7
         if rc == 7:
-            rc, need = workspace_bytes(name, head + _TAIL.pack(0, 0, raw_stream))
+            rc, need = workspace_bytes(name, head + _NO_TAIL)
             if rc == 0:
                 ws = torch.empty(need, dtype=torch.uint8, device=dev)
                 rc = f(head + _TAIL.pack(ws.data_ptr(), need, raw_stream))
@@ -108,10 +116,11 @@ def _run(call, inputs, dev, stream):
             if t is not None:
                 t.record_stream(stream)
         return out
-    if torch.cuda.current_device() != dev.index:
+    index = dev.index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(dev):
-            return call(torch.cuda.current_stream(dev).cuda_stream)
-    return call(torch.cuda.current_stream(dev).cuda_stream)
+            return call(_raw_stream(index))
+    return call(_raw_stream(index))
 
 
 def _common(first_name, first, dtypes=_DTYPES):
@@ -143,6 +152,10 @@ def _check(name, t, shape, dtype, dev):
 
 def _matrix(name, t, shape, dtype, dev):
     """(address, row stride) of a 2-D tensor with unit stride along its rows."""
+    # one test for the ordinary case; the messages come after it
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
+            and t.is_contiguous() and not t.requires_grad):
+        return t.data_ptr(), shape[1]
     _check(name, t, shape, dtype, dev)
     s0, s1 = t.stride()
     if shape[1] > 1 and s1 != 1:
@@ -158,6 +171,9 @@ def _vector(name, t, n, dtype, dev):
     """The address of a contiguous vector, or 0 for None."""
     if t is None:
         return 0
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == (n,)
+            and t.is_contiguous() and not t.requires_grad):
+        return t.data_ptr()
     _check(name, t, (n,), dtype, dev)
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
@@ -188,8 +204,8 @@ def linear(x, w, bias=None, residual=None, *, act="identity", save_z=False, stre
     rp = _matrix("residual", residual, (M, N), dtype, dev) if residual is not None else (0, 0)
 
     def call(raw):
-        d = torch.empty((M, N), dtype=dtype, device=dev)
-        z = torch.empty((M, N), dtype=dtype, device=dev) if save_z else None
+        d = x.new_empty((M, N))
+        z = torch.empty_like(d) if save_z else None
         _queue("ge_linear", _LINEAR.pack(M, N, K, *xp, *wp, bp, *rp, d.data_ptr(), N, z.data_ptr() if save_z else 0,
                                          N, a, _DTYPES[dtype]), dev, raw)
         return (d, z) if save_z else d
@@ -217,8 +233,8 @@ def linear_backward(dd, x, w, z=None, *, act="identity", need_dx=True, need_dw=T
     zp = _matrix("z", z, (M, N), dtype, dev) if z is not None else (0, 0)
 
     def call(raw):
-        dx = torch.empty((M, K), dtype=dtype, device=dev) if need_dx else None
-        dw = torch.empty((N, K), dtype=dtype, device=dev) if need_dw else None
+        dx = dd.new_empty((M, K)) if need_dx else None
+        dw = dd.new_empty((N, K)) if need_dw else None
         db = torch.empty((N,), dtype=torch.float32, device=dev) if need_dbias else None
         _queue("ge_linear_backward",
                _LINEAR_GRAD.pack(M, N, K, *dp, *xp, *wp, *zp, dx.data_ptr() if need_dx else 0, K,
@@ -246,7 +262,7 @@ def linear_xent(x, w, target, *, ignore_index=-100, stream=None):
 
     def call(raw):
         loss = torch.empty((T,), dtype=torch.float32, device=dev)
-        lse = torch.empty((T,), dtype=torch.float32, device=dev)
+        lse = torch.empty_like(loss)
         _queue("ge_linear_xent", _XENT.pack(T, V, K, *xp, *wp, tp, int(ignore_index), loss.data_ptr(),
                                             lse.data_ptr(), _DTYPES[dtype]), dev, raw)
         return loss, lse
@@ -275,8 +291,8 @@ def linear_xent_backward(dloss, x, w, target, lse, *, ignore_index=-100, need_dx
     lp = _vector("lse", lse, T, torch.float32, dev)
 
     def call(raw):
-        dx = torch.empty((T, K), dtype=dtype, device=dev) if need_dx else None
-        dw = torch.empty((V, K), dtype=dtype, device=dev) if need_dw else None
+        dx = x.new_empty((T, K)) if need_dx else None
+        dw = x.new_empty((V, K)) if need_dw else None
         _queue("ge_linear_xent_backward",
                _XENT_GRAD.pack(T, V, K, gp, *xp, *wp, tp, lp, int(ignore_index), dx.data_ptr() if need_dx else 0, K,
                                dw.data_ptr() if need_dw else 0, K, _DTYPES[dtype]), dev, raw)
@@ -322,8 +338,7 @@ def norm_residual(h, y, *, w_post=None, w_pre=None, gate=None, scale=1.0, post="
     yp = _matrix("y", y, (T, H), dtype, dev)
 
     def call(raw):
-        ho = torch.empty((T, H), dtype=sd, device=dev)
-        x = torch.empty((T, H), dtype=dtype, device=dev)
+        ho, x = h.new_empty((T, H)), y.new_empty((T, H))
         _queue("ge_norm_residual", _NORM.pack(T, H, G, *hp, *yp, *mid, scale, eps, ho.data_ptr(), H, x.data_ptr(), H,
                                               _DTYPES[dtype], _STREAM_DTYPES[sd]), dev, raw)
         return ho, x
@@ -344,12 +359,12 @@ def norm_residual_backward(dx, dh_out, h_out, y, *, w_post=None, w_pre=None, gat
     yp = _matrix("y", y, (T, H), dtype, dev)
 
     def call(raw):
-        def new(shape, dt):
-            return torch.empty(shape, dtype=dt, device=dev)
-        dh, dy = new((T, H), sd), new((T, H), dtype)
-        dwo = new((H,), torch.float32) if w_post is not None else None
-        dwi = new((H,), torch.float32) if w_pre is not None else None
-        dg = new((G, H), torch.float32) if gate is not None else None
+        def new32(shape):
+            return torch.empty(shape, dtype=torch.float32, device=dev)
+        dh, dy = h_out.new_empty((T, H)), y.new_empty((T, H))
+        dwo = new32((H,)) if w_post is not None else None
+        dwi = new32((H,)) if w_pre is not None else None
+        dg = new32((G, H)) if gate is not None else None
         _queue("ge_norm_residual_backward",
                _NORM_GRAD.pack(T, H, G, *dxp, *dhp, *hp, *yp, *mid, scale, eps, dh.data_ptr(), H, dy.data_ptr(), H,
                                *(t.data_ptr() if t is not None else 0 for t in (dwo, dwi, dg)), _DTYPES[dtype],

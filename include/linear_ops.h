@@ -115,8 +115,7 @@ typedef struct {
 /* dloss (T) fp32, lse (T) from ge_linear_xent; dX (T, K), dW (V, K), each NULL
  * where it is not wanted.  P = (exp(logit - lse) - [v == target]) dloss, zero in
  * ignored rows, is formed one piece of the vocabulary at a time and rounded to
- * the element type as an operand (scaled by a power of two against fp16's
- * range).  A row whose target is out of range makes its gradients NaN. */
+ * the element type as an operand (scaled into fp16's range).  A row whose target is out of range makes its gradients NaN. */
 typedef struct {
     int64_t T, V, K;
     const float *dloss;

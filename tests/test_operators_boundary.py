@@ -224,3 +224,18 @@ def test_python_refusals():
         ge.norm_residual(x, x)
     with pytest.raises(AttributeError):
         ge.no_such_operator
+
+
+def test_header_is_plain_c(tmp_path):
+    """The header compiles as C99, and every structure is made of 8-byte fields only."""
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    checks = "\n".join(f"typedef char size_{c.name}[sizeof({c.name}_args) == 8 * {len(c.names)} ? 1 : -1];"
+                       for c in CALLS)
+    src = tmp_path / "header.c"
+    src.write_text(f'#include "linear_ops.h"\n{checks}\nint main(void) {{ return 0; }}\n')
+    subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-fsyntax-only", "-I",
+                    os.path.join(ROOT, "include"), str(src)], check=True)
