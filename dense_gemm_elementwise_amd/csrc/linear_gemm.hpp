@@ -299,9 +299,11 @@ struct LinCfg {
     using OA = LinOperand<BM, AKM, NH>;
     using OB = LinOperand<BN, BKM, NH>;
     static constexpr int MAIN = OA::BYTES + OB::BYTES;
-    static constexpr int WN = BN / 2;
-    static constexpr int LDW = WN + 4;  // slab pitch in floats
-    static constexpr int EPI = 4 * 64 * LDW * 4 + BM * 16;
+    // the epilogues' slabs: 64 rows a wave in fp32, or all its BM / 2 in 16
+    // bits; then the rows' data
+    static constexpr int SLAB32 = 64 * (BN / 2) * 4, SLAB16 = (BM / 2) * (BN / 2) * 2;
+    static constexpr int SLABS = 4 * (SLAB32 > SLAB16 ? SLAB32 : SLAB16);
+    static constexpr int EPI = SLABS + BM * 16;
     static constexpr int LDS = MAIN > EPI ? MAIN : EPI;
     static_assert(LDS <= 160 * 1024, "LDS budget");
 };
@@ -400,7 +402,9 @@ __device__ __forceinline__ void mainloop_lin(f32x4 (&acc)[BM / 32][BN / 32], con
         i32x4 ra, rb;
         static_for<NMF>([&](auto M_) {
             constexpr int m = decltype(M_)::value;
-            mfma16_agpr<BF>(acc[m / TN][m % TN], fa[P][m / TN], fb[P][m % TN]);
+            // B first: the block comes out transposed, a lane with 4 consecutive
+            // columns of one row (what the epilogues store)
+            mfma16_agpr<BF>(acc[m / TN][m % TN], fb[P][m % TN], fa[P][m / TN]);
             static_for<NR>([&](auto R_) {
                 constexpr int r = decltype(R_)::value;
                 if constexpr (r * NMF / NR == m) do_read(R_, DN{}, std::integral_constant<int, P ^ 1>{});
@@ -491,32 +495,47 @@ __device__ __forceinline__ void pin_row(f32x4 (&row)[TN])
 }
 
 // ---------------------------------------------------------------------------
-// Epilogues.  The tile goes through LDS 64 rows a wave at a time, so
-// that a lane owns 8 consecutive columns (16-byte accesses).  With p.vec the
-// outputs and the residual go through range-checked buffer accesses (rows
-// past M and, parked, columns past N are dropped; an absent tensor is a
-// descriptor of zero records, which reads as zeros); otherwise through
-// guarded 16-byte accesses at any element alignment, element by element where
-// a row ends inside one.
+// Epilogues.  Lane (li, lg) of wave (wm, wn) holds, of block (i, j), row
+// wm BM/2 + 16 i + li, columns wn BN/2 + 16 j + 4 lg .. + 3.
+//   fp32 outputs (partial sums, the accumulator) go out as they are, 16 bytes a
+//     lane, 64 contiguous bytes a row.
+//   16-bit outputs are rounded there and turned around in LDS (8-byte writes,
+//     16-byte reads) so that a lane stores 16 bytes and 16 lanes a whole row of
+//     the wave's block.
+//   The forward needs its residual next to the fp32 value, so there 64 rows at
+//     a time go through LDS in fp32.
+//   The softmax statistics stay in the accumulator layout.
+// The LDS rows are not padded: the 16-byte chunks of a row are XOR-swizzled
+// with the row so that the writes (16 rows, 2 chunks) and the reads (2 or 4 whole
+// rows) both cover all banks.  Against accumulators the other way around,
+// which took four times the LDS writes and a reduction over 16 lanes for every
+// row's statistics, an epilogue is TODO.
+//
+// With p.vec the outputs and the residual go through range-checked buffer
+// accesses (rows past M and, parked, columns past N are dropped; an absent
+// tensor is a descriptor of zero records, which reads as zeros); otherwise
+// through guarded 16-byte accesses at any element alignment, element by element
+// where a row ends inside one.
 // ---------------------------------------------------------------------------
 template <int BM, int BN, int EPI, int ACT, bool BF>
 __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], const LinParams &p, int m0, int n0,
                                              int tile_n, int split, char *smem)
 {
-    constexpr int TM = BM / 32, TN = BN / 32, WN = BN / 2;
-    constexpr int LDW = WN + 4;
+    using C = LinCfg<BM, BN, false, false>;
+    constexpr int TM = BM / 32, TN = BN / 32, WM = BM / 2, WN = BN / 2;
+    constexpr uint32_t kOut = 0x7FFFFFE0u;  // parked: past every record count, with 16 bytes to spare
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
     const int li = lane & 15, lg = lane >> 4;
     const int rows_here = min(p.M - m0, BM);
+    const int64_t m0l = m0;
     barrier_lds();  // every wave is done with the main loop's LDS
 
     if constexpr (EPI == LE_XFWD) {
-        // Softmax statistics of the tile's columns, in the accumulator layout:
-        // lane (li, lg) of wave (wm, wn) holds rows wm BM/2 + 16 i + 4 lg + r,
-        // columns wn WN + 16 j + li.
-        int *tcol = (int *)smem;                    // the target's column in this tile, or -1
-        float *red = (float *)(smem + BM * 4);      // [2][BM][2]: the two column halves' (max, sum)
+        // a lane's maximum and sum over its 4 TN columns of a row; the 8 lanes
+        // that share a row meet in LDS
+        int *tcol = (int *)smem;                // the target's column in this tile, or -1
+        float *red = (float *)(smem + BM * 4);  // [8][BM][2]
         if (tid < BM) {
             int64_t c = -1;
             if (tid < rows_here) {
@@ -527,55 +546,56 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
         }
         barrier_lds();
         const bool edge = n0 + BN > p.N;
+        const int col0 = wn * WN + 4 * lg;
 #pragma unroll
         for (int i = 0; i < TM; i++) {
             pin_row<TN>(acc[i]);
-            float x[TN][4];
+            const int row = wm * WM + i * 16 + li;
+            f32x4 x[TN];
 #pragma unroll
-            for (int j = 0; j < TN; j++)
-#pragma unroll
-                for (int r = 0; r < 4; r++) x[j][r] = acc[i][j][r];
+            for (int j = 0; j < TN; j++) x[j] = acc[i][j];
             if (edge) {
 #pragma unroll
                 for (int j = 0; j < TN; j++)
-                    if (n0 + wn * WN + j * 16 + li >= p.N)
 #pragma unroll
-                        for (int r = 0; r < 4; r++) x[j][r] = -__builtin_inff();
+                    for (int r = 0; r < 4; r++)
+                        if (n0 + col0 + j * 16 + r >= p.N) x[j][r] = -__builtin_inff();
             }
+            float m = x[0][0];
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const int row = wm * (BM / 2) + i * 16 + 4 * lg + r;
-                float m = x[0][r];
+            for (int j = 0; j < TN; j++)
 #pragma unroll
-                for (int j = 1; j < TN; j++) m = __builtin_fmaxf(m, x[j][r]);
-                m = row16_max(m);
-                // e^(x - m) as 2^(x log2 e - ref), one fma an element; what the
-                // rounding of ref = m log2 e left out is put back once a row
-                const float mf = m == -__builtin_inff() ? 0.0f : m;
-                const float ref = mf * kLog2e;
-                float s = 0.0f;
+                for (int r = 0; r < 4; r++) m = __builtin_fmaxf(m, x[j][r]);
+            // e^(x - m) as 2^(x log2 e - ref), one fma an element; what the
+            // rounding of ref = m log2 e left out is put back once a row
+            const float mf = m == -__builtin_inff() ? 0.0f : m;
+            const float ref = mf * kLog2e;
+            float s[4] = {};
 #pragma unroll
-                for (int j = 0; j < TN; j++) s += exp2_hw(__builtin_fmaf(x[j][r], kLog2e, -ref));
-                s = row16_sum(s) * exp2_hw(-__builtin_fmaf(mf, kLog2e, -ref));
-                if (li == 0) {
-                    red[(wn * BM + row) * 2] = m;
-                    red[(wn * BM + row) * 2 + 1] = s;
-                }
-                const int t = tcol[row] - wn * WN;
-                if (t >= 0 && t < WN && (t & 15) == li) {
-                    float v = x[0][r];
+            for (int j = 0; j < TN; j++)
 #pragma unroll
-                    for (int j = 1; j < TN; j++)
-                        if ((t >> 4) == j) v = x[j][r];
-                    p.tlogit[m0 + row] = v;
-                }
+                for (int r = 0; r < 4; r++) s[r] += exp2_hw(__builtin_fmaf(x[j][r], kLog2e, -ref));
+            float2 ms;
+            ms.x = m;
+            ms.y = ((s[0] + s[1]) + (s[2] + s[3])) * exp2_hw(-__builtin_fmaf(mf, kLog2e, -ref));
+            *(float2 *)(red + ((wn * 4 + lg) * BM + row) * 2) = ms;
+            const int t = tcol[row] - col0;
+            if (t >= 0 && t < WN && (t & 12) == 0) {  // this lane's columns: 16 j + r
+                float v = x[0][0];
+#pragma unroll
+                for (int j = 0; j < TN; j++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        if (t == 16 * j + r) v = x[j][r];
+                p.tlogit[m0 + row] = v;
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         barrier_lds();
         if (tid < rows_here) {
             float m = red[tid * 2], s = red[tid * 2 + 1];
-            softmax_join(m, s, red[(BM + tid) * 2], red[(BM + tid) * 2 + 1]);
+#pragma unroll
+            for (int u = 1; u < 8; u++) softmax_join(m, s, red[(u * BM + tid) * 2], red[(u * BM + tid) * 2 + 1]);
             const int64_t o = (int64_t)(m0 + tid) * p.nparts + tile_n;
             p.part_max[o] = m;
             p.part_sum[o] = s;
@@ -583,172 +603,205 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
         return;
     }
 
-    constexpr int LPR = WN / 8, RPP = 64 / LPR, PASSES = 16 / RPP;
-    float *slab = (float *)(smem + wave * (64 * LDW * 4));
-    int32_t *xrow = (int32_t *)(smem + 4 * 64 * LDW * 4);  // LE_XP: the tile's XentRow entries
-    if constexpr (EPI == LE_XP) {
-        if (tid < BM) {
-            i32x4 r = {0, 0, -1, 1};
-            if (tid < rows_here) r = *(const i32x4 *)(p.rows + m0 + tid);
-            *(i32x4 *)(xrow + 4 * tid) = r;
-        }
-        barrier_lds();
-    }
-    const int ncols = EPI == LE_XP ? p.n_store : p.N;
-    const int scol = 8 * (lane % LPR);
-    const int gcol = n0 + wn * WN + scol;
-    const bool col_in = gcol < ncols;
-    const int64_t m0l = m0;
+    // descriptor of the tile's rows of a tensor of es-byte elements
     auto res_of = [&](const void *ptr, int64_t ld, int es) {
         return epi_rsrc((const char *)ptr + m0l * ld * es, ptr ? (uint32_t)((int64_t)rows_here * ld * es) : 0u);
     };
-    // byte offset of local row `row` in a tensor of `es`-byte elements, or parked
-    auto off_of = [&](int row, int64_t ld, int es) {
-        return col_in ? (row * (int)ld + gcol) * es : (int)0x7FFFFFE0;
+    // a lane's place in the row-wise passes: 8 columns from scol on, one of LPR lanes on a row
+    constexpr int LPR = WN / 8, RPP = 64 / LPR;
+    const int ncols = EPI == LE_XP ? p.n_store : p.N;
+    const int scol = 8 * (lane % LPR), srow0 = lane / LPR;
+    const int gcol = n0 + wn * WN + scol, ncol = ncols - gcol;
+    auto off_of = [&](int row, int64_t ld) {
+        return gcol < ncols ? (row * (int)ld + gcol) * 2 : (int)kOut;
     };
-    float alpha = 1.0f;
-    if constexpr (EPI == LE_OUT)
-        if (p.alpha) alpha = *p.alpha;
-
-    const bool vec = EPI == LE_XP || p.vec || (EPI == LE_OUT && p.acc_out);
     const __amdgpu_buffer_rsrc_t rD = res_of(p.D, p.ldd, 2);
-    const __amdgpu_buffer_rsrc_t rR = res_of(EPI == LE_LINEAR ? p.R : nullptr, p.ldr, 2);
-    const __amdgpu_buffer_rsrc_t rZ = res_of(EPI == LE_LINEAR ? p.Z : nullptr, p.ldz, 2);
-    const __amdgpu_buffer_rsrc_t rC =
-        res_of(EPI == LE_OUT && p.C32 ? p.C32 + (int64_t)split * p.c_split : nullptr, p.ldc, 4);
-    const int ncol = ncols - gcol;  // columns that exist from this lane's first on
-    float bias[8] = {};
-    if (EPI == LE_LINEAR && p.bias) {
-        const half8 b8 = load8(p.bias + gcol, ncol);
-#pragma unroll
-        for (int e = 0; e < 8; e++) bias[e] = ld16<BF>(b8[e]);
-    }
 
-    // 64 rows of the wave's block at a time: the accumulators' part is unrolled
-    // (registers cannot be indexed at run time), the rest is a loop over 16-row
-    // slabs, with the next slab's residual loads in flight
+    if constexpr (EPI == LE_LINEAR) {
+        const __amdgpu_buffer_rsrc_t rR = res_of(p.R, p.ldr, 2), rZ = res_of(p.Z, p.ldz, 2);
+        float bias[8] = {};
+        if (p.bias) {
+            const half8 b8 = load8(p.bias + gcol, ncol);
 #pragma unroll
-    for (int ph = 0; ph < TM / 4; ph++) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            pin_row<TN>(acc[ph * 4 + i]);
-#pragma unroll
-            for (int j = 0; j < TN; j++)
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-                    slab[(i * 16 + 4 * lg + r) * LDW + j * 16 + li] = acc[ph * 4 + i][j][r];
-            __builtin_amdgcn_sched_barrier(0);
+            for (int e = 0; e < 8; e++) bias[e] = ld16<BF>(b8[e]);
         }
-        wave_lds_sync();
-        const int row0 = wm * (BM / 2) + ph * 64;
-        auto slabs = [&](auto VEC_) {
-            constexpr bool VEC = decltype(VEC_)::value;
-            // 8 elements of a 16-bit tensor's row
-            auto get8 = [&](__amdgpu_buffer_rsrc_t r, const _Float16 *t, int64_t ld, int row) {
-                if constexpr (VEC)
-                    return buf_load<half8, 0>(r, off_of(row, ld, 2));
-                else
-                    return t && row < rows_here ? load8(t + (m0l + row) * ld + gcol, ncol) : half8{};
-            };
-            auto put8 = [&](half8 v, __amdgpu_buffer_rsrc_t r, _Float16 *t, int64_t ld, int row) {
-                if constexpr (VEC)
-                    buf_store<half8, EPI == LE_XP ? 0 : 2>(v, r, off_of(row, ld, 2));
-                else if (t && row < rows_here)
-                    store8(t + (m0l + row) * ld + gcol, v, ncol);
-            };
-            half8 rbuf[PASSES] = {};
-            auto fetch = [&](int s) {
-                if constexpr (EPI == LE_LINEAR) {
+        char *slab = smem + wave * C::SLAB32;
+        // 16-byte chunk c of a slab row: WN / 4 chunks, 128 words span one row
+        // of 128 columns or two of 64
+        auto chunk = [](int row, int c) {
+            const int f = WN == 128 ? 2 * (row & 15) | (row & 1) : 2 * ((row >> 1) & 7) | ((row >> 1) & 1);
+            return row * (WN * 4) + (c ^ f) * 16;
+        };
+        constexpr int PASSES = 16 / RPP;
 #pragma unroll
-                    for (int q = 0; q < PASSES; q++)
-                        rbuf[q] = get8(rR, p.R, p.ldr, row0 + s * 16 + q * RPP + lane / LPR);
-                }
-            };
-            fetch(0);
-#pragma unroll 1
-            for (int s = 0; s < 4; s++) {
-                half8 rcur[PASSES];
+        for (int ph = 0; ph < TM / 4; ph++) {
 #pragma unroll
-                for (int q = 0; q < PASSES; q++) rcur[q] = rbuf[q];
-                if (s < 3) fetch(s + 1);
-                f32x4 cin[PASSES][2];
-                if (EPI == LE_OUT && p.acc_in) {
+            for (int i = 0; i < 4; i++) {
+                pin_row<TN>(acc[ph * 4 + i]);
+#pragma unroll
+                for (int j = 0; j < TN; j++)
+                    *(f32x4 *)(slab + chunk(i * 16 + li, 4 * j + lg)) = acc[ph * 4 + i][j];
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            wave_lds_sync();
+            const int row0 = wm * WM + ph * 64;
+            auto slabs = [&](auto VEC_) {
+                constexpr bool VEC = decltype(VEC_)::value;
+                auto put8 = [&](half8 v, __amdgpu_buffer_rsrc_t r, _Float16 *t, int64_t ld, int row) {
+                    if constexpr (VEC)
+                        buf_store<half8, 2>(v, r, off_of(row, ld));
+                    else if (t && row < rows_here)
+                        store8(t + (m0l + row) * ld + gcol, v, ncol);
+                };
+                half8 rbuf[PASSES] = {};
+                auto fetch = [&](int s) {
 #pragma unroll
                     for (int q = 0; q < PASSES; q++) {
-                        const int oc = off_of(row0 + s * 16 + q * RPP + lane / LPR, p.ldc, 4);
-                        cin[q][0] = buf_load<f32x4, 0>(rC, oc);
-                        cin[q][1] = buf_load<f32x4, 0>(rC, oc + 16);
+                        const int row = row0 + s * 16 + q * RPP + srow0;
+                        if constexpr (VEC)
+                            rbuf[q] = buf_load<half8, 0>(rR, off_of(row, p.ldr));
+                        else
+                            rbuf[q] = p.R && row < rows_here ? load8(p.R + (m0l + row) * p.ldr + gcol, ncol) : half8{};
                     }
-                }
+                };
+                fetch(0);
+#pragma unroll 1
+                for (int s = 0; s < 4; s++) {
+                    half8 rcur[PASSES];
 #pragma unroll
-                for (int q = 0; q < PASSES; q++) {
-                    const int srow = s * 16 + q * RPP + lane / LPR, row = row0 + srow;
-                    const float *src = slab + srow * LDW + scol;
-                    const f32x4 v0 = *(const f32x4 *)src, v1 = *(const f32x4 *)(src + 4);
-                    float v[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-                    half8 d;
-                    if constexpr (EPI == LE_LINEAR) {
-                        half8 z;
+                    for (int q = 0; q < PASSES; q++) rcur[q] = rbuf[q];
+                    if (s < 3) fetch(s + 1);  // the next slab's residual flies beside this one's arithmetic
+#pragma unroll
+                    for (int q = 0; q < PASSES; q++) {
+                        const int srow = s * 16 + q * RPP + srow0;
+                        const f32x4 v0 = *(const f32x4 *)(slab + chunk(srow, scol / 4));
+                        const f32x4 v1 = *(const f32x4 *)(slab + chunk(srow, scol / 4 + 1));
+                        half8 d, z;
 #pragma unroll
                         for (int e = 0; e < 8; e++) {
-                            const float t = v[e] + bias[e];
+                            const float t = (e < 4 ? v0[e & 3] : v1[e & 3]) + bias[e];
                             z[e] = st16<BF>(t);
                             d[e] = st16<BF>(lin_act<ACT>(t) + ld16<BF>(rcur[q][e]));
                         }
-                        put8(d, rD, p.D, p.ldd, row);
-                        put8(z, rZ, p.Z, p.ldz, row);
-                    } else if constexpr (EPI == LE_OUT) {
-                        if (p.acc_in) {
-#pragma unroll
-                            for (int e = 0; e < 8; e++) v[e] += cin[q][e >> 2][e & 3];
-                        }
-                        if (p.acc_out) {
-                            const int oc = off_of(row, p.ldc, 4);
-                            buf_store<f32x4, 0>(f32x4{v[0], v[1], v[2], v[3]}, rC, oc);
-                            buf_store<f32x4, 0>(f32x4{v[4], v[5], v[6], v[7]}, rC, oc + 16);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; e++) d[e] = st16<BF>(v[e] * alpha);
-                            put8(d, rD, p.D, p.ldd, row);
-                        }
-                    } else {
-                        // p = 2^(logit log2 e - lse log2 e); the target's 1 is
-                        // taken off in the few lanes that hold one.  An ignored
-                        // row, and columns past the vocabulary, are zeros whatever
-                        // was computed there.
-                        const f32x4 xf = *(const f32x4 *)(xrow + 4 * row);
-                        const float c = xf[0] * kLog2e, scale = xf[1];
-                        const i32x4 xi = __builtin_bit_cast(i32x4, xf);
-                        const int tc = xi[2] - p.v0 - gcol;
-                        float pr[8];
-#pragma unroll
-                        for (int e = 0; e < 8; e++) pr[e] = exp2_hw(__builtin_fmaf(v[e], kLog2e, -c));
-                        if ((unsigned)tc < 8u) {
-#pragma unroll
-                            for (int e = 0; e < 8; e++)
-                                if (e == tc) pr[e] -= 1.0f;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; e++) d[e] = st16<BF>(pr[e] * scale);
-                        if (xi[3] || gcol + 8 > p.N) {
-#pragma unroll
-                            for (int e = 0; e < 8; e++)
-                                if (xi[3] || gcol + e >= p.N) d[e] = (_Float16)0.0f;
-                        }
-                        put8(d, rD, p.D, p.ldd, row);
+                        put8(d, rD, p.D, p.ldd, row0 + srow);
+                        put8(z, rZ, p.Z, p.ldz, row0 + srow);
                     }
                 }
-            }
-        };
-        if constexpr (EPI == LE_XP) {
-            slabs(std::true_type{});
-        } else {
-            if (vec)
+            };
+            if (p.vec)
                 slabs(std::true_type{});
             else
                 slabs(std::false_type{});
+            wave_lds_sync();  // this wave's reads are done before the next 64 rows overwrite its slab
         }
-        wave_lds_sync();  // this wave's reads are done before the next 64 rows overwrite its slabs
+        return;
+    }
+
+    char *slab = smem + wave * C::SLAB16;
+    // byte address of the 8 bytes (4 columns from col on) of a 16-bit slab row
+    auto at16 = [](int row, int col) {
+        const int f = WN == 128 ? row & 15 : (row >> 1) & 7;
+        return row * (WN * 2) + ((col >> 3) ^ f) * 16 + (col & 4) * 2;
+    };
+    auto put4 = [&](int i, int j, f32x4 v, uint32_t keep) {
+        half4 h;
+#pragma unroll
+        for (int r = 0; r < 4; r++) h[r] = st16<BF>(v[r]);
+        i32x2 w = __builtin_bit_cast(i32x2, h);
+        w[0] &= (int)keep;
+        w[1] &= (int)keep;
+        *(i32x2 *)(slab + at16(i * 16 + li, j * 16 + 4 * lg)) = w;
+    };
+
+    if constexpr (EPI == LE_OUT) {
+        const __amdgpu_buffer_rsrc_t rC =
+            res_of(p.C32 ? p.C32 + (int64_t)split * p.c_split : nullptr, p.ldc, 4);
+        const float alpha = p.alpha ? *p.alpha : 1.0f;
+        const int ccol = n0 + wn * WN + 4 * lg;  // (ldc is a multiple of 8: whole chunks exist)
+        auto coff = [&](int i, int j) {
+            return ccol + 16 * j < p.N ? ((wm * WM + i * 16 + li) * (int)p.ldc + ccol + 16 * j) * 4 : (int)kOut;
+        };
+        if (p.acc_out) {
+#pragma unroll
+            for (int i = 0; i < TM; i++) {
+                pin_row<TN>(acc[i]);
+                f32x4 c[TN] = {};
+                if (p.acc_in)
+#pragma unroll
+                    for (int j = 0; j < TN; j++) c[j] = buf_load<f32x4, 0>(rC, coff(i, j));
+#pragma unroll
+                for (int j = 0; j < TN; j++) buf_store<f32x4, 0>(acc[i][j] + c[j], rC, coff(i, j));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < TM; i++) {
+            pin_row<TN>(acc[i]);
+            f32x4 c[TN] = {};
+            if (p.acc_in)
+#pragma unroll
+                for (int j = 0; j < TN; j++) c[j] = buf_load<f32x4, 0>(rC, coff(i, j));
+#pragma unroll
+            for (int j = 0; j < TN; j++) put4(i, j, (acc[i][j] + c[j]) * alpha, ~0u);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else {  // LE_XP
+        i32x4 *xrow = (i32x4 *)(smem + C::SLABS);  // the tile's XentRow entries
+        if (tid < BM) xrow[tid] = tid < rows_here ? *(const i32x4 *)(p.rows + m0 + tid) : i32x4{0, 0, -1, 1};
+        barrier_lds();
+        const bool edge = n0 + BN > p.N;
+        const int col0 = n0 + wn * WN + 4 * lg;
+#pragma unroll
+        for (int i = 0; i < TM; i++) {
+            pin_row<TN>(acc[i]);
+            // p = 2^(logit log2 e - lse log2 e); the target's 1 is taken off in
+            // the few lanes that hold one.  An ignored row, and columns past
+            // the vocabulary, are zeros whatever was computed there.
+            const i32x4 xi = xrow[wm * WM + i * 16 + li];
+            const f32x4 xf = __builtin_bit_cast(f32x4, xi);
+            const float c = xf[0] * kLog2e, scale = xf[1];
+            const int t = xi[2] - p.v0 - col0;
+            const uint32_t keep = xi[3] ? 0u : ~0u;
+            f32x4 x[TN];
+#pragma unroll
+            for (int j = 0; j < TN; j++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) x[j][r] = exp2_hw(__builtin_fmaf(acc[i][j][r], kLog2e, -c));
+            if (t >= 0 && t < WN && (t & 12) == 0) {
+#pragma unroll
+                for (int j = 0; j < TN; j++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        if (t == 16 * j + r) x[j][r] -= 1.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < TN; j++) x[j] *= scale;
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < TN; j++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        if (col0 + j * 16 + r >= p.N) x[j][r] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < TN; j++) put4(i, j, x[j], keep);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // the 16-bit slab, row by row
+    wave_lds_sync();
+    const bool vec = EPI == LE_XP || p.vec;
+#pragma unroll 4
+    for (int q = 0; q < WM / RPP; q++) {
+        const int srow = q * RPP + srow0, row = wm * WM + srow;
+        const half8 v = *(const half8 *)(slab + at16(srow, scol));
+        // P is read again soon, so it is stored plainly
+        if (vec)
+            buf_store<half8, EPI == LE_XP ? 0 : 2>(v, rD, off_of(row, p.ldd));
+        else if (row < rows_here)
+            store8(p.D + (m0l + row) * p.ldd + gcol, v, ncol);
     }
 }
 

@@ -676,7 +676,10 @@ int run_xent(const ge_linear_xent_args *a, const XentPlan &pl)
 // by one product and read by two.  A piece as large as 128 MiB of P (half the
 // last-level cache) keeps those reads off HBM; more pieces cost a round trip of
 // dX's fp32 accumulator each, T K 8 bytes against 2 T K piece operations, so a
-// piece is not made shorter than 8192 columns.
+// piece is not made shorter than 8192 columns.  Within that it is a length that
+// fills whole rounds of tiles, with the rest in a shorter last piece: 4096 x
+// 100003 in 6 pieces of 16384 and one of 1699 takes 25 rounds for each of its
+// products, in 7 even ones (3.5 rounds each) 28.
 constexpr int64_t kPieceBytes = 128 << 20, kPieceMin = 8192;
 
 struct XentGradPlan {
@@ -709,9 +712,13 @@ int plan_xent_grad(const ge_linear_xent_backward_args *a, XentGradPlan &pl)
     if (a->T == 0) return GEMM_EPI_OK;
     Layout lay;
     pl.st = plan_staging2(a->X, a->ldx, a->T, a->W, a->ldw, a->V, a->K, lay);
-    int64_t piece = std::max(kPieceMin, kPieceBytes / (a->T * 2) / 256 * 256);
-    pl.pieces = (int)ceil_div(a->V, piece);
-    piece = round_up(ceil_div(a->V, pl.pieces), 256);  // even pieces
+    const int64_t limit = std::max(kPieceMin, kPieceBytes / (a->T * 2) / 256 * 256);
+    pl.pieces = (int)ceil_div(a->V, limit);
+    int64_t piece = round_up(ceil_div(a->V, pl.pieces), 256);  // even pieces
+    // columns that make whole rounds of 256 x 256 tiles over the chip
+    int64_t tiles_m = ceil_div(a->T, 256), step = 256 * kCUs;
+    for (; tiles_m % 2 == 0 && step > 256; tiles_m /= 2) step /= 2;
+    if (pl.pieces > 1 && step <= limit) piece = limit / step * step;
     pl.pieces = (int)ceil_div(a->V, piece);
     pl.piece = pl.pieces == 1 ? a->V : piece;
     pl.pld = round_up(pl.piece, 8);
