@@ -872,16 +872,17 @@ hipError_t run_norm(const ge_norm_residual_args *a)
     });
 }
 
-// Runs of rows that share a gate row, and workgroups.  About 512 workgroups
-// walk the rows (two per CU), each at least 4 rows, so that the partial column
-// sums stay small beside the rows themselves.
+// Runs of rows that share a gate row, and workgroups: as many as the compute
+// units hold at once (one of more than 512 threads, two of 512, more of the
+// small ones), so that the partial column sums, a row per workgroup, stay small
+// beside the rows themselves.  8192 rows: 4100 columns 149 us with 256, 167
+// with 1024; 4096 columns 127 with 256, 102 with 512; 1024 columns 40 with
+// 512, 36 with 1024.  At least 2 rows each, from 256 rows on.
 struct NormGradPlan {
     int64_t rows_per_gate = 0, rows_per_run = 0, runs = 0, runs_per_block = 1, blocks = 0;
     int runs_per_gate = 1;
     int64_t off_post = 0, off_pre = 0, off_gate = 0, bytes = 0;
 };
-constexpr int64_t kNormBlocks = 512, kNormMinRows = 4;
-
 int plan_norm_grad(const ge_norm_residual_backward_args *a, NormGradPlan &pl)
 {
     if (!a) return GEMM_EPI_ERR_NULL_INPUT;
@@ -900,7 +901,9 @@ int plan_norm_grad(const ge_norm_residual_backward_args *a, NormGradPlan &pl)
     GE_CHECK(check_matrix(a->dH, a->lddh, a->hidden, es, GEMM_EPI_ERR_NULL_OUTPUT));
     GE_CHECK(check_matrix(a->dY, a->lddy, a->hidden, 2, GEMM_EPI_ERR_NULL_OUTPUT));
     pl.rows_per_gate = a->T / a->G;
-    const int64_t blocks = std::min(kNormBlocks, ceil_div(a->T, kNormMinRows));
+    const int64_t threads = round_up(ceil_div(a->hidden, 8), 64);
+    const int64_t most = kCUs * (threads > 512 ? 1 : threads > 256 ? 2 : 4);
+    const int64_t blocks = a->T <= kCUs ? a->T : std::min(most, ceil_div(a->T, 2));
     pl.rows_per_run = std::min(pl.rows_per_gate, ceil_div(a->T, blocks));
     pl.runs_per_gate = (int)ceil_div(pl.rows_per_gate, pl.rows_per_run);
     pl.runs = a->G * pl.runs_per_gate;
@@ -958,17 +961,15 @@ int run_norm_grad(const ge_norm_residual_backward_args *a, const NormGradPlan &p
     p.p_post = post ? (float *)(ws + pl.off_post) : nullptr;
     p.p_pre = a->dw_pre ? (float *)(ws + pl.off_pre) : nullptr;
     p.dgate = !a->dgate || p.gate_direct ? a->dgate : (float *)(ws + pl.off_gate);
-    // 8 elements per thread, in whole waves; two workgroups of up to 640 fit on
-    // a compute unit (rows of single elements take more registers: not there)
+    // 8 elements per thread, in whole waves
     const dim3 g((unsigned)pl.blocks), b((unsigned)round_up(ceil_div(H, 8), 64));
-    const bool quads = H % 4 == 0;
+    const bool tail = H % 4 != 0;
     if (H <= 4096)
-        GE_TRY(launch(quads ? norm_residual_grad_kernel<BF, S32, 512, 4> : norm_residual_grad_kernel<BF, S32, 512, 1>,
+        GE_TRY(launch(tail ? norm_residual_grad_kernel<BF, S32, 512, true> : norm_residual_grad_kernel<BF, S32, 512, false>,
                       g, b, s, p));
-    else if (H <= 5120 && quads)
-        GE_TRY(launch(norm_residual_grad_kernel<BF, S32, 640, 4>, g, b, s, p));
     else
-        GE_TRY(launch(quads ? norm_residual_grad_kernel<BF, S32, 1024, 4> : norm_residual_grad_kernel<BF, S32, 1024, 1>,
+        GE_TRY(launch(tail ? norm_residual_grad_kernel<BF, S32, 1024, true>
+                           : norm_residual_grad_kernel<BF, S32, 1024, false>,
                       g, b, s, p));
     ColSumParams c = {};
     c.partial[0] = p.p_post;

@@ -73,13 +73,15 @@ __device__ __forceinline__ float dpp_rows(float x)
 // thread gets them.  The two LDS buffers alternate from call to call: a thread
 // writes a buffer again only past the other one's barrier, which every thread
 // reaches after its reads of the first.
-template <int N>
+template <int MAXN>
 struct BlockSum {
-    float (*lds)[16][N];
+    float (*lds)[16][MAXN];
     int waves;
     int phase = 0;
+    template <int N>
     __device__ __forceinline__ void operator()(float (&v)[N])
     {
+        static_assert(N <= MAXN, "LDS space");
 #pragma unroll
         for (int i = 0; i < N; i++) {
             // rows of 16 lanes, then row 0 onto 1 and 2 onto 3, then the lower
@@ -228,63 +230,54 @@ struct NormGradParams {
     float *dgate;            // [G][hidden], or [runs][hidden] partial sums, or NULL
 };
 
-// The 8 elements of one row that a thread of the gradient holds, in units of
-// VW consecutive ones: unit u starts at column (u threads + tid) VW.  VW
-// divides the row length (4 or 1), so a unit exists whole or not at all and one
-// comparison guards it; absent units read as zeros.  (Units of 8 took 25 more
-// registers: past the 128 that let two workgroups share a compute unit.)
-template <int VW, typename T>
-struct UnitVec;
-template <typename T>
-struct UnitVec<1, T> {
-    typedef T type;
-};
-template <typename T>
-struct UnitVec<4, T> {
-    typedef T type __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-};
-template <bool BF, typename T, int VW>
+// The 8 elements of one row that a thread of the gradient holds, as two units
+// of 4 consecutive ones: unit u starts at column (u threads + tid) 4.  Without
+// TAIL the row length is a multiple of 4, so a unit exists whole or not at all;
+// with it the row's last unit may be short.  Absent elements read as zeros.
+// (Units of 8 took 25 more registers: past the 128 that let two workgroups
+// share a compute unit.)
+template <bool BF, typename T, bool TAIL>
 struct RowPart {
-    static constexpr int NU = 8 / VW;
-    using V = typename UnitVec<VW, T>::type;
-    V v[NU];
+    typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+    V v[2];
     // (a scalar row address plus a 32-bit offset: one register per unit)
     __device__ __forceinline__ void load(const T *row, int cols, int tid)
     {
-        if constexpr (VW < 8) asm volatile("" : "+v"(tid));
+        asm volatile("" : "+v"(tid));  // the masks are made again every time: kept, they take too many scalar registers
 #pragma unroll
-        for (int u = 0; u < NU; u++) {
-            const int c = (u * (int)blockDim.x + tid) * VW;
+        for (int u = 0; u < 2; u++) {
+            const int c = (u * (int)blockDim.x + tid) * 4;
+            const char *at = (const char *)row + (uint32_t)c * (uint32_t)sizeof(T);
             v[u] = V{};
-            if (c < cols) v[u] = *(const V *)((const char *)row + (uint32_t)c * (uint32_t)sizeof(T));
+            if (TAIL ? c + 4 <= cols : c < cols) {
+                v[u] = *(const V *)at;
+            } else if (TAIL && c < cols) {
+#pragma unroll
+                for (int e = 0; e < 3; e++)
+                    if (c + e < cols) v[u][e] = ((const T *)at)[e];
+            }
         }
     }
     __device__ __forceinline__ void store(T *row, int cols, int tid) const
     {
-        if constexpr (VW < 8) asm volatile("" : "+v"(tid));
+        asm volatile("" : "+v"(tid));
 #pragma unroll
-        for (int u = 0; u < NU; u++) {
-            const int c = (u * (int)blockDim.x + tid) * VW;
-            if (c < cols) *(V *)((char *)row + (uint32_t)c * (uint32_t)sizeof(T)) = v[u];
+        for (int u = 0; u < 2; u++) {
+            const int c = (u * (int)blockDim.x + tid) * 4;
+            char *at = (char *)row + (uint32_t)c * (uint32_t)sizeof(T);
+            if (TAIL ? c + 4 <= cols : c < cols) {
+                *(V *)at = v[u];
+            } else if (TAIL && c < cols) {
+#pragma unroll
+                for (int e = 0; e < 3; e++)
+                    if (c + e < cols) ((T *)at)[e] = v[u][e];
+            }
         }
     }
-    __device__ __forceinline__ void fill(T x)
-    {
-#pragma unroll
-        for (int u = 0; u < NU; u++)
-            if constexpr (VW == 1)
-                v[u] = x;
-            else
-#pragma unroll
-                for (int e = 0; e < VW; e++) v[u][e] = x;
-    }
+    __device__ __forceinline__ void fill(T x) { v[0] = v[1] = V{x, x, x, x}; }
     __device__ __forceinline__ float get(int i) const
     {
-        T x;
-        if constexpr (VW == 1)
-            x = v[i];
-        else
-            x = v[i / VW][i % VW];
+        const T x = v[i / 4][i % 4];
         if constexpr (sizeof(T) == 2)
             return ld16<BF>(x);
         else
@@ -292,35 +285,33 @@ struct RowPart {
     }
     __device__ __forceinline__ void set(int i, float f)
     {
-        T x;
         if constexpr (sizeof(T) == 2)
-            x = st16<BF>(f);
+            v[i / 4][i % 4] = st16<BF>(f);
         else
-            x = f;
-        if constexpr (VW == 1)
-            v[i] = x;
-        else
-            v[i / VW][i % VW] = x;
+            v[i / 4][i % 4] = f;
     }
 };
 
-template <bool BF, bool S32, int MAXT, int VW>
-__global__ __launch_bounds__(MAXT, MAXT == 640 ? 5 : 4) void norm_residual_grad_kernel(NormGradParams p)
+template <bool BF, bool S32, int MAXT, bool TAIL>
+__global__ __launch_bounds__(MAXT, 4) void norm_residual_grad_kernel(NormGradParams p)
 {
     constexpr int NE = 8;
-    // Past 4096 columns the registers (128 a lane in a workgroup of 1024, 96
-    // where two of 640 share a compute unit) hold a row's operands and little
-    // else: the sums of the two weights' gradients and the weights themselves
-    // live in LDS, where each thread only touches its own elements.
+    // Past 4096 columns the registers (128 a lane in a workgroup of 1024) hold a
+    // row's operands, the next row's and little else: the sums of the two
+    // weights' gradients and the weights themselves live in LDS, where each
+    // thread only touches its own elements.
     constexpr bool LDS_ACC = MAXT > 512;
+    // Alone on its compute unit a workgroup loads the next row while it reduces
+    // this one (short last units leave no scalar registers for it).
+    constexpr bool PREFETCH = MAXT > 512 && !TAIL;
     using T = typename std::conditional<S32, float, _Float16>::type;
-    using Half = RowPart<BF, _Float16, VW>;
-    using Stream = RowPart<BF, T, VW>;
-    __shared__ float lds[2][16][3];
+    using Half = RowPart<BF, _Float16, TAIL>;
+    using Stream = RowPart<BF, T, TAIL>;
+    __shared__ float lds[2][16][6];
     using HV = typename Half::V;
-    __shared__ HV w_lds[LDS_ACC ? 3 : 1][LDS_ACC ? 8 / VW : 1][LDS_ACC ? MAXT : 1];
+    __shared__ HV w_lds[LDS_ACC ? 3 : 1][LDS_ACC ? 2 : 1][LDS_ACC ? MAXT : 1];
     __shared__ f32x4 acc_lds[LDS_ACC ? 2 : 1][LDS_ACC ? NE / 4 : 1][LDS_ACC ? MAXT : 1];
-    BlockSum<3> sum{lds, (int)blockDim.x >> 6};
+    BlockSum<6> sum{lds, (int)blockDim.x >> 6};
     const int H = p.hidden, tid = threadIdx.x;
     // (in vector registers: the scalar ones are short by a few)
     float inv_h = 1.0f / (float)H, scale = p.scale, eps = p.eps;
@@ -337,18 +328,16 @@ __global__ __launch_bounds__(MAXT, MAXT == 640 ? 5 : 4) void norm_residual_grad_
         return r;
     };
     // does element i of this thread exist?
-    // (narrow units: masks kept from row to row take more scalar
-    // registers than there are, so the comparison is made again every time)
     auto in_row = [&](int i) {
         int t = tid;
-        if constexpr (VW == 1) asm volatile("" : "+v"(t));
-        return (i / VW * (int)blockDim.x + t) * VW < H;
+        asm volatile("" : "+v"(t));
+        return (i / 4 * (int)blockDim.x + t) * 4 + (TAIL ? i % 4 : 0) < H;
     };
     Half kept[3];  // w_post, w_pre, gate
     auto keep = [&](int k, const Half &r) {
         if constexpr (LDS_ACC) {
 #pragma unroll
-            for (int u = 0; u < 8 / VW; u++) w_lds[k][u][tid] = r.v[u];
+            for (int u = 0; u < 2; u++) w_lds[k][u][tid] = r.v[u];
         } else {
             kept[k] = r;
         }
@@ -357,7 +346,7 @@ __global__ __launch_bounds__(MAXT, MAXT == 640 ? 5 : 4) void norm_residual_grad_
         if constexpr (LDS_ACC) {
             Half r;
 #pragma unroll
-            for (int u = 0; u < 8 / VW; u++) r.v[u] = w_lds[k][u][tid];
+            for (int u = 0; u < 2; u++) r.v[u] = w_lds[k][u][tid];
             return r;
         } else {
             return kept[k];
@@ -384,45 +373,66 @@ __global__ __launch_bounds__(MAXT, MAXT == 640 ? 5 : 4) void norm_residual_grad_
         keep(2, row_of(p.gate ? p.gate + (int64_t)gr * H : nullptr));
 #pragma unroll
         for (int i = 0; i < NE; i++) a_gate[i] = 0.0f;
+        Half dx, y;
+        Stream dho, h;
+        auto fetch = [&](int64_t row, Half &dx_, Stream &h_, Half &y_, Stream &dho_) {
+            dx_.load(p.dX + row * p.lddx, H, tid);
+            h_.load((const T *)p.H_out + row * p.ldho, H, tid);
+            y_.load(p.Y + row * p.ldy, H, tid);
+            dho_.load((const T *)p.dH_out + row * p.lddho, H, tid);
+        };
+        Half dx_next, y_next;
+        Stream dho_next, h_next;
+        if constexpr (PREFETCH) fetch(r0, dx_next, h_next, y_next, dho_next);
         for (int64_t row = r0; row < r1; row++) {
-            Half dx, y;
-            Stream dho, h;
-            dx.load(p.dX + row * p.lddx, H, tid);
-            h.load((const T *)p.H_out + row * p.ldho, H, tid);
-            y.load(p.Y + row * p.ldy, H, tid);
-            dho.load((const T *)p.dH_out + row * p.lddho, H, tid);
+            if constexpr (PREFETCH) {
+                dx = dx_next;
+                h = h_next;
+                y = y_next;
+                dho = dho_next;
+                if (row + 1 < r1) fetch(row + 1, dx_next, h_next, y_next, dho_next);
+            } else {
+                fetch(row, dx, h, y, dho);
+            }
             float dn[NE];  // dX w_pre, then scale gate dH
             {
                 const Half w = weight(1);
 #pragma unroll
                 for (int i = 0; i < NE; i++) dn[i] = dx.get(i) * w.get(i);
             }
-            float mu_h = 0.0f, mu_y = 0.0f, m_dn = 0.0f;
-            float s[3];
-            if (pre_mean || post_mean) {
+            // One pass gives the sums and the sums of squares.  Where a mean is
+            // subtracted and is not small beside the deviation (mean^2 > 16
+            // variance: the difference of the sums would lose more than 4 bits),
+            // a second one takes them about the mean.  (Absent elements are
+            // zeros: they only have to be kept out of that second pass.)
+            float q[6] = {};
+#pragma unroll
+            for (int i = 0; i < NE; i++) {
+                const float hv = h.get(i), yv = y.get(i);
+                q[0] = __builtin_fmaf(hv, hv, q[0]);
+                q[1] = __builtin_fmaf(yv, yv, q[1]);
+                q[2] = __builtin_fmaf(dn[i], hv, q[2]);
+                q[3] += hv;
+                q[4] += yv;
+                q[5] += dn[i];
+            }
+            sum(q);
+            const float mu_h = pre_mean ? q[3] * inv_h : 0.0f, mu_y = post_mean ? q[4] * inv_h : 0.0f;
+            const float m_dn = pre_mean ? q[5] * inv_h : 0.0f;
+            float s[3] = {__builtin_fmaf(-mu_h, q[3], q[0]), __builtin_fmaf(-mu_y, q[4], q[1]),
+                          __builtin_fmaf(-mu_h, q[5], q[2])};
+            // (written so that a NaN, and a variance rounded below zero, take the second pass)
+            if (!(mu_h * mu_h <= 16.0f * s[0] * inv_h && mu_y * mu_y <= 16.0f * s[1] * inv_h)) {
                 s[0] = s[1] = s[2] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NE; i++) {
-                    s[0] += h.get(i);
-                    s[1] += y.get(i);
-                    s[2] += dn[i];
+                    const float hc = in_row(i) ? h.get(i) - mu_h : 0.0f, yc = in_row(i) ? y.get(i) - mu_y : 0.0f;
+                    s[0] = __builtin_fmaf(hc, hc, s[0]);
+                    s[1] = __builtin_fmaf(yc, yc, s[1]);
+                    s[2] = __builtin_fmaf(dn[i], hc, s[2]);
                 }
                 sum(s);
-                mu_h = pre_mean ? s[0] * inv_h : 0.0f;
-                m_dn = pre_mean ? s[2] * inv_h : 0.0f;
-                mu_y = post_mean ? s[1] * inv_h : 0.0f;
             }
-            // (absent elements are zeros: they only have to be kept out of the
-            // sums about a mean)
-            s[0] = s[1] = s[2] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NE; i++) {
-                const float hc = in_row(i) ? h.get(i) - mu_h : 0.0f, yc = in_row(i) ? y.get(i) - mu_y : 0.0f;
-                s[0] = __builtin_fmaf(hc, hc, s[0]);
-                s[1] = __builtin_fmaf(yc, yc, s[1]);
-                s[2] = __builtin_fmaf(dn[i], hc, s[2]);
-            }
-            sum(s);
             const float r_h = 1.0f / sqrtf(s[0] * inv_h + eps);
             const float r_y = post_norm ? 1.0f / sqrtf(s[1] * inv_h + eps) : 1.0f;
             const float c_h = s[2] * inv_h * r_h;  // mean(dn n)
@@ -481,13 +491,13 @@ __global__ __launch_bounds__(MAXT, MAXT == 640 ? 5 : 4) void norm_residual_grad_
             float *dst = p.dgate + (int64_t)(p.gate_direct ? gr : run) * H;
 #pragma unroll
             for (int i = 0; i < NE; i++)
-                if (in_row(i)) dst[(i / VW * (int)blockDim.x + tid) * VW + i % VW] = a_gate[i];
+                if (in_row(i)) dst[(i / 4 * (int)blockDim.x + tid) * 4 + i % 4] = a_gate[i];
         }
     }
 #pragma unroll
     for (int i = 0; i < NE; i++) {
         if (!in_row(i)) continue;
-        const int64_t at = (int64_t)blockIdx.x * H + (i / VW * (int)blockDim.x + tid) * VW + i % VW;
+        const int64_t at = (int64_t)blockIdx.x * H + (i / 4 * (int)blockDim.x + tid) * 4 + i % 4;
         if (p.p_post) p.p_post[at] = LDS_ACC ? acc_lds[0][LDS_ACC ? i / 4 : 0][LDS_ACC ? tid : 0][i % 4] : a_post[LDS_ACC ? 0 : i];
         if (p.p_pre) p.p_pre[at] = LDS_ACC ? acc_lds[LDS_ACC ? 1 : 0][LDS_ACC ? i / 4 : 0][LDS_ACC ? tid : 0][i % 4] : a_pre[LDS_ACC ? 0 : i];
     }
