@@ -22,6 +22,7 @@ import os
 import re
 import shutil
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -80,10 +81,16 @@ def build(verbose: bool = False) -> str:
         cmd = [hipcc(), *flags, "-c", "-o", obj, src]
         if verbose:
             print(" ".join(cmd), flush=True)
-        procs.append((cmd, subprocess.Popen(cmd, stderr=subprocess.PIPE, text=True)))
+        # diagnostics go to a file: the resource remarks of many kernels fill a pipe, and a
+        # compiler that waits for it to be read waits for every process before it in the list
+        err_file = tempfile.TemporaryFile("w+")
+        procs.append((cmd, subprocess.Popen(cmd, stderr=err_file, text=True), err_file))
     failed, resources = [], []
-    for cmd, proc in procs:
-        _, err = proc.communicate()
+    for cmd, proc, err_file in procs:
+        proc.wait()
+        err_file.seek(0)
+        err = err_file.read()
+        err_file.close()
         resources += parse_resources(err)
         if proc.returncode != 0:
             # the compiler's diagnostics, without the resource remarks and their source context

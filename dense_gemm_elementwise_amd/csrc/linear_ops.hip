@@ -200,29 +200,36 @@ struct StagePlan2 {
     int64_t off[2] = {0, 0};
     int64_t ldo = 0;
 };
-// stages up to two operands with `cols` columns
-hipError_t run_staging(const StagePlan2 &st, char *ws, int64_t cols, Operand16 &a, int64_t a_rows, Operand16 &b,
-                       int64_t b_rows, hipStream_t s)
-{
+// The copies of a staging plan (`cols` columns); the operands then are the copies.
+struct StageSet {
     PadParams q = {};
     int n = 0;
+    unsigned blocks = 0;
+};
+StageSet stage_set(const StagePlan2 &st, char *ws, int64_t cols, Operand16 &a, int64_t a_rows, Operand16 &b,
+                   int64_t b_rows)
+{
+    StageSet r;
     Operand16 *op[2] = {&a, &b};
     const int64_t rows[2] = {a_rows, b_rows};
     for (int i = 0; i < 2; i++) {
         if (!st.on[i]) continue;
-        q.src[n] = op[i]->p;
-        q.lds[n] = op[i]->ld;
-        q.rows[n] = rows[i];
-        q.dst[n] = (_Float16 *)(ws + st.off[i]);
-        op[i]->p = q.dst[n];
+        r.q.src[r.n] = op[i]->p;
+        r.q.lds[r.n] = op[i]->ld;
+        r.q.rows[r.n] = rows[i];
+        r.q.dst[r.n] = (_Float16 *)(ws + st.off[i]);
+        op[i]->p = r.q.dst[r.n];
         op[i]->ld = st.ldo;
-        n++;
+        r.n++;
     }
-    if (n == 0) return hipSuccess;
-    q.cols = (int)cols;
-    q.ldo = (int)st.ldo;
-    const int64_t blocks = std::min<int64_t>(ceil_div(std::max(q.rows[0], q.rows[1]) * (st.ldo / 8), 256), 4096);
-    return launch(pad_rows_kernel, dim3((unsigned)blocks, n), dim3(256), s, q);
+    r.q.cols = (int)cols;
+    r.q.ldo = (int)st.ldo;
+    r.blocks = (unsigned)std::min<int64_t>(ceil_div(std::max(r.q.rows[0], r.q.rows[1]) * (st.ldo / 8), 256), 4096);
+    return r;
+}
+hipError_t run_staging(const StageSet &st, hipStream_t s)
+{
+    return st.n ? launch(pad_rows_kernel, dim3(st.blocks, st.n), dim3(256), s, st.q) : hipSuccess;
 }
 StagePlan2 plan_staging2(const void *a, int64_t lda, int64_t a_rows, const void *b, int64_t ldb, int64_t b_rows,
                          int64_t cols, Layout &lay)
@@ -394,7 +401,7 @@ int run_linear(const ge_linear_args *a, const LinearPlan &pl)
         }
     }
     Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
-    GE_TRY(run_staging(pl.st, ws, a->K, x, a->M, w, a->N, s));
+    GE_TRY(run_staging(stage_set(pl.st, ws, a->K, x, a->M, w, a->N), s));
     LinParams p = {};
     set_product(p, pl.pl, a->M, a->N, round_up(a->K, 8));
     p.A = x.p;
@@ -478,11 +485,13 @@ int plan_linear_grad(const ge_linear_backward_args *a, LinearGradPlan &pl)
     Layout lay;
     pl.direct = a->act == GE_ACT_IDENTITY && dma_rows(a->dD, a->lddd, a->N);
     if (!pl.direct) pl.off_dz = lay.take(a->M * pl.N8 * 2);
-    // strips of rows: about 2048 blocks of 256 columns, at least 32 rows each
+    // strips of rows: about 2048 blocks of 256 columns, at least 32 rows each;
+    // one strip, whose sums are dbias itself, up to 128 rows
     const int64_t cols = ceil_div(a->N, 256);
     pl.rows_per_strip = (int)round_up(std::max<int64_t>(32, ceil_div(a->M, std::max<int64_t>(1, 2048 / cols))), 8);
+    if (a->M <= 128) pl.rows_per_strip = 128;
     pl.strips = (int)ceil_div(a->M, pl.rows_per_strip);
-    if (a->dbias) pl.off_bias = lay.take((int64_t)pl.strips * pl.N8 * 4);
+    if (a->dbias && pl.strips > 1) pl.off_bias = lay.take((int64_t)pl.strips * a->N * 4);
     // an unwanted product's operand is not staged (the other operand stands in)
     const void *x = a->dW ? a->X : a->W, *w = a->dX ? a->W : a->X;
     const int64_t ldx = a->dW ? a->ldx : a->ldw, ldw = a->dX ? a->ldw : a->ldx;
@@ -529,7 +538,11 @@ int run_linear_grad(const ge_linear_backward_args *a, const LinearGradPlan &pl)
         return GEMM_EPI_OK;
     }
     Operand16 dz = {(const _Float16 *)a->dD, a->lddd};
-    if (!pl.direct || a->dbias) {
+    Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
+    const StageSet stage = stage_set(pl.st, ws, a->K, x, a->M, w, a->N);
+    if (pl.direct && !a->dbias) {
+        GE_TRY(run_staging(stage, s));
+    } else {
         DzParams q = {};
         q.dD = (const _Float16 *)a->dD;
         q.Z = (const _Float16 *)a->Z;
@@ -537,25 +550,26 @@ int run_linear_grad(const ge_linear_backward_args *a, const LinearGradPlan &pl)
         q.ldz = a->ldz;
         q.ldo = pl.N8;
         q.out = pl.direct ? nullptr : (_Float16 *)(ws + pl.off_dz);
-        q.partial = a->dbias ? (float *)(ws + pl.off_bias) : nullptr;
+        q.partial = pl.strips == 1 ? a->dbias : a->dbias ? (float *)(ws + pl.off_bias) : nullptr;
         q.M = (int)a->M;
         q.N = (int)a->N;
         q.N8 = (int)pl.N8;
         q.rows_per_strip = pl.rows_per_strip;
-        GE_TRY(launch_dz<BF>((int)a->act, q, dim3((unsigned)ceil_div(a->N, 256), pl.strips), s));
+        q.cols_blocks = (int)ceil_div(a->N, 256);
+        q.dz_blocks = q.cols_blocks * pl.strips;
+        q.pad = stage.q;
+        q.pads = stage.n;
+        GE_TRY(launch_dz<BF>((int)a->act, q, dim3((unsigned)q.dz_blocks + (stage.n ? stage.blocks : 0u)), s));
         if (!pl.direct) dz = {q.out, pl.N8};
-        if (a->dbias) {
+        if (a->dbias && pl.strips > 1) {
             ColSumParams c = {};
             c.partial[0] = q.partial;
             c.out[0] = a->dbias;
             c.parts[0] = pl.strips;
-            c.ld = (int)pl.N8;
-            c.cols = (int)a->N;
+            c.ld = c.cols = (int)a->N;
             GE_TRY(launch(colsum_kernel, dim3((unsigned)ceil_div(a->N, 64)), dim3(1024), s, c));
         }
     }
-    Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
-    GE_TRY(run_staging(pl.st, ws, a->K, x, a->M, w, a->N, s));
     float *part = (float *)(ws + pl.off_part);
     if (a->dX) {
         LinParams p = {};
@@ -652,7 +666,7 @@ int run_xent(const ge_linear_xent_args *a, const XentPlan &pl)
         GE_TRY((launch_few_rows<BF, true, ACT_IDENTITY>(q, s)));
     } else {
         Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
-        GE_TRY(run_staging(pl.st, ws, a->K, x, a->T, w, a->V, s));
+        GE_TRY(run_staging(stage_set(pl.st, ws, a->K, x, a->T, w, a->V), s));
         LinParams p = {};
         set_product(p, pl.pl, a->T, a->V, round_up(a->K, 8));
         p.A = x.p;
@@ -755,7 +769,7 @@ int run_xent_grad(const ge_linear_xent_backward_args *a, const XentGradPlan &pl)
     GE_TRY(launch(xent_rows_kernel, dim3(1), dim3(1024), s, (int)a->T, a->V, a->ignore_index, a->dloss, a->lse,
                   a->target, rows, alpha));
     Operand16 x = {(const _Float16 *)a->X, a->ldx}, w = {(const _Float16 *)a->W, a->ldw};
-    GE_TRY(run_staging(pl.st, ws, a->K, x, a->T, w, a->V, s));
+    GE_TRY(run_staging(stage_set(pl.st, ws, a->K, x, a->T, w, a->V), s));
     _Float16 *P = (_Float16 *)(ws + pl.off_p);
     float *acc = pl.pieces > 1 ? (float *)(ws + pl.off_acc) : nullptr;
     float *part = (float *)(ws + pl.off_part);

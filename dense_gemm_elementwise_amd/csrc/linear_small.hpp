@@ -222,28 +222,65 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
 }
 
 // ---------------------------------------------------------------------------
+// Staging: operands whose rows are not 16-byte aligned, or not a multiple of
+// 8 elements long, are copied to rows of ldo elements (a multiple of 8), zeros
+// past the row's end.  One grid row per tensor.
+// ---------------------------------------------------------------------------
+struct PadParams {
+    const _Float16 *src[2];
+    _Float16 *dst[2];
+    int64_t lds[2], rows[2];
+    int cols, ldo;
+};
+// tensor v's part of block `block` of `blocks`
+__device__ __forceinline__ void pad_rows(const PadParams &p, int v, int block, int blocks)
+{
+    const int groups = p.ldo / 8;
+    const int64_t total = p.rows[v] * groups;
+    for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < total; i += (int64_t)blocks * 256) {
+        const int64_t r = i / groups;
+        const int c = (int)(i - r * groups) * 8;
+        *(half8 *)(p.dst[v] + r * p.ldo + c) = load8(p.src[v] + r * p.lds[v] + c, p.cols - c);
+    }
+}
+__global__ __launch_bounds__(256) void pad_rows_kernel(PadParams p)
+{
+    pad_rows(p, blockIdx.y, blockIdx.x, gridDim.x);
+}
+
+// ---------------------------------------------------------------------------
 // dZ = dD act'(Z), rounded once to the element type (it is an MFMA operand),
 // in rows of ldo elements zero-padded to a multiple of 8 columns, and the
 // column sums of the unrounded dZ over each strip of rows.  A block covers 256
 // columns x a strip: 32 lanes of 8 columns by 8 rows at a time; one pass over
-// dD and Z, bound by their bytes.
+// dD and Z, bound by their bytes (8192 x 8192: 72 us, 5.6 TB/s).  The blocks past
+// dz_blocks stage the products' other operands in the same launch.
 // ---------------------------------------------------------------------------
 struct DzParams {
     const _Float16 *dD, *Z;
     int64_t ldd, ldz, ldo;
     _Float16 *out;  // NULL: only the sums (identity, dD usable as it is)
-    float *partial;  // [strips][N8], or NULL
+    float *partial;  // [strips][N], or NULL
     int M, N, N8, rows_per_strip;
+    int cols_blocks, dz_blocks;  // blocks of 256 columns; all blocks of dZ
+    PadParams pad;
+    int pads;  // tensors to stage
 };
 
 template <bool BF, int ACT>
 __global__ __launch_bounds__(256) void dz_kernel(DzParams p)
 {
     __shared__ float red[8][256 + 8];
+    if ((int)blockIdx.x >= p.dz_blocks) {
+        for (int v = 0; v < p.pads; v++)
+            pad_rows(p.pad, v, (int)blockIdx.x - p.dz_blocks, (int)gridDim.x - p.dz_blocks);
+        return;
+    }
+    const int strip = (int)blockIdx.x / p.cols_blocks, cb = (int)blockIdx.x - strip * p.cols_blocks;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int c = blockIdx.x * 256 + tx * 8;
+    const int c = cb * 256 + tx * 8;
     const int n = p.N - c;  // columns that exist from c on
-    const int r0 = blockIdx.y * p.rows_per_strip, r1 = min(p.M, r0 + p.rows_per_strip);
+    const int r0 = strip * p.rows_per_strip, r1 = min(p.M, r0 + p.rows_per_strip);
     float sum[8] = {};
     if (c < p.N8) {
         auto one = [&](int m, half8 d, half8 z) {
@@ -280,11 +317,11 @@ __global__ __launch_bounds__(256) void dz_kernel(DzParams p)
 #pragma unroll
     for (int e = 0; e < 8; e++) red[ty][tx * 8 + e] = sum[e];
     __syncthreads();
-    const int col = blockIdx.x * 256 + threadIdx.x;
+    const int col = cb * 256 + threadIdx.x;
     float s = 0.0f;
 #pragma unroll
     for (int y = 0; y < 8; y++) s += red[y][threadIdx.x];
-    if (col < p.N8) p.partial[(int64_t)blockIdx.y * p.N8 + col] = s;
+    if (col < p.N) p.partial[(int64_t)strip * p.N + col] = s;
 }
 
 // The last step of every column sum: out[c] = sum over parts, in a fixed order,
@@ -389,28 +426,6 @@ __global__ __launch_bounds__(256) void split_sum_kernel(SplitSumParams p)
             for (int e = 0; e < 8; e++) d[e] = st16<BF>(v[e] * alpha);
             store8(p.D + (int64_t)m * p.ldd + c, d, n);
         }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// Staging: operands whose rows are not 16-byte aligned, or not a multiple of
-// 8 elements long, are copied to rows of ldo elements (a multiple of 8), zeros
-// past the row's end.  One grid row per tensor.
-// ---------------------------------------------------------------------------
-struct PadParams {
-    const _Float16 *src[2];
-    _Float16 *dst[2];
-    int64_t lds[2], rows[2];
-    int cols, ldo;
-};
-__global__ __launch_bounds__(256) void pad_rows_kernel(PadParams p)
-{
-    const int v = blockIdx.y, groups = p.ldo / 8;
-    const int64_t total = p.rows[v] * groups;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / groups;
-        const int c = (int)(i - r * groups) * 8;
-        *(half8 *)(p.dst[v] + r * p.ldo + c) = load8(p.src[v] + r * p.lds[v] + c, p.cols - c);
     }
 }
 

@@ -338,7 +338,8 @@ def norm_residual(h, y, *, w_post=None, w_pre=None, gate=None, scale=1.0, post="
     yp = _matrix("y", y, (T, H), dtype, dev)
 
     def call(raw):
-        ho, x = h.new_empty((T, H)), y.new_empty((T, H))
+        ho = torch.empty_like(h) if hp[1] == H else h.new_empty((T, H))
+        x = torch.empty_like(y) if yp[1] == H else y.new_empty((T, H))
         _queue("ge_norm_residual", _NORM.pack(T, H, G, *hp, *yp, *mid, scale, eps, ho.data_ptr(), H, x.data_ptr(), H,
                                               _DTYPES[dtype], _STREAM_DTYPES[sd]), dev, raw)
         return ho, x
