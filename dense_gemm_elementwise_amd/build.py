@@ -33,7 +33,8 @@ SRCS = [os.path.join(PKG, "csrc", f) for f in ("gemm_epi.hip", "gemm_epi_bf16.hi
                                                "linear_fwd_f16.hip", "linear_fwd_bf16.hip",
                                                "linear_xent_f16.hip", "linear_xent_bf16.hip",
                                                "linear_nn_f16.hip", "linear_nn_bf16.hip",
-                                               "linear_tn_f16.hip", "linear_tn_bf16.hip")]
+                                               "linear_tn_f16.hip", "linear_tn_bf16.hip",
+                                               "linear_pair_f16.hip", "linear_pair_bf16.hip")]
 LIB = os.path.join(PKG, "libgemm_epi.so")
 RESOURCES = os.path.join(PKG, "libgemm_epi.resources.json")
 ARCH = "gfx950"

@@ -81,8 +81,8 @@ struct LinParams {
 
 // Activations of the linear operator.  An epilogue's arithmetic runs while the
 // matrix units wait, so these are cheaper forms than those of the epilogue
-// kinds (act_gelu, act_silu): at 8192 x 8192 x 2048 they took the gelu call
-// from 301 us to what the comment at lin_epilogue says.  Relative error 3e-6
+// kinds (act_gelu, act_silu): at 8192 x 8192 x 2048 gelu went from 301 to 237
+// us and silu from 267 to 223, where the product alone takes 210.  Relative error 3e-6
 // (gelu) and a few fp32 units (silu), down into the subnormals.
 //
 // The upper tail Q(|x|) = erfc(|x| / sqrt 2) / 2 of the normal distribution is
@@ -295,7 +295,11 @@ struct LinOperand {
 
 template <int BM, int BN, bool AKM, bool BKM>
 struct LinCfg {
-    static constexpr int NH = (AKM || BKM) ? 6 : 5;
+    // (128 x 256 and 256 x 128 have room for six halves beside each other too,
+    // and gain nothing from them: 2400 x 3232 x 4096 58.5 us with either)
+    static constexpr bool BOTH_KC = !AKM && !BKM;
+    static constexpr int NH = BOTH_KC ? 5 : 6;
+    static constexpr int PERIOD = BOTH_KC ? 10 : (AKM && BKM ? 4 : 12);
     using OA = LinOperand<BM, AKM, NH>;
     using OB = LinOperand<BN, BKM, NH>;
     static constexpr int MAIN = OA::BYTES + OB::BYTES;
@@ -317,8 +321,10 @@ __device__ __forceinline__ void mainloop_lin(f32x4 (&acc)[BM / 32][BN / 32], con
     using OB = typename C::OB;
     constexpr int TM = BM / 32, TN = BN / 32;
     constexpr int NMF = TM * TN, NDA = OA::ND, ND = OA::ND + OB::ND, NRA = OA::NR, NR = OA::NR + OB::NR;
-    constexpr bool BOTH_KC = !AKM && !BKM;
-    constexpr int PERIOD = BOTH_KC ? 10 : (AKM && BKM ? 4 : 12);
+    constexpr bool BOTH_KC = C::BOTH_KC;
+    constexpr int PERIOD = C::PERIOD;
+    // steps newer than the ones whose fills must have landed (see step below)
+    constexpr int NEWER = BOTH_KC ? C::NH - 4 : 2;
     static_assert(NMF >= 3 * ND && NMF >= NR, "the gap schedule needs room");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int nk = (k_end - kb + 31) >> 5;
@@ -385,9 +391,8 @@ __device__ __forceinline__ void mainloop_lin(f32x4 (&acc)[BM / 32][BN / 32], con
                 dma16(r, lds_w + OA::BYTES + (f % OB::NSLOT) * OB::SLOT + q * 4096, ob.off(v, f & 1, q));
         }
     });
-    // step 0 reads the first k-major stage and chunk 0 (two halves): all but
-    // the newest two (both K-contiguous) or three virtual steps
-    wait_vmcnt<(BOTH_KC ? 2 : 3) * ND>();
+    // step 0 reads the first k-major stage and chunk 0 (two halves)
+    wait_vmcnt<(NEWER + 1) * ND>();
     barrier_lds();
     static_for<NR>([&](auto R_) {
         do_read(R_, std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
@@ -438,10 +443,10 @@ __device__ __forceinline__ void mainloop_lin(f32x4 (&acc)[BM / 32][BN / 32], con
     auto step = [&](auto D_, int t) {
         constexpr int D = decltype(D_)::value;
         if constexpr (!BOTH_KC) {
-            wait_vmcnt<2 * ND>();
+            wait_vmcnt<NEWER * ND>();
             barrier_lds();
         } else if constexpr (D & 1) {
-            wait_vmcnt<ND>();
+            wait_vmcnt<NEWER * ND>();
             barrier_lds();
         }
         kstep(D_, t);
@@ -509,7 +514,8 @@ __device__ __forceinline__ void pin_row(f32x4 (&row)[TN])
 // with the row so that the writes (16 rows, 2 chunks) and the reads (2 or 4 whole
 // rows) both cover all banks.  Against accumulators the other way around,
 // which took four times the LDS writes and a reduction over 16 lanes for every
-// row's statistics, an epilogue is TODO.
+// row's statistics, 8192 x 8192 x 2048 with gelu, bias, residual and Z went from
+// 259 to 251 us.
 //
 // With p.vec the outputs and the residual go through range-checked buffer
 // accesses (rows past M and, parked, columns past N are dropped; an absent
@@ -805,12 +811,11 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
     }
 }
 
+// One tile: workgroup `block` of `blocks` of a product.
 template <int BM, int BN, bool AKM, bool BKM, int EPI, int ACT, bool BF>
-__global__ __launch_bounds__(256) void lin_gemm_kernel(LinParams p)
+__device__ __forceinline__ void lin_tile(const LinParams &p, int block, int blocks, char *smem)
 {
-    using C = LinCfg<BM, BN, AKM, BKM>;
-    __shared__ __attribute__((aligned(1024))) char smem[C::LDS];
-    const int lid = xcd_logical_id((int)gridDim.x, (int)blockIdx.x);
+    const int lid = xcd_logical_id(blocks, block);
     const int split = lid / p.num_tiles, t = lid - split * p.num_tiles;
     // tiles in groups of group_m tile rows, column-major inside a group
     const int full = p.group_m * p.tiles_n, g = t / full, first = g * p.group_m;
@@ -826,6 +831,32 @@ __global__ __launch_bounds__(256) void lin_gemm_kernel(LinParams p)
         for (int j = 0; j < BN / 32; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     mainloop_lin<BM, BN, AKM, BKM, BF>(acc, p, m0, n0, kb, k_end, smem);
     lin_epilogue<BM, BN, EPI, ACT, BF>(acc, p, m0, n0, tn, split, smem);
+}
+
+template <int BM, int BN, bool AKM, bool BKM, int EPI, int ACT, bool BF>
+__global__ __launch_bounds__(256) void lin_gemm_kernel(LinParams p)
+{
+    __shared__ __attribute__((aligned(1024))) char smem[LinCfg<BM, BN, AKM, BKM>::LDS];
+    lin_tile<BM, BN, AKM, BKM, EPI, ACT, BF>(p, (int)blockIdx.x, (int)gridDim.x, smem);
+}
+
+// A gradient's two products in one launch, on 128 x 128 tiles: where neither
+// fills the chip they run beside each other instead of one after the other
+// (1001 x 1003 x 1000 with dZ and dbias: 34 us apart, 24 in one launch).
+struct LinPair {
+    LinParams nn, tn;
+    int nn_groups;
+};
+template <bool BF>
+__global__ __launch_bounds__(256) void lin_grad_pair_kernel(LinPair p)
+{
+    constexpr int LN = LinCfg<128, 128, false, true>::LDS, LT = LinCfg<128, 128, true, true>::LDS;
+    __shared__ __attribute__((aligned(1024))) char smem[LN > LT ? LN : LT];
+    const int b = (int)blockIdx.x;
+    if (b < p.nn_groups)
+        lin_tile<128, 128, false, true, LE_OUT, 0, BF>(p.nn, b, p.nn_groups, smem);
+    else
+        lin_tile<128, 128, true, true, LE_OUT, 0, BF>(p.tn, b - p.nn_groups, (int)gridDim.x - p.nn_groups, smem);
 }
 
 }  // namespace gemm_epi

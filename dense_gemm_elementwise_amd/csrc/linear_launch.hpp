@@ -28,6 +28,8 @@ hipError_t lin_launch_xent_f16(int epi, int tile, const LinParams &p, int groups
 hipError_t lin_launch_xent_bf16(int epi, int tile, const LinParams &p, int groups, hipStream_t s);
 hipError_t lin_launch_nn_f16(int tile, const LinParams &p, int groups, hipStream_t s);
 hipError_t lin_launch_nn_bf16(int tile, const LinParams &p, int groups, hipStream_t s);
+hipError_t lin_launch_pair_f16(const LinPair &p, int groups, hipStream_t s);
+hipError_t lin_launch_pair_bf16(const LinPair &p, int groups, hipStream_t s);
 hipError_t lin_launch_tn_f16(int tile, const LinParams &p, int groups, hipStream_t s);
 hipError_t lin_launch_tn_bf16(int tile, const LinParams &p, int groups, hipStream_t s);
 

@@ -94,6 +94,8 @@ int check_workspace(const void *ws, int64_t have, int64_t need)
     return aligned(ws, 16) ? GEMM_EPI_OK : GEMM_EPI_ERR_ALIGN;
 }
 
+constexpr unsigned kAllTiles = 0xF;  // bits: indices into kLinTiles
+
 // ---- tiles and splits ---------------------------------------------------------
 // One product M x N x K on `tile`, its contraction cut into `splits` pieces of
 // k_split (a multiple of 64).
@@ -102,6 +104,7 @@ struct ProductPlan {
     int tiles_m = 0, tiles_n = 0;
     int64_t k_split = 0;
     int64_t part_bytes = 0;  // fp32 partial sums of the splits
+    double cost = 0;         // estimated microseconds
 };
 
 // Estimated microseconds of a plan, from timings of every tile and split on 54
@@ -164,6 +167,7 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsign
         }
     }
     const LinTile t = kLinTiles[best.tile];
+    best.cost = best_cost;
     best.tiles_m = (int)ceil_div(M, t.bm);
     best.tiles_n = (int)ceil_div(N, t.bn);
     best.part_bytes = best.splits > 1 ? best.splits * M * round_up(N, 8) * 4 : 0;
@@ -260,21 +264,42 @@ hipError_t launch_split_sum(int act, const SplitSumParams &q, hipStream_t s)
 }
 
 // A gradient product (NN or TN) into D (16-bit), or into / onto the fp32
-// accumulator acc, through partial sums where the plan splits it.  p holds the
-// operands.
-template <bool BF>
-hipError_t run_grad_product(bool tn, LinParams p, const ProductPlan &pl, int64_t M, int64_t N, int64_t K, void *D,
-                            int64_t ldd, float *acc, bool acc_in, bool acc_out, const float *alpha, float *part,
-                            hipStream_t s)
+// accumulator acc, through partial sums where the plan splits it.
+struct GradProduct {
+    LinParams p;
+    SplitSumParams sum;
+    int tile, groups;
+    bool split;
+};
+// p holds the operands
+GradProduct grad_product(LinParams p, const ProductPlan &pl, int64_t M, int64_t N, int64_t K, void *D, int64_t ldd,
+                         float *acc, bool acc_in, bool acc_out, const float *alpha, float *part)
 {
+    GradProduct g = {};
     set_product(p, pl, M, N, K);
     const int64_t ldc = round_up(N, 8);
     p.ldc = ldc;
     p.ldd = ldd;
-    if (pl.splits > 1) {
+    g.tile = pl.tile;
+    g.groups = p.num_tiles * pl.splits;
+    g.split = pl.splits > 1;
+    if (g.split) {
         p.C32 = part;
         p.c_split = M * ldc;
         p.acc_out = 1;
+        SplitSumParams &q = g.sum;
+        q.part = part;
+        q.splits = pl.splits;
+        q.M = (int)M;
+        q.N = (int)N;
+        q.ldc = ldc;
+        q.c_split = M * ldc;
+        q.D = (_Float16 *)D;
+        q.ldd = ldd;
+        q.C32 = acc;
+        q.acc_in = acc_in;
+        q.acc_out = acc_out;
+        q.alpha = alpha;
     } else {
         p.C32 = acc;
         p.acc_in = acc_in;
@@ -283,27 +308,79 @@ hipError_t run_grad_product(bool tn, LinParams p, const ProductPlan &pl, int64_t
         p.D = (_Float16 *)D;
         p.vec = dma_rows(D, ldd, N);
     }
-    const int groups = p.num_tiles * pl.splits;
+    g.p = p;
+    return g;
+}
+template <bool BF>
+hipError_t run_grad_sum(const GradProduct &g, hipStream_t s)
+{
+    return g.split ? launch_split_sum<BF, LE_OUT>(0, g.sum, s) : hipSuccess;
+}
+template <bool BF>
+hipError_t run_grad_product(bool tn, const GradProduct &g, hipStream_t s)
+{
     hipError_t e;
     if (tn)
-        e = BF ? lin_launch_tn_bf16(pl.tile, p, groups, s) : lin_launch_tn_f16(pl.tile, p, groups, s);
+        e = BF ? lin_launch_tn_bf16(g.tile, g.p, g.groups, s) : lin_launch_tn_f16(g.tile, g.p, g.groups, s);
     else
-        e = BF ? lin_launch_nn_bf16(pl.tile, p, groups, s) : lin_launch_nn_f16(pl.tile, p, groups, s);
-    if (e != hipSuccess || pl.splits == 1) return e;
-    SplitSumParams q = {};
-    q.part = part;
-    q.splits = pl.splits;
-    q.M = (int)M;
-    q.N = (int)N;
-    q.ldc = ldc;
-    q.c_split = M * ldc;
-    q.D = (_Float16 *)D;
-    q.ldd = ldd;
-    q.C32 = acc;
-    q.acc_in = acc_in;
-    q.acc_out = acc_out;
-    q.alpha = alpha;
-    return launch_split_sum<BF, LE_OUT>(0, q, s);
+        e = BF ? lin_launch_nn_bf16(g.tile, g.p, g.groups, s) : lin_launch_nn_f16(g.tile, g.p, g.groups, s);
+    return e == hipSuccess ? run_grad_sum<BF>(g, s) : e;
+}
+
+// The two products of a gradient, dX (M x K over N) and dW (N x K over M):
+// each by its own plan, or both in one launch.
+struct GradPlan {
+    ProductPlan dx, dw;
+    bool pair = false;
+    int64_t off_dx = 0, off_dw = 0;  // partial sums, relative to the plan's own region
+    int64_t part_bytes = 0;
+    bool fits = true;
+};
+GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw)
+{
+    GradPlan g;
+    g.dx = plan_product(M, K, round_up(N, 8), kAllTiles, kAllTiles);
+    g.dw = plan_product(N, K, M, kAllTiles, kAllTiles);
+    g.fits = (!want_dx || product_fits(g.dx)) && (!want_dw || product_fits(g.dw));
+    if (want_dx && want_dw) {
+        // Beside each other two products cost the longer one, and the shorter one
+        // as far as their workgroups are more than the compute units: all of it
+        // from twice 256 more on, less a launch and an idle tail, 5 us.  On 32
+        // shapes: 64^3 14.7 us apart, 10.9 in one launch; 333 x 9999 x 1000 (P in
+        // between) 55 and 45; 512 x 4096 x 4096 59 and 53; 4096^3, where the
+        // large tile wins, 222 and 255.
+        const ProductPlan x = plan_product(M, K, round_up(N, 8), 1u << kLinSmall, 1u << kLinSmall);
+        const ProductPlan w = plan_product(N, K, M, 1u << kLinSmall, 1u << kLinSmall);
+        // The contraction stays cut where the product alone would cut it: a gradient
+        // has the same bits whether or not the other one is wanted (the tile does
+        // not change them, the order of the sum along K does).
+        const bool same = x.k_split == g.dx.k_split && w.k_split == g.dw.k_split;
+        const double groups = (double)x.tiles_m * x.tiles_n * x.splits + (double)w.tiles_m * w.tiles_n * w.splits;
+        const double beside = std::min(1.0, std::max(0.0, (groups - kCUs) / (2.0 * kCUs)));
+        const double pair =
+            std::max(x.cost, w.cost) + beside * std::min(x.cost, w.cost) - (beside == 1.0 ? 5.0 : 0.0);
+        if (same && pair < g.dx.cost + g.dw.cost) {
+            g.pair = true;
+            g.dx = x;
+            g.dw = w;
+        }
+    }
+    g.off_dw = want_dx ? round_up(g.dx.part_bytes, 256) : 0;
+    g.part_bytes = g.off_dw + (want_dw ? g.dw.part_bytes : 0);
+    return g;
+}
+template <bool BF>
+hipError_t run_grad(const GradPlan &pl, const GradProduct *dx, const GradProduct *dw, hipStream_t s)
+{
+    if (pl.pair && dx && dw) {
+        const LinPair p = {dx->p, dw->p, dx->groups};
+        const int groups = dx->groups + dw->groups;
+        hipError_t e = BF ? lin_launch_pair_bf16(p, groups, s) : lin_launch_pair_f16(p, groups, s);
+        if (e == hipSuccess) e = run_grad_sum<BF>(*dx, s);
+        return e == hipSuccess ? run_grad_sum<BF>(*dw, s) : e;
+    }
+    hipError_t e = dx ? run_grad_product<BF>(false, *dx, s) : hipSuccess;
+    return e == hipSuccess && dw ? run_grad_product<BF>(true, *dw, s) : e;
 }
 
 hipError_t run_zero(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes, hipStream_t s)
@@ -453,7 +530,7 @@ struct LinearGradPlan {
     int64_t N8 = 0;
     int strips = 0, rows_per_strip = 0;
     StagePlan2 st;  // X, W
-    ProductPlan dx, dw;
+    GradPlan grad;
     int64_t off_dz = 0, off_bias = 0, off_part = 0, bytes = 0;
 };
 
@@ -500,18 +577,11 @@ int plan_linear_grad(const ge_linear_backward_args *a, LinearGradPlan &pl)
         pl.st.on[0] &= a->dW != nullptr;
         pl.st.on[1] &= a->dX != nullptr;
     }
-    int64_t part = 0;
-    if (a->dX) {
-        pl.dx = plan_product(a->M, a->K, pl.N8, 0xF, 0xF);
-        if (!product_fits(pl.dx)) return GEMM_EPI_ERR_SHAPE;
-        part = std::max(part, pl.dx.part_bytes);
+    if (a->dX || a->dW) {
+        pl.grad = plan_grad(a->M, a->N, a->K, a->dX, a->dW);
+        if (!pl.grad.fits) return GEMM_EPI_ERR_SHAPE;
+        pl.off_part = lay.take(pl.grad.part_bytes);
     }
-    if (a->dW) {
-        pl.dw = plan_product(a->N, a->K, a->M, 0xF, 0xF);
-        if (!product_fits(pl.dw)) return GEMM_EPI_ERR_SHAPE;
-        part = std::max(part, pl.dw.part_bytes);
-    }
-    pl.off_part = lay.take(part);
     pl.bytes = lay.bytes;
     return GEMM_EPI_OK;
 }
@@ -570,7 +640,7 @@ int run_linear_grad(const ge_linear_backward_args *a, const LinearGradPlan &pl)
             GE_TRY(launch(colsum_kernel, dim3((unsigned)ceil_div(a->N, 64)), dim3(1024), s, c));
         }
     }
-    float *part = (float *)(ws + pl.off_part);
+    GradProduct dx, dw;
     if (a->dX) {
         LinParams p = {};
         p.A = dz.p;
@@ -579,8 +649,8 @@ int run_linear_grad(const ge_linear_backward_args *a, const LinearGradPlan &pl)
         p.ldb = w.ld;
         p.n_read = (int)round_up(a->K, 8);
         p.k_rows = (int)a->N;
-        GE_TRY(run_grad_product<BF>(false, p, pl.dx, a->M, a->K, pl.N8, a->dX, a->lddx, nullptr, false, false, nullptr,
-                                    part, s));
+        dx = grad_product(p, pl.grad.dx, a->M, a->K, pl.N8, a->dX, a->lddx, nullptr, false, false, nullptr,
+                          (float *)(ws + pl.off_part));
     }
     if (a->dW) {
         LinParams p = {};
@@ -591,10 +661,10 @@ int run_linear_grad(const ge_linear_backward_args *a, const LinearGradPlan &pl)
         p.ldb = x.ld;
         p.n_read = (int)round_up(a->K, 8);
         p.k_rows = (int)a->M;
-        GE_TRY(run_grad_product<BF>(true, p, pl.dw, a->N, a->K, a->M, a->dW, a->lddw, nullptr, false, false, nullptr,
-                                    part, s));
+        dw = grad_product(p, pl.grad.dw, a->N, a->K, a->M, a->dW, a->lddw, nullptr, false, false, nullptr,
+                          (float *)(ws + pl.off_part + pl.grad.off_dw));
     }
-    return GEMM_EPI_OK;
+    return hip_status(run_grad<BF>(pl.grad, a->dX ? &dx : nullptr, a->dW ? &dw : nullptr, s));
 }
 
 // ---- cross entropy ---------------------------------------------------------------
@@ -700,8 +770,8 @@ struct XentGradPlan {
     StagePlan2 st;
     int64_t piece = 0, pld = 0;
     int pieces = 0;
-    ProductPlan p, dx, dw;            // of a full piece
-    ProductPlan p_last, dx_last, dw_last;
+    ProductPlan p, p_last;  // of a full piece, of the last one
+    GradPlan grad, grad_last;
     int64_t off_rows = 0, off_alpha = 0, off_p = 0, off_acc = 0, off_part = 0, bytes = 0;
 };
 
@@ -737,18 +807,14 @@ int plan_xent_grad(const ge_linear_xent_backward_args *a, XentGradPlan &pl)
     pl.piece = pl.pieces == 1 ? a->V : piece;
     pl.pld = round_up(pl.piece, 8);
     if (pl.pld > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
-    int64_t part = 0;
-    auto plan = [&](int64_t n, ProductPlan &p, ProductPlan &dx, ProductPlan &dw) {
-        p = plan_product(a->T, n, a->K, kSquareTiles, 0);
-        dx = plan_product(a->T, a->K, round_up(n, 8), 0xF, 0xF);
-        dw = plan_product(n, a->K, a->T, 0xF, 0xF);
-        if (a->dX) part = std::max(part, dx.part_bytes);
-        if (a->dW) part = std::max(part, dw.part_bytes);
-        return product_fits(p) && product_fits(dx) && product_fits(dw);
-    };
     const int64_t last = a->V - (pl.pieces - 1) * pl.piece;
-    if (!plan(pl.piece, pl.p, pl.dx, pl.dw) || !plan(last, pl.p_last, pl.dx_last, pl.dw_last))
+    pl.p = plan_product(a->T, pl.piece, a->K, kSquareTiles, 0);
+    pl.p_last = plan_product(a->T, last, a->K, kSquareTiles, 0);
+    pl.grad = plan_grad(a->T, pl.piece, a->K, a->dX, a->dW);
+    pl.grad_last = plan_grad(a->T, last, a->K, a->dX, a->dW);
+    if (!product_fits(pl.p) || !product_fits(pl.p_last) || !pl.grad.fits || !pl.grad_last.fits)
         return GEMM_EPI_ERR_SHAPE;
+    const int64_t part = std::max(pl.grad.part_bytes, pl.grad_last.part_bytes);
     pl.off_rows = lay.take(a->T * (int64_t)sizeof(XentRow));
     pl.off_alpha = lay.take(4);
     pl.off_p = lay.take(a->T * pl.pld * 2);
@@ -790,6 +856,8 @@ int run_xent_grad(const ge_linear_xent_backward_args *a, const XentGradPlan &pl)
         const int tile = last ? pl.p_last.tile : pl.p.tile;
         GE_TRY(BF ? lin_launch_xent_bf16(LE_XP, tile, p, p.num_tiles, s)
                   : lin_launch_xent_f16(LE_XP, tile, p, p.num_tiles, s));
+        const GradPlan &g = last ? pl.grad_last : pl.grad;
+        GradProduct dx, dw;
         if (a->dX) {
             LinParams q = {};
             q.A = P;
@@ -798,8 +866,7 @@ int run_xent_grad(const ge_linear_xent_backward_args *a, const XentGradPlan &pl)
             q.ldb = w.ld;
             q.n_read = (int)round_up(a->K, 8);
             q.k_rows = (int)n;
-            GE_TRY(run_grad_product<BF>(false, q, last ? pl.dx_last : pl.dx, a->T, a->K, round_up(n, 8), a->dX, a->lddx,
-                                        acc, c > 0, !last, alpha, part, s));
+            dx = grad_product(q, g.dx, a->T, a->K, round_up(n, 8), a->dX, a->lddx, acc, c > 0, !last, alpha, part);
         }
         if (a->dW) {
             LinParams q = {};
@@ -810,10 +877,10 @@ int run_xent_grad(const ge_linear_xent_backward_args *a, const XentGradPlan &pl)
             q.ldb = x.ld;
             q.n_read = (int)round_up(a->K, 8);
             q.k_rows = (int)a->T;
-            GE_TRY(run_grad_product<BF>(true, q, last ? pl.dw_last : pl.dw, n, a->K, a->T,
-                                        (char *)a->dW + v0 * a->lddw * 2, a->lddw, nullptr, false, false, alpha, part,
-                                        s));
+            dw = grad_product(q, g.dw, n, a->K, a->T, (char *)a->dW + v0 * a->lddw * 2, a->lddw, nullptr, false, false,
+                              alpha, (float *)((char *)part + g.off_dw));
         }
+        GE_TRY(run_grad<BF>(g, a->dX ? &dx : nullptr, a->dW ? &dw : nullptr, s));
     }
     return GEMM_EPI_OK;
 }
