@@ -660,14 +660,20 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
                         store8(t + (m0l + row) * ld + gcol, v, ncol);
                 };
                 half8 rbuf[PASSES] = {};
+                // At any alignment the loads are made without a branch too (rows past
+                // the last repeat it, columns past N - 8 start there): inside one the
+                // compiler would wait for them at once.  Lanes whose columns end
+                // short read theirs again, in the tiles at the edge only.
+                const bool edge = n0 + wn * WN + WN > p.N;
                 auto fetch = [&](int s) {
 #pragma unroll
                     for (int q = 0; q < PASSES; q++) {
                         const int row = row0 + s * 16 + q * RPP + srow0;
                         if constexpr (VEC)
                             rbuf[q] = buf_load<half8, 0>(rR, off_of(row, p.ldr));
-                        else
-                            rbuf[q] = p.R && row < rows_here ? load8(p.R + (m0l + row) * p.ldr + gcol, ncol) : half8{};
+                        else if (p.R && p.N >= 8)
+                            rbuf[q] = *(const half8u *)(p.R + (m0l + min(row, rows_here - 1)) * p.ldr +
+                                                        min(gcol, p.N - 8));
                     }
                 };
                 fetch(0);
@@ -677,6 +683,13 @@ __device__ __forceinline__ void lin_epilogue(f32x4 (&acc)[BM / 32][BN / 32], con
 #pragma unroll
                     for (int q = 0; q < PASSES; q++) rcur[q] = rbuf[q];
                     if (s < 3) fetch(s + 1);  // the next slab's residual flies beside this one's arithmetic
+                    if (!VEC && edge && p.R && ncol < 8) {
+#pragma unroll
+                        for (int q = 0; q < PASSES; q++) {
+                            const int row = row0 + s * 16 + q * RPP + srow0;
+                            rcur[q] = load8(p.R + (m0l + min(row, rows_here - 1)) * p.ldr + gcol, ncol);
+                        }
+                    }
 #pragma unroll
                     for (int q = 0; q < PASSES; q++) {
                         const int srow = s * 16 + q * RPP + srow0;

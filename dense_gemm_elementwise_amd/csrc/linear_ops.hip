@@ -144,33 +144,37 @@ double product_cost(int64_t M, int64_t N, int64_t K, int tile, int splits)
 }
 
 // tiles: bit mask of the tiles that exist for this product, split_tiles: of
-// those whose split form exists
-ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsigned split_tiles)
+// those whose split form exists; small: the best plan on the 128 x 128 tile, if
+// it is wanted too
+ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsigned split_tiles,
+                         ProductPlan *small = nullptr)
 {
     ProductPlan best;
-    double best_cost = 1e300;
+    best.cost = 1e300;
     for (int i = 0; i < 4; i++) {
         if (!(tiles >> i & 1)) continue;
         const LinTile t = kLinTiles[i];
-        const int64_t grid = ceil_div(M, t.bm) * ceil_div(N, t.bn);
+        ProductPlan of_tile;
+        of_tile.tile = i;
+        of_tile.cost = 1e300;
+        of_tile.tiles_m = (int)ceil_div(M, t.bm);
+        of_tile.tiles_n = (int)ceil_div(N, t.bn);
+        const int64_t grid = (int64_t)of_tile.tiles_m * of_tile.tiles_n;
         for (int want = 1; want <= 64; want *= 2) {
             if (want > 1 && (!(split_tiles >> i & 1) || K < want * 256 || grid * want > 4 * kCUs)) break;
             const int64_t k_split = round_up(ceil_div(K, want), 64);
             const int splits = (int)ceil_div(K, k_split);
-            double c = product_cost(M, N, K, i, splits);
-            if (c < best_cost) {
-                best_cost = c;
-                best.tile = i;
-                best.splits = splits;
-                best.k_split = k_split;
+            const double c = product_cost(M, N, K, i, splits);
+            if (c < of_tile.cost) {
+                of_tile.cost = c;
+                of_tile.splits = splits;
+                of_tile.k_split = k_split;
             }
         }
+        of_tile.part_bytes = of_tile.splits > 1 ? of_tile.splits * M * round_up(N, 8) * 4 : 0;
+        if (small && i == kLinSmall) *small = of_tile;
+        if (of_tile.cost < best.cost) best = of_tile;
     }
-    const LinTile t = kLinTiles[best.tile];
-    best.cost = best_cost;
-    best.tiles_m = (int)ceil_div(M, t.bm);
-    best.tiles_n = (int)ceil_div(N, t.bn);
-    best.part_bytes = best.splits > 1 ? best.splits * M * round_up(N, 8) * 4 : 0;
     return best;
 }
 
@@ -248,9 +252,12 @@ StagePlan2 plan_staging2(const void *a, int64_t lda, int64_t a_rows, const void 
 }
 
 template <bool BF, int EPI>
-hipError_t launch_split_sum(int act, const SplitSumParams &q, hipStream_t s)
+hipError_t launch_split_sum(int act, SplitSumParams q, hipStream_t s)
 {
-    const int64_t blocks = std::min<int64_t>(ceil_div((int64_t)q.M * ((q.N + 7) / 8), 256), 4096);
+    // several lanes for an output while that does not fill the chip
+    const int64_t outputs = (int64_t)q.M * ((q.N + 7) / 8);
+    q.lanes = outputs * 8 <= 512 * kCUs ? (q.splits >= 16 ? 8 : q.splits >= 8 ? 4 : 1) : 1;
+    const int64_t blocks = std::min<int64_t>(ceil_div(outputs * q.lanes, 256), 4096);
     const dim3 g((unsigned)blocks), b(256);
     if constexpr (EPI == LE_LINEAR) {
         switch (act) {
@@ -339,8 +346,9 @@ struct GradPlan {
 GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw)
 {
     GradPlan g;
-    g.dx = plan_product(M, K, round_up(N, 8), kAllTiles, kAllTiles);
-    g.dw = plan_product(N, K, M, kAllTiles, kAllTiles);
+    ProductPlan x, w;  // on the small tile
+    g.dx = plan_product(M, K, round_up(N, 8), kAllTiles, kAllTiles, &x);
+    g.dw = plan_product(N, K, M, kAllTiles, kAllTiles, &w);
     g.fits = (!want_dx || product_fits(g.dx)) && (!want_dw || product_fits(g.dw));
     if (want_dx && want_dw) {
         // Beside each other two products cost the longer one, and the shorter one
@@ -349,8 +357,6 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw)
         // shapes: 64^3 14.7 us apart, 10.9 in one launch; 333 x 9999 x 1000 (P in
         // between) 55 and 45; 512 x 4096 x 4096 59 and 53; 4096^3, where the
         // large tile wins, 222 and 255.
-        const ProductPlan x = plan_product(M, K, round_up(N, 8), 1u << kLinSmall, 1u << kLinSmall);
-        const ProductPlan w = plan_product(N, K, M, 1u << kLinSmall, 1u << kLinSmall);
         // The contraction stays cut where the product alone would cut it: a gradient
         // has the same bits whether or not the other one is wanted (the tile does
         // not change them, the order of the sum along K does).
@@ -397,12 +403,25 @@ constexpr int64_t kDotRows = 2, kSkinnyRows = 16;
 // there are fewer rows of W
 int row_dot_groups(int64_t N) { return (int)std::min<int64_t>(ceil_div(N, 4), 8 * kCUs); }
 
+// columns of the vocabulary per workgroup of skinny_kernel
+constexpr int64_t kSkinnyWide = 32768;
+int64_t skinny_cols(int64_t V) { return V < kSkinnyWide ? 16 : 64; }
+
+template <bool BF, int MODE, int ACT>
+hipError_t launch_skinny(const SkinnyParams &q, hipStream_t s)
+{
+    const dim3 b(256);
+    if constexpr (MODE != SK_LINEAR)
+        if (skinny_cols(q.N) == 64)
+            return launch(skinny_kernel<BF, MODE, ACT, false>, dim3((unsigned)ceil_div(q.N, 64)), b, s, q);
+    return launch(skinny_kernel<BF, MODE, ACT, true>, dim3((unsigned)ceil_div(q.N, 16)), b, s, q);
+}
+
 template <bool BF, bool XENT, int ACT>
 hipError_t launch_few_rows(const SkinnyParams &q, hipStream_t s)
 {
     const dim3 b(256);
-    if (q.M > kDotRows)
-        return launch(skinny_kernel<BF, XENT, ACT>, dim3((unsigned)ceil_div(q.N, XENT ? 64 : 16)), b, s, q);
+    if (q.M > kDotRows) return launch_skinny<BF, XENT ? SK_STATS : SK_LINEAR, ACT>(q, s);
     const dim3 g((unsigned)row_dot_groups(q.N));
     if (q.M == 1) return launch(row_dot_kernel<BF, XENT, ACT, 1>, g, b, s, q);
     return launch(row_dot_kernel<BF, XENT, ACT, 2>, g, b, s, q);
@@ -698,7 +717,7 @@ int plan_xent(const ge_linear_xent_args *a, XentPlan &pl)
     Layout lay;
     pl.skinny = a->T <= kSkinnyRows;
     if (pl.skinny) {
-        pl.nparts = a->T <= kDotRows ? row_dot_groups(a->V) : (int)ceil_div(a->V, 64);
+        pl.nparts = a->T <= kDotRows ? row_dot_groups(a->V) : (int)ceil_div(a->V, skinny_cols(a->V));
     } else {
         pl.st = plan_staging2(a->X, a->ldx, a->T, a->W, a->ldw, a->V, a->K, lay);
         pl.pl = plan_product(a->T, a->V, a->K, kSquareTiles, 0);
@@ -809,9 +828,9 @@ int plan_xent_grad(const ge_linear_xent_backward_args *a, XentGradPlan &pl)
     if (pl.pld > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
     const int64_t last = a->V - (pl.pieces - 1) * pl.piece;
     pl.p = plan_product(a->T, pl.piece, a->K, kSquareTiles, 0);
-    pl.p_last = plan_product(a->T, last, a->K, kSquareTiles, 0);
     pl.grad = plan_grad(a->T, pl.piece, a->K, a->dX, a->dW);
-    pl.grad_last = plan_grad(a->T, last, a->K, a->dX, a->dW);
+    pl.p_last = last == pl.piece ? pl.p : plan_product(a->T, last, a->K, kSquareTiles, 0);
+    pl.grad_last = last == pl.piece ? pl.grad : plan_grad(a->T, last, a->K, a->dX, a->dW);
     if (!product_fits(pl.p) || !product_fits(pl.p_last) || !pl.grad.fits || !pl.grad_last.fits)
         return GEMM_EPI_ERR_SHAPE;
     const int64_t part = std::max(pl.grad.part_bytes, pl.grad_last.part_bytes);
@@ -854,8 +873,24 @@ int run_xent_grad(const ge_linear_xent_backward_args *a, const XentGradPlan &pl)
         p.ldd = pl.pld;
         p.n_store = (int)round_up(n, 8);
         const int tile = last ? pl.p_last.tile : pl.p.tile;
-        GE_TRY(BF ? lin_launch_xent_bf16(LE_XP, tile, p, p.num_tiles, s)
-                  : lin_launch_xent_f16(LE_XP, tile, p, p.num_tiles, s));
+        if (a->T <= kSkinnyRows) {
+            SkinnyParams q = {};
+            q.X = x.p;
+            q.W = p.B;
+            q.ldx = x.ld;
+            q.ldw = w.ld;
+            q.M = (int)a->T;
+            q.N = (int)n;
+            q.K = (int)a->K;
+            q.D = P;
+            q.ldd = pl.pld;
+            q.rows = rows;
+            q.v0 = (int)v0;
+            GE_TRY((launch_skinny<BF, SK_P, ACT_IDENTITY>(q, s)));
+        } else {
+            GE_TRY(BF ? lin_launch_xent_bf16(LE_XP, tile, p, p.num_tiles, s)
+                      : lin_launch_xent_f16(LE_XP, tile, p, p.num_tiles, s));
+        }
         const GradPlan &g = last ? pl.grad_last : pl.grad;
         GradProduct dx, dw;
         if (a->dX) {

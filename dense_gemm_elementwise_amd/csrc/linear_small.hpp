@@ -33,6 +33,8 @@ struct SkinnyParams {
     const int64_t *target;
     float *part_max, *part_sum, *tlogit;
     int nparts;
+    const XentRow *rows;  // SK_P: row data; D is P, W the piece's first row, v0 its vocabulary index
+    int v0;
 };
 
 // Joins the four waves' running (maximum, sum) of M rows and leaves them in the
@@ -130,20 +132,23 @@ __global__ __launch_bounds__(256, 8) void row_dot_kernel(SkinnyParams p)
 //   linear: the workgroup's four waves take turns over K for the same 16
 //     rows (N / 16 workgroups fill the chip from N = 4096 on), their sums meet
 //     in LDS, 256 threads apply the epilogue.
-//   cross entropy: every wave has 16 rows of its own (the vocabulary fills the
-//     chip) and all of K; the workgroup leaves the softmax statistics of its 64
-//     columns.
-template <bool BF, bool XENT, int ACT>
+//   cross entropy: the same below a vocabulary of 32768, and past it 16 rows
+//     and all of K for every wave (64 columns a workgroup fill the chip); the
+//     workgroup leaves the softmax statistics of its columns, or, in the gradient, its part of P (11 rows against 7824 x 2176
+//     f16: 12 us; the 128 x 128 tiles take 22).
+enum SkinnyMode : int { SK_LINEAR = 0, SK_STATS = 1, SK_P = 2 };
+template <bool BF, int MODE, int ACT, bool SPLIT>
 __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
 {
     constexpr int U = 8, SPAN = 32 * U;
-    __shared__ float red[XENT ? 2 * 4 * 16 : 4 * 256];
+    constexpr bool XENT = MODE != SK_LINEAR;
+    __shared__ float red[SPLIT ? 4 * 256 : 2 * 4 * 16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int li = lane & 15, lg = lane >> 4;
-    const int n0 = XENT ? blockIdx.x * 64 + wave * 16 : blockIdx.x * 16;
+    const int n0 = SPLIT ? blockIdx.x * 16 : blockIdx.x * 64 + wave * 16;
     const _Float16 *w = p.W + (int64_t)min(n0 + li, p.N - 1) * p.ldw + lg * 8;
     const _Float16 *x = p.X + (int64_t)min(li, p.M - 1) * p.ldx + lg * 8;
-    const int step = XENT ? SPAN : 4 * SPAN;
+    const int step = SPLIT ? 4 * SPAN : SPAN;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     half8 wv[U], xv[U];
     auto fetch = [&](int k0) {
@@ -161,7 +166,7 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
             }
         }
     };
-    int k0 = XENT ? 0 : wave * SPAN;
+    int k0 = SPLIT ? wave * SPAN : 0;
     if (k0 < p.K) fetch(k0);
     while (k0 < p.K) {
         half8 wc[U], xc[U];
@@ -182,9 +187,16 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
         }
     }
     // lane (li, lg), register r: row li of X, row 4 lg + r of W
-    if constexpr (!XENT) {
+    if constexpr (SPLIT) {
         *(f32x4 *)(red + (wave * 64 + lane) * 4) = acc;
         __syncthreads();
+    }
+    if constexpr (XENT && SPLIT) {  // the first wave goes on with the sums
+        if (wave != 0) return;
+        acc = (acc + *(const f32x4 *)(red + (64 + lane) * 4)) +
+              (*(const f32x4 *)(red + (128 + lane) * 4) + *(const f32x4 *)(red + (192 + lane) * 4));
+    }
+    if constexpr (!XENT) {
         const int wr = tid & 15, xr = tid >> 4;  // adjacent threads on adjacent columns of D
         const int at = ((wr >> 2) * 16 + xr) * 4 + (wr & 3);
         const int n = n0 + wr;
@@ -195,6 +207,21 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
             if (p.Z) p.Z[xr * p.ldz + n] = st16<BF>(z);
             p.D[xr * p.ldd + n] = st16<BF>(lin_act<ACT>(z) + r);
         }
+    } else if constexpr (MODE == SK_P) {
+        // as in the tiles' epilogue: lane (li, lg) has 4 columns of row li
+        const int col = n0 + 4 * lg;
+        if (li >= p.M || col >= (p.N + 7) / 8 * 8) return;
+        const XentRow row = p.rows[li];
+        const float c = row.lse * kLog2e;
+        half4 h;
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            float pr = exp2_hw(__builtin_fmaf(acc[r], kLog2e, -c));
+            if (row.target - p.v0 == col + r) pr -= 1.0f;
+            pr *= row.scale;
+            h[r] = st16<BF>(row.ignored || col + r >= p.N ? 0.0f : pr);
+        }
+        *(half4 *)(p.D + li * p.ldd + col) = h;
     } else {
         float m = -__builtin_inff();
         const int64_t t = li < p.M ? p.target[li] : -1;
@@ -213,6 +240,13 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
         for (int r = 0; r < 4; r++) s += exp2_hw((acc[r] - ref) * kLog2e);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
+        if constexpr (SPLIT) {
+            if (lg == 0 && li < p.M) {
+                p.part_max[(int64_t)li * p.nparts + blockIdx.x] = m;
+                p.part_sum[(int64_t)li * p.nparts + blockIdx.x] = s;
+            }
+            return;
+        }
         if (lg == 0) {
             red[wave * 16 + li] = m;
             red[64 + wave * 16 + li] = s;
@@ -364,12 +398,15 @@ __global__ __launch_bounds__(1024) void colsum_kernel(ColSumParams p)
 }
 
 // ---------------------------------------------------------------------------
-// The sum over the splits of a product's contraction, in split order, and the
-// epilogue the product would have had: 8 columns per thread.
+// The sum over the splits of a product's contraction and the epilogue the
+// product would have had: 8 columns per thread, or, where there are many
+// splits of a small product, per `lanes` adjacent threads that take every
+// lanes-th split (3 x 200 over 64 splits: 19 us in one thread each).  The order is
+// fixed by the plan.
 // ---------------------------------------------------------------------------
 struct SplitSumParams {
     const float *part;  // [splits][M][ldc]
-    int splits, M, N;
+    int splits, lanes, M, N;  // lanes: 1, 4 or 8
     int64_t ldc, c_split;
     const _Float16 *bias, *R;
     _Float16 *D, *Z;
@@ -383,26 +420,37 @@ template <bool BF, int EPI, int ACT>
 __global__ __launch_bounds__(256) void split_sum_kernel(SplitSumParams p)
 {
     const int groups = (p.N + 7) / 8;
-    const int64_t total = (int64_t)p.M * groups;
+    const int64_t total = (int64_t)p.M * groups, step = (int64_t)gridDim.x * 256 / p.lanes;
+    const int lane = threadIdx.x & (p.lanes - 1);
     float alpha = 1.0f;
     if constexpr (EPI == LE_OUT)
         if (p.alpha) alpha = *p.alpha;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    // (whole groups of lanes stay in the loop together: they exchange sums)
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / p.lanes; i < total; i += step) {
         const int m = (int)(i / groups), c = (int)(i - (int64_t)m * groups) * 8, n = p.N - c;
-        const float *src = p.part + (int64_t)m * p.ldc + c;
+        const float *src = p.part + (int64_t)m * p.ldc + c + lane * p.c_split;
         float v[8] = {};
-        if (EPI == LE_OUT && p.acc_in) {
+        if (EPI == LE_OUT && p.acc_in && lane == 0) {
             const float *a = p.C32 + (int64_t)m * p.ldc + c;
 #pragma unroll
             for (int e = 0; e < 8; e++) v[e] = a[e];
         }
-        for (int s = 0; s < p.splits; s++, src += p.c_split) {
+        for (int s = lane; s < p.splits; s += p.lanes, src += p.lanes * p.c_split) {
             const f32x4 a = *(const f32x4 *)src, b = *(const f32x4 *)(src + 4);
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 v[e] += a[e];
                 v[4 + e] += b[e];
             }
+        }
+        if (p.lanes > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                v[e] += __shfl_xor(v[e], 1);
+                v[e] += __shfl_xor(v[e], 2);
+                if (p.lanes > 4) v[e] += __shfl_xor(v[e], 4);
+            }
+            if (lane) continue;
         }
         half8 d, z;
         if constexpr (EPI == LE_LINEAR) {

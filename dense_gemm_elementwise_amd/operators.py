@@ -84,19 +84,32 @@ def _raise(rc):
     raise binding.GemmEpiError(rc, msg)
 
 
-def _queue(name, head, dev, raw_stream):
+# workspace sizes by call and sizes (M, N, K / T, V, K / T, H, G): a guess that
+# saves the query; the call itself says when it is too small
+_sizes = {}
+
+
+def _queue(name, head, dev, raw_stream, sizes=None):
     """Makes one call.  A workspace, where the call needs one, comes from
-    torch's allocator, in the order of the current stream.  ge_linear is tried
-    without one first: the calls where latency counts (few rows) need none."""
+    torch's allocator, in the order of the current stream."""
     fns = _fns or _functions()
     f = fns[name]
-    if name == "ge_norm_residual":
+    if sizes is None:
         rc = f(head + _STREAM.pack(raw_stream))
     else:
-        rc = f(head + _TAIL.pack(0, 0, raw_stream)) if name == "ge_linear" else 7
+        key = (name, sizes)
+        need = _sizes.get(key, 0)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            rc = f(head + _TAIL.pack(ws.data_ptr(), need, raw_stream))
+        else:
+            rc = f(head + _TAIL.pack(0, 0, raw_stream))
         if rc == 7:
             rc, need = workspace_bytes(name, head + _NO_TAIL)
             if rc == 0:
+                if len(_sizes) >= 4096:
+                    _sizes.clear()
+                _sizes[key] = need
                 ws = torch.empty(need, dtype=torch.uint8, device=dev)
                 rc = f(head + _TAIL.pack(ws.data_ptr(), need, raw_stream))
     if rc != 0:
@@ -207,7 +220,7 @@ def linear(x, w, bias=None, residual=None, *, act="identity", save_z=False, stre
         d = x.new_empty((M, N))
         z = torch.empty_like(d) if save_z else None
         _queue("ge_linear", _LINEAR.pack(M, N, K, *xp, *wp, bp, *rp, d.data_ptr(), N, z.data_ptr() if save_z else 0,
-                                         N, a, _DTYPES[dtype]), dev, raw)
+                                         N, a, _DTYPES[dtype]), dev, raw, (M, N, K))
         return (d, z) if save_z else d
     return _run(call, (x, w, bias, residual), dev, stream)
 
@@ -239,7 +252,7 @@ def linear_backward(dd, x, w, z=None, *, act="identity", need_dx=True, need_dw=T
         _queue("ge_linear_backward",
                _LINEAR_GRAD.pack(M, N, K, *dp, *xp, *wp, *zp, dx.data_ptr() if need_dx else 0, K,
                                  dw.data_ptr() if need_dw else 0, K, db.data_ptr() if need_dbias else 0, a,
-                                 _DTYPES[dtype]), dev, raw)
+                                 _DTYPES[dtype]), dev, raw, (M, N, K))
         return dx, dw, db
     return _run(call, (dd, x, w, z), dev, stream)
 
@@ -264,7 +277,7 @@ def linear_xent(x, w, target, *, ignore_index=-100, stream=None):
         loss = torch.empty((T,), dtype=torch.float32, device=dev)
         lse = torch.empty_like(loss)
         _queue("ge_linear_xent", _XENT.pack(T, V, K, *xp, *wp, tp, int(ignore_index), loss.data_ptr(),
-                                            lse.data_ptr(), _DTYPES[dtype]), dev, raw)
+                                            lse.data_ptr(), _DTYPES[dtype]), dev, raw, (T, V, K))
         return loss, lse
     return _run(call, (x, w, target), dev, stream)
 
@@ -295,7 +308,7 @@ def linear_xent_backward(dloss, x, w, target, lse, *, ignore_index=-100, need_dx
         dw = x.new_empty((V, K)) if need_dw else None
         _queue("ge_linear_xent_backward",
                _XENT_GRAD.pack(T, V, K, gp, *xp, *wp, tp, lp, int(ignore_index), dx.data_ptr() if need_dx else 0, K,
-                               dw.data_ptr() if need_dw else 0, K, _DTYPES[dtype]), dev, raw)
+                               dw.data_ptr() if need_dw else 0, K, _DTYPES[dtype]), dev, raw, (T, V, K))
         return dx, dw
     return _run(call, (dloss, x, w, target, lse), dev, stream)
 
@@ -369,6 +382,6 @@ def norm_residual_backward(dx, dh_out, h_out, y, *, w_post=None, w_pre=None, gat
         _queue("ge_norm_residual_backward",
                _NORM_GRAD.pack(T, H, G, *dxp, *dhp, *hp, *yp, *mid, scale, eps, dh.data_ptr(), H, dy.data_ptr(), H,
                                *(t.data_ptr() if t is not None else 0 for t in (dwo, dwi, dg)), _DTYPES[dtype],
-                               _STREAM_DTYPES[sd]), dev, raw)
+                               _STREAM_DTYPES[sd]), dev, raw, (T, H, G))
         return dh, dy, dwo, dwi, dg
     return _run(call, (dx, dh_out, h_out, y, w_post, w_pre, gate), dev, stream)
