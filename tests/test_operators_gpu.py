@@ -688,3 +688,91 @@ def test_guards():
         assert (buf[:256] == 3).all() and (buf[256 + M * ld:] == 3).all()
         assert (d[:, N:] == 3).all()
         assert torch.equal(d[:, :N], ge.linear(x, w))
+
+
+def test_in_place():
+    """D on top of the residual and H' on top of H, through the C entry points, give the same bits."""
+    import struct
+    from dense_gemm_elementwise_amd import operators as o
+    log("[in place]")
+    g = gen(15)
+    s = torch.cuda.current_stream().cuda_stream
+    for M, N, K in ((1, 520, 300), (9, 61, 64), (40, 200, 2304), (300, 264, 72), (300, 263, 72)):
+        x, w, r = rnd(g, M, K), rnd(g, N, K, std=K ** -0.5), rnd(g, M, N)
+        want = ge.linear(x, w, None, r, act="silu")
+        args = o._LINEAR.pack(M, N, K, x.data_ptr(), K, w.data_ptr(), K, 0, r.data_ptr(), N, r.data_ptr(), N, 0, 0, 3, 1)
+        rc, need = o.workspace_bytes("ge_linear", args + struct.pack("@3q", 0, 0, s))
+        assert rc == 0
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+        assert o._functions()["ge_linear"](args + struct.pack("@3q", ws.data_ptr(), need, s)) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(r, want)
+    for H in (513, 4096):
+        h, y = rnd(g, 7, H, t=F32), rnd(g, 7, H)
+        ho, xo = ge.norm_residual(h, y)
+        x = torch.empty_like(y)
+        args = o._NORM.pack(7, H, 1, h.data_ptr(), H, y.data_ptr(), H, 0, 0, 0, 1, 1, 1.0, 1e-5, h.data_ptr(), H,
+                            x.data_ptr(), H, 1, 2)
+        assert o._functions()["ge_norm_residual"](args + struct.pack("@q", s)) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(h, ho) and torch.equal(x, xo)
+
+
+# ---- offsets past 32 bits (operands of more than 4 GiB) ---------------------------
+@pytest.mark.parametrize("T", [2, 9, 40])
+def test_weights_past_32_bits(T):
+    log(f"[past 32 bits] T={T}")
+    g = gen(31)
+    V, K = 530000, 4104  # 4.35 GB
+    x = rnd(g, T, K, std=0.5)
+    w = torch.zeros(V, K, dtype=BF16, device=DEV)
+    w[-64:] = rnd(g, 64, K, std=2 * K ** -0.5)
+    tail = (x.double() @ w[-64:].double().t()).cpu()  # the other logits are 0
+
+    d = ge.linear(x, w)
+    assert (d[:, :-64] == 0).all()
+    close("D", d[:, -64:], tail, (K + 2) * E24 * (x.double().abs() @ w[-64:].double().abs().t()).cpu())
+    dd = torch.zeros_like(d)
+    dd[:, -64:] = rnd(g, T, 64)
+    dx, dw, db = ge.linear_backward(dd, x, w)
+    dd64, x64, w64 = dd[:, -64:].double().cpu(), x.double().cpu(), w[-64:].double().cpu()
+    close("dX", dx, dd64 @ w64, 70 * E24 * (dd64.abs() @ w64.abs()))
+    close("dW", dw[-64:], dd64.t() @ x64, (T + 2) * E24 * (dd64.abs().t() @ x64.abs()))
+    assert (dw[:-64] == 0).all()
+    del dw, d, dd
+
+    target = torch.randint(V - 64, V, (T,), generator=g).to(DEV)
+    loss, lse = ge.linear_xent(x, w, target)
+    want = torch.logsumexp(torch.cat([tail, torch.full((T, 1), math.log(V - 64), dtype=torch.float64)], 1), 1)
+    assert (lse.double().cpu() - want).abs().max() < 1e-4
+    at = (target - (V - 64)).cpu()
+    assert (loss.double().cpu() - (want - tail[torch.arange(T), at])).abs().max() < 1e-4
+    dx, dw = ge.linear_xent_backward(torch.ones(T, device=DEV), x, w, target, lse)
+    P = torch.exp(tail - want[:, None])
+    P[torch.arange(T), at] -= 1
+    close("dX", dx, P @ w64, (u(BF16) + 1e-4) * (P.abs() @ w64.abs()))
+    close("dW", dw[-64:], P.t() @ x64, (u(BF16) + 1e-4) * (P.abs().t() @ x64.abs()))
+    rest = torch.exp(-want) @ x64  # any other row of dW
+    for v in (0, V // 2, V - 65):
+        close("dW row", dw[v], rest, (u(BF16) + 1e-4) * (torch.exp(-want) @ x64.abs()))
+
+
+def test_norms_past_32_bits():
+    log("[past 32 bits] norms")
+    g = gen(32)
+    T, H = 270000, 8192  # 4.4 GB a tensor
+    h = torch.zeros(T, H, dtype=F16, device=DEV)
+    y, dx, dh = torch.zeros_like(h), torch.zeros_like(h), torch.zeros_like(h)
+    for t in (h, y, dx, dh):
+        t[-3:] = rnd(g, 3, H, t=F16)
+    w = rnd(g, H, t=F16, mean=1.0, std=0.1)
+    a = ge.norm_residual(h, y, w_post=w, w_pre=w)
+    b = ge.norm_residual(h[-3:], y[-3:], w_post=w, w_pre=w)
+    for p, q in zip(a, b):
+        assert torch.equal(p[-3:], q) and (p[:-3] == 0).all()
+    a = ge.norm_residual_backward(dx, dh, h, y, w_post=w, w_pre=w)
+    b = ge.norm_residual_backward(dx[-3:], dh[-3:], h[-3:], y[-3:], w_post=w, w_pre=w)
+    for p, q in zip(a[:2], b[:2]):
+        assert torch.equal(p[-3:], q) and (p[:-3] == 0).all()
+    for p, q in zip(a[2:4], b[2:4]):
+        assert (p - q).abs().max() <= 1e-5 * q.abs().max()
