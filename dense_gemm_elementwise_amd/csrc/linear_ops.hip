@@ -178,9 +178,16 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsign
     return best;
 }
 
+// a launch holds fewer than 2^32 threads: 2^24 workgroups of 256
 bool product_fits(const ProductPlan &pl)
 {
-    return (int64_t)pl.tiles_m * pl.tiles_n <= INT32_MAX / 64 / pl.splits;
+    return (int64_t)pl.tiles_m * pl.tiles_n * pl.splits < 1 << 24;
+}
+
+// The grid of a kernel that takes its row from block_row.
+dim3 row_grid(int64_t rows)
+{
+    return dim3((unsigned)std::min(rows, kRowGrid), (unsigned)ceil_div(rows, kRowGrid));
 }
 
 void set_product(LinParams &p, const ProductPlan &pl, int64_t M, int64_t N, int64_t K)
@@ -770,7 +777,7 @@ int run_xent(const ge_linear_xent_args *a, const XentPlan &pl)
         GE_TRY(BF ? lin_launch_xent_bf16(LE_XFWD, pl.pl.tile, p, p.num_tiles, s)
                   : lin_launch_xent_f16(LE_XFWD, pl.pl.tile, p, p.num_tiles, s));
     }
-    return hip_status(launch(xent_loss_kernel, dim3((unsigned)a->T), dim3(pl.nparts > 128 ? 256 : 64), s,
+    return hip_status(launch(xent_loss_kernel, row_grid(a->T), dim3(pl.nparts > 128 ? 256 : 64), s, a->T,
                              (const float *)pmax, (const float *)psum, pl.nparts, (const float *)tlogit, a->target,
                              a->V, a->ignore_index, a->loss, a->lse));
 }
@@ -975,6 +982,7 @@ hipError_t run_norm(const ge_norm_residual_args *a)
     p.ldy = a->ldy;
     p.ldho = a->ldho;
     p.ldx = a->ldx;
+    p.rows = (int)a->T;
     p.hidden = (int)a->hidden;
     p.rows_per_gate = (int)(a->T / a->G);
     p.post = (int)a->post;
@@ -983,7 +991,7 @@ hipError_t run_norm(const ge_norm_residual_args *a)
     p.eps = (float)a->eps;
     return dispatch_row(a->hidden, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-        return launch(norm_residual_kernel<BF, S32, TPR, NV>, dim3((unsigned)a->T), dim3(TPR),
+        return launch(norm_residual_kernel<BF, S32, TPR, NV>, row_grid(a->T), dim3(TPR),
                       (hipStream_t)a->stream, p);
     });
 }

@@ -487,13 +487,19 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(char *dst, int64_t ld_by
 // ---------------------------------------------------------------------------
 // Cross entropy, the row passes.
 // ---------------------------------------------------------------------------
+// Workgroups of one row each: a launch holds fewer than 2^32 threads along x,
+// so past 2^21 rows (1024 threads each at most) the rows go on along y.
+constexpr int64_t kRowGrid = 1 << 21;
+__device__ __forceinline__ int64_t block_row() { return (int64_t)blockIdx.y * kRowGrid + blockIdx.x; }
+
 // Joins the column tiles' (maximum, sum) pairs of one row per block.
-__global__ __launch_bounds__(256) void xent_loss_kernel(const float *part_max, const float *part_sum, int nparts,
-                                                        const float *tlogit, const int64_t *target, int64_t V,
-                                                        int64_t ignore, float *loss, float *lse)
+__global__ __launch_bounds__(256) void xent_loss_kernel(int64_t T, const float *part_max, const float *part_sum,
+                                                        int nparts, const float *tlogit, const int64_t *target,
+                                                        int64_t V, int64_t ignore, float *loss, float *lse)
 {
     __shared__ float rm[4], rs[4];
-    const int64_t row = blockIdx.x;
+    const int64_t row = block_row();
+    if (row >= T) return;
     const float *pm = part_max + row * nparts, *ps = part_sum + row * nparts;
     float m = -__builtin_inff(), s = 0.0f;
     for (int i = threadIdx.x; i < nparts; i += blockDim.x) softmax_join(m, s, pm[i], ps[i]);
@@ -538,7 +544,7 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, int64
 {
     __shared__ float red[16];
     float top = 0.0f;
-    for (int t = threadIdx.x; t < T; t += 1024) {
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
         const float a = __builtin_fabsf(dloss[t]);
         if (target[t] != ignore && a < __builtin_inff()) top = __builtin_fmaxf(top, a);
     }
@@ -550,7 +556,7 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, int64
     for (int u = 0; u < 16; u++) top = __builtin_fmaxf(top, red[u]);
     if (threadIdx.x == 0) *alpha = top * 0x1p-14f;
     const float div = top > 0.0f ? top : 1.0f;
-    for (int t = threadIdx.x; t < T; t += 1024) {
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
         const int64_t c = target[t];
         XentRow r;
         r.lse = lse[t];

@@ -114,7 +114,7 @@ struct NormParams {
     void *H_out;
     _Float16 *X;
     int64_t ldh, ldy, ldho, ldx;
-    int hidden, rows_per_gate, post, pre;
+    int rows, hidden, rows_per_gate, post, pre;
     float scale, eps;
 };
 
@@ -123,11 +123,12 @@ __global__ __launch_bounds__(TPR) void norm_residual_kernel(NormParams p)
 {
     __shared__ float lds[2][16][1];
     BlockSum<1> sum{lds, TPR / 64};
-    const int64_t row = blockIdx.x;
+    const int64_t row = block_row();
+    if (row >= p.rows) return;
     const int H = p.hidden;
     const float inv_h = 1.0f / (float)H;
     const _Float16 *gate =
-        p.gate ? p.gate + (int64_t)__builtin_amdgcn_readfirstlane((int)blockIdx.x / p.rows_per_gate) * H : nullptr;
+        p.gate ? p.gate + (int64_t)__builtin_amdgcn_readfirstlane((int)row / p.rows_per_gate) * H : nullptr;
 
     half8 y[NV], wpo[NV], wpr[NV], g[NV];
     StreamVec<BF, S32> h[NV];

@@ -776,3 +776,35 @@ def test_norms_past_32_bits():
         assert torch.equal(p[-3:], q) and (p[:-3] == 0).all()
     for p, q in zip(a[2:4], b[2:4]):
         assert (p - q).abs().max() <= 1e-5 * q.abs().max()
+
+
+def test_rows_past_one_grid_axis():
+    """2^26 rows of a wave each are 2^32 threads: more than a launch takes along x."""
+    log("[many rows] norms")
+    g = gen(33)
+    T, H = (1 << 26) + 35, 2
+    h = torch.zeros(T, H, dtype=F16, device=DEV)
+    y = torch.zeros_like(h)
+    some = torch.tensor([0, 1, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, 1 << 25, T - 2, T - 1], device=DEV)
+    for t in (h, y):
+        t[some] = rnd(g, len(some), H, t=F16)
+    a = ge.norm_residual(h, y)
+    b = ge.norm_residual(h[some], y[some])
+    for p, q in zip(a, b):
+        assert torch.equal(p[some], q)
+        p[some] = 0
+        assert (p == 0).all()
+    log("[many rows] cross entropy")
+    T, K, V = (1 << 26) + 35, 8, 24
+    x = torch.zeros(T, K, dtype=F16, device=DEV)
+    x[-100:] = rnd(g, 100, K, t=F16)
+    w = rnd(g, V, K, t=F16)
+    target = torch.zeros(T, dtype=torch.int64, device=DEV)
+    target[-100:] = torch.arange(100, device=DEV) % V
+    a = ge.linear_xent(x, w, target)
+    b = ge.linear_xent(x[-100:], w, target[-100:])
+    # (another tile may add the 24 exponentials in another order: some 30 roundings
+    # of 2^-24 on values below 64)
+    for p, q in zip(a, b):
+        assert (p[-100:] - q).abs().max() <= 30 * 64 * 2.0 ** -24
+        assert (p[:-100] - math.log(V)).abs().max() <= 30 * 4 * 2.0 ** -24
