@@ -996,12 +996,27 @@ hipError_t run_norm(const ge_norm_residual_args *a)
     });
 }
 
+// Elements a thread of the gradient holds.  A row of 8 a thread past 4096
+// columns is a workgroup that has its compute unit alone; with 12 a thread two
+// workgroups of up to 512 threads share it up to 6144 columns, one's reductions
+// beside the other's loads.  8190 rows, us with 8 and with 12, 16-bit stream:
+// 4100 columns 152 and 115, 5120 157 and 123, 6144 168 and 143; rows of an odd
+// length (no loads in flight behind the reductions with 8): 4101 215 and 153.
+// An fp32 stream of whole units stays with 8, whose next row's loads are in
+// flight: 4100 columns 133 and 142, 6144 196 and 202; odd 4101: 225 and 163.
+int norm_grad_elements(int64_t H, bool s32)
+{
+    return H > 4096 && H <= 6144 && !(s32 && H % 4 == 0) ? 12 : 8;
+}
+// its threads, in whole waves
+int64_t norm_grad_threads(int64_t H, bool s32) { return round_up(ceil_div(H, norm_grad_elements(H, s32)), 64); }
+
 // Runs of rows that share a gate row, and workgroups: as many as the compute
 // units hold at once (one of more than 512 threads, two of 512, more of the
 // small ones), so that the partial column sums, a row per workgroup, stay small
-// beside the rows themselves.  8192 rows: 4100 columns 149 us with 256, 167
-// with 1024; 4096 columns 127 with 256, 102 with 512; 1024 columns 40 with
-// 512, 36 with 1024.  At least 2 rows each, from 256 rows on.
+// beside the rows themselves.  8192 rows: 4100 columns at 8 a thread 149 us
+// with 256, 167 with 1024; 4096 columns 127 with 256, 102 with 512; 1024
+// columns 40 with 512, 36 with 1024.  At least 2 rows each, from 256 rows on.
 struct NormGradPlan {
     int64_t rows_per_gate = 0, rows_per_run = 0, runs = 0, runs_per_block = 1, blocks = 0;
     int runs_per_gate = 1;
@@ -1025,7 +1040,7 @@ int plan_norm_grad(const ge_norm_residual_backward_args *a, NormGradPlan &pl)
     GE_CHECK(check_matrix(a->dH, a->lddh, a->hidden, es, GEMM_EPI_ERR_NULL_OUTPUT));
     GE_CHECK(check_matrix(a->dY, a->lddy, a->hidden, 2, GEMM_EPI_ERR_NULL_OUTPUT));
     pl.rows_per_gate = a->T / a->G;
-    const int64_t threads = round_up(ceil_div(a->hidden, 8), 64);
+    const int64_t threads = norm_grad_threads(a->hidden, a->stream_dtype == GEMM_EPI_F32);
     const int64_t most = kCUs * (threads > 512 ? 1 : threads > 256 ? 2 : 4);
     const int64_t blocks = a->T <= kCUs ? a->T : std::min(most, ceil_div(a->T, 2));
     pl.rows_per_run = std::min(pl.rows_per_gate, ceil_div(a->T, blocks));
@@ -1085,16 +1100,21 @@ int run_norm_grad(const ge_norm_residual_backward_args *a, const NormGradPlan &p
     p.p_post = post ? (float *)(ws + pl.off_post) : nullptr;
     p.p_pre = a->dw_pre ? (float *)(ws + pl.off_pre) : nullptr;
     p.dgate = !a->dgate || p.gate_direct ? a->dgate : (float *)(ws + pl.off_gate);
-    // 8 elements per thread, in whole waves
-    const dim3 g((unsigned)pl.blocks), b((unsigned)round_up(ceil_div(H, 8), 64));
-    const bool tail = H % 4 != 0;
-    if (H <= 4096)
-        GE_TRY(launch(tail ? norm_residual_grad_kernel<BF, S32, 512, true> : norm_residual_grad_kernel<BF, S32, 512, false>,
-                      g, b, s, p));
+    const dim3 g((unsigned)pl.blocks), b((unsigned)norm_grad_threads(H, S32));
+    auto run = [&](auto most, auto units) {
+        constexpr int MAXT = decltype(most)::value, NU = decltype(units)::value;
+        if (H % 4 != 0) return launch(norm_residual_grad_kernel<BF, S32, MAXT, NU, true>, g, b, s, p);
+        if constexpr (!(S32 && NU == 3))
+            return launch(norm_residual_grad_kernel<BF, S32, MAXT, NU, false>, g, b, s, p);
+        return hipErrorInvalidValue;  // norm_grad_elements
+    };
+    using std::integral_constant;
+    if (norm_grad_elements(H, S32) == 12)
+        GE_TRY(run(integral_constant<int, 512>{}, integral_constant<int, 3>{}));
+    else if (H <= 4096)
+        GE_TRY(run(integral_constant<int, 512>{}, integral_constant<int, 2>{}));
     else
-        GE_TRY(launch(tail ? norm_residual_grad_kernel<BF, S32, 1024, true>
-                           : norm_residual_grad_kernel<BF, S32, 1024, false>,
-                      g, b, s, p));
+        GE_TRY(run(integral_constant<int, 1024>{}, integral_constant<int, 2>{}));
     ColSumParams c = {};
     c.partial[0] = p.p_post;
     c.out[0] = post ? a->dw_post : nullptr;

@@ -231,22 +231,22 @@ struct NormGradParams {
     float *dgate;            // [G][hidden], or [runs][hidden] partial sums, or NULL
 };
 
-// The 8 elements of one row that a thread of the gradient holds, as two units
+// The elements of one row that a thread of the gradient holds, as NU units
 // of 4 consecutive ones: unit u starts at column (u threads + tid) 4.  Without
 // TAIL the row length is a multiple of 4, so a unit exists whole or not at all;
 // with it the row's last unit may be short.  Absent elements read as zeros.
 // (Units of 8 took 25 more registers: past the 128 that let two workgroups
 // share a compute unit.)
-template <bool BF, typename T, bool TAIL>
+template <bool BF, typename T, bool TAIL, int NU>
 struct RowPart {
     typedef T V __attribute__((ext_vector_type(4), aligned(sizeof(T))));
-    V v[2];
+    V v[NU];
     // (a scalar row address plus a 32-bit offset: one register per unit)
     __device__ __forceinline__ void load(const T *row, int cols, int tid)
     {
         asm volatile("" : "+v"(tid));  // the masks are made again every time: kept, they take too many scalar registers
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
+        for (int u = 0; u < NU; u++) {
             const int c = (u * (int)blockDim.x + tid) * 4;
             const char *at = (const char *)row + (uint32_t)c * (uint32_t)sizeof(T);
             v[u] = V{};
@@ -263,7 +263,7 @@ struct RowPart {
     {
         asm volatile("" : "+v"(tid));
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
+        for (int u = 0; u < NU; u++) {
             const int c = (u * (int)blockDim.x + tid) * 4;
             char *at = (char *)row + (uint32_t)c * (uint32_t)sizeof(T);
             if (TAIL ? c + 4 <= cols : c < cols) {
@@ -275,7 +275,11 @@ struct RowPart {
             }
         }
     }
-    __device__ __forceinline__ void fill(T x) { v[0] = v[1] = V{x, x, x, x}; }
+    __device__ __forceinline__ void fill(T x)
+    {
+#pragma unroll
+        for (int u = 0; u < NU; u++) v[u] = V{x, x, x, x};
+    }
     __device__ __forceinline__ float get(int i) const
     {
         const T x = v[i / 4][i % 4];
@@ -293,24 +297,26 @@ struct RowPart {
     }
 };
 
-template <bool BF, bool S32, int MAXT, bool TAIL>
+template <bool BF, bool S32, int MAXT, int NU, bool TAIL>
 __global__ __launch_bounds__(MAXT, 4) void norm_residual_grad_kernel(NormGradParams p)
 {
-    constexpr int NE = 8;
-    // Past 4096 columns the registers (128 a lane in a workgroup of 1024) hold a
-    // row's operands, the next row's and little else: the sums of the two
-    // weights' gradients and the weights themselves live in LDS, where each
-    // thread only touches its own elements.
-    constexpr bool LDS_ACC = MAXT > 512;
+    constexpr int NE = 4 * NU;
+    // Past 4096 columns the registers (128 a lane: 16 waves on a compute unit)
+    // hold a row's operands and little else: the sums of the two weights'
+    // gradients and the weights themselves live in LDS, where each thread only
+    // touches its own elements (with 12 elements the gate stays in registers:
+    // 74 KB, so that two workgroups fit).
+    constexpr bool LDS_ACC = MAXT > 512 || NU > 2;
+    constexpr int LDS_W = !LDS_ACC ? 0 : NU > 2 ? 2 : 3;
     // Alone on its compute unit a workgroup loads the next row while it reduces
     // this one (short last units leave no scalar registers for it).
     constexpr bool PREFETCH = MAXT > 512 && !TAIL;
     using T = typename std::conditional<S32, float, _Float16>::type;
-    using Half = RowPart<BF, _Float16, TAIL>;
-    using Stream = RowPart<BF, T, TAIL>;
+    using Half = RowPart<BF, _Float16, TAIL, NU>;
+    using Stream = RowPart<BF, T, TAIL, NU>;
     __shared__ float lds[2][16][6];
     using HV = typename Half::V;
-    __shared__ HV w_lds[LDS_ACC ? 3 : 1][LDS_ACC ? 2 : 1][LDS_ACC ? MAXT : 1];
+    __shared__ HV w_lds[LDS_ACC ? LDS_W : 1][LDS_ACC ? NU : 1][LDS_ACC ? MAXT : 1];
     __shared__ f32x4 acc_lds[LDS_ACC ? 2 : 1][LDS_ACC ? NE / 4 : 1][LDS_ACC ? MAXT : 1];
     BlockSum<6> sum{lds, (int)blockDim.x >> 6};
     const int H = p.hidden, tid = threadIdx.x;
@@ -335,27 +341,27 @@ __global__ __launch_bounds__(MAXT, 4) void norm_residual_grad_kernel(NormGradPar
         return (i / 4 * (int)blockDim.x + t) * 4 + (TAIL ? i % 4 : 0) < H;
     };
     Half kept[3];  // w_post, w_pre, gate
-    auto keep = [&](int k, const Half &r) {
-        if constexpr (LDS_ACC) {
+    auto keep = [&](auto k, const Half &r) {
+        if constexpr (k.value < LDS_W) {
 #pragma unroll
-            for (int u = 0; u < 2; u++) w_lds[k][u][tid] = r.v[u];
+            for (int u = 0; u < NU; u++) w_lds[k][u][tid] = r.v[u];
         } else {
             kept[k] = r;
         }
     };
-    auto weight = [&](int k) {
-        if constexpr (LDS_ACC) {
+    auto weight = [&](auto k) {
+        if constexpr (k.value < LDS_W) {
             Half r;
 #pragma unroll
-            for (int u = 0; u < 2; u++) r.v[u] = w_lds[k][u][tid];
+            for (int u = 0; u < NU; u++) r.v[u] = w_lds[k][u][tid];
             return r;
         } else {
             return kept[k];
         }
     };
     float a_post[LDS_ACC ? 1 : NE], a_pre[LDS_ACC ? 1 : NE], a_gate[NE];
-    keep(0, row_of(p.w_post));
-    keep(1, row_of(p.w_pre));
+    keep(std::integral_constant<int, 0>{}, row_of(p.w_post));
+    keep(std::integral_constant<int, 1>{}, row_of(p.w_pre));
     if constexpr (LDS_ACC) {
 #pragma unroll
         for (int k = 0; k < NE / 4; k++) acc_lds[0][k][tid] = acc_lds[1][k][tid] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -371,7 +377,7 @@ __global__ __launch_bounds__(MAXT, 4) void norm_residual_grad_kernel(NormGradPar
         const int in_gate = (run - gr * p.runs_per_gate) * p.rows_per_run;
         const int64_t r0 = (int64_t)gr * p.rows_per_gate + in_gate;
         const int64_t r1 = r0 + min(p.rows_per_run, p.rows_per_gate - in_gate);
-        keep(2, row_of(p.gate ? p.gate + (int64_t)gr * H : nullptr));
+        keep(std::integral_constant<int, 2>{}, row_of(p.gate ? p.gate + (int64_t)gr * H : nullptr));
 #pragma unroll
         for (int i = 0; i < NE; i++) a_gate[i] = 0.0f;
         Half dx, y;
@@ -397,7 +403,7 @@ __global__ __launch_bounds__(MAXT, 4) void norm_residual_grad_kernel(NormGradPar
             }
             float dn[NE];  // dX w_pre, then scale gate dH
             {
-                const Half w = weight(1);
+                const Half w = weight(std::integral_constant<int, 1>{});
 #pragma unroll
                 for (int i = 0; i < NE; i++) dn[i] = dx.get(i) * w.get(i);
             }
@@ -439,7 +445,7 @@ __global__ __launch_bounds__(MAXT, 4) void norm_residual_grad_kernel(NormGradPar
             const float c_h = s[2] * inv_h * r_h;  // mean(dn n)
             s[0] = s[1] = s[2] = 0.0f;
             {
-                const Half wo = weight(0), ga = weight(2);
+                const Half wo = weight(std::integral_constant<int, 0>{}), ga = weight(std::integral_constant<int, 2>{});
 #pragma unroll
                 for (int k = 0; k < NE / 4; k++) {
                     f32x4 d_post, d_pre;
@@ -479,7 +485,7 @@ __global__ __launch_bounds__(MAXT, 4) void norm_residual_grad_kernel(NormGradPar
                 c_y = s[1] * inv_h;
             }
             {
-                const Half wo = weight(0);
+                const Half wo = weight(std::integral_constant<int, 0>{});
 #pragma unroll
                 for (int i = 0; i < NE; i++) {
                     const float yn = (y.get(i) - mu_y) * r_y;

@@ -808,3 +808,11 @@ def test_rows_past_one_grid_axis():
     for p, q in zip(a, b):
         assert (p[-100:] - q).abs().max() <= 30 * 64 * 2.0 ** -24
         assert (p[:-100] - math.log(V)).abs().max() <= 30 * 4 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("t,s", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)],
+                         ids=["bf16", "f16", "bf16-f32", "f16-f32"])
+@pytest.mark.parametrize("shape", [(9, 4104, 1), (520, 5120, 2), (6, 6143, 3), (300, 6144, 1), (3, 6145, 1),
+                                   (7, 4097, 7)], ids=str)
+def test_norm_residual_wide(shape, t, s):
+    test_norm_residual(shape, t, s)
