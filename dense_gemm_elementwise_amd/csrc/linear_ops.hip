@@ -827,17 +827,20 @@ int plan_xent_grad(const ge_linear_xent_backward_args *a, XentGradPlan &pl)
     if (a->T == 0) return GEMM_EPI_OK;
     Layout lay;
     pl.st = plan_staging2(a->X, a->ldx, a->T, a->W, a->ldw, a->V, a->K, lay);
-    const int64_t limit = std::max(kPieceMin, kPieceBytes / (a->T * 2) / 256 * 256);
+    // a piece is a row of P, at most GE_MAX_COLS long (few rows of X would take longer ones)
+    const int64_t limit =
+        std::min<int64_t>(std::max(kPieceMin, kPieceBytes / (a->T * 2) / 256 * 256), GE_MAX_COLS);
     pl.pieces = (int)ceil_div(a->V, limit);
-    int64_t piece = round_up(ceil_div(a->V, pl.pieces), 256);  // even pieces
-    // columns that make whole rounds of 256 x 256 tiles over the chip
-    int64_t tiles_m = ceil_div(a->T, 256), step = 256 * kCUs;
-    for (; tiles_m % 2 == 0 && step > 256; tiles_m /= 2) step /= 2;
-    if (pl.pieces > 1 && step <= limit) piece = limit / step * step;
-    pl.pieces = (int)ceil_div(a->V, piece);
-    pl.piece = pl.pieces == 1 ? a->V : piece;
+    pl.piece = a->V;
+    if (pl.pieces > 1) {
+        pl.piece = std::min<int64_t>(round_up(ceil_div(a->V, pl.pieces), 256), limit / 256 * 256);  // even pieces
+        // columns that make whole rounds of 256 x 256 tiles over the chip
+        int64_t tiles_m = ceil_div(a->T, 256), step = 256 * kCUs;
+        for (; tiles_m % 2 == 0 && step > 256; tiles_m /= 2) step /= 2;
+        if (step <= limit) pl.piece = limit / step * step;
+        pl.pieces = (int)ceil_div(a->V, pl.piece);
+    }
     pl.pld = round_up(pl.piece, 8);
-    if (pl.pld > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
     const int64_t last = a->V - (pl.pieces - 1) * pl.piece;
     pl.p = plan_product(a->T, pl.piece, a->K, kSquareTiles, 0);
     pl.grad = plan_grad(a->T, pl.piece, a->K, a->dX, a->dW);

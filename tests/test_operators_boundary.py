@@ -210,6 +210,17 @@ def test_workspace_sizes():
     assert rc == 0 and b < 1.5 * a                # nor does the workspace grow with the vocabulary
 
 
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 31, 32, 33, 64])
+@pytest.mark.parametrize("V", [2096897, 2097000, 2097001, 3000000, 2 ** 31 - 257])
+def test_xent_gradient_takes_every_vocabulary_of_the_forward(T, V):
+    """A small batch would fit more columns in one piece than a row may have."""
+    assert XENT.workspace(T=T, V=V)[0] == 0
+    rc, need = XENT_B.workspace(T=T, V=V)
+    assert rc == 0
+    # one piece of P, and no more than that grows with the vocabulary
+    assert need < T * 2097000 * 2 + (256 << 20)
+
+
 def test_python_refusals():
     x, w = torch.zeros(4, 8, dtype=torch.float16), torch.zeros(6, 8, dtype=torch.float16)
     with pytest.raises(ValueError, match="GPU device"):

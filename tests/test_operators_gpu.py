@@ -816,3 +816,37 @@ def test_rows_past_one_grid_axis():
                                    (7, 4097, 7)], ids=str)
 def test_norm_residual_wide(shape, t, s):
     test_norm_residual(shape, t, s)
+
+
+# ---- long vocabularies, long batches ----------------------------------------------
+@pytest.mark.parametrize("T", [1, 9, 17])
+def test_xent_few_rows_several_pieces(T):
+    """Few rows over a vocabulary longer than a row of P may be: two pieces, the second one short."""
+    log(f"[xent few rows, pieces] T={T}")
+    g = gen(34 + T)
+    V, K = 2100011, 8
+    x, w = rnd(g, T, K), rnd(g, V, K, std=0.7).abs()  # (weights of one sign: a piece left out of dX would show)
+    target = torch.randint(0, V, (T,), generator=g)
+    target[0] = V - 1
+    if T > 2:
+        target[1], target[2] = 0, IGNORE
+    target, dloss = target.to(DEV), torch.linspace(0.25, 1.0, T, device=DEV)
+    loss, lse = ge.linear_xent(x, w, target)
+    dx, dw = ge.linear_xent_backward(dloss, x, w, target, lse)
+    x64, w64 = x.double(), w.double()
+    logits = x64 @ w64.t()
+    be = (K + 2) * E24 * (x64.abs() @ w64.abs().t())
+    want = torch.logsumexp(logits, 1)
+    # of lse: a logit's error, and under 400 joins of partial sums of 3 roundings each
+    bl = be.amax(1) + 1200 * E24 + want.abs() * 2.0 ** -23
+    close("lse", lse, want, bl)
+    live = target != IGNORE
+    at = torch.where(live, target, 0)[:, None]
+    scale = torch.where(live, dloss.double(), 0.0)[:, None]
+    p = torch.exp(logits - want[:, None]) * scale
+    ep = p * (be + bl[:, None] + 2e-6 * (1 + (logits - want[:, None]).abs()))
+    P = p.scatter_add_(1, at, -scale)
+    ep = ep + (u(BF16) + 4 * E24) * P.abs()
+    # fp32 sums over V entries: their roundings have either sign, 8 standard deviations
+    close("dX", dx, P @ w64, ep @ w64 + 8 * math.sqrt(V) * E24 * (P.abs() @ w64))
+    close("dW", dw, P.t() @ x64, ep.t() @ x64.abs() + (T + 9) * E24 * (P.abs().t() @ x64.abs()))
