@@ -565,7 +565,8 @@ int check_linear_grad(const ge_linear_backward_args *a)
     if (!a) return GEMM_EPI_ERR_NULL_INPUT;
     GE_CHECK(check_dims(a->M, a->N, a->K));
     if (a->N > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
-    if (!a->dX && !a->dW && !a->dbias) return GEMM_EPI_ERR_NULL_OUTPUT;
+    // (with no rows dX is empty: an allocator gives it no address)
+    if (a->M > 0 && !a->dX && !a->dW && !a->dbias) return GEMM_EPI_ERR_NULL_OUTPUT;
     if (a->act < GE_ACT_IDENTITY || a->act > GE_ACT_SILU) return GEMM_EPI_ERR_KIND;
     GE_CHECK(check_dtype(a->dtype));
     if (a->M > 0) {
@@ -810,7 +811,7 @@ int check_xent_grad(const ge_linear_xent_backward_args *a)
 {
     if (!a) return GEMM_EPI_ERR_NULL_INPUT;
     GE_CHECK(check_dims(a->T, a->V, a->K));
-    if (!a->dX && !a->dW) return GEMM_EPI_ERR_NULL_OUTPUT;
+    if (a->T > 0 && !a->dX && !a->dW) return GEMM_EPI_ERR_NULL_OUTPUT;
     if (!a->W || (a->T > 0 && (!a->X || !a->target || !a->lse || !a->dloss))) return GEMM_EPI_ERR_NULL_INPUT;
     GE_CHECK(check_dtype(a->dtype));
     GE_CHECK(check_matrix(a->W, a->ldw, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));

@@ -70,7 +70,7 @@ typedef struct {
  * may be NULL, for the identity); dX (M, K), dW (N, K), dbias (N) fp32, each
  * NULL where it is not wanted.  dZ is rounded to the element type as an operand
  * of the two products (dbias sums it unrounded).  With M = 0, dW and dbias
- * are set to zero. */
+ * are set to zero, and all three may be NULL (an empty dX has no address). */
 typedef struct {
     int64_t M, N, K;
     const void *dD;
@@ -115,7 +115,9 @@ typedef struct {
 /* dloss (T) fp32, lse (T) from ge_linear_xent; dX (T, K), dW (V, K), each NULL
  * where it is not wanted.  P = (exp(logit - lse) - [v == target]) dloss, zero in
  * ignored rows, is formed one piece of the vocabulary at a time and rounded to
- * the element type as an operand (scaled into fp16's range).  A row whose target is out of range makes its gradients NaN. */
+ * the element type as an operand (scaled into fp16's range).  A row whose
+ * target is out of range makes its gradients NaN.  With T = 0, dW is set to
+ * zero, and both may be NULL. */
 typedef struct {
     int64_t T, V, K;
     const float *dloss;

@@ -221,6 +221,16 @@ def test_xent_gradient_takes_every_vocabulary_of_the_forward(T, V):
     assert need < T * 2097000 * 2 + (256 << 20)
 
 
+def test_empty_batch_needs_no_output_address():
+    """An empty dX has no memory: with no rows, its address may be NULL and the only output."""
+    assert LINEAR_B.run(M=0, dX=0, dW=0, dbias=0) == 0
+    assert LINEAR_B.workspace(M=0, dX=0, dW=0, dbias=0) == (0, 0)
+    assert XENT_B.run(T=0, dX=0, dW=0) == 0
+    assert XENT_B.workspace(T=0, dX=0, dW=0) == (0, 0)
+    assert LINEAR.run(M=0, X=0, D=0, residual=0, Z=0) == 0
+    assert XENT.run(T=0, X=0, target=0, loss=0, lse=0) == 0
+
+
 def test_python_refusals():
     x, w = torch.zeros(4, 8, dtype=torch.float16), torch.zeros(6, 8, dtype=torch.float16)
     with pytest.raises(ValueError, match="GPU device"):

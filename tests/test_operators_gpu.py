@@ -850,3 +850,20 @@ def test_xent_few_rows_several_pieces(T):
     # fp32 sums over V entries: their roundings have either sign, 8 standard deviations
     close("dX", dx, P @ w64, ep @ w64 + 8 * math.sqrt(V) * E24 * (P.abs() @ w64))
     close("dW", dw, P.t() @ x64, ep.t() @ x64.abs() + (T + 9) * E24 * (P.abs().t() @ x64.abs()))
+
+
+def test_empty_batches_one_gradient():
+    """Each gradient of an empty batch alone: an empty dX, zeros for the rest."""
+    log("[empty, one gradient]")
+    x, w = torch.empty(0, 64, dtype=BF16, device=DEV), torch.ones(48, 64, dtype=BF16, device=DEV)
+    d, t = torch.empty(0, 48, dtype=BF16, device=DEV), torch.empty(0, dtype=torch.int64, device=DEV)
+    f = torch.empty(0, device=DEV)
+    for act in ("identity", "gelu"):
+        for need in ((1, 0, 0), (0, 1, 0), (0, 0, 1)):
+            got = ge.linear_backward(d, x, w, d, act=act, need_dx=need[0], need_dw=need[1], need_dbias=need[2])
+            for o, n, shape in zip(got, need, ((0, 64), (48, 64), (48,))):
+                assert (o is not None and o.shape == shape and (o == 0).all()) if n else o is None
+    dx, dw = ge.linear_xent_backward(f, x, w, t, f, need_dw=False)
+    assert dx.shape == (0, 64) and dw is None
+    dx, dw = ge.linear_xent_backward(f, x, w, t, f, need_dx=False)
+    assert dx is None and (dw == 0).all()
