@@ -65,7 +65,8 @@ __global__ __launch_bounds__(256, 8) void row_dot_kernel(SkinnyParams p)
     const int mine = lane < p.M ? lane : 0;  // lanes 0 .. M-1 finish one row of X each
     const int64_t target = XENT ? p.target[mine] : 0;
     float top = -__builtin_inff(), sum = 0.0f;
-    for (int n = blockIdx.x * 4 + wave; n < p.N; n += gridDim.x * 4) {
+    // (unsigned: the step past the last row of a vocabulary near 2^31 leaves int)
+    for (uint32_t n = blockIdx.x * 4 + wave; n < (uint32_t)p.N; n += gridDim.x * 4) {
         const _Float16 *w = p.W + (int64_t)n * p.ldw;
         float bias = 0.0f, res = 0.0f;
         if constexpr (!XENT) {
