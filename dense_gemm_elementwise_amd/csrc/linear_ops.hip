@@ -184,7 +184,7 @@ bool product_fits(const ProductPlan &pl)
     return (int64_t)pl.tiles_m * pl.tiles_n * pl.splits < 1 << 24;
 }
 
-// The grid of a kernel that takes its row from block_row.
+// The grid of a kernel that takes its row, or its block of columns, from block_row.
 dim3 row_grid(int64_t rows)
 {
     return dim3((unsigned)std::min(rows, kRowGrid), (unsigned)ceil_div(rows, kRowGrid));
@@ -420,8 +420,8 @@ hipError_t launch_skinny(const SkinnyParams &q, hipStream_t s)
     const dim3 b(256);
     if constexpr (MODE != SK_LINEAR)
         if (skinny_cols(q.N) == 64)
-            return launch(skinny_kernel<BF, MODE, ACT, false>, dim3((unsigned)ceil_div(q.N, 64)), b, s, q);
-    return launch(skinny_kernel<BF, MODE, ACT, true>, dim3((unsigned)ceil_div(q.N, 16)), b, s, q);
+            return launch(skinny_kernel<BF, MODE, ACT, false>, row_grid(ceil_div(q.N, 64)), b, s, q);
+    return launch(skinny_kernel<BF, MODE, ACT, true>, row_grid(ceil_div(q.N, 16)), b, s, q);
 }
 
 template <bool BF, bool XENT, int ACT>

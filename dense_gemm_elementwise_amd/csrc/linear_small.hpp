@@ -11,6 +11,12 @@
 
 namespace gemm_epi {
 
+// Workgroups of one row (or one block of columns) each: a launch holds fewer
+// than 2^32 threads along x, so past 2^21 rows (1024 threads each at most) the
+// rows go on along y.
+constexpr int64_t kRowGrid = 1 << 21;
+__device__ __forceinline__ int64_t block_row() { return (int64_t)blockIdx.y * kRowGrid + blockIdx.x; }
+
 // ---------------------------------------------------------------------------
 // Products with at most 16 rows of X (single tokens, small batches of them):
 // bound by reading W once.  No LDS on the way in, 16-byte loads at any
@@ -38,9 +44,9 @@ struct SkinnyParams {
 };
 
 // Joins the four waves' running (maximum, sum) of M rows and leaves them in the
-// workgroup's column of the partial statistics; red: [2][4][MX].
+// workgroup's column (`part`) of the partial statistics; red: [2][4][MX].
 template <int MX>
-__device__ __forceinline__ void xent_part(float *red, int M, float *part_max, float *part_sum, int nparts)
+__device__ __forceinline__ void xent_part(float *red, int M, float *part_max, float *part_sum, int nparts, int part)
 {
     __syncthreads();
     const int tid = threadIdx.x;
@@ -48,7 +54,7 @@ __device__ __forceinline__ void xent_part(float *red, int M, float *part_max, fl
     float m = red[tid], s = red[4 * MX + tid];
 #pragma unroll
     for (int u = 1; u < 4; u++) softmax_join(m, s, red[u * MX + tid], red[4 * MX + u * MX + tid]);
-    const int64_t o = (int64_t)tid * nparts + blockIdx.x;
+    const int64_t o = (int64_t)tid * nparts + part;
     part_max[o] = m;
     part_sum[o] = s;
 }
@@ -122,7 +128,7 @@ __global__ __launch_bounds__(256, 8) void row_dot_kernel(SkinnyParams p)
             red[wave * MX + lane] = top;
             red[4 * MX + wave * MX + lane] = sum;
         }
-        xent_part<MX>(red, p.M, p.part_max, p.part_sum, p.nparts);
+        xent_part<MX>(red, p.M, p.part_max, p.part_sum, p.nparts, blockIdx.x);
     }
 }
 
@@ -146,7 +152,9 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
     __shared__ float red[SPLIT ? 4 * 256 : 2 * 4 * 16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int li = lane & 15, lg = lane >> 4;
-    const int n0 = SPLIT ? blockIdx.x * 16 : blockIdx.x * 64 + wave * 16;
+    const int block = (int)block_row();
+    if (block >= (p.N + (SPLIT ? 15 : 63)) / (SPLIT ? 16 : 64)) return;  // (the grid's last row of blocks)
+    const int n0 = SPLIT ? block * 16 : block * 64 + wave * 16;
     const _Float16 *w = p.W + (int64_t)min(n0 + li, p.N - 1) * p.ldw + lg * 8;
     const _Float16 *x = p.X + (int64_t)min(li, p.M - 1) * p.ldx + lg * 8;
     const int step = SPLIT ? 4 * SPAN : SPAN;
@@ -243,8 +251,8 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
         s += __shfl_xor(s, 32);
         if constexpr (SPLIT) {
             if (lg == 0 && li < p.M) {
-                p.part_max[(int64_t)li * p.nparts + blockIdx.x] = m;
-                p.part_sum[(int64_t)li * p.nparts + blockIdx.x] = s;
+                p.part_max[(int64_t)li * p.nparts + block] = m;
+                p.part_sum[(int64_t)li * p.nparts + block] = s;
             }
             return;
         }
@@ -252,7 +260,7 @@ __global__ __launch_bounds__(256) void skinny_kernel(SkinnyParams p)
             red[wave * 16 + li] = m;
             red[64 + wave * 16 + li] = s;
         }
-        xent_part<16>(red, p.M, p.part_max, p.part_sum, p.nparts);
+        xent_part<16>(red, p.M, p.part_max, p.part_sum, p.nparts, block);
     }
 }
 
@@ -488,11 +496,6 @@ __global__ __launch_bounds__(256) void zero_rows_kernel(char *dst, int64_t ld_by
 // ---------------------------------------------------------------------------
 // Cross entropy, the row passes.
 // ---------------------------------------------------------------------------
-// Workgroups of one row each: a launch holds fewer than 2^32 threads along x,
-// so past 2^21 rows (1024 threads each at most) the rows go on along y.
-constexpr int64_t kRowGrid = 1 << 21;
-__device__ __forceinline__ int64_t block_row() { return (int64_t)blockIdx.y * kRowGrid + blockIdx.x; }
-
 // Joins the column tiles' (maximum, sum) pairs of one row per block.
 __global__ __launch_bounds__(256) void xent_loss_kernel(int64_t T, const float *part_max, const float *part_sum,
                                                         int nparts, const float *tlogit, const int64_t *target,

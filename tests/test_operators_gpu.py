@@ -872,23 +872,23 @@ def test_empty_batches_one_gradient():
 LONGEST = 2 ** 31 - 257  # the longest vocabulary and batch that the calls take
 
 
-def longest_vocabulary(T, V=LONGEST):
+def longest_vocabulary(T, V=LONGEST, std=8.0, joins=1000):
     """Loss and lse of T rows over V columns of K = 1; all but 64 logits are 0."""
     g = gen(35 + T)
     x = rnd(g, T, 1)
     w = torch.zeros(V, 1, dtype=BF16, device=DEV)
     some = torch.cat([torch.arange(32), torch.arange(V - 32, V)]).to(DEV)
-    w[some] = rnd(g, 64, 1, std=8.0)
-    target = some[torch.arange(T, device=DEV) * 7 + 31]  # from both ends
+    w[some] = rnd(g, 64, 1, std=std)
+    at = (torch.arange(T, device=DEV) * 7 + 31) % 64  # targets from both ends
+    target = some[at]
     loss, lse = ge.linear_xent(x, w, target)
     logits = x.double() @ w[some].double().t()
     rest = torch.full((T, 1), math.log(V - 64), dtype=torch.float64, device=DEV)
     want = torch.logsumexp(torch.cat([logits, rest], 1), 1)
-    # sums of ones are exact up to 2^24; a wave's 2^18 rows, the 64 others and under
-    # 1000 joins of partial sums leave that many roundings, 3 each
-    b = 3000 * E24 + want.abs() * 2.0 ** -22
+    # sums of ones are exact up to 2^24 (a wave's 2^18 rows); every join of partial sums
+    # leaves 3 roundings
+    b = 3 * joins * E24 + want.abs() * 2.0 ** -22
     close("lse", lse, want, b)
-    at = torch.arange(T, device=DEV) * 7 + 31
     close("loss", loss, want - logits.gather(1, at[:, None])[:, 0], b + 2 * E24 * logits.abs().amax(1))
 
 
@@ -896,3 +896,11 @@ def longest_vocabulary(T, V=LONGEST):
 def test_xent_longest_vocabulary_row_dot(T):
     log(f"[longest vocabulary] T={T}")
     longest_vocabulary(T)
+
+
+@pytest.mark.parametrize("T,V", [(3, LONGEST), (16, LONGEST), (3, (1 << 30) + 64), (3, (1 << 27) + 1)])
+def test_xent_longest_vocabulary_skinny(T, V):
+    """Blocks of 64 columns past one grid axis (2^21 of them) and past 2^32 threads (2^24)."""
+    log(f"[longest vocabulary] T={T} V={V}")
+    # 256 threads join the V / 64 partial sums of a row
+    longest_vocabulary(T, V, std=1.0, joins=1000 + V // 2 ** 14)
