@@ -323,7 +323,8 @@ __global__ __launch_bounds__(256) void dz_kernel(DzParams p)
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int c = cb * 256 + tx * 8;
     const int n = p.N - c;  // columns that exist from c on
-    const int r0 = strip * p.rows_per_strip, r1 = min(p.M, r0 + p.rows_per_strip);
+    // (the strip's length before the end: r0 + rows_per_strip may pass 2^31)
+    const int r0 = strip * p.rows_per_strip, r1 = r0 + min(p.M - r0, p.rows_per_strip);
     float sum[8] = {};
     if (c < p.N8) {
         auto one = [&](int m, half8 d, half8 z) {

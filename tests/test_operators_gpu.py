@@ -904,3 +904,18 @@ def test_xent_longest_vocabulary_skinny(T, V):
     log(f"[longest vocabulary] T={T} V={V}")
     # 256 threads join the V / 64 partial sums of a row
     longest_vocabulary(T, V, std=1.0, joins=1000 + V // 2 ** 14)
+
+
+def test_linear_backward_longest_batch_dbias():
+    """The last strip of rows ends past 2^31 before it is cut to the batch."""
+    log("[longest batch] dbias")
+    g = gen(36)
+    M, N, K = LONGEST, 8, 1
+    dd = torch.zeros(M, N, dtype=BF16, device=DEV)  # 34 GB
+    some = torch.tensor([0, 1, 1 << 30, M - (1 << 20), M - 4096, M - 2, M - 1], device=DEV)
+    dd[some] = rnd(g, len(some), N)
+    x = torch.zeros(M, K, dtype=BF16, device=DEV)
+    w = torch.zeros(N, K, dtype=BF16, device=DEV)
+    _, _, db = ge.linear_backward(dd, x, w, need_dx=False, need_dw=False)
+    v = dd[some].double()
+    close("dbias", db, v.sum(0), len(some) * E24 * v.abs().sum(0))  # (zeros add no rounding)
