@@ -369,7 +369,8 @@ __global__ __launch_bounds__(MAXT, 4) void norm_residual_grad_kernel(NormGradPar
 #pragma unroll
         for (int i = 0; i < NE; i++) a_post[i] = a_pre[i] = 0.0f;
     }
-    const int u0 = (int)blockIdx.x * p.runs_per_block, u1 = min(p.runs, u0 + p.runs_per_block);
+    // (the block's share before the end: u0 + runs_per_block may pass 2^31)
+    const int u0 = (int)blockIdx.x * p.runs_per_block, u1 = u0 + min(p.runs - u0, p.runs_per_block);
     for (int run = u0; run < u1; run++) {
         // (the quotient of two scalars is computed in vector registers: without
         // the readfirstlane every row address would live there too)

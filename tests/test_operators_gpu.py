@@ -919,3 +919,21 @@ def test_linear_backward_longest_batch_dbias():
     _, _, db = ge.linear_backward(dd, x, w, need_dx=False, need_dw=False)
     v = dd[some].double()
     close("dbias", db, v.sum(0), len(some) * E24 * v.abs().sum(0))  # (zeros add no rounding)
+
+
+def test_norm_gradient_longest_batch_of_gates():
+    """A gate row for each of 2^31 - 1 rows: the last workgroup's share ends past 2^31 before it is cut."""
+    log("[longest batch] norm gates")
+    g = gen(37)
+    T, H = 2 ** 31 - 1, 1
+    some = torch.tensor([0, 1, 1 << 21, 1 << 30, T - (1 << 21), T - 12345, T - 2, T - 1], device=DEV)
+    dx, dh, h, y, gate = (torch.zeros(T, H, dtype=F16, device=DEV) for _ in range(5))
+    for t in (dx, dh, h, y, gate):
+        t[some] = rnd(g, len(some), H, t=F16)
+    kw = dict(scale=0.7, post="none", pre="rms")
+    a = ge.norm_residual_backward(dx, dh, h, y, gate=gate, **kw)
+    b = ge.norm_residual_backward(dx[some], dh[some], h[some], y[some], gate=gate[some], **kw)
+    for i in (0, 1, 4):
+        assert torch.equal(a[i][some], b[i]), i
+        a[i][some] = 0
+        assert a[i].count_nonzero() == 0, i
