@@ -835,7 +835,8 @@ __device__ __forceinline__ void lin_tile(const LinParams &p, int block, int bloc
     const int gm = min(p.tiles_m - first, p.group_m), rr = t - g * full;
     const int tm = first + rr % gm, tn = rr / gm;
     const int m0 = tm * BM, n0 = tn * BN;
-    const int kb = split * p.k_split, k_end = min(p.K, kb + p.k_split);
+    // (the split's length before the end: kb + k_split may pass 2^31)
+    const int kb = split * p.k_split, k_end = kb + min(p.K - kb, p.k_split);
 
     f32x4 acc[BM / 32][BN / 32];
 #pragma unroll

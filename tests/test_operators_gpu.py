@@ -937,3 +937,16 @@ def test_norm_gradient_longest_batch_of_gates():
         assert torch.equal(a[i][some], b[i]), i
         a[i][some] = 0
         assert a[i].count_nonzero() == 0, i
+
+
+def test_linear_backward_longest_batch_dw():
+    """The contraction's last part ends past 2^31 before it is cut to the batch."""
+    log("[longest batch] dW")
+    g = gen(38)
+    M, N, K = LONGEST, 8, 8
+    some = torch.tensor([0, 1, 1 << 30, M - (1 << 20), M - 4096, M - 2, M - 1], device=DEV)
+    dd, x = (torch.zeros(M, 8, dtype=BF16, device=DEV) for _ in range(2))  # 34 GB each
+    dd[some], x[some] = rnd(g, len(some), N), rnd(g, len(some), K)
+    _, dw, _ = ge.linear_backward(dd, x, torch.zeros(N, K, dtype=BF16, device=DEV), need_dx=False, need_dbias=False)
+    d64, x64 = dd[some].double(), x[some].double()
+    close("dW", dw, d64.t() @ x64, len(some) * E24 * (d64.abs().t() @ x64.abs()))  # (zeros add no rounding)
