@@ -179,10 +179,9 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsign
 }
 
 // a launch holds fewer than 2^32 threads: 2^24 workgroups of 256
-bool product_fits(const ProductPlan &pl)
-{
-    return (int64_t)pl.tiles_m * pl.tiles_n * pl.splits < 1 << 24;
-}
+constexpr int64_t kMaxGroups = (1 << 24) - 1;
+int64_t product_groups(const ProductPlan &pl) { return (int64_t)pl.tiles_m * pl.tiles_n * pl.splits; }
+bool product_fits(const ProductPlan &pl) { return product_groups(pl) <= kMaxGroups; }
 
 // The grid of a kernel that takes its row, or its block of columns, from block_row.
 dim3 row_grid(int64_t rows)
@@ -368,11 +367,11 @@ GradPlan plan_grad(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw)
         // has the same bits whether or not the other one is wanted (the tile does
         // not change them, the order of the sum along K does).
         const bool same = x.k_split == g.dx.k_split && w.k_split == g.dw.k_split;
-        const double groups = (double)x.tiles_m * x.tiles_n * x.splits + (double)w.tiles_m * w.tiles_n * w.splits;
-        const double beside = std::min(1.0, std::max(0.0, (groups - kCUs) / (2.0 * kCUs)));
+        const int64_t groups = product_groups(x) + product_groups(w);
+        const double beside = std::min(1.0, std::max(0.0, (double)(groups - kCUs) / (2.0 * kCUs)));
         const double pair =
             std::max(x.cost, w.cost) + beside * std::min(x.cost, w.cost) - (beside == 1.0 ? 5.0 : 0.0);
-        if (same && pair < g.dx.cost + g.dw.cost) {
+        if (same && groups <= kMaxGroups && pair < g.dx.cost + g.dw.cost) {
             g.pair = true;
             g.dx = x;
             g.dw = w;

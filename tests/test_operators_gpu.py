@@ -950,3 +950,24 @@ def test_linear_backward_longest_batch_dw():
     _, dw, _ = ge.linear_backward(dd, x, torch.zeros(N, K, dtype=BF16, device=DEV), need_dx=False, need_dbias=False)
     d64, x64 = dd[some].double(), x[some].double()
     close("dW", dw, d64.t() @ x64, len(some) * E24 * (d64.abs().t() @ x64.abs()))  # (zeros add no rounding)
+
+
+def test_linear_backward_longest_batch():
+    """All three gradients of 2^31 - 257 rows: the two products together have more workgroups than
+    one launch takes."""
+    log("[longest batch] linear_backward")
+    g = gen(38)
+    M, N, K = LONGEST, 8, 8
+    some = torch.tensor([0, 1, 1 << 30, M - (1 << 20), M - 4096, M - 2, M - 1], device=DEV)
+    dd, x = (torch.zeros(M, 8, dtype=BF16, device=DEV) for _ in range(2))  # 34 GB each
+    dd[some], x[some] = rnd(g, len(some), N), rnd(g, len(some), K)
+    w = rnd(g, N, K)
+    dx, dw, db = ge.linear_backward(dd, x, w)
+    d64, x64, w64 = dd[some].double(), x[some].double(), w.double()
+    n = len(some)  # (zeros add no rounding)
+    close("dX", dx[some], d64 @ w64, (N + 2) * E24 * (d64.abs() @ w64.abs()))
+    close("dW", dw, d64.t() @ x64, n * E24 * (d64.abs().t() @ x64.abs()))
+    close("dbias", db, d64.sum(0), n * E24 * d64.abs().sum(0))
+    dx[some] = 0
+    for part in dx.split(1 << 28):
+        assert part.count_nonzero() == 0
