@@ -143,14 +143,20 @@ double product_cost(int64_t M, int64_t N, int64_t K, int tile, int splits)
     return us;
 }
 
+// a launch holds fewer than 2^32 threads: 2^24 workgroups of 256
+constexpr int64_t kMaxGroups = (1 << 24) - 1;
+int64_t product_groups(const ProductPlan &pl) { return (int64_t)pl.tiles_m * pl.tiles_n * pl.splits; }
+bool product_fits(const ProductPlan &pl) { return product_groups(pl) <= kMaxGroups; }
+
 // tiles: bit mask of the tiles that exist for this product, split_tiles: of
 // those whose split form exists; small: the best plan on the 128 x 128 tile, if
-// it is wanted too
+// it is wanted too.  Of the tiles whose grid one launch holds the cheapest (a
+// larger tile where a smaller one would be too many); where none is, the plan does
+// not pass product_fits.
 ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsigned split_tiles,
                          ProductPlan *small = nullptr)
 {
     ProductPlan best;
-    best.cost = 1e300;
     for (int i = 0; i < 4; i++) {
         if (!(tiles >> i & 1)) continue;
         const LinTile t = kLinTiles[i];
@@ -173,15 +179,11 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, unsigned tiles, unsign
         }
         of_tile.part_bytes = of_tile.splits > 1 ? of_tile.splits * M * round_up(N, 8) * 4 : 0;
         if (small && i == kLinSmall) *small = of_tile;
-        if (of_tile.cost < best.cost) best = of_tile;
+        const bool fits = product_fits(of_tile), best_fits = best.tiles_m > 0 && product_fits(best);
+        if (best.tiles_m == 0 || (fits == best_fits ? of_tile.cost < best.cost : fits)) best = of_tile;
     }
     return best;
 }
-
-// a launch holds fewer than 2^32 threads: 2^24 workgroups of 256
-constexpr int64_t kMaxGroups = (1 << 24) - 1;
-int64_t product_groups(const ProductPlan &pl) { return (int64_t)pl.tiles_m * pl.tiles_n * pl.splits; }
-bool product_fits(const ProductPlan &pl) { return product_groups(pl) <= kMaxGroups; }
 
 // The grid of a kernel that takes its row, or its block of columns, from block_row.
 dim3 row_grid(int64_t rows)

@@ -38,8 +38,10 @@ extern "C" {
 typedef enum { GE_ACT_IDENTITY = 0, GE_ACT_RELU = 1, GE_ACT_GELU = 2, GE_ACT_SILU = 3 } ge_act;
 typedef enum { GE_NORM_NONE = 0, GE_NORM_RMS = 1, GE_NORM_LAYER = 2 } ge_norm;
 
-/* Row strides and row lengths (N, K) are at most GE_MAX_COLS, M, T and V below
- * 2^31; hidden is at most GE_MAX_HIDDEN, and GE_MAX_HIDDEN_GRAD in the gradient. */
+/* Row strides and row lengths (N, K) are at most GE_MAX_COLS, M, T and V at most
+ * 2^31 - 257 (2^31 - 1 rows in the norms); hidden is at most GE_MAX_HIDDEN, and
+ * GE_MAX_HIDDEN_GRAD in the gradient.  A product of more than 16 rows has fewer
+ * than 2^24 tiles of 256 x 256; one past that is refused with the shape status. */
 #define GE_MAX_COLS 2097000
 #define GE_MAX_HIDDEN 16384
 #define GE_MAX_HIDDEN_GRAD 8192

@@ -231,6 +231,22 @@ def test_empty_batch_needs_no_output_address():
     assert XENT.run(T=0, X=0, target=0, loss=0, lse=0) == 0
 
 
+@pytest.mark.parametrize("T", [1, 3, 16, 17, 128, 129, 256, 257, 512])
+def test_longest_vocabulary_is_taken(T):
+    """Up to 2^24 tiles of 256 x 256, whichever tile would be the fastest."""
+    V = 2 ** 31 - 257
+    assert XENT.workspace(T=T, V=V, K=8, ldx=8, ldw=8)[0] == 0
+    assert XENT.workspace(T=V, V=T, K=8, ldx=8, ldw=8)[0] == 0
+    assert LINEAR_B.workspace(M=V, N=min(T, 256), K=8, ldx=8, ldw=8, lddd=1024, ldz=1024, lddx=8, lddw=8)[0] == 0
+
+
+def test_products_past_a_launch_are_refused():
+    assert XENT.workspace(T=513, V=2 ** 31 - 257, K=8, ldx=8, ldw=8)[0] == 1
+    assert XENT.workspace(T=2 ** 20, V=2 ** 20 - 256, K=8, ldx=8, ldw=8)[0] == 0
+    assert XENT.workspace(T=2 ** 20, V=2 ** 20, K=8, ldx=8, ldw=8)[0] == 1
+    assert LINEAR.workspace(M=2 ** 31 - 257, N=1024, ldr=1024, ldd=1024, ldz=1024)[0] == 1
+
+
 def test_python_refusals():
     x, w = torch.zeros(4, 8, dtype=torch.float16), torch.zeros(6, 8, dtype=torch.float16)
     with pytest.raises(ValueError, match="GPU device"):

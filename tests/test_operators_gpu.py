@@ -971,3 +971,11 @@ def test_linear_backward_longest_batch():
     dx[some] = 0
     for part in dx.split(1 << 28):
         assert part.count_nonzero() == 0
+
+
+@pytest.mark.parametrize("T", [17, 256])
+def test_xent_longest_vocabulary_tiles(T):
+    """2^24 tiles of 128 columns, and 256 rows, where only the larger tile is few enough workgroups."""
+    log(f"[longest vocabulary] T={T}")
+    # 256 threads join the V / 128 or V / 256 partial sums of a row
+    longest_vocabulary(T, std=1.0, joins=1000 + LONGEST // 2 ** 15)
