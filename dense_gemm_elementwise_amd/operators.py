@@ -12,7 +12,8 @@ checks and marshals arguments, and allocates outputs and workspaces from
 torch's allocator.  Every call is queued on `stream` (a torch.cuda.Stream;
 default: the current stream of the tensors' device) and returns without
 waiting.  There is no autograd node: the gradients are calls of their own, and
-a tensor that requires grad is refused while gradients are recorded.
+a tensor that requires grad is refused while gradients are recorded, one with
+a forward-mode tangent always.
 
 Matrices are 2-D float16 or bfloat16 GPU tensors with unit stride along the
 rows and any row stride of at least the row's length (a column slice of a wider
@@ -22,6 +23,7 @@ import ctypes
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding
 
@@ -116,10 +118,22 @@ def _queue(name, head, dev, raw_stream, sizes=None):
         _raise(rc)
 
 
+def _refuse_tangents(inputs):
+    """Tangents of forward-mode differentiation would be dropped silently: they
+    are refused, like requires_grad."""
+    for t in inputs:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("an input carries a forward-mode tangent: these calls record no derivative (use "
+                             "torch.autograd.forward_ad.unpack_dual(...).primal)")
+
+
 def _run(call, inputs, dev, stream):
     """Runs call(raw stream) with `dev` current and, if a stream is given, that
     stream current too, so that outputs and workspaces belong to it; the inputs
     are marked as in use there."""
+    # (outside every dual level there are no tangents: one comparison a call)
+    if getattr(forward_ad, "_current_level", 0) >= 0:
+        _refuse_tangents(inputs)
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")

@@ -276,3 +276,16 @@ def test_header_is_plain_c(tmp_path):
     src.write_text(f'#include "linear_ops.h"\n{checks}\nint main(void) {{ return 0; }}\n')
     subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-fsyntax-only", "-I",
                     os.path.join(ROOT, "include"), str(src)], check=True)
+
+
+def test_forward_mode_tangents_are_refused():
+    """A dual tensor's tangent would vanish: no call may take its address."""
+    from torch.autograd import forward_ad
+    x = torch.zeros(4, 8, dtype=torch.float16)
+    calls = []
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        for inputs in ((dual,), (x, None, dual)):
+            with pytest.raises(ValueError, match="tangent"):
+                operators._run(calls.append, inputs, torch.device("cuda:0"), None)
+    assert not calls

@@ -979,3 +979,22 @@ def test_xent_longest_vocabulary_tiles(T):
     log(f"[longest vocabulary] T={T}")
     # 256 threads join the V / 128 or V / 256 partial sums of a row
     longest_vocabulary(T, std=1.0, joins=1000 + LONGEST // 2 ** 15)
+
+
+def test_forward_mode_tangents():
+    """Every call refuses an input with a forward-mode tangent, and takes its primal."""
+    from torch.autograd import forward_ad
+    x, w = torch.ones(4, 8, dtype=F16, device=DEV), torch.ones(8, 8, dtype=F16, device=DEV)
+    t = torch.zeros(4, dtype=torch.int64, device=DEV)
+    f = torch.ones(4, device=DEV)
+    calls = [lambda v: ge.linear(v, w), lambda v: ge.linear(x, w, None, v), lambda v: ge.linear_backward(v, x, w),
+             lambda v: ge.linear_xent(v, w, t), lambda v: ge.linear_xent_backward(f, v, w, t, f),
+             lambda v: ge.norm_residual(x, v), lambda v: ge.norm_residual_backward(x, v, x, x)]
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        for call in calls:
+            with pytest.raises(ValueError, match="tangent"):
+                call(dual)
+            a, b = call(forward_ad.unpack_dual(dual).primal), call(x)
+            for p, q in zip(a, b) if isinstance(a, tuple) else ((a, b),):
+                assert (p is None and q is None) or torch.equal(p, q)
