@@ -998,3 +998,66 @@ def test_forward_mode_tangents():
             a, b = call(forward_ad.unpack_dual(dual).primal), call(x)
             for p, q in zip(a, b) if isinstance(a, tuple) else ((a, b),):
                 assert (p is None and q is None) or torch.equal(p, q)
+
+
+@pytest.mark.parametrize("t,s", [(BF16, BF16), (F16, F16), (BF16, F32), (F16, F32)],
+                         ids=["bf16", "f16", "bf16-f32", "f16-f32"])
+@pytest.mark.parametrize("H", [3, 40, 513, 1000, 2052, 4101, 5000, 6148, 8191])
+def test_norm_gradient_large_means(H, t, s):
+    """Rows whose mean is 20 deviations, of H', of Y and of both: the gradient then takes its sums
+    about the mean in a second pass."""
+    log(f"[norm gradient, means] {H} {t} {s}")
+    T, G, eps = 6, 2, 1e-5
+    for n, (mh, my, post, pre) in enumerate(((40.0, 0.25, "layer", "layer"), (-0.5, -60.0, "layer", "layer"),
+                                             (40.0, -60.0, "layer", "layer"), (-40.0, 60.0, "rms", "layer"),
+                                             (40.0, 60.0, "layer", "rms"), (40.0, 60.0, "none", "layer"))):
+        g = gen(40 + H + n)
+        h, y = rnd(g, T, H, std=2.0, mean=mh, t=s), rnd(g, T, H, std=3.0, mean=my, t=t)
+        h[1], y[2] = h[1] - mh, y[2] - my  # a row without one between the others
+        gate, wi = rnd(g, G, H, std=0.3, mean=0.5, t=t), rnd(g, H, std=0.1, mean=1.0, t=t)
+        wo = rnd(g, H, std=0.1, mean=1.0, t=t) if post != "none" else None
+        dx, dho = rnd(g, T, H, t=t), rnd(g, T, H, t=s)
+        got = ge.norm_residual_backward(dx, dho, h, y, w_post=wo, w_pre=wi, gate=gate, scale=0.7, post=post, pre=pre,
+                                        eps=eps)
+        one = torch.ones(H, dtype=torch.float64)
+        h64, y64, dx64, dho64 = (v.double().cpu() for v in (h, y, dx, dho))
+        g64, wi64 = gate.double().cpu().repeat_interleave(T // G, 0), wi.double().cpu()
+        wo64 = wo.double().cpu() if wo is not None else one
+
+        def normed(v, kind):
+            """(rows, reciprocal scale, error of the rows): the mean is off by at most 24 roundings of the
+            largest element (12 terms a thread, 10 steps across the workgroup), the scale by 4e-6."""
+            if kind == "none":
+                return v, None, v.abs() * E24
+            vn, r, _ = norm64(v, kind, eps)
+            return vn, r, 4e-6 * vn.abs() + r * v.abs().amax(1, keepdim=True) * 24 * E24
+
+        hn, rh, ehn = normed(h64, pre)
+        dn = dx64 * wi64
+        c_h = (dn * hn).mean(1, keepdim=True)
+        m_d = dn.mean(1, keepdim=True) if pre == "layer" else 0.0
+        dh = dho64 + (dn - hn * c_h - m_d) * rh
+        mag = dn.abs() + hn.abs() * (dn * hn).abs().mean(1, keepdim=True) + dn.abs().mean(1, keepdim=True)
+        edh = rh * (1e-5 * mag + ehn * c_h.abs() + hn.abs() * (dn.abs() * ehn).mean(1, keepdim=True)) \
+            + 4 * E24 * dh.abs() + E24 * dho64.abs()
+        close("dH", got[0], dh, edh)
+        yn, ry, eyn = normed(y64, post)
+        dyw = 0.7 * g64 * dh
+        edyw = 0.7 * g64.abs() * edh + 3 * E24 * dyw.abs()
+        d, ed = dyw * wo64, edyw * wo64.abs()
+        dy, edy = dyw, edyw
+        if post != "none":
+            c_y = (d * yn).mean(1, keepdim=True)
+            m_y = d.mean(1, keepdim=True) if post == "layer" else 0.0
+            dy = (d - yn * c_y - m_y) * ry
+            magy = d.abs() + yn.abs() * (d * yn).abs().mean(1, keepdim=True) + d.abs().mean(1, keepdim=True)
+            edy = ry * (1e-5 * magy + ed + ed.mean(1, keepdim=True) + eyn * c_y.abs()
+                        + yn.abs() * (ed * yn.abs() + d.abs() * eyn).mean(1, keepdim=True))
+            close("dw_post", got[2], (dyw * yn).sum(0), (edyw * yn.abs() + dyw.abs() * eyn).sum(0)
+                  + (T + 4) * E24 * (dyw * yn).abs().sum(0))
+        close("dY", got[1], dy, edy)
+        close("dw_pre", got[3], (dx64 * hn).sum(0), (dx64.abs() * ehn).sum(0) + (T + 4) * E24 * (dx64 * hn).abs().sum(0))
+        v = 0.7 * yn * wo64 * dh
+        e = 0.7 * wo64.abs() * (yn.abs() * edh + eyn * dh.abs()) + 4 * E24 * v.abs()
+        close("dgate", got[4], v.view(G, T // G, H).sum(1),
+              e.view(G, T // G, H).sum(1) + (T + 4) * E24 * v.abs().view(G, T // G, H).sum(1))
