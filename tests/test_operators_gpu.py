@@ -1061,3 +1061,27 @@ def test_norm_gradient_large_means(H, t, s):
         e = 0.7 * wo64.abs() * (yn.abs() * edh + eyn * dh.abs()) + 4 * E24 * v.abs()
         close("dgate", got[4], v.view(G, T // G, H).sum(1),
               e.view(G, T // G, H).sum(1) + (T + 4) * E24 * v.abs().view(G, T // G, H).sum(1))
+
+
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("M", [1, 3, 20])
+def test_activation_everywhere(M, act, t):
+    """act(z) at every finite z, through the bias of a product of zeros: each of the three paths."""
+    log(f"[act] M={M} {act} {t}")
+    z = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(t)
+    z = z[z.isfinite()]
+    x, w = torch.zeros(M, 8, dtype=t, device=DEV), torch.zeros(len(z), 8, dtype=t, device=DEV)
+    d, kept = ge.linear(x, w, z.to(DEV), act=act, save_z=True)
+    assert torch.equal(kept, z.to(DEV).expand(M, -1))
+    z64 = z.double()
+    want, a = act64(z64, act), z64.abs()
+    if act == "gelu":
+        # |z| Q(|z|) by a fit to 2e-6, with four roundings and an exponent z^2 / 4 that is off by 3
+        # half units in fp32, twice
+        bound = (4e-6 + 1.5 * E24 * a * a) * 0.5 * a * torch.erfc(a * 0.5 ** 0.5) + 2 * E24 * want.abs()
+    else:
+        # e^-|z| from an exponent |z| / 2 that is off by 2 half units, twice; exponential and
+        # reciprocal to a unit, four roundings
+        bound = (1e-6 + 2 * E24 * a) * want.abs()
+    close(act, d, want.expand(M, -1), bound.nan_to_num(nan=0.0).expand(M, -1))
