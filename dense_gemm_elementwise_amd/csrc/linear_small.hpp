@@ -537,7 +537,11 @@ __global__ __launch_bounds__(256) void xent_loss_kernel(int64_t T, const float *
 // divided by the largest of their magnitudes (fp32) and multiplied by 2^14:
 // |P| stays below 2^14 + 1 < 65504 and a probability down to 2^-28 is still a
 // normal number.  The products' fp32 sums are multiplied by that magnitude
-// times 2^-14 (`alpha`) before their one rounding.  Dividing by the magnitude
+// times 2^-14 (`alpha`) before their one rounding.  There is one factor for all
+// rows, because dW adds them up: in a row whose incoming gradient is r times the
+// largest, fp16 keeps all its digits down to a probability of 2^-28 / r, and
+// entries below are off by at most 2^-39 of the largest incoming gradient (bf16
+// has fp32's range and keeps them).  Dividing by the magnitude
 // itself, not by the power of two below it, keeps the entry at the target, near
 // -1 in a row of the largest gradient, where 16 bits hold it best: a mean over
 // the batch has only such rows, and fp16 gradients of a 333 x 9999 batch came

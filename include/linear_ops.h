@@ -71,7 +71,9 @@ typedef struct {
 /* dD (M, N), X (M, K), W (N, K), Z (M, N) as ge_linear kept it (not read, and
  * may be NULL, for the identity); dX (M, K), dW (N, K), dbias (N) fp32, each
  * NULL where it is not wanted.  dZ is rounded to the element type as an operand
- * of the two products (dbias sums it unrounded).  With M = 0, dW and dbias
+ * of the two products (dbias sums it unrounded); it is not scaled, so in fp16 it has
+ * the range that dD has, less a factor of 1.13 (the largest |act'|): the caller's
+ * loss scale keeps both.  With M = 0, dW and dbias
  * are set to zero, and all three may be NULL (an empty dX has no address). */
 typedef struct {
     int64_t M, N, K;
@@ -117,9 +119,10 @@ typedef struct {
 /* dloss (T) fp32, lse (T) from ge_linear_xent; dX (T, K), dW (V, K), each NULL
  * where it is not wanted.  P = (exp(logit - lse) - [v == target]) dloss, zero in
  * ignored rows, is formed one piece of the vocabulary at a time and rounded to
- * the element type as an operand (scaled into fp16's range).  A row whose
- * target is out of range makes its gradients NaN.  With T = 0, dW is set to
- * zero, and both may be NULL. */
+ * the element type as an operand (fp16: after a common factor for all rows, so that
+ * an entry is off by its rounding and at most 2^-39 of the largest |dloss|).  A
+ * row whose target is out of range makes its gradients NaN.  With T = 0, dW is
+ * set to zero, and both may be NULL. */
 typedef struct {
     int64_t T, V, K;
     const float *dloss;

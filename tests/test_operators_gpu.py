@@ -1085,3 +1085,30 @@ def test_activation_everywhere(M, act, t):
         # reciprocal to a unit, four roundings
         bound = (1e-6 + 2 * E24 * a) * want.abs()
     close(act, d, want.expand(M, -1), bound.nan_to_num(nan=0.0).expand(M, -1))
+
+
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("T", [12, 40])
+def test_xent_gradient_unequal_rows(T, t):
+    """Incoming gradients from 2^12 down to 2^-12 of either sign in one batch: P is held with one
+    factor for all rows."""
+    log(f"[xent unequal rows] T={T} {t}")
+    g = gen(41)
+    V, K = 1003, 64
+    x, w = rnd(g, T, K, t=t), rnd(g, V, K, std=2 * K ** -0.5, t=t)
+    target = torch.randint(0, V, (T,), generator=g).to(DEV)
+    dloss = (torch.tensor([(-1.0) ** i * 2.0 ** (12 - 24 * i / (T - 1)) for i in range(T)])).to(DEV)
+    logits, be, lse, _, _, at = xent_ref(x, w, target)
+    _, got_lse = ge.linear_xent(x, w, target)
+    dx, dw = ge.linear_xent_backward(dloss, x, w, target, got_lse)
+    # of lse: as in test_linear_xent; of P: its logit's, lse's and the exponential's errors, the
+    # rounding to the element type, and in fp16 half the smallest subnormal at 2^14 over the largest
+    bl = be.amax(1) + 1e-5 + lse.abs() * 2.0 ** -23
+    scale = dloss.double().cpu()[:, None]
+    p = torch.exp(logits - lse[:, None])
+    P = (p - torch.zeros_like(p).scatter_(1, at, 1.0)) * scale
+    eP = p * scale.abs() * (be + bl[:, None] + 2e-6 * (1 + (logits - lse[:, None]).abs())) \
+        + (u(t) + 4 * E24) * P.abs() + (2.0 ** -39 * scale.abs().max() if t == F16 else 0.0)
+    x64, w64 = x.double().cpu(), w.double().cpu()
+    close("dX", dx, P @ w64, eP @ w64.abs() + (V + 9) * E24 * (P.abs() @ w64.abs()))
+    close("dW", dw, P.t() @ x64, eP.t() @ x64.abs() + (T + 9) * E24 * (P.abs().t() @ x64.abs()))
