@@ -127,15 +127,15 @@ __device__ __forceinline__ float lin_act(float z)
     }
 }
 
-// act'(z).  The clamps only replace values where the derivative has long
-// reached 0 or 1 (they keep infinity times zero out); a NaN passes through.
+// act'(z) of gelu and silu.  The clamps only replace values where the derivative
+// has long reached 0 or 1 (they keep infinity times zero out); a NaN passes
+// through.
 template <int ACT>
 __device__ __forceinline__ float lin_act_grad(float z)
 {
 #pragma clang fp contract(off)
-    if constexpr (ACT == ACT_RELU) {
-        return z > 0.0f ? 1.0f : 0.0f;
-    } else if constexpr (ACT == ACT_GELU) {
+    static_assert(ACT == ACT_GELU || ACT == ACT_SILU, "the others have no factor");
+    if constexpr (ACT == ACT_GELU) {
         // Phi(z) + z phi(z), phi(z) = e^(-z^2/2) / sqrt(2 pi)
         z = z < -40.0f ? -40.0f : (z > 40.0f ? 40.0f : z);
         float q, h;
@@ -143,12 +143,10 @@ __device__ __forceinline__ float lin_act_grad(float z)
         const float e = h * h;
         const float cdf = z < 0.0f ? q * e : 1.0f - q * e;
         return cdf + z * (0.398942280401432678f * e);
-    } else if constexpr (ACT == ACT_SILU) {
+    } else {
         // s (1 + z (1 - s)), s = sigmoid(z), 1 - s = sigmoid(-z)
         z = z < -200.0f ? -200.0f : (z > 200.0f ? 200.0f : z);
         return act_sigmoid(z) * __builtin_fmaf(z, act_sigmoid(-z), 1.0f);
-    } else {
-        return z != z ? z : 1.0f;
     }
 }
 

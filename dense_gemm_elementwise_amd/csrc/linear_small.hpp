@@ -332,7 +332,12 @@ __global__ __launch_bounds__(256) void dz_kernel(DzParams p)
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 float v = ld16<BF>(d[e]);
-                if constexpr (ACT != ACT_IDENTITY) v *= lin_act_grad<ACT>(ld16<BF>(z[e]));
+                if constexpr (ACT == ACT_RELU)
+                    // a mask: an infinity or a NaN that arrives at z <= 0 does not
+                    // pass either; a NaN z, which the forward keeps, lets dD pass
+                    v = ld16<BF>(z[e]) <= 0.0f ? 0.0f : v;
+                else if constexpr (ACT != ACT_IDENTITY)
+                    v *= lin_act_grad<ACT>(ld16<BF>(z[e]));
                 if (e >= n) v = 0.0f;
                 sum[e] += v;
                 o[e] = st16<BF>(v);

@@ -69,12 +69,13 @@ typedef struct {
 } ge_linear_args;
 
 /* dD (M, N), X (M, K), W (N, K), Z (M, N) as ge_linear kept it (not read, and
- * may be NULL, for the identity); dX (M, K), dW (N, K), dbias (N) fp32, each
- * NULL where it is not wanted.  dZ is rounded to the element type as an operand
- * of the two products (dbias sums it unrounded); it is not scaled, so in fp16 it has
- * the range that dD has, less a factor of 1.13 (the largest |act'|): the caller's
- * loss scale keeps both.  With M = 0, dW and dbias
- * are set to zero, and all three may be NULL (an empty dX has no address). */
+ * may be NULL, for the identity; relu masks: dD where Z <= 0 does not count,
+ * whatever it is); dX (M, K), dW (N, K), dbias (N) fp32, each NULL where it is
+ * not wanted.  dZ is rounded to the element type as an operand of the two
+ * products (dbias sums it unrounded); it is not scaled, so in fp16 it has the
+ * range that dD has, less a factor of 1.13 (the largest |act'|): the caller's
+ * loss scale keeps both.  With M = 0, dW and dbias are set to zero, and all three
+ * may be NULL (an empty dX has no address). */
 typedef struct {
     int64_t M, N, K;
     const void *dD;

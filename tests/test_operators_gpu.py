@@ -1112,3 +1112,29 @@ def test_xent_gradient_unequal_rows(T, t):
     x64, w64 = x.double().cpu(), w.double().cpu()
     close("dX", dx, P @ w64, eP @ w64.abs() + (V + 9) * E24 * (P.abs() @ w64.abs()))
     close("dW", dw, P.t() @ x64, eP.t() @ x64.abs() + (T + 9) * E24 * (P.abs().t() @ x64.abs()))
+
+
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+def test_relu_gradient_masks(t):
+    """What arrives where relu is 0 does not pass, an infinity or a NaN neither; a NaN z, which the
+    forward keeps, does not count as masked."""
+    log(f"[relu masks] {t}")
+    g = gen(42)
+    M, N, K = 40, 24, 16
+    x, w, dd = rnd(g, M, K, t=t), rnd(g, N, K, t=t), rnd(g, M, N, t=t)
+    z = rnd(g, M, N, t=t)
+    z[3, 5], z[4, 6], z[5, 7] = -1.0, 0.0, -0.5
+    want = ge.linear_backward(torch.where(z > 0, dd, 0.0), x, w)  # the identity's
+    dd[3, 5], dd[4, 6], dd[5, 7] = float("inf"), float("nan"), float("-inf")
+    got = ge.linear_backward(dd, x, w, z, act="relu")
+    for p, q in zip(got, want):
+        assert q.isfinite().all() and torch.equal(p, q)
+    # the same rows through autograd's relu
+    z32 = z.float().requires_grad_()
+    dz, = torch.autograd.grad(torch.relu(z32), z32, dd.float())
+    assert torch.equal(dz, torch.where(z > 0, dd, 0.0).float())
+    z[7, 2] = float("nan")
+    dx, dw, db = ge.linear_backward(torch.where(dd.isfinite(), dd, 0.0), x, w, z, act="relu")
+    want = ge.linear_backward(torch.where((z > 0) | z.isnan(), dd, 0.0), x, w)
+    for p, q in zip((dx, dw, db), want):
+        assert torch.equal(p, q)
