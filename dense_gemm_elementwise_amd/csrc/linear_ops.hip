@@ -405,8 +405,10 @@ hipError_t run_zero(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes, hipS
 
 // ---- linear -------------------------------------------------------------------
 // Rows of X up to which a product reads W through row_dot_kernel, and through
-// skinny_kernel (one MFMA block); past them it takes the tiles.
-constexpr int64_t kDotRows = 2, kSkinnyRows = 16;
+// skinny_kernel (one MFMA block); past them it takes the tiles.  linear_small.hpp
+// has the times on both sides of the first.
+constexpr int64_t dot_rows(bool bf) { return bf ? 1 : 2; }
+constexpr int64_t kSkinnyRows = 16;
 // workgroups of row_dot_kernel: eight of four waves on every CU, fewer where
 // there are fewer rows of W
 int row_dot_groups(int64_t N) { return (int)std::min<int64_t>(ceil_div(N, 4), 8 * kCUs); }
@@ -429,10 +431,11 @@ template <bool BF, bool XENT, int ACT>
 hipError_t launch_few_rows(const SkinnyParams &q, hipStream_t s)
 {
     const dim3 b(256);
-    if (q.M > kDotRows) return launch_skinny<BF, XENT ? SK_STATS : SK_LINEAR, ACT>(q, s);
     const dim3 g((unsigned)row_dot_groups(q.N));
     if (q.M == 1) return launch(row_dot_kernel<BF, XENT, ACT, 1>, g, b, s, q);
-    return launch(row_dot_kernel<BF, XENT, ACT, 2>, g, b, s, q);
+    if constexpr (dot_rows(BF) == 2)
+        if (q.M == 2) return launch(row_dot_kernel<BF, XENT, ACT, 2>, g, b, s, q);
+    return launch_skinny<BF, XENT ? SK_STATS : SK_LINEAR, ACT>(q, s);
 }
 
 struct LinearPlan {
@@ -731,7 +734,7 @@ int plan_xent(const ge_linear_xent_args *a, XentPlan &pl)
     Layout lay;
     pl.skinny = a->T <= kSkinnyRows;
     if (pl.skinny) {
-        pl.nparts = a->T <= kDotRows ? row_dot_groups(a->V) : (int)ceil_div(a->V, skinny_cols(a->V));
+        pl.nparts = a->T <= dot_rows(a->dtype == GEMM_EPI_BF16) ? row_dot_groups(a->V) : (int)ceil_div(a->V, skinny_cols(a->V));
     } else {
         pl.st = plan_staging2(a->X, a->ldx, a->T, a->W, a->ldw, a->V, a->K, lay);
         pl.pl = plan_product(a->T, a->V, a->K, kSquareTiles, 0);

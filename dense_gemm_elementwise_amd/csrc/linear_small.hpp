@@ -20,14 +20,19 @@ __device__ __forceinline__ int64_t block_row() { return (int64_t)blockIdx.y * kR
 // ---------------------------------------------------------------------------
 // Products with at most 16 rows of X (single tokens, small batches of them):
 // bound by reading W once.  No LDS on the way in, 16-byte loads at any
-// alignment, and plain loads: non-temporal ones were 15-18% slower.  V = 100003,
-// K = 4096, one row of X, bf16, W in HBM:
-//   row_dot_kernel (1 or 2 rows): a wave reads one row of W, 1 KB contiguous
-//     per load, against the rows of X in fp32 multiply-adds: 116 us, 7.1 TB/s;
-//   skinny_kernel (3 to 16): a wave reads 16 rows of W, 64 bytes of each per
-//     load, straight into the operand layout of one 16x16x32 MFMA against all
-//     rows of X: 132 us, 6.2 TB/s whatever the rows of X, where the
-//     multiply-adds of the other would take over from the loads.
+// alignment, and plain loads: non-temporal ones were 15-18% slower.
+//   row_dot_kernel: a wave reads one row of W, 1 KB contiguous per load,
+//     against the rows of X in fp32 multiply-adds;
+//   skinny_kernel: a wave reads 16 rows of W, 64 bytes of each per load,
+//     straight into the operand layout of one 16x16x32 MFMA against all rows of
+//     X, as fast whatever the rows of X.
+// Whole calls with W in HBM, us, row_dot_kernel first: one row of X, bf16,
+// 100003 x 4096 (loss) 137 and 161 (6.0 and 5.1 TB/s), 28672 x 8192 82 and 92,
+// 8192 x 4096 14.2 and 16.2, 4096 x 11008 23.1 and 21.9; fp16 the same within 15%
+// (20.4 and 21.9).  Two rows, where the multiply-adds start to count: fp16, whose
+// operands convert inside them, 154 and 162, 93.7 and 93.3, 14.8 and 16.5, 22.6
+// and 21.8; bf16, with a shift for each, 169 and 162, 103 and 93, 18.6 and 16.5,
+// 30.4 and 21.8.  So row_dot_kernel takes one row, and two of fp16.
 // ---------------------------------------------------------------------------
 struct SkinnyParams {
     const _Float16 *X, *W;

@@ -1138,3 +1138,29 @@ def test_relu_gradient_masks(t):
     want = ge.linear_backward(torch.where((z > 0) | z.isnan(), dd, 0.0), x, w)
     for p, q in zip((dx, dw, db), want):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("t", [BF16, F16], ids=["bf16", "f16"])
+def test_two_rows(t):
+    """Two rows of X: fp16 in multiply-adds, bf16 in one MFMA block."""
+    for shape in ((2, 64, 64), (2, 1003, 999), (2, 520, 300), (2, 5, 3), (2, 1, 1), (2, 4104, 2056)):
+        test_linear(shape, t)
+    for shape in ((2, 1000, 64), (2, 257, 33), (2, 33000, 520), (2, 1, 1)):
+        test_linear_xent(shape, t)
+
+
+def test_xent_longest_vocabulary_two_rows_f16():
+    """The second row's loop past 2^31 - 8192 columns in the type that still takes it."""
+    log("[longest vocabulary] two rows, f16")
+    g = gen(43)
+    V = LONGEST
+    x, w = rnd(g, 2, 1, t=F16), torch.zeros(V, 1, dtype=F16, device=DEV)
+    w[-32:] = rnd(g, 32, 1, t=F16)
+    target = torch.tensor([V - 1, 5], device=DEV)
+    loss, lse = ge.linear_xent(x, w, target)
+    logits = x.double() @ w[-32:].double().t()
+    rest = torch.full((2, 1), math.log(V - 32), dtype=torch.float64, device=DEV)
+    want = torch.logsumexp(torch.cat([logits, rest], 1), 1)
+    b = 3000 * E24 + want.abs() * 2.0 ** -22  # as in longest_vocabulary
+    close("lse", lse, want, b)
+    close("loss", loss, want - torch.stack([logits[0, -1], 0 * logits[1, 0]]), b + 2 * E24 * logits.abs().max())
