@@ -796,7 +796,8 @@ int run_xent(const ge_linear_xent_args *a, const XentPlan &pl)
 // by one product and read by two.  A piece as large as 128 MiB of P (half the
 // last-level cache) keeps those reads off HBM; more pieces cost a round trip of
 // dX's fp32 accumulator each, T K 8 bytes against 2 T K piece operations, so a
-// piece is not made shorter than 8192 columns.  Within that it is a length that
+// piece is not made shorter than 8192 columns (P then takes 16 KiB a row of X
+// past 8192 rows, whatever the vocabulary).  Within that it is a length that
 // fills whole rounds of tiles, with the rest in a shorter last piece: 4096 x
 // 100003 in 6 pieces of 16384 and one of 1699 takes 25 rounds for each of its
 // products, in 7 even ones (3.5 rounds each) 28.

@@ -122,8 +122,9 @@ typedef struct {
  * ignored rows, is formed one piece of the vocabulary at a time and rounded to
  * the element type as an operand (fp16: after a common factor for all rows, so that
  * an entry is off by its rounding and at most 2^-39 of the largest |dloss|).  A
- * row whose target is out of range makes its gradients NaN.  With T = 0, dW is
- * set to zero, and both may be NULL. */
+ * row whose target is out of range makes its gradients NaN.  A piece of P is
+ * 128 MiB, or 8192 columns where that is more: past 8192 rows the workspace
+ * grows by 16 KiB a row, and 4 K bytes for dX between the pieces.  With T = 0, dW is set to zero, and both may be NULL. */
 typedef struct {
     int64_t T, V, K;
     const float *dloss;
