@@ -594,8 +594,8 @@ int plan_linear_grad(const ge_linear_backward_args *a, LinearGradPlan &pl)
     pl.direct = a->act == GE_ACT_IDENTITY && dma_rows(a->dD, a->lddd, a->N);
     if (!pl.direct) pl.off_dz = lay.take(a->M * pl.N8 * 2);
     // strips of rows: about 2048 blocks of 256 columns, at least 32 rows each (a
-    // thread's four loads in flight), 16 where 32 leave most compute units fewer
-    // than three blocks: 1001 x 1003 of K = 1000, gelu, fp16, 24.0 us the call
+    // thread's four loads in flight), 16 (two rows a thread, one after the other)
+    // where 32 leave most compute units fewer than three blocks: 1001 x 1003 of K = 1000, gelu, fp16, 24.0 us the call
     // with 32 and 22.0 with 16, 200 x 4099 x 1023 35.3 and 29.5, 1500 x 3000 x
     // 1000 47.6 and 45.9; but 2000 x 3001 x 2001 (756 blocks) 76.4 and 77.8, and
     // 8 rows are no faster than 16 anywhere.  One strip, whose sums are dbias
