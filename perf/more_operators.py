@@ -1,0 +1,361 @@
+"""8-bit products with block scales and a mixture of experts for a few tokens: what is measured, and their plain forms.
+
+quantize     8-bit floating point with one power-of-two scale (e8m0) for each block: 128 consecutive elements of a row
+             (ROWS) or 128 x 128 elements (TILES).  scale = the smallest power of two s with max |x| <= MAX s over the
+             block, 1 for a block of zeros; q = x / s to nearest even.  Also the transposed matrix, its blocks along
+             the other axis (ROWS) or the same ones (TILES), from the same pass.
+linear8      Z = X W^T + bias, D = act(Z) + residual, X (M, K) and W (N, K) in 8 bits, X with a scale for each block
+             of a row, W for each tile; X may also come in 16 bits and is then quantised within the call.
+             Gradient: dZ = dD act'(Z), quantised along its rows for dX = dZ W and along its columns for dW = dZ^T X;
+             dbias = sum of the unquantised dZ over rows.  X and W come transposed (K, M), (K, N), as quantize made
+             them.
+moe          a whole mixture-of-experts layer: softmax of the router's logits x Wr^T, the top_k experts of each token
+             (ties: the lowest index) with their probabilities divided by their sum, h = silu(gate) up with
+             [gate; up] = Wup[e] x, out = sum of weight Wdown[e] h.  Wr (E, H), Wup (E, 2 I, H), Wdown (E, H, I),
+             the experts' weights in 16 bits or in 8 with a scale for each tile.
+"""
+import math
+
+import torch
+
+own = False
+
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+FORMATS = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+BLOCK = 128
+
+
+def listed():
+    return [
+        # the weights of a projection after an optimizer's step: both orientations, for the forward and for dX
+        {"name": "quantize_weight", "op": "quantize", "R": 8192, "C": 8192, "block": "tile", "format": "e4m3",
+         "dtype": "bf16"},
+        # activations of a ragged batch, every row at an odd offset: along rows for D, along columns for dW
+        {"name": "quantize_rows_odd", "op": "quantize", "R": 2400, "C": 3233, "block": "row", "format": "e5m2",
+         "dtype": "f16"},
+        # one token through a projection of a decoder, from 16 bits: bound by reading W once, and by latency
+        {"name": "linear8_token", "op": "linear8", "dir": "fwd", "M": 1, "N": 8192, "K": 4096, "act": "silu",
+         "x8": False, "dtype": "bf16"},
+        # a prompt through the framework's 2400 x 3232 x 4096 shape, from 16 bits, with Z kept
+        {"name": "linear8_prompt", "op": "linear8", "dir": "fwd", "M": 2400, "N": 3232, "K": 4096, "act": "gelu",
+         "x8": False, "dtype": "f16"},
+        # the framework's headline size, X quantised before (by a trainer that keeps both orientations)
+        {"name": "linear8_8192", "op": "linear8", "dir": "fwd", "M": 8192, "N": 8192, "K": 8192, "act": "gelu",
+         "x8": True, "dtype": "bf16"},
+        # the gradient of an up projection over a training batch
+        {"name": "linear8_grad", "op": "linear8", "dir": "bwd", "M": 8192, "N": 8192, "K": 2048, "act": "silu",
+         "x8": True, "dtype": "bf16"},
+        # odd and ragged: blocks, tiles and 16-byte rows all end short
+        {"name": "linear8_grad_odd", "op": "linear8", "dir": "bwd", "M": 1001, "N": 1003, "K": 999, "act": "relu",
+         "x8": True, "dtype": "f16"},
+        # one token through a layer of 64 experts: 8 of them are read
+        {"name": "moe_token", "op": "moe", "T": 1, "H": 4096, "E": 64, "I": 1024, "k": 8, "w8": False,
+         "dtype": "bf16"},
+        # the same with weights in 8 bits
+        {"name": "moe_token_8", "op": "moe", "T": 1, "H": 4096, "E": 64, "I": 1024, "k": 8, "w8": True,
+         "dtype": "bf16"},
+        # a few tokens, every size odd in its way
+        {"name": "moe_odd", "op": "moe", "T": 7, "H": 1000, "E": 13, "I": 333, "k": 3, "w8": False, "dtype": "f16"},
+        # a batch of 64 sequences, a token each: every expert is read, for 8 tokens on average
+        {"name": "moe_batch_8", "op": "moe", "T": 64, "H": 4096, "E": 64, "I": 1024, "k": 8, "w8": True,
+         "dtype": "bf16"},
+    ]
+
+
+def _spread(rng, lo, hi):
+    """A size between lo and hi, even over the logarithm; a third of them multiples of 64, a third of 8."""
+    v = int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    m = rng.choice((1, 8, 64))
+    return max(lo, v // m * m) if v >= m else v
+
+
+def draw(rng):
+    op = rng.choice(("quantize", "linear8", "linear8", "moe"))
+    dtype = rng.choice(("bf16", "f16"))
+    if op == "quantize":
+        return {"op": op, "R": _spread(rng, 1, 8192), "C": _spread(rng, 64, 8192), "block": rng.choice(("row", "tile")),
+                "format": rng.choice(("e4m3", "e5m2")), "dtype": dtype}
+    if op == "linear8":
+        way = rng.choice(("fwd", "bwd"))
+        return {"op": op, "dir": way, "M": _spread(rng, 1, 8192), "N": _spread(rng, 64, 8192),
+                "K": _spread(rng, 64, 4096), "act": rng.choice(("identity", "relu", "gelu", "silu")),
+                "x8": way == "bwd" or rng.choice((False, True)), "dtype": dtype}
+    e = _spread(rng, 4, 64)
+    return {"op": op, "T": _spread(rng, 1, 64), "H": _spread(rng, 64, 4096), "E": e, "I": _spread(rng, 64, 1024),
+            "k": rng.randint(1, min(8, e)), "w8": rng.choice((False, True)), "dtype": dtype}
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = TYPES[case["dtype"]]
+
+    def normal(*shape, std=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * std).to(t)
+
+    s = dict(case)
+    if case["op"] == "quantize":
+        # rows of different sizes, as of tokens or output features
+        r = case["R"]
+        s["x"] = (normal(r, case["C"]).float() * torch.exp2(4 * torch.randn((r, 1), generator=g, device="cuda"))
+                  .clamp(2.0 ** -10, 2.0 ** 10)).to(t)
+    elif case["op"] == "linear8":
+        m, n, k = case["M"], case["N"], case["K"]
+        x = normal(m, k)
+        w = normal(n, k, std=k ** -0.5)
+        if case["dir"] == "fwd":
+            if case["x8"]:
+                s["x"], s["x_scale"] = _keep8(*_quantize(x, "row", "e4m3"))
+            else:
+                s["x"], s["x_scale"] = x, None
+            s["w"], s["w_scale"] = _keep8(*_quantize(w, "tile", "e4m3"))
+            s["bias"], s["residual"] = normal(n, std=0.5), normal(m, n)
+        else:
+            s["xt"], s["xt_scale"] = _keep8(*_quantize(x.t(), "row", "e4m3"))
+            s["wt"], s["wt_scale"] = _keep8(*_quantize(w.t(), "tile", "e4m3"))
+            s["z"], s["dd"] = normal(m, n), normal(m, n)
+    else:
+        n, h, e, i = case["T"], case["H"], case["E"], case["I"]
+        s["x"] = normal(n, h)
+        s["w_router"] = normal(e, h, std=1.5 * h ** -0.5)
+        up, down = normal(e, 2 * i, h, std=h ** -0.5), normal(e, h, i, std=2.0 * i ** -0.5)
+        s["up_scale"] = s["down_scale"] = None
+        if case["w8"]:
+            up, s["up_scale"] = _keep8(*_quantize(up, "tile", "e4m3"))
+            down, s["down_scale"] = _keep8(*_quantize(down, "tile", "e4m3"))
+        s["up"], s["down"] = up, down
+    return s
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"quantize": _plain_quantize, "linear8": _plain_linear8, "moe": _plain_moe}[state["op"]](state)
+
+
+def _own(s):
+    import dense_gemm_elementwise_amd as ops
+    if s["op"] == "quantize":
+        return ops.quantize_fp8(s["x"], block=s["block"], format=s["format"], transpose=True)
+    if s["op"] == "linear8":
+        if s["dir"] == "bwd":
+            return ops.linear_fp8_backward(s["dd"], s["xt"], s["xt_scale"], s["wt"], s["wt_scale"], s["z"],
+                                           act=s["act"])
+        return ops.linear_fp8(s["x"], s["w"], s["w_scale"], s["bias"], s["residual"], x_scale=s["x_scale"],
+                              act=s["act"], save_z=s["M"] > 1)  # serving keeps no Z
+    return ops.moe(s["x"], s["w_router"], s["up"], s["down"], top_k=s["k"], up_scale=s["up_scale"],
+                   down_scale=s["down_scale"], act="silu")
+
+
+# The plain forms: elementary operations on fp32 copies, rounded once at the end.
+
+def _blocked(x, block):
+    """x (..., R, C) padded with zeros to whole blocks, as (..., blocks of rows, rows, blocks of columns, columns)."""
+    b = BLOCK if block == "tile" else 1
+    r, c = x.shape[-2:]
+    x = torch.nn.functional.pad(x, (0, -c % BLOCK, 0, -r % b))
+    return x.unflatten(-1, (-1, BLOCK)).unflatten(-3, (-1, b))
+
+
+def _quantize(x, block, format):
+    """(q, scale) as fp32 values: q (..., R, C), scale (..., blocks of rows, blocks of columns)."""
+    top, largest = (448.0, 8) if format == "e4m3" else (57344.0, 15)
+    r, c = x.shape[-2:]
+    v = _blocked(x.float(), block)
+    a = v.abs().amax((-3, -1))
+    # a = m 2^p with m in [1/2, 1): a <= top 2^e, top = 1.75 2^largest, from e = p - 1 - largest on, or one more
+    m, p = torch.frexp(a)
+    e = p - 1 - largest + (2 * m > top * 2.0 ** -largest).to(p.dtype)
+    scale = torch.where(a > 0, torch.ldexp(torch.ones_like(a), e.clamp(-127, 127)), 1.0)
+    q = (v / scale[..., :, None, :, None]).flatten(-2).flatten(-3, -2)[..., :r, :c]
+    return q.to(FORMATS[format]).float(), scale
+
+
+def _keep8(q, scale, format="e4m3"):
+    return q.to(FORMATS[format]).contiguous(), scale.to(torch.float8_e8m0fnu).contiguous()
+
+
+def _value(q, scale, block):
+    """The fp32 values that q and its scales stand for."""
+    b = BLOCK if block == "tile" else 1
+    r, c = q.shape[-2:]
+    s = scale.float().repeat_interleave(b, -2)[..., :r, :].repeat_interleave(BLOCK, -1)[..., :c]
+    return q.float() * s
+
+
+def _plain_quantize(s):
+    out = []
+    q, scale = _quantize(s["x"], s["block"], s["format"])
+    out += _keep8(q, scale, s["format"])
+    qt, scale_t = _quantize(s["x"].t(), s["block"], s["format"])
+    out += _keep8(qt, scale_t, s["format"])
+    return tuple(out)
+
+
+def _act(z, act):
+    if act == "relu":
+        return z.clamp(min=0)
+    if act == "silu":
+        return z / (1 + torch.exp(-z))
+    if act == "gelu":
+        return 0.5 * z * (1 + torch.erf(z * 0.5 ** 0.5))
+    return z
+
+
+def _act_grad(z, act):
+    if act == "relu":
+        return (z > 0).float()
+    if act == "silu":
+        p = 1 / (1 + torch.exp(-z))
+        return p * (1 + z * (1 - p))
+    if act == "gelu":
+        return 0.5 * (1 + torch.erf(z * 0.5 ** 0.5)) + z * torch.exp(-0.5 * z * z) * (2 * math.pi) ** -0.5
+    return torch.ones_like(z)
+
+
+def _plain_linear8(s):
+    if s["dir"] == "bwd":
+        t = s["dd"].dtype
+        dz = s["dd"].float() * _act_grad(s["z"].float(), s["act"])
+        rows = _value(*_quantize(dz, "row", "e4m3"), "row")
+        columns = _value(*_quantize(dz.t(), "row", "e4m3"), "row")
+        dx = rows @ _value(s["wt"], s["wt_scale"], "tile").t()
+        dw = columns @ _value(s["xt"], s["xt_scale"], "row").t()
+        return dx.to(t), dw.to(t), dz.sum(0)
+    t = s["residual"].dtype
+    x = _value(s["x"], s["x_scale"], "row") if s["x8"] else _value(*_quantize(s["x"], "row", "e4m3"), "row")
+    z = x @ _value(s["w"], s["w_scale"], "tile").t() + s["bias"].float()
+    d = (_act(z, s["act"]) + s["residual"].float()).to(t)
+    return (d, z.to(t)) if s["M"] > 1 else d
+
+
+def _plain_moe(s):
+    n, k, i = s["T"], s["k"], s["I"]
+    x = s["x"].float()
+    # logits in 64 bits, since they decide: two of them may lie close together
+    logits = s["x"].double() @ s["w_router"].double().t()
+    p = (logits - logits.amax(1, keepdim=True)).exp()
+    p = (p / p.sum(1, keepdim=True)).float()
+    chosen = torch.sort(logits, dim=1, descending=True, stable=True)[1][:, :k]
+    weight = p.gather(1, chosen)
+    weight = weight / weight.sum(1, keepdim=True)
+    up, down, up_scale, down_scale = s["up"], s["down"], s["up_scale"], s["down_scale"]
+    if n * k < s["E"]:  # the chosen experts' weights alone
+        at = chosen.flatten()
+        up, down = up[at], down[at]
+        if s["w8"]:
+            up_scale, down_scale = up_scale.float()[at], down_scale.float()[at]
+    if s["w8"]:
+        up, down = _value(up, up_scale, "tile"), _value(down, down_scale, "tile")
+    up, down = up.float(), down.float()
+    if n * k < s["E"]:
+        hidden = torch.bmm(up, x.repeat_interleave(k, 0)[:, :, None])[..., 0]
+        hidden = _act(hidden[:, :i], "silu") * hidden[:, i:]
+        out = torch.bmm(down, hidden[:, :, None])[..., 0] * weight.flatten()[:, None]
+        return out.view(n, k, -1).sum(1).to(s["x"].dtype)
+    # all experts for all tokens, the ones that were not chosen with weight 0
+    share = torch.zeros_like(p).scatter_(1, chosen, weight)
+    hidden = (x @ up.flatten(0, 1).t()).view(n, -1, 2 * i)
+    hidden = _act(hidden[..., :i], "silu") * hidden[..., i:] * share[:, :, None]
+    return (hidden.flatten(1) @ down.transpose(1, 2).flatten(0, 1)).to(s["x"].dtype)
+
+
+def _ceil(n):
+    return -(-n // BLOCK)
+
+
+def work(case):
+    """Inputs read once, outputs written once, and the products that no form can do without."""
+    if case["op"] == "quantize":
+        r, c = case["R"], case["C"]
+        scales = 2 * _ceil(r) * _ceil(c) if case["block"] == "tile" else r * _ceil(c) + c * _ceil(r)
+        return {"bytes": 4 * r * c + scales, "flops": 4 * r * c}
+    if case["op"] == "linear8":
+        m, n, k = case["M"], case["N"], case["K"]
+        scales = m * _ceil(k) + _ceil(n) * _ceil(k)
+        if case["dir"] == "fwd":
+            x = m * k * (1 if case["x8"] else 2)
+            return {"bytes": x + n * k + scales + 2 * (n + m * n * (2 if m == 1 else 3)), "flops": 2 * m * n * k}
+        return {"bytes": m * k + n * k + scales + 2 * (m * k + n * k + 2 * m * n) + 4 * n, "flops": 4 * m * n * k}
+    t, h, e, i, k = (case[x] for x in ("T", "H", "E", "I", "k"))
+    # experts that are read: how many of them t tokens choose on average
+    active = e * (1 - (1 - k / e) ** t)
+    weights = active * 3 * i * h * (1 if case["w8"] else 2)
+    return {"bytes": weights + 2 * e * h + 4 * t * h, "flops": 6 * t * k * i * h + 2 * t * e * h}
+
+
+def exact(case, seed):
+    """The definitions in 64 bits: what is held in 8 bits is rounded as the definition says, the gradients come from
+    differentiating the activation."""
+    s = prepare(case, seed)
+
+    def scale_of(a, top):
+        # the smallest power of two that reaches a / top, found from below by doubling what is too small
+        e = torch.floor(torch.log2(torch.where(a > 0, a, 1.0) / top)) - 1
+        for _ in range(3):
+            e = torch.where(torch.exp2(e) * top < a, e + 1, e)
+        return torch.where(a > 0, torch.exp2(e.clamp(-127, 127)), 1.0)
+
+    def nearest(v, mantissa, least):
+        # steps of 2^-mantissa of the leading power of two, none smaller than the smallest subnormal
+        lead = torch.floor(torch.log2(torch.where(v == 0, 1.0, v.abs())))
+        step = torch.exp2(torch.clamp(lead - mantissa, min=least))
+        return torch.round(v / step) * step  # (round: half to even)
+
+    def rows(v, format):
+        """(q, scale) with a scale for each 128 of a row, block by block."""
+        top, mantissa, least = (448.0, 3, -9) if format == "e4m3" else (57344.0, 2, -16)
+        parts = v.double().split(BLOCK, 1)
+        scales = [scale_of(b.abs().amax(1), top) for b in parts]
+        return (torch.cat([nearest(b / c[:, None], mantissa, least) for b, c in zip(parts, scales)], 1),
+                torch.stack(scales, 1))
+
+    def tiles(v, format):
+        top, mantissa, least = (448.0, 3, -9) if format == "e4m3" else (57344.0, 2, -16)
+        q, scales = [], []
+        for band in v.double().split(BLOCK, 0):
+            a = torch.stack([b.abs().amax() for b in band.split(BLOCK, 1)])
+            c = scale_of(a, top)
+            q.append(nearest(band / torch.repeat_interleave(c, BLOCK)[None, :v.shape[1]], mantissa, least))
+            scales.append(c)
+        return torch.cat(q), torch.stack(scales)
+
+    def meant(q, scale, tall):
+        v = q.double()
+        c = torch.repeat_interleave(scale.double(), BLOCK, -1)[..., :v.shape[-1]]
+        if tall:
+            c = torch.repeat_interleave(c, BLOCK, -2)[..., :v.shape[-2], :]
+        return v * c
+
+    if case["op"] == "quantize":
+        f = rows if case["block"] == "row" else tiles
+        return (*f(s["x"], case["format"]), *f(s["x"].t(), case["format"]))
+    if case["op"] == "linear8":
+        f = {"identity": lambda z: z, "relu": torch.nn.functional.relu, "silu": torch.nn.functional.silu,
+             "gelu": torch.nn.functional.gelu}[case["act"]]
+        if case["dir"] == "bwd":
+            with torch.enable_grad():
+                z = s["z"].double().requires_grad_()
+                dz, = torch.autograd.grad(f(z), z, s["dd"].double())
+            dx = torch.mm(meant(*rows(dz, "e4m3"), False), meant(s["wt"], s["wt_scale"], True).t())
+            dw = torch.mm(meant(*rows(dz.t(), "e4m3"), False), meant(s["xt"], s["xt_scale"], False).t())
+            return dx, dw, dz.sum(0)
+        x = meant(s["x"], s["x_scale"], False) if case["x8"] else meant(*rows(s["x"], "e4m3"), False)
+        z = torch.mm(x, meant(s["w"], s["w_scale"], True).t()) + s["bias"].double()[None, :]
+        d = f(z) + s["residual"].double()
+        return (d, z) if case["M"] > 1 else d
+    x = s["x"].double()
+    p = torch.softmax(torch.mm(x, s["w_router"].double().t()), 1)
+    out = torch.zeros_like(x)
+    order = torch.argsort(-p, dim=1, stable=True)[:, :case["k"]]
+    share = torch.zeros_like(p).scatter_(1, order, p.gather(1, order))
+    share = share / share.sum(1, keepdim=True)
+    for e in range(case["E"]):
+        here = torch.nonzero(share[:, e] > 0)[:, 0]
+        if len(here):
+            up, down = s["up"][e], s["down"][e]
+            if case["w8"]:
+                up, down = meant(up, s["up_scale"][e], True), meant(down, s["down_scale"][e], True)
+            gate, lift = torch.mm(x[here], up.double().t()).split(case["I"], 1)
+            y = torch.mm(torch.nn.functional.silu(gate) * lift, down.double().t())
+            out.index_add_(0, here, y * share[here, e][:, None])
+    return out
