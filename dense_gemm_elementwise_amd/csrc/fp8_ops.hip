@@ -1,0 +1,466 @@
+// fp8_ops.hip -- the C ABI of include/fp8_ops.h for the 8-bit products:
+// argument checks, plans (tiles, splits, workspace layout) and launches.
+#include <hip/hip_runtime.h>
+#include <algorithm>
+#include <stdint.h>
+
+#include "fp8_launch.hpp"
+#include "fp8_ops.h"
+#include "fp8_quant.hpp"
+#include "ops_host.hpp"
+
+using namespace gemm_epi;
+
+namespace {
+
+int64_t blocks_of(int64_t n) { return ceil_div(n, kBlock); }
+
+int check_bytes(const void *p, int64_t ld, int64_t cols, int64_t limit, int null_status)
+{
+    if (!p) return null_status;
+    return ld < cols || ld > limit ? GEMM_EPI_ERR_SHAPE : GEMM_EPI_OK;
+}
+int check_format(int64_t f) { return f == GE_FP8_E4M3 || f == GE_FP8_E5M2 ? GEMM_EPI_OK : GEMM_EPI_ERR_DTYPE; }
+
+// ---- quantisation ---------------------------------------------------------------
+template <int SRC, bool TILE, bool BOTH>
+hipError_t launch_quant3(int format, const QuantParams &q, hipStream_t s)
+{
+    const dim3 g((unsigned)blocks_of(q.C), (unsigned)blocks_of(q.R)), b(256);
+    return format == GE_FP8_E4M3 ? launch(quant_kernel<SRC, TILE, BOTH, 0, kNoGrad>, g, b, s, q)
+                                 : launch(quant_kernel<SRC, TILE, BOTH, 1, kNoGrad>, g, b, s, q);
+}
+template <int SRC>
+hipError_t launch_quant2(bool tile, int format, const QuantParams &q, hipStream_t s)
+{
+    if (tile) return q.QT ? launch_quant3<SRC, true, true>(format, q, s) : launch_quant3<SRC, true, false>(format, q, s);
+    return q.QT ? launch_quant3<SRC, false, true>(format, q, s) : launch_quant3<SRC, false, false>(format, q, s);
+}
+hipError_t launch_quant(int64_t dtype, bool tile, int format, const QuantParams &q, hipStream_t s)
+{
+    switch (dtype) {
+    case GEMM_EPI_F32: return launch_quant2<QS_F32>(tile, format, q, s);
+    case GEMM_EPI_BF16: return launch_quant2<QS_BF16>(tile, format, q, s);
+    default: return launch_quant2<QS_F16>(tile, format, q, s);
+    }
+}
+
+int check_quantize(const ge_quantize_fp8_args *a)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    if (a->R < 0 || a->R > GE_MAX_COLS || a->C < 1 || a->C > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
+    if (a->block != GE_BLOCK_ROW && a->block != GE_BLOCK_TILE) return GEMM_EPI_ERR_KIND;
+    GE_CHECK(check_format(a->format));
+    if (a->dtype < GEMM_EPI_F16 || a->dtype > GEMM_EPI_F32) return GEMM_EPI_ERR_DTYPE;
+    if (a->R == 0) return GEMM_EPI_OK;
+    const bool tile = a->block == GE_BLOCK_TILE;
+    const int64_t rb = blocks_of(a->R), cb = blocks_of(a->C);
+    GE_CHECK(check_matrix(a->X, a->ldx, a->C, a->dtype == GEMM_EPI_F32 ? 4 : 2, GEMM_EPI_ERR_NULL_INPUT));
+    GE_CHECK(check_bytes(a->Q, a->ldq, a->C, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_OUTPUT));
+    GE_CHECK(check_bytes(a->S, a->lds, cb, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (!a->QT != !a->ST) return GEMM_EPI_ERR_NULL_OUTPUT;
+    if (a->QT) {
+        GE_CHECK(check_bytes(a->QT, a->ldqt, a->R, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_OUTPUT));
+        GE_CHECK(check_bytes(a->ST, a->ldst, tile ? rb : rb, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_OUTPUT));
+    }
+    return GEMM_EPI_OK;
+}
+
+// ---- operands -------------------------------------------------------------------
+// An 8-bit matrix with its scales as the products read them: in place, or a copy.
+struct Operand8 {
+    const uint8_t *q, *s;
+    int64_t ldq, lds;
+};
+struct Staging {
+    PadBytes p = {};
+    int n = 0;
+    int64_t most = 0;
+    void add(const uint8_t *&src, int64_t &ld, int64_t rows, int64_t cols, int64_t ldo, uint8_t *dst)
+    {
+        p.src[n] = src;
+        p.lds[n] = ld;
+        p.rows[n] = rows;
+        p.cols[n] = cols;
+        p.ldo[n] = ldo;
+        p.dst[n] = dst;
+        n++;
+        most = std::max(most, rows * ldo / 4);
+        src = dst;
+        ld = ldo;
+    }
+    hipError_t run(hipStream_t s) const
+    {
+        if (!n) return hipSuccess;
+        const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(most, 256), 4096);
+        return launch(pad_bytes_kernel, dim3(blocks, n), dim3(256), s, p);
+    }
+};
+bool rows16(const void *p, int64_t ld) { return aligned(p, 16) && ld % 16 == 0; }
+bool rows4(const void *p, int64_t ld) { return aligned(p, 4) && ld % 4 == 0; }
+
+// Where an operand's copies lie; negative: read in place.
+struct StageAt {
+    int64_t q = -1, s = -1;
+};
+StageAt plan_operand(const void *q, int64_t ldq, const void *s, int64_t lds, int64_t rows, int64_t srows, int64_t cols,
+                     Layout &lay)
+{
+    StageAt at;
+    if (!rows16(q, ldq)) at.q = lay.take(rows * round_up(cols, 16));
+    if (!rows4(s, lds)) at.s = lay.take(srows * round_up(blocks_of(cols), 4));
+    return at;
+}
+void stage_operand(const StageAt &at, Operand8 &o, int64_t rows, int64_t srows, int64_t cols, char *ws, Staging &st)
+{
+    if (at.q >= 0) st.add(o.q, o.ldq, rows, cols, round_up(cols, 16), (uint8_t *)ws + at.q);
+    if (at.s >= 0) st.add(o.s, o.lds, srows, blocks_of(cols), round_up(blocks_of(cols), 4), (uint8_t *)ws + at.s);
+}
+
+// ---- products -------------------------------------------------------------------
+struct Plan8 {
+    int splits = 1;
+    int64_t tiles_m = 0, tiles_n = 0, k_split = 0, part_bytes = 0;
+};
+bool plan_fits(const Plan8 &p) { return p.tiles_m * p.tiles_n * p.splits <= kMaxGroups; }
+Plan8 plan_fp8(int64_t M, int64_t N, int64_t K)
+{
+    Plan8 p;
+    p.tiles_m = ceil_div(M, 128);
+    p.tiles_n = ceil_div(N, 128);
+    p.k_split = round_up(K, 512);
+    return p;
+}
+
+void set_product8(Fp8Params &p, const Plan8 &pl, int64_t M, int64_t N, int64_t K, const Operand8 &a, const Operand8 &b,
+                  int shift_b, bool a_e5m2)
+{
+    p.A = a.q;
+    p.SA = a.s;
+    p.lda = a.ldq;
+    p.ldsa = a.lds;
+    p.B = b.q;
+    p.SB = b.s;
+    p.ldb = b.ldq;
+    p.ldsb = b.lds;
+    p.K = (int)K;
+    p.shift_b = shift_b;
+    p.a_e5m2 = a_e5m2;
+    p.e.M = (int)M;
+    p.e.N = (int)N;
+    p.e.tiles_m = (int)pl.tiles_m;
+    p.e.tiles_n = (int)pl.tiles_n;
+    p.e.num_tiles = (int)(pl.tiles_m * pl.tiles_n);
+    p.e.group_m = 8;
+    p.e.k_split = (int)pl.k_split;
+}
+
+// C = A B^T into D (16-bit)
+hipError_t run_product8(bool bf, const Plan8 &pl, Fp8Params p, void *D, int64_t ldd, float *part, hipStream_t s)
+{
+    const int groups = (int)(pl.tiles_m * pl.tiles_n * pl.splits);
+    if (pl.splits == 1) {
+        p.e.D = (_Float16 *)D;
+        p.e.ldd = ldd;
+        p.e.vec = dma_rows(D, ldd, p.e.N);
+        return bf ? fp8_launch_out_bf16(p, groups, s) : fp8_launch_out_f16(p, groups, s);
+    }
+    const int64_t ldc = round_up(p.e.N, 8);
+    p.e.C32 = part;
+    p.e.ldc = ldc;
+    p.e.c_split = p.e.M * ldc;
+    p.e.acc_out = 1;
+    const hipError_t e = bf ? fp8_launch_out_bf16(p, groups, s) : fp8_launch_out_f16(p, groups, s);
+    if (e != hipSuccess) return e;
+    SplitSumParams q = {};
+    q.part = part;
+    q.splits = pl.splits;
+    q.M = p.e.M;
+    q.N = p.e.N;
+    q.ldc = ldc;
+    q.c_split = p.e.c_split;
+    q.D = (_Float16 *)D;
+    q.ldd = ldd;
+    return run_split_sum_out(bf, q, s);
+}
+
+// ---- linear ---------------------------------------------------------------------
+struct LinearPlan8 {
+    StageAt x, w;
+    Plan8 pl;
+    int64_t off_q = 0, off_s = 0, off_part = 0, bytes = 0;
+};
+
+int check_linear8(const ge_linear_fp8_args *a)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_dims(a->M, a->N, a->K));
+    if (a->N > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
+    if (a->act < GE_ACT_IDENTITY || a->act > GE_ACT_SILU) return GEMM_EPI_ERR_KIND;
+    GE_CHECK(check_dtype(a->dtype));
+    GE_CHECK(check_format(a->format));
+    GE_CHECK(check_bytes(a->W, a->ldw, a->K, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_INPUT));
+    GE_CHECK(check_bytes(a->WS, a->ldws, blocks_of(a->K), GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_INPUT));
+    if (a->M == 0) return GEMM_EPI_OK;
+    if (a->XS) {
+        GE_CHECK(check_bytes(a->X, a->ldx, a->K, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_INPUT));
+        GE_CHECK(check_bytes(a->XS, a->ldxs, blocks_of(a->K), GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_INPUT));
+    } else {
+        GE_CHECK(check_matrix(a->X, a->ldx, a->K, 2, GEMM_EPI_ERR_NULL_INPUT));
+    }
+    GE_CHECK(check_matrix(a->D, a->ldd, a->N, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->residual) GE_CHECK(check_matrix(a->residual, a->ldr, a->N, 2, GEMM_EPI_ERR_NULL_INPUT));
+    if (a->Z) GE_CHECK(check_matrix(a->Z, a->ldz, a->N, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->bias && !aligned(a->bias, 2)) return GEMM_EPI_ERR_ALIGN;
+    return GEMM_EPI_OK;
+}
+
+int plan_linear8(const ge_linear_fp8_args *a, LinearPlan8 &pl)
+{
+    GE_CHECK(check_linear8(a));
+    if (a->M == 0) return GEMM_EPI_OK;
+    Layout lay;
+    if (a->XS) {
+        pl.x = plan_operand(a->X, a->ldx, a->XS, a->ldxs, a->M, a->M, a->K, lay);
+    } else {
+        pl.off_q = lay.take(a->M * round_up(a->K, 16));
+        pl.off_s = lay.take(a->M * round_up(blocks_of(a->K), 4));
+    }
+    pl.w = plan_operand(a->W, a->ldw, a->WS, a->ldws, a->N, blocks_of(a->N), a->K, lay);
+    pl.pl = plan_fp8(a->M, a->N, a->K);
+    if (!plan_fits(pl.pl)) return GEMM_EPI_ERR_SHAPE;
+    pl.off_part = lay.take(pl.pl.part_bytes);
+    pl.bytes = lay.bytes;
+    return GEMM_EPI_OK;
+}
+
+int run_linear8(const ge_linear_fp8_args *a, const LinearPlan8 &pl)
+{
+    hipStream_t s = (hipStream_t)a->stream;
+    char *ws = (char *)a->workspace;
+    const bool bf = a->dtype == GEMM_EPI_BF16;
+    Operand8 x = {(const uint8_t *)a->X, (const uint8_t *)a->XS, a->ldx, a->ldxs};
+    Operand8 w = {(const uint8_t *)a->W, (const uint8_t *)a->WS, a->ldw, a->ldws};
+    Staging st;
+    if (a->XS) {
+        stage_operand(pl.x, x, a->M, a->M, a->K, ws, st);
+    } else {
+        QuantParams q = {};
+        q.X = a->X;
+        q.ldx = a->ldx;
+        q.R = (int)a->M;
+        q.C = (int)a->K;
+        q.Q = (uint8_t *)ws + pl.off_q;
+        q.ldq = round_up(a->K, 16);
+        q.S = (uint8_t *)ws + pl.off_s;
+        q.lds = round_up(blocks_of(a->K), 4);
+        GE_TRY(launch_quant(a->dtype, false, (int)a->format, q, s));
+        x = {q.Q, q.S, q.ldq, q.lds};
+    }
+    stage_operand(pl.w, w, a->N, blocks_of(a->N), a->K, ws, st);
+    GE_TRY(st.run(s));
+    Fp8Params p = {};
+    set_product8(p, pl.pl, a->M, a->N, a->K, x, w, 7, a->format == GE_FP8_E5M2);
+    p.e.bias = (const _Float16 *)a->bias;
+    p.e.R = (const _Float16 *)a->residual;
+    p.e.D = (_Float16 *)a->D;
+    p.e.Z = (_Float16 *)a->Z;
+    p.e.ldr = a->ldr;
+    p.e.ldd = a->ldd;
+    p.e.ldz = a->ldz;
+    p.e.vec = dma_rows(a->D, a->ldd, a->N) && (!a->Z || dma_rows(a->Z, a->ldz, a->N)) &&
+              (!a->residual || dma_rows(a->residual, a->ldr, a->N));
+    const int groups = (int)(pl.pl.tiles_m * pl.pl.tiles_n);
+    return hip_status(bf ? fp8_launch_fwd_bf16((int)a->act, p, groups, s) : fp8_launch_fwd_f16((int)a->act, p, groups, s));
+}
+
+// ---- linear, backward -------------------------------------------------------------
+struct LinearGradPlan8 {
+    StageAt x, w;
+    Plan8 dx, dw;
+    int64_t off_q = 0, off_s = 0, off_qt = 0, off_st = 0, off_bias = 0, off_part = 0, bytes = 0;
+};
+
+int check_linear_grad8(const ge_linear_fp8_backward_args *a)
+{
+    if (!a) return GEMM_EPI_ERR_NULL_INPUT;
+    GE_CHECK(check_dims(a->M, a->N, a->K));
+    if (a->N > GE_MAX_COLS || a->M > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
+    if (a->M > 0 && !a->dX && !a->dW && !a->dbias) return GEMM_EPI_ERR_NULL_OUTPUT;
+    if (a->act < GE_ACT_IDENTITY || a->act > GE_ACT_SILU) return GEMM_EPI_ERR_KIND;
+    GE_CHECK(check_dtype(a->dtype));
+    GE_CHECK(check_format(a->format));
+    if (a->M > 0) {
+        GE_CHECK(check_matrix(a->dD, a->lddd, a->N, 2, GEMM_EPI_ERR_NULL_INPUT));
+        if (a->act != GE_ACT_IDENTITY) GE_CHECK(check_matrix(a->Z, a->ldz, a->N, 2, GEMM_EPI_ERR_NULL_INPUT));
+        if (a->dW) {
+            GE_CHECK(check_bytes(a->XT, a->ldxt, a->M, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_INPUT));
+            GE_CHECK(check_bytes(a->XTS, a->ldxts, blocks_of(a->M), GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_INPUT));
+        }
+        if (a->dX) {
+            GE_CHECK(check_bytes(a->WT, a->ldwt, a->N, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_INPUT));
+            GE_CHECK(check_bytes(a->WTS, a->ldwts, blocks_of(a->N), GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_INPUT));
+        }
+    }
+    if (a->dX) GE_CHECK(check_matrix(a->dX, a->lddx, a->K, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->dW) GE_CHECK(check_matrix(a->dW, a->lddw, a->K, 2, GEMM_EPI_ERR_NULL_OUTPUT));
+    if (a->dbias && !aligned(a->dbias, 4)) return GEMM_EPI_ERR_ALIGN;
+    return GEMM_EPI_OK;
+}
+
+int plan_linear_grad8(const ge_linear_fp8_backward_args *a, LinearGradPlan8 &pl)
+{
+    GE_CHECK(check_linear_grad8(a));
+    if (a->M == 0) return GEMM_EPI_OK;
+    Layout lay;
+    pl.off_q = lay.take(a->M * round_up(a->N, 16));
+    pl.off_s = lay.take(a->M * round_up(blocks_of(a->N), 4));
+    pl.off_qt = lay.take(a->N * round_up(a->M, 16));
+    pl.off_st = lay.take(a->N * round_up(blocks_of(a->M), 4));
+    if (a->dbias && a->M > kBlock) pl.off_bias = lay.take(blocks_of(a->M) * a->N * 4);
+    int64_t part = 0;
+    if (a->dX) {
+        pl.w = plan_operand(a->WT, a->ldwt, a->WTS, a->ldwts, a->K, blocks_of(a->K), a->N, lay);
+        pl.dx = plan_fp8(a->M, a->K, a->N);
+        if (!plan_fits(pl.dx)) return GEMM_EPI_ERR_SHAPE;
+        part = std::max(part, pl.dx.part_bytes);
+    }
+    if (a->dW) {
+        pl.x = plan_operand(a->XT, a->ldxt, a->XTS, a->ldxts, a->K, a->K, a->M, lay);
+        pl.dw = plan_fp8(a->N, a->K, a->M);
+        if (!plan_fits(pl.dw)) return GEMM_EPI_ERR_SHAPE;
+        part = std::max(part, pl.dw.part_bytes);
+    }
+    pl.off_part = lay.take(part);
+    pl.bytes = lay.bytes;
+    return GEMM_EPI_OK;
+}
+
+template <int SRC, int ACT>
+hipError_t launch_dz3(int format, const QuantParams &q, hipStream_t s)
+{
+    const dim3 g((unsigned)blocks_of(q.C), (unsigned)blocks_of(q.R)), b(256);
+    return format == GE_FP8_E4M3 ? launch(quant_kernel<SRC, false, true, 0, ACT>, g, b, s, q)
+                                 : launch(quant_kernel<SRC, false, true, 1, ACT>, g, b, s, q);
+}
+template <int SRC>
+hipError_t launch_dz2(int act, int format, const QuantParams &q, hipStream_t s)
+{
+    switch (act) {
+    case ACT_RELU: return launch_dz3<SRC, ACT_RELU>(format, q, s);
+    case ACT_GELU: return launch_dz3<SRC, ACT_GELU>(format, q, s);
+    case ACT_SILU: return launch_dz3<SRC, ACT_SILU>(format, q, s);
+    default: return launch_dz3<SRC, ACT_IDENTITY>(format, q, s);
+    }
+}
+
+int run_linear_grad8(const ge_linear_fp8_backward_args *a, const LinearGradPlan8 &pl)
+{
+    hipStream_t s = (hipStream_t)a->stream;
+    char *ws = (char *)a->workspace;
+    const bool bf = a->dtype == GEMM_EPI_BF16, e5m2 = a->format == GE_FP8_E5M2;
+    if (a->M == 0) {
+        if (a->dW) GE_TRY(run_zero(a->dW, a->lddw * 2, a->N, a->K * 2, s));
+        if (a->dbias) GE_TRY(run_zero(a->dbias, a->N * 4, 1, a->N * 4, s));
+        return GEMM_EPI_OK;
+    }
+    QuantParams q = {};
+    q.X = a->dD;
+    q.ldx = a->lddd;
+    q.Z = a->Z;
+    q.ldz = a->ldz;
+    q.R = (int)a->M;
+    q.C = (int)a->N;
+    q.Q = (uint8_t *)ws + pl.off_q;
+    q.ldq = round_up(a->N, 16);
+    q.S = (uint8_t *)ws + pl.off_s;
+    q.lds = round_up(blocks_of(a->N), 4);
+    q.QT = (uint8_t *)ws + pl.off_qt;
+    q.ldqt = round_up(a->M, 16);
+    q.ST = (uint8_t *)ws + pl.off_st;
+    q.ldst = round_up(blocks_of(a->M), 4);
+    const int bands = (int)blocks_of(a->M);
+    q.partial = !a->dbias ? nullptr : bands == 1 ? a->dbias : (float *)(ws + pl.off_bias);
+    GE_TRY(bf ? launch_dz2<QS_BF16>((int)a->act, (int)a->format, q, s)
+              : launch_dz2<QS_F16>((int)a->act, (int)a->format, q, s));
+    if (a->dbias && bands > 1) GE_TRY(run_colsum(q.partial, a->dbias, bands, (int)a->N, s));
+    Staging st;
+    Operand8 w = {(const uint8_t *)a->WT, (const uint8_t *)a->WTS, a->ldwt, a->ldwts};
+    Operand8 x = {(const uint8_t *)a->XT, (const uint8_t *)a->XTS, a->ldxt, a->ldxts};
+    if (a->dX) stage_operand(pl.w, w, a->K, blocks_of(a->K), a->N, ws, st);
+    if (a->dW) stage_operand(pl.x, x, a->K, a->K, a->M, ws, st);
+    GE_TRY(st.run(s));
+    float *part = (float *)(ws + pl.off_part);
+    if (a->dX) {
+        Fp8Params p = {};
+        set_product8(p, pl.dx, a->M, a->K, a->N, {q.Q, q.S, q.ldq, q.lds}, w, 7, e5m2);
+        GE_TRY(run_product8(bf, pl.dx, p, a->dX, a->lddx, part, s));
+    }
+    if (a->dW) {
+        Fp8Params p = {};
+        set_product8(p, pl.dw, a->N, a->K, a->M, {q.QT, q.ST, q.ldqt, q.ldst}, x, 0, e5m2);
+        GE_TRY(run_product8(bf, pl.dw, p, a->dW, a->lddw, part, s));
+    }
+    return GEMM_EPI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ge_quantize_fp8(const ge_quantize_fp8_args *a)
+{
+    GE_CHECK(check_quantize(a));
+    if (a->R == 0) return GEMM_EPI_OK;
+    QuantParams q = {};
+    q.X = a->X;
+    q.ldx = a->ldx;
+    q.R = (int)a->R;
+    q.C = (int)a->C;
+    q.Q = (uint8_t *)a->Q;
+    q.ldq = a->ldq;
+    q.S = (uint8_t *)a->S;
+    q.lds = a->lds;
+    q.QT = (uint8_t *)a->QT;
+    q.ldqt = a->ldqt;
+    q.ST = (uint8_t *)a->ST;
+    q.ldst = a->ldst;
+    return hip_status(
+        launch_quant(a->dtype, a->block == GE_BLOCK_TILE, (int)a->format, q, (hipStream_t)a->stream));
+}
+
+int ge_linear_fp8_workspace(const ge_linear_fp8_args *a, int64_t *bytes)
+{
+    LinearPlan8 pl;
+    GE_CHECK(plan_linear8(a, pl));
+    if (!bytes) return GEMM_EPI_ERR_NULL_OUTPUT;
+    *bytes = pl.bytes;
+    return GEMM_EPI_OK;
+}
+
+int ge_linear_fp8(const ge_linear_fp8_args *a)
+{
+    LinearPlan8 pl;
+    GE_CHECK(plan_linear8(a, pl));
+    GE_CHECK(check_workspace(a->workspace, a->workspace_bytes, pl.bytes));
+    return a->M == 0 ? GEMM_EPI_OK : run_linear8(a, pl);
+}
+
+int ge_linear_fp8_backward_workspace(const ge_linear_fp8_backward_args *a, int64_t *bytes)
+{
+    LinearGradPlan8 pl;
+    GE_CHECK(plan_linear_grad8(a, pl));
+    if (!bytes) return GEMM_EPI_ERR_NULL_OUTPUT;
+    *bytes = pl.bytes;
+    return GEMM_EPI_OK;
+}
+
+int ge_linear_fp8_backward(const ge_linear_fp8_backward_args *a)
+{
+    LinearGradPlan8 pl;
+    GE_CHECK(plan_linear_grad8(a, pl));
+    GE_CHECK(check_workspace(a->workspace, a->workspace_bytes, pl.bytes));
+    return run_linear_grad8(a, pl);
+}
+
+}  // extern "C"

@@ -1,0 +1,292 @@
+// fp8_quant.hpp -- quantisation to 8-bit floating point with a power-of-two
+// scale for each block of 128 (include/fp8_ops.h), alone and of the gradient dZ.
+//
+// A block's largest finite magnitude is a = 1.m 2^k; the largest element of the
+// format is 1.75 2^t (e4m3: t = 8, e5m2: t = 15), so the smallest power of two
+// that holds the block is 2^e, e = k - t, or one more where 1.m > 1.75: adding
+// 0x1FFFFF to the bits of a carries into the exponent in exactly those cases.
+// Division by 2^e is exact, so an element is rounded once.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "linear_gemm.hpp"
+#include "ops_host.hpp"
+
+namespace gemm_epi {
+
+constexpr int kBlock = 128;
+
+struct QuantParams {
+    const void *X;
+    int64_t ldx;
+    int R, C;
+    uint8_t *Q, *S, *QT, *ST;
+    int64_t ldq, lds, ldqt, ldst;
+    // gradient: X is dD; Z and the column sums of dZ over each band of 128 rows
+    const void *Z;
+    int64_t ldz;
+    float *partial;  // [bands][C], or NULL
+};
+
+enum QuantSrc : int { QS_F16 = 0, QS_BF16 = 1, QS_F32 = 2 };
+constexpr int kNoGrad = -1;
+
+// The exponent of a block's scale; top: t of the format.
+__device__ __forceinline__ int block_exponent(float a, int top)
+{
+    const int k = (int)((__builtin_bit_cast(uint32_t, a) + 0x1FFFFFu) >> 23) - 127 - top;
+    return a > 0.0f ? max(k, -127) : 0;
+}
+__device__ __forceinline__ float pow2f(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
+
+// four elements to bytes, the first in the lowest
+template <int FMT>
+__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d)
+{
+    int r = 0;
+    if constexpr (FMT == 0) {
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    } else {
+        r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, r, false);
+        r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
+    }
+    return (uint32_t)r;
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x2 u32x2u __attribute__((aligned(1)));
+typedef u32x4 u32x4u __attribute__((aligned(1)));
+
+// 8 bytes at any address, the first n of which exist
+__device__ __forceinline__ void store_bytes8(uint8_t *p, u32x2 v, int n)
+{
+    if (n >= 8) {
+        *(u32x2u *)p = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; e++)
+        if (e < n) p[e] = (uint8_t)(v[e >> 2] >> ((e & 3) * 8));
+}
+
+// |v|, 0 where it is not finite
+__device__ __forceinline__ float finite_abs(float v)
+{
+    const float a = __builtin_fabsf(v);
+    return a < __builtin_inff() ? a : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// One workgroup quantises one 128 x 128 block of X in registers: thread (tx, ty)
+// holds rows 8 ty .. + 7 of columns 8 tx .. + 7, so a row's maximum is one over
+// 16 adjacent lanes, a column's one over 4 lanes and the 4 waves.  The row-wise bytes
+// leave as they are, 128 bytes a row; the transposed ones are turned around in
+// LDS, 8 rows of a column (8 bytes) at a time.  Bound by the bytes: 2 in, 1 or 2 out.
+// ---------------------------------------------------------------------------
+template <int SRC, bool TILE, bool BOTH, int FMT, int GRAD>
+__global__ __launch_bounds__(256) void quant_kernel(QuantParams p)
+{
+    constexpr int TOP = FMT == 0 ? 8 : 15;
+    constexpr bool BF = SRC == QS_BF16;
+    constexpr int PITCH = 136;  // bytes of a column in LDS: 8-byte aligned, off the bank stride
+    __shared__ float colmax[4][kBlock];
+    __shared__ float tilemax[4];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[BOTH ? kBlock * PITCH : 8];
+    __shared__ float colsum[GRAD >= 0 ? 4 : 1][kBlock];
+    const int tid = threadIdx.x, wave = tid >> 6, tx = tid & 15, ty = tid >> 4;
+    const int r0 = (int)blockIdx.y * kBlock, c0 = (int)blockIdx.x * kBlock;
+    const int rows = min(p.R - r0, kBlock), cols = min(p.C - c0, kBlock);
+    const int n = cols - tx * 8;  // columns that exist from this thread's on
+
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int r = ty * 8 + i;
+        const bool here = r < rows && n > 0;
+        if constexpr (SRC == QS_F32) {
+            const float *x = (const float *)p.X + (int64_t)(r0 + r) * p.ldx + c0 + tx * 8;
+            if (here && n >= 8) {
+                const f32x4 a = *(const f32x4u *)x, b = *(const f32x4u *)(x + 4);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    v[i][e] = a[e];
+                    v[i][4 + e] = b[e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[i][e] = here && e < n ? x[e] : 0.0f;
+            }
+        } else {
+            half8 x = {}, z = {};
+            if (here) x = load8((const _Float16 *)p.X + (int64_t)(r0 + r) * p.ldx + c0 + tx * 8, n);
+            if constexpr (GRAD > ACT_IDENTITY)
+                if (here) z = load8((const _Float16 *)p.Z + (int64_t)(r0 + r) * p.ldz + c0 + tx * 8, n);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                float d = ld16<BF>(x[e]);
+                if constexpr (GRAD == ACT_RELU)
+                    d = ld16<BF>(z[e]) <= 0.0f ? 0.0f : d;  // a mask, as in linear_backward
+                else if constexpr (GRAD > ACT_IDENTITY)
+                    d = e < n && here ? d * lin_act_grad<GRAD>(ld16<BF>(z[e])) : 0.0f;
+                v[i][e] = d;
+            }
+        }
+    }
+
+    if constexpr (GRAD >= 0) {
+        if (p.partial) {
+            float s[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                s[e] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) s[e] += v[i][e];
+                s[e] += __shfl_xor(s[e], 16);
+                s[e] += __shfl_xor(s[e], 32);
+            }
+            if ((tid & 63) < 16) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) colsum[wave][tx * 8 + e] = s[e];
+            }
+            __syncthreads();
+            if (tid < cols)
+                p.partial[(int64_t)blockIdx.y * p.C + c0 + tid] =
+                    (colsum[0][tid] + colsum[1][tid]) + (colsum[2][tid] + colsum[3][tid]);
+        }
+    }
+
+    // the rows' maxima; where one is infinite, the finite elements' alone
+    // (v_max drops a NaN by itself)
+    float rm[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        rm[i] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; e++) rm[i] = __builtin_fmaxf(rm[i], __builtin_fabsf(v[i][e]));
+        if (!(rm[i] < __builtin_inff())) {
+            rm[i] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; e++) rm[i] = __builtin_fmaxf(rm[i], finite_abs(v[i][e]));
+        }
+    }
+    int ex[8];
+    if constexpr (TILE) {
+        float m = rm[0];
+#pragma unroll
+        for (int i = 1; i < 8; i++) m = __builtin_fmaxf(m, rm[i]);
+        m = row16_max(m);
+        m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+        m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+        if ((tid & 63) == 0) tilemax[wave] = m;
+        __syncthreads();
+        m = __builtin_fmaxf(__builtin_fmaxf(tilemax[0], tilemax[1]), __builtin_fmaxf(tilemax[2], tilemax[3]));
+        const int e = block_exponent(m, TOP);
+#pragma unroll
+        for (int i = 0; i < 8; i++) ex[i] = e;
+        if (tid == 0) {
+            if (p.S) p.S[(int64_t)blockIdx.y * p.lds + blockIdx.x] = (uint8_t)(e + 127);
+            if (BOTH) p.ST[(int64_t)blockIdx.x * p.ldst + blockIdx.y] = (uint8_t)(e + 127);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) ex[i] = block_exponent(row16_max(rm[i]), TOP);
+        if (p.S && tx == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (ty * 8 + i < rows)
+                    p.S[(int64_t)(r0 + ty * 8 + i) * p.lds + blockIdx.x] = (uint8_t)(ex[i] + 127);
+        }
+    }
+    if (!BOTH || p.Q) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float f = pow2f(-ex[i]);
+            const u32x2 q = {cvt4<FMT>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f),
+                             cvt4<FMT>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f)};
+            if (ty * 8 + i < rows) store_bytes8(p.Q + (int64_t)(r0 + ty * 8 + i) * p.ldq + c0 + tx * 8, q, n);
+        }
+    }
+    if constexpr (BOTH) {
+        int ec[8];
+        if constexpr (TILE) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) ec[e] = ex[0];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                float m = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) m = __builtin_fmaxf(m, __builtin_fabsf(v[i][e]));
+                if (!(m < __builtin_inff())) {
+                    m = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) m = __builtin_fmaxf(m, finite_abs(v[i][e]));
+                }
+                m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+                m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+                if ((tid & 63) < 16) colmax[wave][tx * 8 + e] = m;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int c = tx * 8 + e;
+                ec[e] = block_exponent(__builtin_fmaxf(__builtin_fmaxf(colmax[0][c], colmax[1][c]),
+                                                       __builtin_fmaxf(colmax[2][c], colmax[3][c])),
+                                       TOP);
+                if (ty == 0 && e < n) p.ST[(int64_t)(c0 + c) * p.ldst + blockIdx.y] = (uint8_t)(ec[e] + 127);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const float f = pow2f(-ec[e]);
+            const u32x2 q = {cvt4<FMT>(v[0][e] * f, v[1][e] * f, v[2][e] * f, v[3][e] * f),
+                             cvt4<FMT>(v[4][e] * f, v[5][e] * f, v[6][e] * f, v[7][e] * f)};
+            *(u32x2 *)(turned + (tx * 8 + e) * PITCH + ty * 8) = q;
+        }
+        __syncthreads();
+        // 8 threads a column, 16 bytes each
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int c = i * 32 + (tid >> 3), at = (tid & 7) * 16, m = rows - at;
+            const u32x2 lo = *(const u32x2 *)(turned + c * PITCH + at), hi = *(const u32x2 *)(turned + c * PITCH + at + 8);
+            if (c < cols && m > 0) {
+                uint8_t *q = p.QT + (int64_t)(c0 + c) * p.ldqt + r0 + at;
+                if (m >= 16) {
+                    *(u32x4u *)q = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                } else {
+                    store_bytes8(q, lo, m);
+                    if (m > 8) store_bytes8(q + 8, hi, m - 8);
+                }
+            }
+        }
+    }
+}
+
+// Operands and scales that the products cannot read in place (rows off the
+// 16-byte rule, scales off the 4-byte rule): copied to rows of ldo bytes, byte
+// by byte.  One grid row per matrix.
+struct PadBytes {
+    const uint8_t *src[4];
+    uint8_t *dst[4];
+    int64_t lds[4], ldo[4], rows[4], cols[4];
+};
+__global__ __launch_bounds__(256) void pad_bytes_kernel(PadBytes p)
+{
+    const int v = blockIdx.y;
+    const int64_t groups = p.ldo[v] / 4, total = p.rows[v] * groups;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / groups, c = (i - r * groups) * 4;
+        const uint8_t *s = p.src[v] + r * p.lds[v] + c;
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (c + e < p.cols[v]) w |= (uint32_t)s[e] << (8 * e);
+        *(uint32_t *)(p.dst[v] + r * p.ldo[v] + c) = w;
+    }
+}
+
+}  // namespace gemm_epi

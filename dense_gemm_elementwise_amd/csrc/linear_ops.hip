@@ -14,85 +14,11 @@
 #include "linear_ops.h"
 #include "linear_small.hpp"
 #include "norm_residual.hpp"
-
-namespace gemm_epi {
-void set_last_hip_error(int e);  // gemm_epi.hip
-}
+#include "ops_host.hpp"
 
 using namespace gemm_epi;
 
 namespace {
-
-constexpr int kCUs = 256;
-
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
-
-int hip_status(hipError_t e)
-{
-    if (e == hipSuccess) return GEMM_EPI_OK;
-    set_last_hip_error((int)e);
-    return GEMM_EPI_ERR_HIP;
-}
-
-#define GE_TRY(call)                                  \
-    do {                                              \
-        const int ge_rc = hip_status(call);           \
-        if (ge_rc != GEMM_EPI_OK) return ge_rc;       \
-    } while (0)
-
-// (arguments convert to the kernel's own parameter types)
-template <typename T>
-struct Same {
-    using type = T;
-};
-template <typename... P>
-hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, typename Same<P>::type... a)
-{
-    void *args[] = {(void *)&a...};
-    return hipLaunchKernel((const void *)kernel, grid, block, args, 0, s);
-}
-
-// a matrix operand: NULL, alignment and row stride
-int check_matrix(const void *p, int64_t ld, int64_t cols, uintptr_t es, int null_status)
-{
-    if (!p) return null_status;
-    if (!aligned(p, es)) return GEMM_EPI_ERR_ALIGN;
-    if (ld < cols || ld > GE_MAX_COLS) return GEMM_EPI_ERR_SHAPE;
-    return GEMM_EPI_OK;
-}
-#define GE_CHECK(call)                          \
-    do {                                        \
-        const int ge_rc = (call);               \
-        if (ge_rc != GEMM_EPI_OK) return ge_rc; \
-    } while (0)
-
-int check_dims(int64_t rows, int64_t rows2, int64_t cols)
-{
-    if (rows < 0 || rows > INT32_MAX - 256 || rows2 < 1 || rows2 > INT32_MAX - 256 || cols < 1 || cols > GE_MAX_COLS)
-        return GEMM_EPI_ERR_SHAPE;
-    return GEMM_EPI_OK;
-}
-int check_dtype(int64_t dtype) { return dtype == GEMM_EPI_F16 || dtype == GEMM_EPI_BF16 ? GEMM_EPI_OK : GEMM_EPI_ERR_DTYPE; }
-
-// A region of the workspace.
-struct Layout {
-    int64_t bytes = 0;
-    int64_t take(int64_t n)
-    {
-        const int64_t at = bytes;
-        bytes = round_up(bytes + n, 256);
-        return at;
-    }
-};
-
-int check_workspace(const void *ws, int64_t have, int64_t need)
-{
-    if (need == 0) return GEMM_EPI_OK;
-    if (!ws || have < need) return GEMM_EPI_ERR_WORKSPACE;
-    return aligned(ws, 16) ? GEMM_EPI_OK : GEMM_EPI_ERR_ALIGN;
-}
 
 constexpr unsigned kAllTiles = 0xF;  // bits: indices into kLinTiles
 
@@ -143,8 +69,6 @@ double product_cost(int64_t M, int64_t N, int64_t K, int tile, int splits)
     return us;
 }
 
-// a launch holds fewer than 2^32 threads: 2^24 workgroups of 256
-constexpr int64_t kMaxGroups = (1 << 24) - 1;
 int64_t product_groups(const ProductPlan &pl) { return (int64_t)pl.tiles_m * pl.tiles_n * pl.splits; }
 bool product_fits(const ProductPlan &pl) { return product_groups(pl) <= kMaxGroups; }
 
@@ -202,9 +126,6 @@ void set_product(LinParams &p, const ProductPlan &pl, int64_t M, int64_t N, int6
     p.group_m = 8;
     p.k_split = (int)pl.k_split;
 }
-
-// rows that the 16-byte DMA of the products can read
-bool dma_rows(const void *p, int64_t ld, int64_t cols) { return cols % 8 == 0 && ld % 8 == 0 && aligned(p, 16); }
 
 // An operand as the products read it: in place, or a padded copy.
 struct Operand16 {
@@ -395,12 +316,6 @@ hipError_t run_grad(const GradPlan &pl, const GradProduct *dx, const GradProduct
     }
     hipError_t e = dx ? run_grad_product<BF>(false, *dx, s) : hipSuccess;
     return e == hipSuccess && dw ? run_grad_product<BF>(true, *dw, s) : e;
-}
-
-hipError_t run_zero(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes, hipStream_t s)
-{
-    const int64_t blocks = std::min<int64_t>(ceil_div(rows * (bytes / 2), 256), 4096);
-    return launch(zero_rows_kernel, dim3((unsigned)blocks), dim3(256), s, (char *)p, ld_bytes, rows, bytes / 2);
 }
 
 // ---- linear -------------------------------------------------------------------
@@ -668,12 +583,7 @@ int run_linear_grad(const ge_linear_backward_args *a, const LinearGradPlan &pl)
         GE_TRY(launch_dz<BF>((int)a->act, q, dim3((unsigned)q.dz_blocks + (stage.n ? stage.blocks : 0u)), s));
         if (!pl.direct) dz = {q.out, pl.N8};
         if (a->dbias && pl.strips > 1) {
-            ColSumParams c = {};
-            c.partial[0] = q.partial;
-            c.out[0] = a->dbias;
-            c.parts[0] = pl.strips;
-            c.ld = c.cols = (int)a->N;
-            GE_TRY(launch(colsum_kernel, dim3((unsigned)ceil_div(a->N, 64)), dim3(1024), s, c));
+            GE_TRY(run_colsum(q.partial, a->dbias, pl.strips, (int)a->N, s));
         }
     }
     GradProduct dx, dw;
@@ -1146,6 +1056,36 @@ int run_norm_grad(const ge_norm_residual_backward_args *a, const NormGradPlan &p
 }
 
 }  // namespace
+
+namespace gemm_epi {
+
+hipError_t run_split_sum_linear(bool bf, int act, const SplitSumParams &q, hipStream_t s)
+{
+    return bf ? launch_split_sum<true, LE_LINEAR>(act, q, s) : launch_split_sum<false, LE_LINEAR>(act, q, s);
+}
+
+hipError_t run_split_sum_out(bool bf, const SplitSumParams &q, hipStream_t s)
+{
+    return bf ? launch_split_sum<true, LE_OUT>(0, q, s) : launch_split_sum<false, LE_OUT>(0, q, s);
+}
+
+hipError_t run_colsum(const float *partial, float *out, int parts, int cols, hipStream_t s)
+{
+    ColSumParams c = {};
+    c.partial[0] = partial;
+    c.out[0] = out;
+    c.parts[0] = parts;
+    c.ld = c.cols = cols;
+    return launch(colsum_kernel, dim3((unsigned)ceil_div(cols, 64)), dim3(1024), s, c);
+}
+
+hipError_t run_zero(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes, hipStream_t s)
+{
+    const int64_t blocks = std::min<int64_t>(ceil_div(rows * (bytes / 2), 256), 4096);
+    return launch(zero_rows_kernel, dim3((unsigned)blocks), dim3(256), s, (char *)p, ld_bytes, rows, bytes / 2);
+}
+
+}  // namespace gemm_epi
 
 extern "C" {
 

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "linear_gemm.hpp"
+#include "ops_host.hpp"
 
 namespace gemm_epi {
 
@@ -424,18 +425,6 @@ __global__ __launch_bounds__(1024) void colsum_kernel(ColSumParams p)
 // lanes-th split (3 x 200 over 64 splits: 19 us in one thread each).  The order is
 // fixed by the plan.
 // ---------------------------------------------------------------------------
-struct SplitSumParams {
-    const float *part;  // [splits][M][ldc]
-    int splits, lanes, M, N;  // lanes: 1, 4 or 8
-    int64_t ldc, c_split;
-    const _Float16 *bias, *R;
-    _Float16 *D, *Z;
-    int64_t ldr, ldd, ldz;
-    float *C32;  // LE_OUT: accumulator, rows of ldc
-    int acc_in, acc_out;
-    const float *alpha;
-};
-
 template <bool BF, int EPI, int ACT>
 __global__ __launch_bounds__(256) void split_sum_kernel(SplitSumParams p)
 {

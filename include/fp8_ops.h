@@ -1,0 +1,183 @@
+/*
+ * fp8_ops.h -- C ABI of the 8-bit products with block scales and of the
+ * mixture-of-experts layer, in libgemm_epi.so (AMD Instinct MI355X, gfx950).
+ *
+ * ge_quantize_fp8         8-bit elements with a power-of-two scale for each block, both orientations in one pass
+ * ge_linear_fp8           Z = X W^T + bias, D = act(Z) + residual, X and W in 8 bits
+ * ge_linear_fp8_backward  dZ = dD act'(Z), quantised; dX = dZ W, dW = dZ^T X, dbias = sum of dZ over rows
+ * ge_moe                  router, top_k experts of each token, their gated products, the weighted sum
+ *
+ * The conventions are those of linear_ops.h: one argument structure of 8-byte
+ * fields, checks on the host before any HIP call, kernels queued on
+ * args->stream and nothing else (the calls record into HIP graphs), scratch
+ * memory of the size that the matching ge_*_workspace call gives, rows of unit
+ * element stride, no atomics on results, sums in fp32, each output rounded once.
+ *
+ * 8-bit matrices.  An element is OCP e4m3 (GE_FP8_E4M3: largest 448, no
+ * infinity) or e5m2 (GE_FP8_E5M2: largest 57344), a scale is one e8m0 byte b: the
+ * power of two 2^(b - 127), and 255 a NaN.  With GE_BLOCK_ROW a matrix (R, C) has scales
+ * (R, ceil(C / 128)), one for 128 consecutive elements of a row; with
+ * GE_BLOCK_TILE (ceil(R / 128), ceil(C / 128)), one for 128 x 128 elements.  The
+ * last block of a row or column may be short.  Rows of 8-bit matrices and of
+ * scales start anywhere; where they start at multiples of 16 and of 4 bytes the
+ * products read them in place, others are copied through the workspace first.
+ *
+ * The 8-bit matrix instruction adds groups of 8 consecutive products in fixed
+ * point, cut 13 binary places below the power of two of the group's largest
+ * product, and the groups' sums in fp32: a product is off by at most 7 2^-13
+ * (largest |x|) (largest |w|) of each group beside the fp32 sums' rounding, measured
+ * 2^-19 of the sum of the magnitudes for normal values.  Integers below 2^13 times
+ * the smallest come out exactly.
+ */
+#ifndef FP8_OPS_H
+#define FP8_OPS_H
+
+#include <stdint.h>
+
+#include "linear_ops.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { GE_FP8_E4M3 = 0, GE_FP8_E5M2 = 1 } ge_fp8;
+typedef enum { GE_BLOCK_ROW = 0, GE_BLOCK_TILE = 1 } ge_block;
+
+#define GE_MOE_MAX_EXPERTS 1024
+#define GE_MOE_MAX_TOP_K 32
+
+/* X (R, C) of dtype (GEMM_EPI_F16, GEMM_EPI_BF16 or GEMM_EPI_F32); Q (R, C) and
+ * its scales S; QT (C, R), X transposed, and its scales ST, or both NULL.  A
+ * block's scale is the smallest power of two s, of at least 2^-127, with
+ * max |x| <= largest s over the block's finite elements, and 1 where they are all
+ * zero; q = x / s to nearest even.  A NaN stays one, an infinity too where the
+ * format has it (e4m3: a NaN).  With GE_BLOCK_ROW the blocks of QT run along its
+ * own rows, with GE_BLOCK_TILE QT and ST are Q and S transposed.  Bytes behind a
+ * row's end are left as they were.  R may be 0.  R and C at most GE_MAX_COLS. */
+typedef struct {
+    int64_t R, C;
+    const void *X;
+    int64_t ldx;
+    void *Q;
+    int64_t ldq;
+    void *S;
+    int64_t lds;
+    void *QT;
+    int64_t ldqt;
+    void *ST;
+    int64_t ldst;
+    int64_t block, format, dtype;
+    void *stream;
+} ge_quantize_fp8_args;
+
+/* X (M, K) in 8 bits (format) with scales XS by GE_BLOCK_ROW, or, with XS NULL,
+ * of dtype, and then quantised by GE_BLOCK_ROW to format within the call; W (N, K)
+ * in e4m3 with scales WS by GE_BLOCK_TILE; bias (N) or NULL, residual (M, N) or
+ * NULL, D (M, N), Z (M, N) or NULL, all of dtype (GEMM_EPI_F16 or GEMM_EPI_BF16).
+ * act: ge_act.  D may be the residual itself.  M may be 0. */
+typedef struct {
+    int64_t M, N, K;
+    const void *X;
+    int64_t ldx;
+    const void *XS;
+    int64_t ldxs;
+    const void *W;
+    int64_t ldw;
+    const void *WS;
+    int64_t ldws;
+    const void *bias;
+    const void *residual;
+    int64_t ldr;
+    void *D;
+    int64_t ldd;
+    void *Z;
+    int64_t ldz;
+    int64_t act, dtype, format;
+    void *workspace;
+    int64_t workspace_bytes;
+    void *stream;
+} ge_linear_fp8_args;
+
+/* dD (M, N), Z (M, N) as ge_linear_fp8 kept it (not read, and may be NULL, for
+ * the identity); XT (K, M) e4m3 with scales XTS by GE_BLOCK_ROW and WT (K, N)
+ * e4m3 with scales WTS by GE_BLOCK_TILE: X and W transposed, as ge_quantize_fp8
+ * makes them.  dX (M, K), dW (N, K) of dtype, dbias (N) fp32, each NULL where it
+ * is not wanted.  dZ = dD act'(Z) is quantised to format from fp32, along its rows for
+ * dX = dZ W and along its columns for dW = dZ^T X; dbias sums it unquantised.  The
+ * gradient is that of the product at the quantised X and W.  M at most
+ * GE_MAX_COLS (a row of XT); with M = 0, dW and dbias are set to zero. */
+typedef struct {
+    int64_t M, N, K;
+    const void *dD;
+    int64_t lddd;
+    const void *XT;
+    int64_t ldxt;
+    const void *XTS;
+    int64_t ldxts;
+    const void *WT;
+    int64_t ldwt;
+    const void *WTS;
+    int64_t ldwts;
+    const void *Z;
+    int64_t ldz;
+    void *dX;
+    int64_t lddx;
+    void *dW;
+    int64_t lddw;
+    float *dbias;
+    int64_t act, dtype, format;
+    void *workspace;
+    int64_t workspace_bytes;
+    void *stream;
+} ge_linear_fp8_backward_args;
+
+/* X (T, hidden) of dtype, Wr (experts, hidden) of dtype.  Up: for each expert,
+ * up_stride elements apart, a matrix of `inner` rows (gated = 0) or of 2 inner rows, the
+ * gate's first (gated = 1), of `hidden` columns; Down: for each expert a matrix
+ * (hidden, inner).  Both are of dtype, with US and DS NULL, or e4m3 with
+ * scales by GE_BLOCK_TILE (US: us_stride bytes between experts).
+ *   p = softmax of X Wr^T; each token takes the top_k experts of the largest
+ *   logits (ties: the lowest index), weight p, or with renormalize p over the
+ *   sum of the chosen ones;
+ *   h = act(Up x), gated: act(gate) up, rounded to dtype;
+ *   D = residual + sum over the chosen experts of weight Down h.
+ * D (T, hidden) may be the residual (or NULL: none), not X.  A NaN logit ranks below
+ * every number and makes the token's weights NaN.  T may be 0, and any number: the
+ * weights are read once for each 64 tokens. */
+typedef struct {
+    int64_t T, hidden, experts, inner, top_k;
+    const void *X;
+    int64_t ldx;
+    const void *Wr;
+    int64_t ldwr;
+    const void *Up;
+    int64_t ldu, up_stride;
+    const void *US;
+    int64_t ldus, us_stride;
+    const void *Down;
+    int64_t lddn, down_stride;
+    const void *DS;
+    int64_t ldds, ds_stride;
+    const void *residual;
+    int64_t ldr;
+    void *D;
+    int64_t ldd;
+    int64_t act, gated, renormalize, dtype;
+    void *workspace;
+    int64_t workspace_bytes;
+    void *stream;
+} ge_moe_args;
+
+int ge_quantize_fp8(const ge_quantize_fp8_args *args);
+int ge_linear_fp8(const ge_linear_fp8_args *args);
+int ge_linear_fp8_workspace(const ge_linear_fp8_args *args, int64_t *bytes);
+int ge_linear_fp8_backward(const ge_linear_fp8_backward_args *args);
+int ge_linear_fp8_backward_workspace(const ge_linear_fp8_backward_args *args, int64_t *bytes);
+int ge_moe(const ge_moe_args *args);
+int ge_moe_workspace(const ge_moe_args *args, int64_t *bytes);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP8_OPS_H */
