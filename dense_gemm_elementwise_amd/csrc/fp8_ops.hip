@@ -2,6 +2,7 @@
 // argument checks, plans (tiles, splits, workspace layout) and launches.
 #include <hip/hip_runtime.h>
 #include <algorithm>
+#include <math.h>
 #include <stdint.h>
 
 #include "fp8_launch.hpp"
@@ -119,21 +120,77 @@ void stage_operand(const StageAt &at, Operand8 &o, int64_t rows, int64_t srows, 
 
 // ---- products -------------------------------------------------------------------
 struct Plan8 {
-    int splits = 1;
+    int tile = kFp8Small, splits = 1;
     int64_t tiles_m = 0, tiles_n = 0, k_split = 0, part_bytes = 0;
 };
-bool plan_fits(const Plan8 &p) { return p.tiles_m * p.tiles_n * p.splits <= kMaxGroups; }
+int64_t plan_groups(const Plan8 &p) { return p.tiles_m * p.tiles_n * p.splits; }
+bool plan_fits(const Plan8 &p) { return plan_groups(p) <= kMaxGroups; }
+
+// Estimated microseconds of a tile and split, fitted to timings of all of them on
+// 34 shapes (128^3 to 8192^3, 32 rows against 4096 x 4096, 300 x 300 x 8192): a
+// round of workgroups costs a fixed time and a time per unit of K, which grows
+// with the share of the chip at work.  Fixed us, and ns per unit of K from few
+// workgroups to a full chip:
+//   256 x 256               10.7;  7.7 .. 8.6
+//   128 x 256                7.7;  4.0 .. 5.2
+//   128 x 128, deep rings    5.5;  2.5 .. 3.1   (4.7; 3.1 .. 5.6 with the others)
+//   128 x 128, two on a CU   6.5;  5.9
+// Past two rounds the last one costs a third of one.  A split adds a launch and its
+// partial sums' round trip.  The pick was within 5% of the fastest on all 34 (for
+// instance 2400 x 3232 x 4096: 128 x 256 29.7, 128 x 128 32.5, 256 x 256 43.2;
+// 1536 x 1536 x 4096: deep 16.6, 24.1 without; 1024 x 1024 x 8192: 27.3, in
+// 4 splits 21.0).  256 x 128 was no faster than 128 x 256 by more than 3%.
+double cost8(int64_t M, int64_t N, int64_t K, int tile, int splits)
+{
+    const Fp8Tile t = kFp8Tiles[tile];
+    const double groups = (double)(ceil_div(M, t.bm) * ceil_div(N, t.bn) * splits);
+    const double k = (double)round_up(ceil_div(K, splits), splits > 1 ? 512 : 128) * 1e-3;
+    const double share = std::min(1.0, groups / kCUs);
+    double slots = kCUs, round;
+    switch (tile) {
+    case kFp8Big: round = 10.7 + k * (7.7 + 0.9 * share); break;
+    case kFp8Wide: round = 7.7 + k * (4.0 + 1.1 * share); break;
+    case kFp8Deep: round = 5.5 + k * (2.5 + 0.6 * share); break;
+    default:
+        if (groups > kCUs) slots = 2 * kCUs;
+        round = groups > kCUs ? 6.5 + k * 5.9 : 4.7 + k * (3.1 + 2.5 * share);
+    }
+    const double rounds = groups / slots;
+    double us = round * (rounds <= 2.0 ? ceil(rounds) : rounds + 0.34);
+    if (splits > 1) us += 3.5 + 0.04 * splits + (double)splits * M * N * 8 / 8.8e6;
+    return us;
+}
+
+// The cheapest plan of those whose grid one launch holds.  k_split is a multiple of
+// 512: four blocks, a dword of scales.
 Plan8 plan_fp8(int64_t M, int64_t N, int64_t K)
 {
-    Plan8 p;
-    p.tiles_m = ceil_div(M, 128);
-    p.tiles_n = ceil_div(N, 128);
-    p.k_split = round_up(K, 512);
-    return p;
+    Plan8 best;
+    double least = 0;
+    for (int i = 0; i < (int)(sizeof(kFp8Tiles) / sizeof(kFp8Tiles[0])); i++) {
+        const Fp8Tile t = kFp8Tiles[i];
+        for (int want = 1; want <= 16; want *= 2) {
+            Plan8 p;
+            p.tile = i;
+            p.tiles_m = ceil_div(M, t.bm);
+            p.tiles_n = ceil_div(N, t.bn);
+            if (want > 1 && (K < want * 512 || p.tiles_m * p.tiles_n * want > 4 * kCUs)) break;
+            p.k_split = round_up(ceil_div(K, want), 512);
+            p.splits = (int)ceil_div(K, p.k_split);
+            p.part_bytes = p.splits > 1 ? p.splits * M * round_up(N, 8) * 4 : 0;
+            const double c = cost8(M, N, K, i, p.splits);
+            const bool fits = plan_fits(p), best_fits = best.tiles_m > 0 && plan_fits(best);
+            if (best.tiles_m == 0 || (fits == best_fits ? c < least : fits)) {
+                best = p;
+                least = c;
+            }
+        }
+    }
+    return best;
 }
 
 void set_product8(Fp8Params &p, const Plan8 &pl, int64_t M, int64_t N, int64_t K, const Operand8 &a, const Operand8 &b,
-                  int shift_b, bool a_e5m2)
+                  int shift_b)
 {
     p.A = a.q;
     p.SA = a.s;
@@ -145,7 +202,6 @@ void set_product8(Fp8Params &p, const Plan8 &pl, int64_t M, int64_t N, int64_t K
     p.ldsb = b.lds;
     p.K = (int)K;
     p.shift_b = shift_b;
-    p.a_e5m2 = a_e5m2;
     p.e.M = (int)M;
     p.e.N = (int)N;
     p.e.tiles_m = (int)pl.tiles_m;
@@ -155,23 +211,26 @@ void set_product8(Fp8Params &p, const Plan8 &pl, int64_t M, int64_t N, int64_t K
     p.e.k_split = (int)pl.k_split;
 }
 
-// C = A B^T into D (16-bit)
-hipError_t run_product8(bool bf, const Plan8 &pl, Fp8Params p, void *D, int64_t ldd, float *part, hipStream_t s)
+hipError_t launch_fwd8(bool bf, bool e5m2, int act, int tile, const Fp8Params &p, int groups, hipStream_t s)
 {
-    const int groups = (int)(pl.tiles_m * pl.tiles_n * pl.splits);
-    if (pl.splits == 1) {
-        p.e.D = (_Float16 *)D;
-        p.e.ldd = ldd;
-        p.e.vec = dma_rows(D, ldd, p.e.N);
-        return bf ? fp8_launch_out_bf16(p, groups, s) : fp8_launch_out_f16(p, groups, s);
-    }
+    if (e5m2)
+        return bf ? fp8_launch_fwd_e5m2_bf16(act, tile, p, groups, s) : fp8_launch_fwd_e5m2_f16(act, tile, p, groups, s);
+    return bf ? fp8_launch_fwd_e4m3_bf16(act, tile, p, groups, s) : fp8_launch_fwd_e4m3_f16(act, tile, p, groups, s);
+}
+hipError_t launch_out8(bool bf, bool e5m2, int tile, const Fp8Params &p, int groups, hipStream_t s)
+{
+    if (e5m2) return bf ? fp8_launch_out_e5m2_bf16(tile, p, groups, s) : fp8_launch_out_e5m2_f16(tile, p, groups, s);
+    return bf ? fp8_launch_out_e4m3_bf16(tile, p, groups, s) : fp8_launch_out_e4m3_f16(tile, p, groups, s);
+}
+
+// Turns a product into one that leaves fp32 partial sums at `part`; returns their sum's operands.
+SplitSumParams set_split8(Fp8Params &p, const Plan8 &pl, float *part)
+{
     const int64_t ldc = round_up(p.e.N, 8);
     p.e.C32 = part;
     p.e.ldc = ldc;
     p.e.c_split = p.e.M * ldc;
     p.e.acc_out = 1;
-    const hipError_t e = bf ? fp8_launch_out_bf16(p, groups, s) : fp8_launch_out_f16(p, groups, s);
-    if (e != hipSuccess) return e;
     SplitSumParams q = {};
     q.part = part;
     q.splits = pl.splits;
@@ -179,6 +238,22 @@ hipError_t run_product8(bool bf, const Plan8 &pl, Fp8Params p, void *D, int64_t 
     q.N = p.e.N;
     q.ldc = ldc;
     q.c_split = p.e.c_split;
+    return q;
+}
+
+// C = A B^T into D (16-bit)
+hipError_t run_product8(bool bf, bool e5m2, const Plan8 &pl, Fp8Params p, void *D, int64_t ldd, float *part, hipStream_t s)
+{
+    const int groups = (int)plan_groups(pl);
+    if (pl.splits == 1) {
+        p.e.D = (_Float16 *)D;
+        p.e.ldd = ldd;
+        p.e.vec = dma_rows(D, ldd, p.e.N);
+        return launch_out8(bf, e5m2, pl.tile, p, groups, s);
+    }
+    SplitSumParams q = set_split8(p, pl, part);
+    const hipError_t e = launch_out8(bf, e5m2, pl.tile, p, groups, s);
+    if (e != hipSuccess) return e;
     q.D = (_Float16 *)D;
     q.ldd = ldd;
     return run_split_sum_out(bf, q, s);
@@ -260,7 +335,21 @@ int run_linear8(const ge_linear_fp8_args *a, const LinearPlan8 &pl)
     stage_operand(pl.w, w, a->N, blocks_of(a->N), a->K, ws, st);
     GE_TRY(st.run(s));
     Fp8Params p = {};
-    set_product8(p, pl.pl, a->M, a->N, a->K, x, w, 7, a->format == GE_FP8_E5M2);
+    set_product8(p, pl.pl, a->M, a->N, a->K, x, w, 7);
+    const bool e5m2 = a->format == GE_FP8_E5M2;
+    const int groups = (int)plan_groups(pl.pl);
+    if (pl.pl.splits > 1) {
+        SplitSumParams q = set_split8(p, pl.pl, (float *)(ws + pl.off_part));
+        q.bias = (const _Float16 *)a->bias;
+        q.R = (const _Float16 *)a->residual;
+        q.D = (_Float16 *)a->D;
+        q.Z = (_Float16 *)a->Z;
+        q.ldr = a->ldr;
+        q.ldd = a->ldd;
+        q.ldz = a->ldz;
+        GE_TRY(launch_out8(bf, e5m2, pl.pl.tile, p, groups, s));
+        return hip_status(run_split_sum_linear(bf, (int)a->act, q, s));
+    }
     p.e.bias = (const _Float16 *)a->bias;
     p.e.R = (const _Float16 *)a->residual;
     p.e.D = (_Float16 *)a->D;
@@ -270,8 +359,7 @@ int run_linear8(const ge_linear_fp8_args *a, const LinearPlan8 &pl)
     p.e.ldz = a->ldz;
     p.e.vec = dma_rows(a->D, a->ldd, a->N) && (!a->Z || dma_rows(a->Z, a->ldz, a->N)) &&
               (!a->residual || dma_rows(a->residual, a->ldr, a->N));
-    const int groups = (int)(pl.pl.tiles_m * pl.pl.tiles_n);
-    return hip_status(bf ? fp8_launch_fwd_bf16((int)a->act, p, groups, s) : fp8_launch_fwd_f16((int)a->act, p, groups, s));
+    return hip_status(launch_fwd8(bf, e5m2, (int)a->act, pl.pl.tile, p, groups, s));
 }
 
 // ---- linear, backward -------------------------------------------------------------
@@ -393,13 +481,13 @@ int run_linear_grad8(const ge_linear_fp8_backward_args *a, const LinearGradPlan8
     float *part = (float *)(ws + pl.off_part);
     if (a->dX) {
         Fp8Params p = {};
-        set_product8(p, pl.dx, a->M, a->K, a->N, {q.Q, q.S, q.ldq, q.lds}, w, 7, e5m2);
-        GE_TRY(run_product8(bf, pl.dx, p, a->dX, a->lddx, part, s));
+        set_product8(p, pl.dx, a->M, a->K, a->N, {q.Q, q.S, q.ldq, q.lds}, w, 7);
+        GE_TRY(run_product8(bf, e5m2, pl.dx, p, a->dX, a->lddx, part, s));
     }
     if (a->dW) {
         Fp8Params p = {};
-        set_product8(p, pl.dw, a->N, a->K, a->M, {q.QT, q.ST, q.ldqt, q.ldst}, x, 0, e5m2);
-        GE_TRY(run_product8(bf, pl.dw, p, a->dW, a->lddw, part, s));
+        set_product8(p, pl.dw, a->N, a->K, a->M, {q.QT, q.ST, q.ldqt, q.ldst}, x, 0);
+        GE_TRY(run_product8(bf, e5m2, pl.dw, p, a->dW, a->lddw, part, s));
     }
     return GEMM_EPI_OK;
 }

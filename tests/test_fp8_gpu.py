@@ -248,6 +248,21 @@ def test_linear_from_16_bits(M, N, K, dtype):
     check_product(d, z, value(x8, xs, "row"), value(w8, ws, "tile"), bias, residual, "silu", t)
 
 
+# each tile and a split contraction: (rows, columns, length) that the plan gives to 256 x 256, 128 x 256, two 128 x 128
+# on a compute unit, one with deep rings, and splits
+LARGE = [(4096, 4104, 650), (4000, 2500, 1037), (1100, 4096, 4096), (700, 8190, 900), (8200, 1000, 384),
+         (1536, 1537, 1000), (128, 8192, 4000), (300, 310, 8190)]
+
+
+@pytest.mark.parametrize("format", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("M, N, K", LARGE)
+def test_linear_large(M, N, K, format):
+    x8, xs, w8, ws = operands(M, N, K, M + N + K, format)
+    bias, residual = normal(N, seed=9, std=0.5, to=torch.bfloat16), normal(M, N, seed=10, to=torch.bfloat16)
+    d, z = ge.linear_fp8(x8, w8, ws, bias, residual, x_scale=xs, act="silu", save_z=True)
+    check_product(d, z, value(x8, xs, "row"), value(w8, ws, "tile"), bias, residual, "silu", torch.bfloat16)
+
+
 @pytest.mark.parametrize("M, N, K", [(1, 3000, 4096), (8, 3000, 4096), (300, 515, 1283), (600, 600, 8192)])
 def test_linear_error_on_average(M, N, K):
     """The cut of the 8-bit MFMA on average: a group loses at most 7 2^-13 of its largest product, the mean of which is
@@ -342,7 +357,7 @@ def test_linear_empty_batch():
 # ---- its gradient ----------------------------------------------------------------------
 
 GRAD_SHAPES = [(1, 1, 1), (1, 200, 300), (3, 129, 127), (128, 128, 128), (130, 70, 260), (300, 515, 383),
-               (1000, 33, 640), (257, 2048, 129)]
+               (1000, 33, 640), (257, 2048, 129), (3000, 1300, 2050), (5000, 200, 300)]
 
 
 @pytest.mark.parametrize("format", ["e4m3", "e5m2"])
