@@ -70,23 +70,31 @@ int plan_moe(const ge_moe_args *a, MoePlan &pl)
     return GEMM_EPI_OK;
 }
 
+// One block of 16 tokens at a time, or two where the experts have 12 and more on average.
 template <bool BF, bool W8, int ACT, bool GATED>
-hipError_t launch_up(const MoeParams &q, hipStream_t s)
+hipError_t launch_up(const MoeParams &q, int by_choice, int shared, dim3 g, hipStream_t s)
 {
-    const dim3 g((unsigned)ceil_div(q.I, 16), (unsigned)(q.T * q.k)), b(256);
-    if (q.T <= 16) return launch(moe_up_kernel<BF, W8, ACT, GATED, 1>, g, b, s, q);
-    return launch(moe_up_kernel<BF, W8, ACT, GATED, 4>, g, b, s, q);
+    if (q.T > 16 && q.T * q.k >= 12 * q.E)
+        return launch(moe_up_kernel<BF, W8, ACT, GATED, 2>, g, dim3(256), s, q, by_choice, shared);
+    return launch(moe_up_kernel<BF, W8, ACT, GATED, 1>, g, dim3(256), s, q, by_choice, shared);
 }
 template <bool BF, bool W8, int ACT>
 hipError_t launch_moe2(const MoeParams &q, hipStream_t s)
 {
-    const dim3 rg((unsigned)ceil_div(q.E, 16), (unsigned)ceil_div(q.T, 16));
-    hipError_t e = launch(moe_router_kernel<BF>, rg, dim3(1024), s, q);
-    if (e == hipSuccess) e = q.gated ? launch_up<BF, W8, ACT, true>(q, s) : launch_up<BF, W8, ACT, false>(q, s);
+    hipError_t e = launch(moe_router_kernel<BF>, dim3((unsigned)ceil_div(q.E, 4), (unsigned)ceil_div(q.T, 4)), dim3(256),
+                          s, q);
     if (e != hipSuccess) return e;
-    const dim3 g((unsigned)ceil_div(q.H, 16)), b(512);
-    if (q.T <= 16) return launch(moe_down_kernel<BF, W8, 1>, g, b, s, q);
-    return launch(moe_down_kernel<BF, W8, 4>, g, b, s, q);
+    // workgroups by expert, or by choice where those are fewer
+    const int by_choice = q.T * q.k < q.E;
+    const int64_t rows = by_choice ? q.T * q.k : q.E;
+    // a wave to a tile of 16 inner rows where that fills the chip's 8 waves a compute unit
+    const int64_t row_tiles = ceil_div(q.I, 16);
+    const int shared = rows * row_tiles < 8 * kCUs;
+    const dim3 g((unsigned)(shared ? row_tiles : ceil_div(row_tiles, 4)), (unsigned)rows);
+    e = q.gated ? launch_up<BF, W8, ACT, true>(q, by_choice, shared, g, s)
+                : launch_up<BF, W8, ACT, false>(q, by_choice, shared, g, s);
+    if (e != hipSuccess) return e;
+    return launch(moe_down_kernel<BF, W8>, dim3((unsigned)ceil_div(q.H, 16)), dim3(64 * kDownWaves), s, q);
 }
 template <bool BF, bool W8>
 hipError_t launch_moe(int act, const MoeParams &q, hipStream_t s)

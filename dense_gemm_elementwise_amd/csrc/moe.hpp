@@ -2,15 +2,17 @@
 //
 // Three kernels for a chunk of up to 64 tokens: the router's logits; the
 // chosen experts' up products with the activation; their down products with the
-// weighted sum.  All are bound by reading the chosen experts' weights once, so
-// the weights go from memory straight into the operand layout of 16x16x32
-// MFMAs, against all the chunk's tokens (the columns of up to 4 blocks), and the
-// matrix units wait for memory.  No kernel waits for another's workgroups: each
-// derives from the logits what it needs of the choice.
+// weighted sum.  All are bound by reading the chosen experts' weights once.  They
+// are one operand of 16x16x32 MFMAs, whose other operand are the tokens that
+// chose the expert (16 rows), and the matrix units wait for memory.  No kernel waits for another's
+// workgroups: each derives from the logits what it needs of the choice (one
+// kernel for router and experts would need a wait across the whole grid).
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "linear_gemm.hpp"
 #include "ops_host.hpp"
@@ -47,164 +49,387 @@ __device__ __forceinline__ uint32_t logit_key(float v)
 
 typedef int i32x4b __attribute__((ext_vector_type(4), aligned(1)));
 
-// A lane's 16 consecutive k of a row from column k on (n exist) as the operands of two MFMAs.
+// A lane's 16 consecutive columns of a row, as the operands of two MFMAs.
 struct Pair8 {
     half8 v[2];
 };
-__device__ __forceinline__ Pair8 load16(const _Float16 *p, int n) { return {{load8(p, n), load8(p + 8, n - 8)}}; }
+// v moved down by n bytes (0 .. 16), zeros behind
+__device__ __forceinline__ i32x4 move_down(i32x4 v, int n)
+{
+    const uint64_t lo = (uint64_t)(uint32_t)v[1] << 32 | (uint32_t)v[0], hi = (uint64_t)(uint32_t)v[3] << 32 | (uint32_t)v[2];
+    const int s = n * 8 & 63;
+    const uint64_t high = hi >> s, low = lo >> s | (s ? hi << (64 - s) : 0);
+    const uint64_t a = n >= 16 ? 0 : n >= 8 ? high : low, b = n >= 8 ? 0 : high;
+    return i32x4{(int)(uint32_t)a, (int)(uint32_t)(a >> 32), (int)(uint32_t)b, (int)(uint32_t)(b >> 32)};
+}
+// 16 bytes at any element-aligned address
+template <int ES>
+__device__ __forceinline__ i32x4 load_piece(const char *p) { return *(const i32x4b *)p; }
+// The same where a row of K elements of ES bytes ends inside them or before (n
+// exist; the rest are zeros), without reading outside the row: its last 16 bytes,
+// moved down; of a shorter row element by element.
+template <int ES>
+__device__ __forceinline__ i32x4 load_piece_end(const char *p, int n, int K)
+{
+    constexpr int P = 16 / ES;
+    if (K >= P) {
+        const int miss = max(P - n, 0);
+        return move_down(load_piece<ES>(p - (int64_t)miss * ES), min(miss, P) * ES);
+    }
+    uint32_t v[4] = {};
+#pragma unroll 1
+    for (int e = 0; e < P; e++) {  // (the elements move down, one after the other)
+        const char *at = p + (int64_t)min(e, n - 1) * ES;
+        const uint32_t x = ES == 1 ? *(const uint8_t *)at : *(const uint16_t *)at;
+#pragma unroll
+        for (int d = 0; d < 3; d++) v[d] = v[d] >> (8 * ES) | v[d + 1] << (32 - 8 * ES);
+        v[3] = v[3] >> (8 * ES) | (e < n ? x << (32 - 8 * ES) : 0);
+    }
+    return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+}
 template <bool BF>
 __device__ __forceinline__ Pair8 widen(i32x4 q)
 {
     // e4m3 has fewer digits and a smaller range than either 16-bit type: exact
-    Pair8 r;
+    i32x4 r[2];
 #pragma unroll
     for (int u = 0; u < 4; u++) {
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            uint32_t w;
-            if constexpr (BF)
-                w = __builtin_bit_cast(uint32_t, h ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[u], 1.0f, true)
-                                                   : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[u], 1.0f, false));
-            else
-                w = __builtin_bit_cast(uint32_t, h ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[u], 1.0f, true)
-                                                   : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[u], 1.0f, false));
-            const int at = (u & 1) * 4 + h * 2;
-            r.v[u >> 1][at] = __builtin_bit_cast(_Float16, (uint16_t)w);
-            r.v[u >> 1][at + 1] = __builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
+        int lo, hi;
+        if constexpr (BF) {
+            lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[u], 1.0f, false));
+            hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[u], 1.0f, true));
+        } else {
+            lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[u], 1.0f, false));
+            hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[u], 1.0f, true));
         }
+        r[u >> 1][(u & 1) * 2] = lo;
+        r[u >> 1][(u & 1) * 2 + 1] = hi;
     }
-    return r;
+    return {{__builtin_bit_cast(half8, r[0]), __builtin_bit_cast(half8, r[1])}};
 }
-// 16 bytes at any address, the first n of which exist (the rest read as zeros)
-__device__ __forceinline__ i32x4 load_bytes16(const uint8_t *p, int n)
-{
-    if (n >= 16) return *(const i32x4b *)p;
-    i32x4 v = {};
-#pragma unroll
-    for (int e = 0; e < 15; e++)
-        if (e < n) v[e >> 2] |= (int)p[e] << (8 * (e & 3));
-    return v;
-}
-
+// Lane (li, lg) ends with 4 tokens (4 lg ..) of weight row li, so that a row's scale is the lane's own.
 template <bool BF>
-__device__ __forceinline__ f32x4 mfma_pair(const Pair8 &w, const Pair8 &x, f32x4 acc)
+__device__ __forceinline__ f32x4 mfma_pair(const Pair8 &x, const Pair8 &w, f32x4 acc)
 {
 #pragma unroll
     for (int u = 0; u < 2; u++) {
         if constexpr (BF)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v[u]),
-                                                          __builtin_bit_cast(bf16x8, x.v[u]), acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x.v[u]),
+                                                          __builtin_bit_cast(bf16x8, w.v[u]), acc, 0, 0, 0);
         else
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[u], x.v[u], acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.v[u], w.v[u], acc, 0, 0, 0);
     }
     return acc;
 }
 
-// logits [T][E]: a workgroup takes 16 experts and 16 tokens, its 16 waves parts of the contraction.
+// logits [T][E]: a wave takes one expert and up to 4 tokens, 8 columns a lane and turn.
+// (In MFMAs, 16 experts a workgroup, the few workgroups' loads took 6.3 us for
+// one token and 64 experts of 4096, and 10 us for 64 tokens; this 3.9 and 6.)
 template <bool BF>
-__global__ __launch_bounds__(1024) void moe_router_kernel(MoeParams p)
+__global__ __launch_bounds__(256) void moe_router_kernel(MoeParams p)
 {
-    __shared__ float red[16][64][4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, lg = lane >> 4;
-    const int e0 = (int)blockIdx.x * 16, t0 = (int)blockIdx.y * 16;
-    const _Float16 *w = p.Wr + (int64_t)min(e0 + li, p.E - 1) * p.ldwr;
-    const _Float16 *x = p.X + (int64_t)min(t0 + li, p.T - 1) * p.ldx;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = wave * 64 + lg * 16; k - lg * 16 < p.H; k += 1024)
-        acc = mfma_pair<BF>(load16(w + k, p.H - k), load16(x + k, p.H - k), acc);
-    *(f32x4 *)red[wave][lane] = acc;
-    __syncthreads();
-    if (tid < 256) {
-        const int t = tid >> 4, e = tid & 15;  // token t is lane t of a row of lanes, expert 4 lg + r
-        float s = 0.0f;
+    const int lane = threadIdx.x & 63, e = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6), t0 = (int)blockIdx.y * 4;
+    if (e >= p.E) return;
+    const _Float16 *w = p.Wr + (int64_t)e * p.ldwr;
+    const _Float16 *x[4];
+    float acc[4] = {};
 #pragma unroll
-        for (int u = 0; u < 16; u++) s += red[u][(e >> 2) * 16 + t][e & 3];
-        if (t0 + t < p.T && e0 + e < p.E) p.logits[(int64_t)(t0 + t) * p.E + e0 + e] = s;
-    }
-}
-
-// The weights of one operand row block: 16-bit, or 8-bit with block scales.
-template <bool BF, bool W8>
-struct MoeRows {
-    const void *row;      // this lane's row
-    const uint8_t *s[2];  // 8-bit: scales of the tile of the block's first and last row
-    int edge;             // rows from this one on are of the second tile
-    __device__ __forceinline__ void init(const void *base, int64_t ld, const uint8_t *scales, int64_t lds, int r0,
-                                         int rows, int li)
-    {
-        const int64_t at = (int64_t)min(r0 + li, rows - 1) * ld;
-        if constexpr (W8) {
-            row = (const uint8_t *)base + at;
-            const int last = min(r0 + 15, rows - 1);
-            s[0] = scales + (int64_t)(r0 >> 7) * lds;
-            s[1] = scales + (int64_t)(last >> 7) * lds;
-            edge = (last >> 7 << 7) - r0;
-        } else {
-            row = (const _Float16 *)base + at;
+    for (int t = 0; t < 4; t++) x[t] = p.X + (int64_t)min(t0 + t, p.T - 1) * p.ldx;
+    auto add = [&](half8 wv, half8 xv, int t) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[t] = __builtin_fmaf(ld16<BF>(wv[i]), ld16<BF>(xv[i]), acc[t]);
+    };
+    int k = lane * 8;
+    const int some = min(4, p.T - t0);
+    for (; k + 1536 + 8 <= p.H; k += 2048) {
+        half8 wv[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) wv[u] = *(const half8u *)(w + k + u * 512);
+#pragma unroll
+        for (int t = 0; t < 4; t++) {
+            if (t >= some) break;
+            half8 xv[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++) xv[u] = *(const half8u *)(x[t] + k + u * 512);
+#pragma unroll
+            for (int u = 0; u < 4; u++) add(wv[u], xv[u], t);
         }
     }
-    __device__ __forceinline__ Pair8 load(int k, int K) const
-    {
-        if constexpr (W8)
-            return widen<BF>(load_bytes16((const uint8_t *)row + k, K - k));
-        else
-            return load16((const _Float16 *)row + k, K - k);
-    }
-    // the scales of a lane's four rows (4 lg + r) in block b
-    __device__ __forceinline__ f32x4 scale(int b, int lg) const
-    {
-        const uint32_t a = s[0][b], c = s[1][b];
-        f32x4 v;
+    for (; k < p.H; k += 512) {
+        const half8 wv = load8(w + k, p.H - k);
 #pragma unroll
-        for (int r = 0; r < 4; r++) v[r] = e8m0(4 * lg + r < edge ? a : c);
-        return v;
+        for (int t = 0; t < 4; t++) add(wv, load8(x[t] + k, p.H - k), t);
     }
-    __device__ static __forceinline__ float e8m0(uint32_t b)
+    float v = 0.0f;  // lane t: token t0 + t
+#pragma unroll
+    for (int t = 0; t < 4; t++) {
+        float a = row16_sum(acc[t]);
+        a += __shfl_xor(a, 16);
+        a += __shfl_xor(a, 32);
+        if (lane == t) v = a;
+    }
+    if (lane < some) p.logits[(int64_t)(t0 + lane) * p.E + e] = v;
+}
+
+// 16 rows of a matrix, blocks of 128 columns at a time (ES: bytes of an element).
+// A load takes 16 bytes a lane, adjacent lanes along a row: 8 rows of 128 bytes or 4 of 256.  That is not
+// the layout of an MFMA operand (lane l has row l % 16), so a block is turned
+// around in the wave's own LDS.  Loads in the operand layout, 64 bytes of 16 rows
+// each, ask the L1 for four times as many lines and made it the bound: 64
+// experts of 2 x 1024 x 4096 in 8 bits 122 us, 101 us (5.3 TB/s) this way.
+template <int ES>
+struct MoeRows {
+    static constexpr int LPR = 8 * ES, NL = 2 * ES, RPL = 8 / ES;  // lanes a row, loads a block, rows a load
+    static constexpr int BYTES = 16 * 128 * ES;                   // of a block
+    const char *base;  // shared by all lanes
+    uint32_t off[NL];  // this lane's rows and its 16 bytes of them
+    // row(i): the byte offset of row i
+    template <typename F>
+    __device__ __forceinline__ void init(const char *ptr, int lane, F &&row)
+    {
+        base = ptr;
+#pragma unroll
+        for (int v = 0; v < NL; v++) off[v] = row(v * RPL + lane / LPR) + (uint32_t)(lane % LPR) * 16;
+    }
+    __device__ __forceinline__ void load(i32x4 (&f)[NL], int block) const
+    {
+#pragma unroll
+        for (int v = 0; v < NL; v++) f[v] = load_piece<ES>(base + (off[v] + (uint32_t)block * (128 * ES)));
+    }
+    // block: the one in which the row of K elements ends
+    __device__ __forceinline__ void load_end(i32x4 (&f)[NL], int block, int K, int lane) const
+    {
+        const int n = K - block * 128 - lane % LPR * (16 / ES);
+#pragma unroll
+        for (int v = 0; v < NL; v++)
+            f[v] = load_piece_end<ES>(base + (off[v] + (uint32_t)block * (128 * ES)), n, K);
+    }
+    __device__ static __forceinline__ int at(int row, int piece) { return row * (128 * ES) + (piece ^ swz_a<LPR>(row)) * 16; }
+    __device__ static __forceinline__ void put(char *lds, const i32x4 (&f)[NL], int lane)
+    {
+#pragma unroll
+        for (int v = 0; v < NL; v++) *(i32x4 *)(lds + at(v * RPL + lane / LPR, lane % LPR)) = f[v];
+    }
+    // columns 64 u + 16 lg .. of row li
+    template <bool BF>
+    __device__ static __forceinline__ Pair8 get(const char *lds, int u, int li, int lg)
+    {
+        if constexpr (ES == 1)
+            return widen<BF>(*(const i32x4 *)(lds + at(li, u * 4 + lg)));
+        else
+            return {{*(const half8 *)(lds + at(li, u * 8 + lg * 2)), *(const half8 *)(lds + at(li, u * 8 + lg * 2 + 1))}};
+    }
+};
+
+// The scales of 16 rows by tiles, for MFMA row li.
+struct MoeScales {
+    const uint8_t *s;  // of the first row's tile
+    uint32_t off;      // from there to this lane's
+    __device__ __forceinline__ void init(const uint8_t *scales, int64_t lds, int r0, int rows, int li)
+    {
+        s = scales + (int64_t)(r0 >> 7) * lds;
+        off = (min(r0 + li, rows - 1) >> 7) > (r0 >> 7) ? (uint32_t)lds : 0u;
+    }
+    __device__ __forceinline__ uint32_t byte(int block) const { return s[off + (uint32_t)block]; }
+    __device__ static __forceinline__ float value(uint32_t b)
     {
         return __builtin_bit_cast(float, b == 255 ? 0x7FC00000u : b ? b << 23 : 0x00400000u);
     }
 };
 
-// h = act(Up x) of one expert and 16 of its inner rows, for the chunk's tokens
-// that chose it.  A workgroup is (token, rank) of the choice, so that only chosen
-// experts have workgroups; the first token of an expert serves all of its tokens.
-// Four waves share the contraction.  TB: blocks of 16 tokens.
-template <bool BF, bool W8, int ACT, bool GATED, int TB>
-__global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p)
-{
-    __shared__ uint32_t keys[kMoeExperts];
-    __shared__ int ranks[kMoeChunk];  // the expert's rank in each token's choice; k and more: not chosen
-    __shared__ int found;
-    __shared__ float red[4][GATED ? 2 : 1][TB][64][4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, lg = lane >> 4;
-    const int owner = (int)blockIdx.y / p.k, rank = (int)blockIdx.y - owner * p.k;
-    const int i0 = (int)blockIdx.x * 16;
+template <bool W8, int G, int NB>
+constexpr int moe_turn_bytes() { return G * MoeRows<W8 ? 1 : 2>::BYTES + NB * MoeRows<2>::BYTES; }
 
-    for (int e = tid; e < p.E; e += 256) keys[e] = logit_key(p.logits[(int64_t)owner * p.E + e]);
-    __syncthreads();
-    for (int e = tid; e < p.E; e += 256) {
-        const uint32_t mine = keys[e];
-        int above = 0;
-        for (int j = 0; j < p.E; j++) above += keys[j] > mine || (keys[j] == mine && j < e);
-        if (above == rank) found = e;
+// One block of 128 columns: the weights of G times 16 rows and NB times 16 tokens, on their way.
+template <bool BF, bool W8, int G, int NB>
+struct MoeBlock {
+    using W = MoeRows<W8 ? 1 : 2>;
+    using X = MoeRows<2>;
+    i32x4 w[G][W::NL];
+    i32x4 x[NB][X::NL];
+    uint32_t s[G];
+
+    __device__ __forceinline__ void fetch(const W (&wr)[G], const MoeScales (&scales)[G], const X (&xr)[NB], int block)
+    {
+#pragma unroll
+        for (int g = 0; g < G; g++) wr[g].load(w[g], block);
+#pragma unroll
+        for (int b = 0; b < NB; b++) xr[b].load(x[b], block);
+        if constexpr (W8)
+#pragma unroll
+            for (int g = 0; g < G; g++) s[g] = scales[g].byte(block);
     }
-    __syncthreads();
-    const int expert = found;
-    for (int t = wave; t < p.T; t += 4) {
-        const float *row = p.logits + (int64_t)t * p.E;
-        const uint32_t mine = logit_key(row[expert]);
-        int above = 0;
-        for (int j = lane; j < p.E; j += 64) {
-            const uint32_t key = logit_key(row[j]);
-            above += key > mine || (key == mine && j < expert);
+    __device__ __forceinline__ void fetch_end(const W (&wr)[G], const MoeScales (&scales)[G], const X (&xr)[NB],
+                                              int block, int K, int lane)
+    {
+#pragma unroll
+        for (int g = 0; g < G; g++) wr[g].load_end(w[g], block, K, lane);
+#pragma unroll
+        for (int b = 0; b < NB; b++) xr[b].load_end(x[b], block, K, lane);
+        if constexpr (W8)
+#pragma unroll
+            for (int g = 0; g < G; g++) s[g] = scales[g].byte(block);
+    }
+    // acc[g][b] += rows g times the tokens of block b; turned: moe_turn_bytes of LDS, the wave's own
+    __device__ __forceinline__ void use(f32x4 (&acc)[G][NB], char *turned, int lane) const
+    {
+        const int li = lane & 15, lg = lane >> 4;
+        char *xs = turned + G * W::BYTES;
+#pragma unroll
+        for (int g = 0; g < G; g++) W::put(turned + g * W::BYTES, w[g], lane);
+#pragma unroll
+        for (int b = 0; b < NB; b++) X::put(xs + b * X::BYTES, x[b], lane);
+        wave_lds_sync();
+        f32x4 part[G][NB];  // 8-bit: the sums of the block, before its scales
+        if constexpr (W8)
+#pragma unroll
+            for (int g = 0; g < G; g++)
+#pragma unroll
+                for (int b = 0; b < NB; b++) part[g][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            Pair8 xv[NB];
+#pragma unroll
+            for (int b = 0; b < NB; b++) xv[b] = X::template get<BF>(xs + b * X::BYTES, u, li, lg);
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const Pair8 wv = W::template get<BF>(turned + g * W::BYTES, u, li, lg);
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    if constexpr (W8)
+                        part[g][b] = mfma_pair<BF>(xv[b], wv, part[g][b]);
+                    else
+                        acc[g][b] = mfma_pair<BF>(xv[b], wv, acc[g][b]);
+                }
+            }
+        }
+        if constexpr (W8)
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                const float v = MoeScales::value(s[g]);
+#pragma unroll
+                for (int b = 0; b < NB; b++) acc[g][b] += v * part[g][b];
+            }
+        wave_lds_sync();
+    }
+};
+
+// acc[g][b] += rows g times the 16 tokens of block b, over every step-th block of
+// 128 columns from `first` on; K: the columns that exist.  DEPTH blocks' loads are
+// in flight together.  turned: moe_turn_bytes of LDS, the wave's own.  The blocks are taken
+// from block `turn` on, around the end, so that workgroups do not all walk their rows from the start.
+template <bool BF, bool W8, int G, int NB, int DEPTH>
+__device__ __forceinline__ void moe_product(f32x4 (&acc)[G][NB], const MoeRows<W8 ? 1 : 2> (&w)[G],
+                                            const MoeScales (&scales)[G], const MoeRows<2> (&x)[NB], char *turned,
+                                            int first, int step, int K, int turn, int lane)
+{
+    MoeBlock<BF, W8, G, NB> ring[DEPTH];
+    // The steady loop has no branch around its loads, and the order of loads and uses
+    // is fixed, before it too: where paths join, the compiler waits for as many loads
+    // as either path would need.
+    const int blocks = K >> 7;
+    int left = blocks > first ? (blocks - first + step - 1) / step : 0;
+    int j = first + turn;  // the block, before it is wrapped around
+    j -= j >= blocks ? blocks : 0;
+    auto number = [&](int d) {  // of the d-th block from j on (d step < blocks)
+        const int i = j + d * step;
+        return i >= blocks ? i - blocks : i;
+    };
+    auto advance = [&](int d) {
+        j += d * step;
+        j -= j >= blocks ? blocks : 0;
+    };
+    if (left >= DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) {
+            ring[d].fetch(w, scales, x, number(d));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll 1
+        for (; left >= 2 * DEPTH; left -= DEPTH) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; d++) {
+                ring[d].use(acc, turned, lane);
+                __builtin_amdgcn_sched_barrier(0);
+                if (d == 0) advance(DEPTH);
+                ring[d].fetch(w, scales, x, number(d));
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) above += __shfl_xor(above, o);
-        if (lane == 0) ranks[t] = above;
+        for (int d = 0; d < DEPTH; d++) ring[d].use(acc, turned, lane);
+        advance(DEPTH);
+        left -= DEPTH;
+    }
+    if (left > 0) {  // fewer than DEPTH: together, the last one again where there is none
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) ring[d].fetch(w, scales, x, number(min(d, left - 1)));
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++)
+            if (d < left) ring[d].use(acc, turned, lane);
+    }
+    if ((K & 127) && (blocks - first) % step == 0) {  // the short block is this wave's
+        ring[0].fetch_end(w, scales, x, blocks, K, lane);
+        ring[0].use(acc, turned, lane);
+    }
+}
+
+// h = act(Up x) of one expert and some tiles of 16 of its inner rows, for the
+// chunk's tokens that chose it.  A workgroup's expert is blockIdx.y, or, where the choices are
+// fewer than the experts (by_choice), the one of rank blockIdx.y % k of token
+// blockIdx.y / k, whose other choosers' workgroups then have nothing to do.
+// Where there are few tiles (shared) the four waves share the contraction of one,
+// otherwise each takes a tile of its own and streams its rows whole.  Experts of
+// 2 x 1024 x 4096 in 8 bits: 64 of them 101 us with tiles of the waves' own, 122
+// shared; the 8 of one token 21.8 and 17.2.
+template <bool BF, bool W8, int ACT, bool GATED, int NB>
+__global__ __launch_bounds__(256, 2) void moe_up_kernel(MoeParams p, int by_choice, int shared)
+{
+    constexpr int G = GATED ? 2 : 1;
+    __shared__ uint32_t keys[kMoeExperts];
+    __shared__ int ranks[kMoeChunk];  // the expert's rank in each token's choice; k and more: not chosen
+    __shared__ int list[kMoeChunk];   // the tokens that chose it
+    __shared__ int found;
+    __shared__ float red[4][G][NB][64][4];
+    __shared__ __attribute__((aligned(16))) char turned[4][moe_turn_bytes<W8, G, NB>()];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), li = lane & 15,
+              lg = lane >> 4;
+    int expert = (int)blockIdx.y, owner = 0;
+    if (by_choice) {
+        owner = expert / p.k;
+        const int rank = expert - owner * p.k;
+        for (int e = tid; e < p.E; e += 256) keys[e] = logit_key(p.logits[(int64_t)owner * p.E + e]);
+        __syncthreads();
+        for (int e = tid; e < p.E; e += 256) {
+            const uint32_t mine = keys[e];
+            int above = 0;
+            for (int j = 0; j < p.E; j++) above += keys[j] > mine || (keys[j] == mine && j < e);
+            if (above == rank) found = e;
+        }
+        __syncthreads();
+        expert = __builtin_amdgcn_readfirstlane(found);
+    }
+    {  // four adjacent threads a token
+        const int t = tid >> 2, part = tid & 3;
+        int above = 0;
+        if (t < p.T) {
+            const float *row = p.logits + (int64_t)t * p.E;
+            const uint32_t mine = logit_key(row[expert]);
+#pragma unroll 8
+            for (int j = part; j < p.E; j += 4) {
+                const uint32_t key = logit_key(row[j]);
+                above += key > mine || (key == mine && j < expert);
+            }
+        }
+        above += __shfl_xor(above, 1);
+        above += __shfl_xor(above, 2);
+        if (part == 0) ranks[t] = t < p.T ? above : p.k;
     }
     __syncthreads();
-    for (int t = 0; t < owner; t++)
-        if (ranks[t] < p.k) return;  // an earlier token's workgroup has this expert
+    const unsigned long long who = __ballot(ranks[lane] < p.k);
+    if (who == 0 || (by_choice && __ffsll(who) - 1 != owner)) return;  // (an earlier token's workgroup has the expert)
+    const int n = __popcll(who);
+    if (wave == 0 && (who >> lane & 1)) list[__popcll(who & ((1ull << lane) - 1))] = lane;
     if (blockIdx.x == 0) {  // this workgroup writes the choice down
         for (int t = wave; t < p.T; t += 4) {
             if (ranks[t] >= p.k) continue;
@@ -223,185 +448,262 @@ __global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p)
             }
         }
     }
+    __syncthreads();
 
-    constexpr int G = GATED ? 2 : 1;
-    const int rows = G * p.I;
-    MoeRows<BF, W8> w[G];
     const char *base = (const char *)p.Up + (int64_t)expert * p.up_stride * (W8 ? 1 : 2);
     const uint8_t *scales = W8 ? p.US + (int64_t)expert * p.us_stride : nullptr;
+    const int i0 = (shared ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave) * 16;
+    if (i0 >= p.I) return;  // (of a shared tile all four waves stay)
+    MoeRows<W8 ? 1 : 2> w[G];
+    MoeScales ws[G];
 #pragma unroll
-    for (int g = 0; g < G; g++) w[g].init(base, p.ldu, scales, p.ldus, g * p.I + i0, g ? rows : p.I, li);
-    // (the columns of tokens that did not choose the expert repeat the owner's; they are not stored)
-    const _Float16 *x[TB];
-#pragma unroll
-    for (int b = 0; b < TB; b++) {
-        const int t = b * 16 + li;
-        x[b] = p.X + (int64_t)(t < p.T && ranks[min(t, p.T - 1)] < p.k ? t : owner) * p.ldx;
+    for (int g = 0; g < G; g++) {
+        const int r0 = g * p.I + i0, end = g ? 2 * p.I : p.I;
+        w[g].init(base + (int64_t)r0 * p.ldu * (W8 ? 1 : 2), lane,
+                  [&](int r) { return (uint32_t)(min(r, end - 1 - r0) * (int)p.ldu) * (W8 ? 1 : 2); });
+        if constexpr (W8) ws[g].init(scales, p.ldus, r0, end, li);
     }
-    f32x4 acc[G][TB];
-#pragma unroll
-    for (int g = 0; g < G; g++)
-#pragma unroll
-        for (int b = 0; b < TB; b++) acc[g][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // 128 columns a turn: one block of the scales
-    for (int k0 = wave * 128; k0 < p.H; k0 += 512) {
-        f32x4 part[G][TB];
-#pragma unroll
-        for (int g = 0; g < G; g++)
-#pragma unroll
-            for (int b = 0; b < TB; b++) part[g][b] = W8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[g][b];
-#pragma unroll
-        for (int u = 0; u < 2; u++) {
-            const int k = k0 + u * 64 + lg * 16;
-            Pair8 xv[TB];
-#pragma unroll
-            for (int b = 0; b < TB; b++) xv[b] = load16(x[b] + k, p.H - k);
-#pragma unroll
-            for (int g = 0; g < G; g++) {
-                const Pair8 wv = w[g].load(k, p.H);
-#pragma unroll
-                for (int b = 0; b < TB; b++) part[g][b] = mfma_pair<BF>(wv, xv[b], part[g][b]);
-            }
-        }
-#pragma unroll
-        for (int g = 0; g < G; g++) {
-            if constexpr (W8) {
-                const f32x4 s = w[g].scale(k0 >> 7, lg);
-#pragma unroll
-                for (int b = 0; b < TB; b++) acc[g][b] += s * part[g][b];
-            } else {
-#pragma unroll
-                for (int b = 0; b < TB; b++) acc[g][b] = part[g][b];
-            }
-        }
-    }
-#pragma unroll
-    for (int g = 0; g < G; g++)
-#pragma unroll
-        for (int b = 0; b < TB; b++) *(f32x4 *)red[wave][g][b][lane] = acc[g][b];
-    __syncthreads();
-    // thread: token tid / 16 of a block, inner row i0 + tid % 16
-    const int r = tid & 15, at = (r >> 2) * 16 + (tid >> 4);
-#pragma unroll
-    for (int b = 0; b < TB; b++) {
-        const int t = b * 16 + (tid >> 4);
-        if (t >= p.T || i0 + r >= p.I || ranks[t] >= p.k) continue;
-        float v[G];
-#pragma unroll
-        for (int g = 0; g < G; g++)
-            v[g] = (red[0][g][b][at][r & 3] + red[1][g][b][at][r & 3]) +
-                   (red[2][g][b][at][r & 3] + red[3][g][b][at][r & 3]);
+    const int turn = (i0 / 16 * 5 + expert * 3) % max(p.H >> 7, 1);
+    // 16 bits: an operand of the down product
+    auto store = [&](const float (&v)[G], int c, int r) {
         float h = lin_act<ACT>(v[0]);
         if constexpr (GATED) h *= v[1];
-        // 16 bits: an operand of the down product
+        const int t = list[c];
         p.hidden[((int64_t)t * p.k + ranks[t]) * p.I + i0 + r] = st16<BF>(h);
+    };
+    // 16 NB tokens at a time (more read the weights again, from the caches)
+    for (int n0 = 0; n0 < n; n0 += 16 * NB) {
+        MoeRows<2> x[NB];
+        f32x4 acc[G][NB];
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+            // (rows past the last token repeat it)
+            x[b].init((const char *)p.X, lane, [&](int r) {
+                return (uint32_t)(list[min(n0 + b * 16 + r, n - 1)] * (int)p.ldx) * 2;
+            });
+#pragma unroll
+            for (int g = 0; g < G; g++) acc[g][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        moe_product<BF, W8, G, NB, NB == 1 ? (W8 ? 3 : 2) : (W8 ? 2 : 1)>(acc, w, ws, x, turned[wave], shared ? wave : 0, shared ? 4 : 1,
+                                                      p.H, turn, lane);
+        if (!shared) {
+            // lane: row li, tokens 4 lg .. + 3 of a block
+#pragma unroll
+            for (int b = 0; b < NB; b++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int c = n0 + b * 16 + lg * 4 + e;
+                    float v[G];
+#pragma unroll
+                    for (int g = 0; g < G; g++) v[g] = acc[g][b][e];
+                    if (c < n && i0 + li < p.I) store(v, c, li);
+                }
+            continue;
+        }
+#pragma unroll
+        for (int g = 0; g < G; g++)
+#pragma unroll
+            for (int b = 0; b < NB; b++) *(f32x4 *)red[wave][g][b][lane] = acc[g][b];
+        __syncthreads();
+        // thread: column tid / 16 of a block, row tid % 16
+        const int r = tid & 15, col = tid >> 4, at = (col >> 2) * 16 + r, el = col & 3;
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+            const int c = n0 + b * 16 + col;
+            float v[G];
+#pragma unroll
+            for (int g = 0; g < G; g++)
+                v[g] = (red[0][g][b][at][el] + red[1][g][b][at][el]) + (red[2][g][b][at][el] + red[3][g][b][at][el]);
+            if (c < n && i0 + r < p.I) store(v, c, r);
+        }
+        __syncthreads();
     }
 }
 
 // D = residual + sum of weight Down h for 16 of the layer's columns and all
-// tokens of the chunk.  The experts that were chosen, and parts of 512 of their
-// contraction, are dealt out over the 8 waves.
-template <bool BF, bool W8, int TB>
-__global__ __launch_bounds__(512) void moe_down_kernel(MoeParams p)
+// tokens of the chunk.  The work is a list of units: a chosen expert, up to 16 of
+// its tokens and a part of its inner columns.  They are dealt out over the 8 waves,
+// each of which adds up its own sums of all tokens in LDS, in a fixed order.  What
+// bounds it is the bytes in flight: a wave streams over the ends of its units (64
+// experts of 4096 x 1024 in 8 bits 58 us, 4.6 TB/s; with units of 4 blocks that each
+// drained before the next began 75 us).  Workgroups begin at different units.
+// Where all began at the first one and the same rows of h, that was 101 us.
+constexpr int kDownWaves = 8;
+constexpr int kDownUnits = kMoeExperts + kMoeChunk * kMoeTop / 16;  // sum of ceil(tokens / 16) over the experts
+template <bool BF, bool W8>
+__global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
 {
+    constexpr int THREADS = 64 * kDownWaves, PAIRS = kMoeChunk * kMoeTop / THREADS, DEPTH = W8 ? 4 : 3;
     __shared__ unsigned long long users[kMoeExperts];  // tokens of each expert
-    __shared__ uint16_t list[kMoeExperts];
+    __shared__ uint16_t start[kMoeExperts];            // where its choices start in the list
+    __shared__ uint16_t list[kMoeChunk * kMoeTop];     // the choices (t k + r), expert by expert, by token
+    __shared__ uint16_t unit_expert[kDownUnits], unit_start[kDownUnits];
+    __shared__ uint8_t unit_tokens[kDownUnits];
     __shared__ int count;
     __shared__ float share[kMoeChunk * kMoeTop];
-    __shared__ uint16_t expert_of[kMoeChunk * kMoeTop];
-    __shared__ float red[8][TB][64][4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, li = lane & 15, lg = lane >> 4;
-    const int h0 = (int)blockIdx.x * 16;
-    for (int e = tid; e < p.E; e += 512) users[e] = 0;
-    __syncthreads();
-    for (int i = tid; i < p.T * p.k; i += 512) {
-        const int t = i / p.k, e = p.chosen[i];
+    __shared__ float sums[kDownWaves][kMoeChunk][16];
+    __shared__ __attribute__((aligned(16))) char turned[kDownWaves][moe_turn_bytes<W8, 1, 1>()];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), li = lane & 15,
+              lg = lane >> 4;
+    const int h0 = (int)blockIdx.x * 16, rows = (p.T + 15) / 16 * 16;
+    for (int e = tid; e < p.E; e += THREADS) users[e] = 0;
+    int expert[PAIRS];
+#pragma unroll
+    for (int j = 0; j < PAIRS; j++) {
+        const int i = tid + j * THREADS;
+        expert[j] = -1;
+        if (i >= p.T * p.k) continue;
+        expert[j] = p.chosen[i];
+        const int t = i / p.k;
         float sum = 0.0f;
-        if (p.renormalize)
-            for (int j = 0; j < p.k; j++) sum += p.weight[t * p.k + j];
-        else
+        if (p.renormalize) {
+#pragma unroll 8
+            for (int r = 0; r < p.k; r++) sum += p.weight[t * p.k + r];
+        } else {
             sum = p.total[t];
+        }
         share[i] = p.weight[i] / sum;
-        expert_of[i] = (uint16_t)e;
-        atomicOr(&users[e], 1ull << t);
     }
+    for (int i = lane; i < rows * 16; i += 64) sums[wave][i >> 4][i & 15] = 0.0f;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PAIRS; j++)
+        if (expert[j] >= 0) atomicOr(&users[expert[j]], 1ull << ((tid + j * THREADS) / p.k));
     __syncthreads();
     if (wave == 0) {
-        int n = 0;
+        int n = 0, at = 0;  // units, choices
         for (int e0 = 0; e0 < p.E; e0 += 64) {
-            const bool on = e0 + lane < p.E && users[e0 + lane];
-            const unsigned long long m = __ballot(on);
-            if (on) list[n + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(e0 + lane);
-            n += __popcll(m);
+            const int tokens = e0 + lane < p.E ? __popcll(users[e0 + lane]) : 0, groups = (tokens + 15) / 16;
+            int sum = tokens << 16 | groups;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(sum, o);
+                if (lane >= o) sum += v;
+            }
+            const int first = at + (sum >> 16) - tokens, unit = n + (sum & 0xFFFF) - groups;
+            if (e0 + lane < p.E) start[e0 + lane] = (uint16_t)first;
+            for (int g = 0; g < groups; g++) {
+                unit_expert[unit + g] = (uint16_t)(e0 + lane);
+                unit_start[unit + g] = (uint16_t)(first + g * 16);
+                unit_tokens[unit + g] = (uint8_t)min(16, tokens - g * 16);
+            }
+            const int all = __shfl(sum, 63);
+            n += all & 0xFFFF;
+            at += all >> 16;
         }
         if (lane == 0) count = n;
     }
     __syncthreads();
-    const int parts = (p.I + 511) / 512, units = count * parts;
-    f32x4 acc[TB];
 #pragma unroll
-    for (int b = 0; b < TB; b++) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int u = wave; u < units; u += 8) {
-        const int e = list[u / parts], part = u % parts;
-        const unsigned long long who = users[e];
-        MoeRows<BF, W8> w;
-        w.init((const char *)p.Down + (int64_t)e * p.down_stride * (W8 ? 1 : 2), p.lddn,
-               W8 ? p.DS + (int64_t)e * p.ds_stride : nullptr, p.ldds, h0, p.H, li);
-        // (the columns of tokens that did not choose the expert repeat those of one that did)
-        const int some = __ffsll(who) - 1;
-        const _Float16 *h[TB];
-        float by[TB];
-        uint32_t in = 0;
-#pragma unroll
-        for (int b = 0; b < TB; b++) {
-            const bool here = who >> (b * 16 + li) & 1;
-            const int t = here ? b * 16 + li : some;
-            int r = 0;
-            while (r < p.k - 1 && expert_of[t * p.k + r] != e) r++;
-            in |= here ? 1u << b : 0u;
-            by[b] = share[t * p.k + r];
-            h[b] = p.hidden + ((int64_t)t * p.k + r) * p.I;
+    for (int j = 0; j < PAIRS; j++) {
+        const int i = tid + j * THREADS, t = i / p.k;
+        if (expert[j] >= 0) list[start[expert[j]] + __popcll(users[expert[j]] & ((1ull << t) - 1))] = (uint16_t)i;
+    }
+    __syncthreads();
+    // parts of whole blocks of 128, so that every wave has a unit where that is
+    // possible; the short block at the end belongs to the last part
+    const int entries = __builtin_amdgcn_readfirstlane(count), whole = p.I / 128;
+    const int len = max(whole / min(max(whole, 1), (kDownWaves + entries - 1) / entries), 1);
+    const int parts = max((whole + len - 1) / len, 1), units = entries * parts;
+    using Block = MoeBlock<BF, W8, 1, 1>;
+    struct Unit {
+        typename Block::W w[1];
+        MoeScales ws[1];
+        MoeRows<2> h[1];
+        int first, n, last;  // blocks: the first one, how many whole ones, whether the short one is among them
+        int at, tokens;      // in the list
+    };
+    const int shift = blockIdx.x * kDownWaves % units;
+    auto place = [&](int u) { return u + shift < units ? u + shift : u + shift - units; };
+    auto open = [&](int u) {
+        Unit q;
+        const int i = place(u) / parts, part = place(u) - i * parts, e = __builtin_amdgcn_readfirstlane(unit_expert[i]);
+        q.at = __builtin_amdgcn_readfirstlane(unit_start[i]);
+        q.tokens = __builtin_amdgcn_readfirstlane(unit_tokens[i]);
+        q.first = part * len;
+        q.n = min(whole - q.first, len);
+        q.last = part == parts - 1 && whole * 128 < p.I;
+        q.w[0].init((const char *)p.Down + ((int64_t)e * p.down_stride + h0 * p.lddn) * (W8 ? 1 : 2), lane,
+                    [&](int r) { return (uint32_t)(min(r, p.H - 1 - h0) * (int)p.lddn) * (W8 ? 1 : 2); });
+        if constexpr (W8) q.ws[0].init(p.DS + (int64_t)e * p.ds_stride, p.ldds, h0, p.H, li);
+        // (rows past the last token repeat it; below 2^32 bytes: 2048 rows of 2^20)
+        q.h[0].init((const char *)p.hidden, lane,
+                    [&](int r) { return (uint32_t)list[q.at + min(r, q.tokens - 1)] * p.I * 2; });
+        return q;
+    };
+    f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
+    auto close = [&](const Unit &q) {
+        if (q.last) {
+            Block f;
+            f.fetch_end(q.w, q.ws, q.h, whole, p.I, lane);
+            f.use(acc, turned[wave], lane);
         }
-        f32x4 sum[TB];
+        // the lane has tokens 4 lg .. of the 16, of column li
+        float *at[4], old[4], by[4];
 #pragma unroll
-        for (int b = 0; b < TB; b++) sum[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int end = min(p.I, part * 512 + 512);
-        for (int k0 = part * 512; k0 < end; k0 += 128) {
-            f32x4 s8[TB];
+        for (int j = 0; j < 4; j++) {
+            const int c = list[q.at + min(lg * 4 + j, q.tokens - 1)];
+            by[j] = share[c];
+            at[j] = &sums[wave][c / p.k][li];
+            old[j] = *at[j];
+        }
 #pragma unroll
-            for (int b = 0; b < TB; b++) s8[b] = W8 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : sum[b];
+        for (int j = 0; j < 4; j++)
+            if (lg * 4 + j < q.tokens) *at[j] = old[j] + by[j] * acc[0][0][j];
+        acc[0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    if (whole == 0) {
+        for (int u = wave; u < units; u += kDownWaves) close(open(u));
+    } else if (wave < units) {
+        // A wave streams the whole blocks of its units: the first loads of the next
+        // unit follow the last ones of this.  (What a unit lacks to groups of DEPTH
+        // blocks is fetched again and not used.)
+        Block ring[DEPTH];
+        Unit q = open(wave);
 #pragma unroll
-            for (int v = 0; v < 2; v++) {
-                const int k = k0 + v * 64 + lg * 16;
-                const Pair8 wv = w.load(k, p.I);
+        for (int d = 0; d < DEPTH; d++) {
+            ring[d].fetch(q.w, q.ws, q.h, q.first + min(d, q.n - 1));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int u = wave;;) {
+            int g = 0;
+#pragma unroll 1
+            for (; g + DEPTH < q.n; g += DEPTH) {
 #pragma unroll
-                for (int b = 0; b < TB; b++) {
-                    s8[b] = mfma_pair<BF>(wv, load16(h[b] + k, p.I - k), s8[b]);
+                for (int d = 0; d < DEPTH; d++) {
+                    ring[d].use(acc, turned[wave], lane);
+                    __builtin_amdgcn_sched_barrier(0);
+                    ring[d].fetch(q.w, q.ws, q.h, q.first + min(g + DEPTH + d, q.n - 1));
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            if constexpr (W8) {
-                const f32x4 s = w.scale(k0 >> 7, lg);
+            u += kDownWaves;
+            if (u >= units) {
 #pragma unroll
-                for (int b = 0; b < TB; b++) sum[b] += s * s8[b];
-            } else {
-#pragma unroll
-                for (int b = 0; b < TB; b++) sum[b] = s8[b];
+                for (int d = 0; d < DEPTH; d++)
+                    if (g + d < q.n) ring[d].use(acc, turned[wave], lane);
+                close(q);
+                break;
             }
+            const Unit next = open(u);
+#pragma unroll
+            for (int d = 0; d < DEPTH; d++) {
+                if (g + d < q.n) ring[d].use(acc, turned[wave], lane);
+                __builtin_amdgcn_sched_barrier(0);
+                ring[d].fetch(next.w, next.ws, next.h, next.first + min(d, next.n - 1));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            close(q);
+            q = next;
         }
-        // (a token that did not choose the expert takes nothing of it, not a NaN either)
-#pragma unroll
-        for (int b = 0; b < TB; b++)
-            if (in >> b & 1) acc[b] += by[b] * sum[b];
     }
-#pragma unroll
-    for (int b = 0; b < TB; b++) *(f32x4 *)red[wave][b][lane] = acc[b];
     __syncthreads();
-    for (int i = tid; i < TB * 256; i += 512) {
-        const int t = i >> 4, r = i & 15, at = (r >> 2) * 16 + (t & 15);
+    for (int i = tid; i < rows * 16; i += THREADS) {
+        const int t = i >> 4, r = i & 15;
         if (t >= p.T || h0 + r >= p.H) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 8; u++) v += red[u][t >> 4][at][r & 3];
+        for (int u = 0; u < kDownWaves; u++) v += sums[u][t][r];
         if (p.R) v += ld16<BF>(p.R[t * p.ldr + h0 + r]);
         p.D[t * p.ldd + h0 + r] = st16<BF>(v);
     }

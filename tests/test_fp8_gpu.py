@@ -499,8 +499,8 @@ def ref_moe(x, wr, up, down, us, ds, top_k, act, renormalize, residual, t):
     E, _, I = down.shape  # noqa: E741
     xd, wd = x.double(), wr.double()
     logits = xd @ wd.t()
-    # every choice is clear: the gap at the border is above the error of the fp32 sums, whose 16 parts take 64 of each
-    # 1024 columns one after the other and are then added up
+    # every choice is clear: the gap at the border is above the error of fp32 sums in 16 parts of 64 of each 1024 columns
+    # (the kernel's parts are shorter)
     order = torch.argsort(-logits, dim=1, stable=True)
     ranked = logits.gather(1, order)
     depth = min(H, 64 * -(-H // 1024) + 16)
@@ -560,6 +560,13 @@ def check_moe(T, H, E, I, top_k, dtype, act="silu", gated=True, w8=False, renorm
     (65, 72, 9, 40, 3), (130, 96, 12, 33, 2), (3, 64, 300, 24, 32), (5, 40, 1024, 8, 3)])
 def test_moe(T, H, E, I, k, dtype, w8):  # noqa: E741
     check_moe(T, H, E, I, k, dtype, w8=w8)
+
+
+@pytest.mark.parametrize("w8", [False, True])
+@pytest.mark.parametrize("T,H,E,I,k", [(40, 136, 64, 520, 4), (64, 200, 16, 2100, 4), (70, 264, 33, 1000, 12)])
+def test_moe_many_tiles(T, H, E, I, k, w8):  # noqa: E741
+    """So many inner rows that every wave has a tile of its own; one and two blocks of tokens at a time."""
+    check_moe(T, H, E, I, k, "bf16", w8=w8, seed=42)
 
 
 @pytest.mark.parametrize("act", list(ACTS))
