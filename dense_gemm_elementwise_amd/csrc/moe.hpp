@@ -16,6 +16,7 @@
 
 #include "linear_gemm.hpp"
 #include "ops_host.hpp"
+#include "row_pieces.hpp"
 
 namespace gemm_epi {
 
@@ -47,46 +48,10 @@ __device__ __forceinline__ uint32_t logit_key(float v)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-typedef int i32x4b __attribute__((ext_vector_type(4), aligned(1)));
-
 // A lane's 16 consecutive columns of a row, as the operands of two MFMAs.
 struct Pair8 {
     half8 v[2];
 };
-// v moved down by n bytes (0 .. 16), zeros behind
-__device__ __forceinline__ i32x4 move_down(i32x4 v, int n)
-{
-    const uint64_t lo = (uint64_t)(uint32_t)v[1] << 32 | (uint32_t)v[0], hi = (uint64_t)(uint32_t)v[3] << 32 | (uint32_t)v[2];
-    const int s = n * 8 & 63;
-    const uint64_t high = hi >> s, low = lo >> s | (s ? hi << (64 - s) : 0);
-    const uint64_t a = n >= 16 ? 0 : n >= 8 ? high : low, b = n >= 8 ? 0 : high;
-    return i32x4{(int)(uint32_t)a, (int)(uint32_t)(a >> 32), (int)(uint32_t)b, (int)(uint32_t)(b >> 32)};
-}
-// 16 bytes at any element-aligned address
-template <int ES>
-__device__ __forceinline__ i32x4 load_piece(const char *p) { return *(const i32x4b *)p; }
-// The same where a row of K elements of ES bytes ends inside them or before (n
-// exist; the rest are zeros), without reading outside the row: its last 16 bytes,
-// moved down; of a shorter row element by element.
-template <int ES>
-__device__ __forceinline__ i32x4 load_piece_end(const char *p, int n, int K)
-{
-    constexpr int P = 16 / ES;
-    if (K >= P) {
-        const int miss = max(P - n, 0);
-        return move_down(load_piece<ES>(p - (int64_t)miss * ES), min(miss, P) * ES);
-    }
-    uint32_t v[4] = {};
-#pragma unroll 1
-    for (int e = 0; e < P; e++) {  // (the elements move down, one after the other)
-        const char *at = p + (int64_t)min(e, n - 1) * ES;
-        const uint32_t x = ES == 1 ? *(const uint8_t *)at : *(const uint16_t *)at;
-#pragma unroll
-        for (int d = 0; d < 3; d++) v[d] = v[d] >> (8 * ES) | v[d + 1] << (32 - 8 * ES);
-        v[3] = v[3] >> (8 * ES) | (e < n ? x << (32 - 8 * ES) : 0);
-    }
-    return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
-}
 template <bool BF>
 __device__ __forceinline__ Pair8 widen(i32x4 q)
 {
@@ -171,55 +136,16 @@ __global__ __launch_bounds__(256) void moe_router_kernel(MoeParams p)
     if (lane < some) p.logits[(int64_t)(t0 + lane) * p.E + e] = v;
 }
 
-// 16 rows of a matrix, blocks of 128 columns at a time (ES: bytes of an element).
-// A load takes 16 bytes a lane, adjacent lanes along a row: 8 rows of 128 bytes or 4 of 256.  That is not
-// the layout of an MFMA operand (lane l has row l % 16), so a block is turned
-// around in the wave's own LDS.  Loads in the operand layout, 64 bytes of 16 rows
-// each, ask the L1 for four times as many lines and made it the bound: 64
-// experts of 2 x 1024 x 4096 in 8 bits 122 us, 101 us (5.3 TB/s) this way.
-template <int ES>
-struct MoeRows {
-    static constexpr int LPR = 8 * ES, NL = 2 * ES, RPL = 8 / ES;  // lanes a row, loads a block, rows a load
-    static constexpr int BYTES = 16 * 128 * ES;                   // of a block
-    const char *base;  // shared by all lanes
-    uint32_t off[NL];  // this lane's rows and its 16 bytes of them
-    // row(i): the byte offset of row i
-    template <typename F>
-    __device__ __forceinline__ void init(const char *ptr, int lane, F &&row)
-    {
-        base = ptr;
-#pragma unroll
-        for (int v = 0; v < NL; v++) off[v] = row(v * RPL + lane / LPR) + (uint32_t)(lane % LPR) * 16;
-    }
-    __device__ __forceinline__ void load(i32x4 (&f)[NL], int block) const
-    {
-#pragma unroll
-        for (int v = 0; v < NL; v++) f[v] = load_piece<ES>(base + (off[v] + (uint32_t)block * (128 * ES)));
-    }
-    // block: the one in which the row of K elements ends
-    __device__ __forceinline__ void load_end(i32x4 (&f)[NL], int block, int K, int lane) const
-    {
-        const int n = K - block * 128 - lane % LPR * (16 / ES);
-#pragma unroll
-        for (int v = 0; v < NL; v++)
-            f[v] = load_piece_end<ES>(base + (off[v] + (uint32_t)block * (128 * ES)), n, K);
-    }
-    __device__ static __forceinline__ int at(int row, int piece) { return row * (128 * ES) + (piece ^ swz_a<LPR>(row)) * 16; }
-    __device__ static __forceinline__ void put(char *lds, const i32x4 (&f)[NL], int lane)
-    {
-#pragma unroll
-        for (int v = 0; v < NL; v++) *(i32x4 *)(lds + at(v * RPL + lane / LPR, lane % LPR)) = f[v];
-    }
-    // columns 64 u + 16 lg .. of row li
-    template <bool BF>
-    __device__ static __forceinline__ Pair8 get(const char *lds, int u, int li, int lg)
-    {
-        if constexpr (ES == 1)
-            return widen<BF>(*(const i32x4 *)(lds + at(li, u * 4 + lg)));
-        else
-            return {{*(const half8 *)(lds + at(li, u * 8 + lg * 2)), *(const half8 *)(lds + at(li, u * 8 + lg * 2 + 1))}};
-    }
-};
+// columns 64 u + 16 lg .. of row li of a block in LDS
+template <int ES, bool BF>
+__device__ __forceinline__ Pair8 get_pair(const char *lds, int u, int li, int lg)
+{
+    using R = RowBlocks<ES>;
+    if constexpr (ES == 1)
+        return widen<BF>(*(const i32x4 *)(lds + R::at(li, u * 4 + lg)));
+    else
+        return {{*(const half8 *)(lds + R::at(li, u * 8 + lg * 2)), *(const half8 *)(lds + R::at(li, u * 8 + lg * 2 + 1))}};
+}
 
 // The scales of 16 rows by tiles, for MFMA row li.
 struct MoeScales {
@@ -238,13 +164,15 @@ struct MoeScales {
 };
 
 template <bool W8, int G, int NB>
-constexpr int moe_turn_bytes() { return G * MoeRows<W8 ? 1 : 2>::BYTES + NB * MoeRows<2>::BYTES; }
+constexpr int moe_turn_bytes() { return G * RowBlocks<W8 ? 1 : 2>::BYTES + NB * RowBlocks<2>::BYTES; }
+
+constexpr int kShortRow = 16;  // elements; of shorter rows there is no piece of 16 bytes in 8 bits
 
 // One block of 128 columns: the weights of G times 16 rows and NB times 16 tokens, on their way.
 template <bool BF, bool W8, int G, int NB>
 struct MoeBlock {
-    using W = MoeRows<W8 ? 1 : 2>;
-    using X = MoeRows<2>;
+    using W = RowBlocks<W8 ? 1 : 2>;
+    using X = RowBlocks<2>;
     i32x4 w[G][W::NL];
     i32x4 x[NB][X::NL];
     uint32_t s[G];
@@ -259,16 +187,23 @@ struct MoeBlock {
 #pragma unroll
             for (int g = 0; g < G; g++) s[g] = scales[g].byte(block);
     }
-    __device__ __forceinline__ void fetch_end(const W (&wr)[G], const MoeScales (&scales)[G], const X (&xr)[NB],
-                                              int block, int K, int lane)
+    __device__ __forceinline__ void fetch_short(const W (&wr)[G], const MoeScales (&scales)[G], const X (&xr)[NB])
     {
 #pragma unroll
-        for (int g = 0; g < G; g++) wr[g].load_end(w[g], block, K, lane);
+        for (int g = 0; g < G; g++) wr[g].load_short(w[g]);
 #pragma unroll
-        for (int b = 0; b < NB; b++) xr[b].load_end(x[b], block, K, lane);
+        for (int b = 0; b < NB; b++) xr[b].load_short(x[b]);
         if constexpr (W8)
 #pragma unroll
-            for (int g = 0; g < G; g++) s[g] = scales[g].byte(block);
+            for (int g = 0; g < G; g++) s[g] = scales[g].byte(0);
+    }
+    // for the block in which the rows end, before use()
+    __device__ __forceinline__ void finish(const W (&wr)[G], const X (&xr)[NB], int block)
+    {
+#pragma unroll
+        for (int g = 0; g < G; g++) wr[g].finish(w[g], block);
+#pragma unroll
+        for (int b = 0; b < NB; b++) xr[b].finish(x[b], block);
     }
     // acc[g][b] += rows g times the tokens of block b; turned: moe_turn_bytes of LDS, the wave's own
     __device__ __forceinline__ void use(f32x4 (&acc)[G][NB], char *turned, int lane) const
@@ -290,10 +225,10 @@ struct MoeBlock {
         for (int u = 0; u < 2; u++) {
             Pair8 xv[NB];
 #pragma unroll
-            for (int b = 0; b < NB; b++) xv[b] = X::template get<BF>(xs + b * X::BYTES, u, li, lg);
+            for (int b = 0; b < NB; b++) xv[b] = get_pair<2, BF>(xs + b * X::BYTES, u, li, lg);
 #pragma unroll
             for (int g = 0; g < G; g++) {
-                const Pair8 wv = W::template get<BF>(turned + g * W::BYTES, u, li, lg);
+                const Pair8 wv = get_pair<W8 ? 1 : 2, BF>(turned + g * W::BYTES, u, li, lg);
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
                     if constexpr (W8)
@@ -319,25 +254,29 @@ struct MoeBlock {
 // in flight together.  turned: moe_turn_bytes of LDS, the wave's own.  The blocks are taken
 // from block `turn` on, around the end, so that workgroups do not all walk their rows from the start.
 template <bool BF, bool W8, int G, int NB, int DEPTH>
-__device__ __forceinline__ void moe_product(f32x4 (&acc)[G][NB], const MoeRows<W8 ? 1 : 2> (&w)[G],
-                                            const MoeScales (&scales)[G], const MoeRows<2> (&x)[NB], char *turned,
+__device__ __forceinline__ void moe_product(f32x4 (&acc)[G][NB], const RowBlocks<W8 ? 1 : 2> (&w)[G],
+                                            const MoeScales (&scales)[G], const RowBlocks<2> (&x)[NB], char *turned,
                                             int first, int step, int K, int turn, int lane)
 {
     MoeBlock<BF, W8, G, NB> ring[DEPTH];
+    if (K < kShortRow) {
+        if (first == 0) {
+            ring[0].fetch_short(w, scales, x);
+            ring[0].use(acc, turned, lane);
+        }
+        return;
+    }
     // The steady loop has no branch around its loads, and the order of loads and uses
     // is fixed, before it too: where paths join, the compiler waits for as many loads
     // as either path would need.
-    const int blocks = K >> 7;
-    int left = blocks > first ? (blocks - first + step - 1) / step : 0;
+    const int whole = K >> 7;
+    const bool tail = (K & 127) && first <= whole && (whole - first) % step == 0;  // the last block this wave takes
+    int left = (whole > first ? (whole - first + step - 1) / step : 0) + tail;
     int j = first + turn;  // the block, before it is wrapped around
-    j -= j >= blocks ? blocks : 0;
-    auto number = [&](int d) {  // of the d-th block from j on (d step < blocks)
+    j -= j >= whole ? whole : 0;
+    auto number = [&](int d) {  // of the d-th block from j on
         const int i = j + d * step;
-        return i >= blocks ? i - blocks : i;
-    };
-    auto advance = [&](int d) {
-        j += d * step;
-        j -= j >= blocks ? blocks : 0;
+        return tail && d == left - 1 ? whole : i >= whole ? i - whole : i;
     };
     if (left >= DEPTH) {
 #pragma unroll
@@ -346,31 +285,36 @@ __device__ __forceinline__ void moe_product(f32x4 (&acc)[G][NB], const MoeRows<W
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll 1
-        for (; left >= 2 * DEPTH; left -= DEPTH) {
+        while (left >= 2 * DEPTH) {
 #pragma unroll
             for (int d = 0; d < DEPTH; d++) {
                 ring[d].use(acc, turned, lane);
                 __builtin_amdgcn_sched_barrier(0);
-                if (d == 0) advance(DEPTH);
-                ring[d].fetch(w, scales, x, number(d));
+                ring[d].fetch(w, scales, x, number(d + DEPTH));
                 __builtin_amdgcn_sched_barrier(0);
             }
+            left -= DEPTH;
+            j += DEPTH * step;
+            j -= j >= whole ? whole : 0;
         }
 #pragma unroll
-        for (int d = 0; d < DEPTH; d++) ring[d].use(acc, turned, lane);
-        advance(DEPTH);
+        for (int d = 0; d < DEPTH; d++) {
+            if (d == DEPTH - 1 && tail && left == DEPTH) ring[d].finish(w, x, whole);
+            ring[d].use(acc, turned, lane);
+        }
         left -= DEPTH;
+        j += DEPTH * step;
+        j -= j >= whole ? whole : 0;
     }
     if (left > 0) {  // fewer than DEPTH: together, the last one again where there is none
 #pragma unroll
         for (int d = 0; d < DEPTH; d++) ring[d].fetch(w, scales, x, number(min(d, left - 1)));
 #pragma unroll
-        for (int d = 0; d < DEPTH; d++)
-            if (d < left) ring[d].use(acc, turned, lane);
-    }
-    if ((K & 127) && (blocks - first) % step == 0) {  // the short block is this wave's
-        ring[0].fetch_end(w, scales, x, blocks, K, lane);
-        ring[0].use(acc, turned, lane);
+        for (int d = 0; d < DEPTH; d++) {
+            if (d >= left) continue;
+            if (tail && d == left - 1) ring[d].finish(w, x, whole);
+            ring[d].use(acc, turned, lane);
+        }
     }
 }
 
@@ -454,12 +398,12 @@ __global__ __launch_bounds__(256, 2) void moe_up_kernel(MoeParams p, int by_choi
     const uint8_t *scales = W8 ? p.US + (int64_t)expert * p.us_stride : nullptr;
     const int i0 = (shared ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave) * 16;
     if (i0 >= p.I) return;  // (of a shared tile all four waves stay)
-    MoeRows<W8 ? 1 : 2> w[G];
+    RowBlocks<W8 ? 1 : 2> w[G];
     MoeScales ws[G];
 #pragma unroll
     for (int g = 0; g < G; g++) {
         const int r0 = g * p.I + i0, end = g ? 2 * p.I : p.I;
-        w[g].init(base + (int64_t)r0 * p.ldu * (W8 ? 1 : 2), lane,
+        w[g].init(base + (int64_t)r0 * p.ldu * (W8 ? 1 : 2), p.H, lane,
                   [&](int r) { return (uint32_t)(min(r, end - 1 - r0) * (int)p.ldu) * (W8 ? 1 : 2); });
         if constexpr (W8) ws[g].init(scales, p.ldus, r0, end, li);
     }
@@ -473,12 +417,12 @@ __global__ __launch_bounds__(256, 2) void moe_up_kernel(MoeParams p, int by_choi
     };
     // 16 NB tokens at a time (more read the weights again, from the caches)
     for (int n0 = 0; n0 < n; n0 += 16 * NB) {
-        MoeRows<2> x[NB];
+        RowBlocks<2> x[NB];
         f32x4 acc[G][NB];
 #pragma unroll
         for (int b = 0; b < NB; b++) {
             // (rows past the last token repeat it)
-            x[b].init((const char *)p.X, lane, [&](int r) {
+            x[b].init((const char *)p.X, p.H, lane, [&](int r) {
                 return (uint32_t)(list[min(n0 + b * 16 + r, n - 1)] * (int)p.ldx) * 2;
             });
 #pragma unroll
@@ -525,7 +469,7 @@ __global__ __launch_bounds__(256, 2) void moe_up_kernel(MoeParams p, int by_choi
 // its tokens and a part of its inner columns.  They are dealt out over the 8 waves,
 // each of which adds up its own sums of all tokens in LDS, in a fixed order.  What
 // bounds it is the bytes in flight: a wave streams over the ends of its units (64
-// experts of 4096 x 1024 in 8 bits 58 us, 4.6 TB/s; with units of 4 blocks that each
+// experts of 4096 x 1024 in 8 bits 61 us, 4.4 TB/s; with units of 4 blocks that each
 // drained before the next began 75 us).  Workgroups begin at different units.
 // Where all began at the first one and the same rows of h, that was 101 us.
 constexpr int kDownWaves = 8;
@@ -533,7 +477,7 @@ constexpr int kDownUnits = kMoeExperts + kMoeChunk * kMoeTop / 16;  // sum of ce
 template <bool BF, bool W8>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
 {
-    constexpr int THREADS = 64 * kDownWaves, PAIRS = kMoeChunk * kMoeTop / THREADS, DEPTH = W8 ? 4 : 3;
+    constexpr int THREADS = 64 * kDownWaves, PAIRS = kMoeChunk * kMoeTop / THREADS, DEPTH = 3;
     __shared__ unsigned long long users[kMoeExperts];  // tokens of each expert
     __shared__ uint16_t start[kMoeExperts];            // where its choices start in the list
     __shared__ uint16_t list[kMoeChunk * kMoeTop];     // the choices (t k + r), expert by expert, by token
@@ -600,18 +544,17 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
         if (expert[j] >= 0) list[start[expert[j]] + __popcll(users[expert[j]] & ((1ull << t) - 1))] = (uint16_t)i;
     }
     __syncthreads();
-    // parts of whole blocks of 128, so that every wave has a unit where that is
-    // possible; the short block at the end belongs to the last part
-    const int entries = __builtin_amdgcn_readfirstlane(count), whole = p.I / 128;
-    const int len = max(whole / min(max(whole, 1), (kDownWaves + entries - 1) / entries), 1);
-    const int parts = max((whole + len - 1) / len, 1), units = entries * parts;
+    // parts of whole blocks of 128, so that every wave has a unit where that is possible
+    const int entries = __builtin_amdgcn_readfirstlane(count), blocks = (p.I + 127) >> 7;
+    const int len = blocks / min(blocks, (kDownWaves + entries - 1) / entries);
+    const int parts = (blocks + len - 1) / len, units = entries * parts, tail = p.I & 127 ? blocks - 1 : -1;
     using Block = MoeBlock<BF, W8, 1, 1>;
     struct Unit {
         typename Block::W w[1];
         MoeScales ws[1];
-        MoeRows<2> h[1];
-        int first, n, last;  // blocks: the first one, how many whole ones, whether the short one is among them
-        int at, tokens;      // in the list
+        RowBlocks<2> h[1];
+        int first, n;    // blocks
+        int at, tokens;  // in the list
     };
     const int shift = blockIdx.x * kDownWaves % units;
     auto place = [&](int u) { return u + shift < units ? u + shift : u + shift - units; };
@@ -621,23 +564,17 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
         q.at = __builtin_amdgcn_readfirstlane(unit_start[i]);
         q.tokens = __builtin_amdgcn_readfirstlane(unit_tokens[i]);
         q.first = part * len;
-        q.n = min(whole - q.first, len);
-        q.last = part == parts - 1 && whole * 128 < p.I;
-        q.w[0].init((const char *)p.Down + ((int64_t)e * p.down_stride + h0 * p.lddn) * (W8 ? 1 : 2), lane,
+        q.n = min(blocks - q.first, len);
+        q.w[0].init((const char *)p.Down + ((int64_t)e * p.down_stride + h0 * p.lddn) * (W8 ? 1 : 2), p.I, lane,
                     [&](int r) { return (uint32_t)(min(r, p.H - 1 - h0) * (int)p.lddn) * (W8 ? 1 : 2); });
         if constexpr (W8) q.ws[0].init(p.DS + (int64_t)e * p.ds_stride, p.ldds, h0, p.H, li);
         // (rows past the last token repeat it; below 2^32 bytes: 2048 rows of 2^20)
-        q.h[0].init((const char *)p.hidden, lane,
+        q.h[0].init((const char *)p.hidden, p.I, lane,
                     [&](int r) { return (uint32_t)list[q.at + min(r, q.tokens - 1)] * p.I * 2; });
         return q;
     };
     f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
     auto close = [&](const Unit &q) {
-        if (q.last) {
-            Block f;
-            f.fetch_end(q.w, q.ws, q.h, whole, p.I, lane);
-            f.use(acc, turned[wave], lane);
-        }
         // the lane has tokens 4 lg .. of the 16, of column li
         float *at[4], old[4], by[4];
 #pragma unroll
@@ -652,50 +589,63 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
             if (lg * 4 + j < q.tokens) *at[j] = old[j] + by[j] * acc[0][0][j];
         acc[0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     };
-    if (whole == 0) {
-        for (int u = wave; u < units; u += kDownWaves) close(open(u));
+    if (p.I < kShortRow) {
+        for (int u = wave; u < units; u += kDownWaves) {
+            const Unit q = open(u);
+            Block f;
+            f.fetch_short(q.w, q.ws, q.h);
+            f.use(acc, turned[wave], lane);
+            close(q);
+        }
     } else if (wave < units) {
-        // A wave streams the whole blocks of its units: the first loads of the next
-        // unit follow the last ones of this.  (What a unit lacks to groups of DEPTH
-        // blocks is fetched again and not used.)
+        // A wave streams the blocks of its units: the first loads of the next unit
+        // follow the last ones of this.  A unit's first group of DEPTH blocks is filled
+        // up with blocks that are fetched and not used, so that its last one ends a group.
         Block ring[DEPTH];
         Unit q = open(wave);
-#pragma unroll
-        for (int d = 0; d < DEPTH; d++) {
-            ring[d].fetch(q.w, q.ws, q.h, q.first + min(d, q.n - 1));
+        int g = 0;  // the number in the unit of ring[0]'s block
+        auto fetch = [&](int d, const Unit &of, int block) {
+            ring[d].fetch(of.w, of.ws, of.h, of.first + max(block, 0));
             __builtin_amdgcn_sched_barrier(0);
-        }
+        };
+        auto use = [&](int d) {
+            if (g + d >= 0) ring[d].use(acc, turned[wave], lane);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto end = [&]() {
+            if (q.first + q.n - 1 == tail) ring[DEPTH - 1].finish(q.w, q.h, tail);
+        };
+        auto begin = [&](int n) { return n - (n + DEPTH - 1) / DEPTH * DEPTH; };
+        g = begin(q.n);
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) fetch(d, q, g + d);
         for (int u = wave;;) {
-            int g = 0;
 #pragma unroll 1
             for (; g + DEPTH < q.n; g += DEPTH) {
 #pragma unroll
                 for (int d = 0; d < DEPTH; d++) {
-                    ring[d].use(acc, turned[wave], lane);
-                    __builtin_amdgcn_sched_barrier(0);
-                    ring[d].fetch(q.w, q.ws, q.h, q.first + min(g + DEPTH + d, q.n - 1));
-                    __builtin_amdgcn_sched_barrier(0);
+                    use(d);
+                    fetch(d, q, g + DEPTH + d);
                 }
             }
             u += kDownWaves;
-            if (u >= units) {
-#pragma unroll
-                for (int d = 0; d < DEPTH; d++)
-                    if (g + d < q.n) ring[d].use(acc, turned[wave], lane);
-                close(q);
-                break;
-            }
+            if (u >= units) break;
             const Unit next = open(u);
+            const int from = begin(next.n);
 #pragma unroll
             for (int d = 0; d < DEPTH; d++) {
-                if (g + d < q.n) ring[d].use(acc, turned[wave], lane);
-                __builtin_amdgcn_sched_barrier(0);
-                ring[d].fetch(next.w, next.ws, next.h, next.first + min(d, next.n - 1));
-                __builtin_amdgcn_sched_barrier(0);
+                if (d == DEPTH - 1) end();
+                use(d);
+                fetch(d, next, from + d);
             }
             close(q);
             q = next;
+            g = from;
         }
+        end();
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) use(d);
+        close(q);
     }
     __syncthreads();
     for (int i = tid; i < rows * 16; i += THREADS) {
