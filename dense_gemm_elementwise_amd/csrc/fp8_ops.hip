@@ -27,7 +27,7 @@ int check_format(int64_t f) { return f == GE_FP8_E4M3 || f == GE_FP8_E5M2 ? GEMM
 template <int SRC, bool TILE, bool BOTH>
 hipError_t launch_quant3(int format, const QuantParams &q, hipStream_t s)
 {
-    const dim3 g((unsigned)blocks_of(q.C), (unsigned)blocks_of(q.R)), b(256);
+    const dim3 g((unsigned)blocks_of(q.C), (unsigned)blocks_of(q.R)), b(512);
     return format == GE_FP8_E4M3 ? launch(quant_kernel<SRC, TILE, BOTH, 0, kNoGrad>, g, b, s, q)
                                  : launch(quant_kernel<SRC, TILE, BOTH, 1, kNoGrad>, g, b, s, q);
 }
@@ -427,7 +427,7 @@ int plan_linear_grad8(const ge_linear_fp8_backward_args *a, LinearGradPlan8 &pl)
 template <int SRC, int ACT>
 hipError_t launch_dz3(int format, const QuantParams &q, hipStream_t s)
 {
-    const dim3 g((unsigned)blocks_of(q.C), (unsigned)blocks_of(q.R)), b(256);
+    const dim3 g((unsigned)blocks_of(q.C), (unsigned)blocks_of(q.R)), b(512);
     return format == GE_FP8_E4M3 ? launch(quant_kernel<SRC, false, true, 0, ACT>, g, b, s, q)
                                  : launch(quant_kernel<SRC, false, true, 1, ACT>, g, b, s, q);
 }

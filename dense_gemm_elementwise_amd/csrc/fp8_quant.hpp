@@ -13,6 +13,7 @@
 
 #include "linear_gemm.hpp"
 #include "ops_host.hpp"
+#include "row_pieces.hpp"
 
 namespace gemm_epi {
 
@@ -82,69 +83,103 @@ __device__ __forceinline__ float finite_abs(float v)
 
 // ---------------------------------------------------------------------------
 // One workgroup quantises one 128 x 128 block of X in registers: thread (tx, ty)
-// holds rows 8 ty .. + 7 of columns 8 tx .. + 7, so a row's maximum is one over
-// 16 adjacent lanes, a column's one over 4 lanes and the 4 waves.  The row-wise bytes
+// holds rows 4 ty .. + 3 of columns 8 tx .. + 7, so a row's maximum is one over
+// 16 adjacent lanes, a column's one over 4 lanes and the 8 waves.  The row-wise bytes
 // leave as they are, 128 bytes a row; the transposed ones are turned around in
-// LDS, 8 rows of a column (8 bytes) at a time.  Bound by the bytes: 2 in, 1 or 2 out.
+// LDS, 4 rows of a column (4 bytes) at a time.  Bound by the bytes: 2 in, 1 or 2 out.
+// All loads are issued together, at the edge too: a row's last 16 bytes where the
+// row ends inside them, moved down (with a branch a row and single elements at
+// the edge, 2400 x 3233 of fp16 into both orientations 13.8 us, @QODD@ so).
 // ---------------------------------------------------------------------------
 template <int SRC, bool TILE, bool BOTH, int FMT, int GRAD>
-__global__ __launch_bounds__(256) void quant_kernel(QuantParams p)
+__global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
 {
-    constexpr int TOP = FMT == 0 ? 8 : 15;
+    constexpr int TOP = FMT == 0 ? 8 : 15, RT = 4, WAVES = 8;  // RT: rows a thread
     constexpr bool BF = SRC == QS_BF16;
-    constexpr int PITCH = 136;  // bytes of a column in LDS: 8-byte aligned, off the bank stride
-    __shared__ float colmax[4][kBlock];
-    __shared__ float tilemax[4];
+    constexpr int PITCH = 132;  // bytes of a column in LDS, off the bank stride
+    constexpr bool WITH_Z = GRAD > ACT_IDENTITY;
+    __shared__ float colmax[WAVES][kBlock];
+    __shared__ float tilemax[WAVES];
     __shared__ __attribute__((aligned(16))) uint8_t turned[BOTH ? kBlock * PITCH : 8];
-    __shared__ float colsum[GRAD >= 0 ? 4 : 1][kBlock];
+    __shared__ float colsum[GRAD >= 0 ? WAVES : 1][kBlock];
     const int tid = threadIdx.x, wave = tid >> 6, tx = tid & 15, ty = tid >> 4;
     const int r0 = (int)blockIdx.y * kBlock, c0 = (int)blockIdx.x * kBlock;
     const int rows = min(p.R - r0, kBlock), cols = min(p.C - c0, kBlock);
     const int n = cols - tx * 8;  // columns that exist from this thread's on
 
-    float v[8][8];
+    float v[RT][8];
+    if constexpr (SRC == QS_F32) {
+        i32x4 x[RT][2];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int r = ty * 8 + i;
-        const bool here = r < rows && n > 0;
-        if constexpr (SRC == QS_F32) {
-            const float *x = (const float *)p.X + (int64_t)(r0 + r) * p.ldx + c0 + tx * 8;
-            if (here && n >= 8) {
-                const f32x4 a = *(const f32x4u *)x, b = *(const f32x4u *)(x + 4);
+        for (int i = 0; i < RT; i++) {
+            const float *row = (const float *)p.X + (int64_t)(r0 + min(ty * RT + i, rows - 1)) * p.ldx;
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    v[i][e] = a[e];
-                    v[i][4 + e] = b[e];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; e++) v[i][e] = here && e < n ? x[e] : 0.0f;
+            for (int h = 0; h < 2; h++) {
+                const int c = c0 + tx * 8 + h * 4;
+                x[i][h] = p.C >= 4 ? load_piece<4>((const char *)(row + min(c, p.C - 4)))
+                                   : load_piece_short<4>((const char *)(row + c), p.C - c);
             }
-        } else {
-            half8 x = {}, z = {};
-            if (here) x = load8((const _Float16 *)p.X + (int64_t)(r0 + r) * p.ldx + c0 + tx * 8, n);
-            if constexpr (GRAD > ACT_IDENTITY)
-                if (here) z = load8((const _Float16 *)p.Z + (int64_t)(r0 + r) * p.ldz + c0 + tx * 8, n);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                if (cols < kBlock && p.C >= 4) x[i][h] = move_down(x[i][h], min(max(4 - (n - h * 4), 0), 4) * 4);
+                const f32x4 f = __builtin_bit_cast(f32x4, x[i][h]);
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[i][h * 4 + e] = f[e];
+            }
+    } else {
+        i32x4 x[RT], z[WITH_Z ? RT : 1];
+        auto load = [&](i32x4 (&f)[RT], const void *from, int64_t ld) {
+            const int c = c0 + tx * 8;
+#pragma unroll
+            for (int i = 0; i < RT; i++) {
+                const _Float16 *row = (const _Float16 *)from + (int64_t)(r0 + min(ty * RT + i, rows - 1)) * ld;
+                f[i] = p.C >= 8 ? load_piece<2>((const char *)(row + min(c, p.C - 8)))
+                                : load_piece_short<2>((const char *)(row + c), p.C - c);
+            }
+        };
+        load(x, p.X, p.ldx);
+        if constexpr (WITH_Z) load(z, p.Z, p.ldz);
+        if (cols < kBlock && p.C >= 8) {
+            const int miss = min(max(8 - n, 0), 8) * 2;
+#pragma unroll
+            for (int i = 0; i < RT; i++) {
+                x[i] = move_down(x[i], miss);
+                if constexpr (WITH_Z) z[i] = move_down(z[i], miss);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; i++) {
+            const half8 xv = __builtin_bit_cast(half8, x[i]);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                float d = ld16<BF>(x[e]);
-                if constexpr (GRAD == ACT_RELU)
-                    d = ld16<BF>(z[e]) <= 0.0f ? 0.0f : d;  // a mask, as in linear_backward
-                else if constexpr (GRAD > ACT_IDENTITY)
-                    d = e < n && here ? d * lin_act_grad<GRAD>(ld16<BF>(z[e])) : 0.0f;
+                float d = ld16<BF>(xv[e]);
+                if constexpr (WITH_Z) {
+                    const float zv = ld16<BF>(__builtin_bit_cast(half8, z[i])[e]);
+                    if constexpr (GRAD == ACT_RELU)
+                        d = zv <= 0.0f ? 0.0f : d;  // a mask, as in linear_backward
+                    else
+                        d *= lin_act_grad<GRAD>(zv);  // (behind the row's end both are 0, and the slope of 0 is finite)
+                }
                 v[i][e] = d;
             }
         }
     }
+    if (rows < kBlock)  // (the last row stands for those that are not there)
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+            if (ty * RT + i >= rows)
+#pragma unroll
+                for (int e = 0; e < 8; e++) v[i][e] = 0.0f;
 
     if constexpr (GRAD >= 0) {
         if (p.partial) {
             float s[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                s[e] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; i++) s[e] += v[i][e];
+                s[e] = (v[0][e] + v[1][e]) + (v[2][e] + v[3][e]);
                 s[e] += __shfl_xor(s[e], 16);
                 s[e] += __shfl_xor(s[e], 32);
             }
@@ -153,17 +188,20 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantParams p)
                 for (int e = 0; e < 8; e++) colsum[wave][tx * 8 + e] = s[e];
             }
             __syncthreads();
-            if (tid < cols)
-                p.partial[(int64_t)blockIdx.y * p.C + c0 + tid] =
-                    (colsum[0][tid] + colsum[1][tid]) + (colsum[2][tid] + colsum[3][tid]);
+            if (tid < cols) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WAVES; w += 2) sum += colsum[w][tid] + colsum[w + 1][tid];
+                p.partial[(int64_t)blockIdx.y * p.C + c0 + tid] = sum;
+            }
         }
     }
 
     // the rows' maxima; where one is infinite, the finite elements' alone
     // (v_max drops a NaN by itself)
-    float rm[8];
+    float rm[RT];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
+    for (int i = 0; i < RT; i++) {
         rm[i] = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; e++) rm[i] = __builtin_fmaxf(rm[i], __builtin_fabsf(v[i][e]));
@@ -173,41 +211,41 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantParams p)
             for (int e = 0; e < 8; e++) rm[i] = __builtin_fmaxf(rm[i], finite_abs(v[i][e]));
         }
     }
-    int ex[8];
+    int ex[RT];
     if constexpr (TILE) {
-        float m = rm[0];
-#pragma unroll
-        for (int i = 1; i < 8; i++) m = __builtin_fmaxf(m, rm[i]);
+        float m = __builtin_fmaxf(__builtin_fmaxf(rm[0], rm[1]), __builtin_fmaxf(rm[2], rm[3]));
         m = row16_max(m);
         m = __builtin_fmaxf(m, __shfl_xor(m, 16));
         m = __builtin_fmaxf(m, __shfl_xor(m, 32));
         if ((tid & 63) == 0) tilemax[wave] = m;
         __syncthreads();
-        m = __builtin_fmaxf(__builtin_fmaxf(tilemax[0], tilemax[1]), __builtin_fmaxf(tilemax[2], tilemax[3]));
+        m = tilemax[0];
+#pragma unroll
+        for (int w = 1; w < WAVES; w++) m = __builtin_fmaxf(m, tilemax[w]);
         const int e = block_exponent(m, TOP);
 #pragma unroll
-        for (int i = 0; i < 8; i++) ex[i] = e;
+        for (int i = 0; i < RT; i++) ex[i] = e;
         if (tid == 0) {
             if (p.S) p.S[(int64_t)blockIdx.y * p.lds + blockIdx.x] = (uint8_t)(e + 127);
             if (BOTH) p.ST[(int64_t)blockIdx.x * p.ldst + blockIdx.y] = (uint8_t)(e + 127);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) ex[i] = block_exponent(row16_max(rm[i]), TOP);
+        for (int i = 0; i < RT; i++) ex[i] = block_exponent(row16_max(rm[i]), TOP);
         if (p.S && tx == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (ty * 8 + i < rows)
-                    p.S[(int64_t)(r0 + ty * 8 + i) * p.lds + blockIdx.x] = (uint8_t)(ex[i] + 127);
+            for (int i = 0; i < RT; i++)
+                if (ty * RT + i < rows)
+                    p.S[(int64_t)(r0 + ty * RT + i) * p.lds + blockIdx.x] = (uint8_t)(ex[i] + 127);
         }
     }
     if (!BOTH || p.Q) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
+        for (int i = 0; i < RT; i++) {
             const float f = pow2f(-ex[i]);
             const u32x2 q = {cvt4<FMT>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f),
                              cvt4<FMT>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f)};
-            if (ty * 8 + i < rows) store_bytes8(p.Q + (int64_t)(r0 + ty * 8 + i) * p.ldq + c0 + tx * 8, q, n);
+            if (ty * RT + i < rows) store_bytes8(p.Q + (int64_t)(r0 + ty * RT + i) * p.ldq + c0 + tx * 8, q, n);
         }
     }
     if constexpr (BOTH) {
@@ -220,46 +258,49 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantParams p)
             for (int e = 0; e < 8; e++) {
                 float m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; i++) m = __builtin_fmaxf(m, __builtin_fabsf(v[i][e]));
+                for (int i = 0; i < RT; i++) m = __builtin_fmaxf(m, __builtin_fabsf(v[i][e]));
                 if (!(m < __builtin_inff())) {
                     m = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 8; i++) m = __builtin_fmaxf(m, finite_abs(v[i][e]));
+                    for (int i = 0; i < RT; i++) m = __builtin_fmaxf(m, finite_abs(v[i][e]));
                 }
                 m = __builtin_fmaxf(m, __shfl_xor(m, 16));
                 m = __builtin_fmaxf(m, __shfl_xor(m, 32));
                 if ((tid & 63) < 16) colmax[wave][tx * 8 + e] = m;
             }
             __syncthreads();
+            if (tid < kBlock) {  // the column's scale, for all that hold a part of it
+                float m = colmax[0][tid];
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int c = tx * 8 + e;
-                ec[e] = block_exponent(__builtin_fmaxf(__builtin_fmaxf(colmax[0][c], colmax[1][c]),
-                                                       __builtin_fmaxf(colmax[2][c], colmax[3][c])),
-                                       TOP);
-                if (ty == 0 && e < n) p.ST[(int64_t)(c0 + c) * p.ldst + blockIdx.y] = (uint8_t)(ec[e] + 127);
+                for (int w = 1; w < WAVES; w++) m = __builtin_fmaxf(m, colmax[w][tid]);
+                const int e = block_exponent(m, TOP);
+                if (tid < cols) p.ST[(int64_t)(c0 + tid) * p.ldst + blockIdx.y] = (uint8_t)(e + 127);
+                colmax[0][tid] = __builtin_bit_cast(float, e);
             }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; e++) ec[e] = __builtin_bit_cast(int, colmax[0][tx * 8 + e]);
         }
 #pragma unroll
         for (int e = 0; e < 8; e++) {
             const float f = pow2f(-ec[e]);
-            const u32x2 q = {cvt4<FMT>(v[0][e] * f, v[1][e] * f, v[2][e] * f, v[3][e] * f),
-                             cvt4<FMT>(v[4][e] * f, v[5][e] * f, v[6][e] * f, v[7][e] * f)};
-            *(u32x2 *)(turned + (tx * 8 + e) * PITCH + ty * 8) = q;
+            *(uint32_t *)(turned + (tx * 8 + e) * PITCH + ty * RT) =
+                cvt4<FMT>(v[0][e] * f, v[1][e] * f, v[2][e] * f, v[3][e] * f);
         }
         __syncthreads();
         // 8 threads a column, 16 bytes each
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int c = i * 32 + (tid >> 3), at = (tid & 7) * 16, m = rows - at;
-            const u32x2 lo = *(const u32x2 *)(turned + c * PITCH + at), hi = *(const u32x2 *)(turned + c * PITCH + at + 8);
+        for (int i = 0; i < 2; i++) {
+            const int c = i * 64 + (tid >> 3), at = (tid & 7) * 16, m = rows - at;
+            const uint32_t *from = (const uint32_t *)(turned + c * PITCH + at);
+            const u32x4 w = {from[0], from[1], from[2], from[3]};
             if (c < cols && m > 0) {
                 uint8_t *q = p.QT + (int64_t)(c0 + c) * p.ldqt + r0 + at;
                 if (m >= 16) {
-                    *(u32x4u *)q = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                    *(u32x4u *)q = w;
                 } else {
-                    store_bytes8(q, lo, m);
-                    if (m > 8) store_bytes8(q + 8, hi, m - 8);
+                    store_bytes8(q, u32x2{w[0], w[1]}, m);
+                    if (m > 8) store_bytes8(q + 8, u32x2{w[2], w[3]}, m - 8);
                 }
             }
         }

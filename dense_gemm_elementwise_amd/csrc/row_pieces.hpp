@@ -22,25 +22,20 @@ __device__ __forceinline__ i32x4 move_down(i32x4 v, int n)
 // 16 bytes at any element-aligned address
 template <int ES>
 __device__ __forceinline__ i32x4 load_piece(const char *p) { return *(const i32x4b *)p; }
-// The same where a row of K elements of ES bytes ends inside them or before (n
-// exist; the rest are zeros), without reading outside the row: its last 16 bytes,
-// moved down; of a shorter row element by element.
+// The same of a row that has fewer than 16 bytes, element by element: the first n
+// exist (the last of them at p + n - 1 where n is not positive), the rest are zeros.
 template <int ES>
-__device__ __forceinline__ i32x4 load_piece_end(const char *p, int n, int K)
+__device__ __forceinline__ i32x4 load_piece_short(const char *p, int n)
 {
     constexpr int P = 16 / ES;
-    if (K >= P) {
-        const int miss = max(P - n, 0);
-        return move_down(load_piece<ES>(p - (int64_t)miss * ES), min(miss, P) * ES);
-    }
     uint32_t v[4] = {};
 #pragma unroll 1
     for (int e = 0; e < P; e++) {  // (the elements move down, one after the other)
         const char *at = p + (int64_t)min(e, n - 1) * ES;
-        const uint32_t x = ES == 1 ? *(const uint8_t *)at : *(const uint16_t *)at;
+        const uint32_t x = ES == 1 ? *(const uint8_t *)at : ES == 2 ? *(const uint16_t *)at : *(const uint32_t *)at;
 #pragma unroll
-        for (int d = 0; d < 3; d++) v[d] = v[d] >> (8 * ES) | v[d + 1] << (32 - 8 * ES);
-        v[3] = v[3] >> (8 * ES) | (e < n ? x << (32 - 8 * ES) : 0);
+        for (int d = 0; d < 3; d++) v[d] = (uint64_t)v[d] >> (8 * ES) | v[d + 1] << (32 - 8 * ES);
+        v[3] = (uint64_t)v[3] >> (8 * ES) | (e < n ? x << (32 - 8 * ES) : 0);
     }
     return i32x4{(int)v[0], (int)v[1], (int)v[2], (int)v[3]};
 }
@@ -85,7 +80,7 @@ struct RowBlocks {
     {
         const int K = (last + 16) / ES;
 #pragma unroll
-        for (int v = 0; v < NL; v++) f[v] = load_piece_end<ES>(base + (off[v] + (uint32_t)col), K - col / ES, K);
+        for (int v = 0; v < NL; v++) f[v] = load_piece_short<ES>(base + (off[v] + (uint32_t)col), K - col / ES);
     }
     __device__ static __forceinline__ int at(int row, int piece) { return row * (128 * ES) + (piece ^ swz_a<LPR>(row)) * 16; }
     __device__ static __forceinline__ void put(char *lds, const i32x4 (&f)[NL], int lane)
