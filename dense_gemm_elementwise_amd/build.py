@@ -36,7 +36,7 @@ SRCS = [os.path.join(PKG, "csrc", f) for f in ("gemm_epi.hip", "gemm_epi_bf16.hi
                                                "linear_tn_f16.hip", "linear_tn_bf16.hip",
                                                "linear_pair_f16.hip", "linear_pair_bf16.hip",
                                                "fp8_ops.hip", "fp8_e4m3_f16.hip", "fp8_e4m3_bf16.hip",
-                                               "fp8_e5m2_f16.hip", "fp8_e5m2_bf16.hip", "moe.hip")]
+                                               "fp8_e5m2_f16.hip", "fp8_e5m2_bf16.hip", "fp8_rows.hip", "moe.hip")]
 LIB = os.path.join(PKG, "libgemm_epi.so")
 RESOURCES = os.path.join(PKG, "libgemm_epi.resources.json")
 ARCH = "gfx950"

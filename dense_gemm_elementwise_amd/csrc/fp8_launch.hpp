@@ -27,6 +27,10 @@ hipError_t fp8_launch_out_e4m3_bf16(int tile, const Fp8Params &p, int groups, hi
 hipError_t fp8_launch_out_e5m2_f16(int tile, const Fp8Params &p, int groups, hipStream_t s);
 hipError_t fp8_launch_out_e5m2_bf16(int tile, const Fp8Params &p, int groups, hipStream_t s);
 
+// Up to 16 rows (fp8_rows.hpp).  Without scales p.X has 16 bits and up to 4 rows.
+struct FewRows8;
+hipError_t fp8_launch_rows(bool bf, bool e5m2, const FewRows8 &p, hipStream_t s);
+
 template <int T, int EPI, int ACT, bool BF, int FA>
 hipError_t fp8_launch_one(const Fp8Params &p, int groups, hipStream_t stream)
 {

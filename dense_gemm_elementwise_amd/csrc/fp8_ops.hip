@@ -8,6 +8,7 @@
 #include "fp8_launch.hpp"
 #include "fp8_ops.h"
 #include "fp8_quant.hpp"
+#include "fp8_rows.hpp"
 #include "ops_host.hpp"
 
 using namespace gemm_epi;
@@ -261,6 +262,7 @@ hipError_t run_product8(bool bf, bool e5m2, const Plan8 &pl, Fp8Params p, void *
 
 // ---- linear ---------------------------------------------------------------------
 struct LinearPlan8 {
+    bool few = false;  // rows: fp8_rows.hpp
     StageAt x, w;
     Plan8 pl;
     int64_t off_q = 0, off_s = 0, off_part = 0, bytes = 0;
@@ -295,6 +297,15 @@ int plan_linear8(const ge_linear_fp8_args *a, LinearPlan8 &pl)
     GE_CHECK(check_linear8(a));
     if (a->M == 0) return GEMM_EPI_OK;
     Layout lay;
+    pl.few = a->M <= kFewRows;
+    if (pl.few) {
+        if (!a->XS && a->M > kFewRows16Bit) {
+            pl.off_q = lay.take(a->M * round_up(a->K, 16));
+            pl.off_s = lay.take(a->M * round_up(blocks_of(a->K), 4));
+        }
+        pl.bytes = lay.bytes;
+        return GEMM_EPI_OK;
+    }
     if (a->XS) {
         pl.x = plan_operand(a->X, a->ldx, a->XS, a->ldxs, a->M, a->M, a->K, lay);
     } else {
@@ -316,8 +327,11 @@ int run_linear8(const ge_linear_fp8_args *a, const LinearPlan8 &pl)
     const bool bf = a->dtype == GEMM_EPI_BF16;
     Operand8 x = {(const uint8_t *)a->X, (const uint8_t *)a->XS, a->ldx, a->ldxs};
     Operand8 w = {(const uint8_t *)a->W, (const uint8_t *)a->WS, a->ldw, a->ldws};
+    const bool e5m2 = a->format == GE_FP8_E5M2;
     Staging st;
-    if (a->XS) {
+    if (pl.few && (a->XS || a->M <= kFewRows16Bit)) {
+        // X is read as it is
+    } else if (a->XS) {
         stage_operand(pl.x, x, a->M, a->M, a->K, ws, st);
     } else {
         QuantParams q = {};
@@ -332,11 +346,33 @@ int run_linear8(const ge_linear_fp8_args *a, const LinearPlan8 &pl)
         GE_TRY(launch_quant(a->dtype, false, (int)a->format, q, s));
         x = {q.Q, q.S, q.ldq, q.lds};
     }
+    if (pl.few) {
+        FewRows8 f = {};
+        f.X = x.q;
+        f.XS = x.s;
+        f.ldx = x.ldq;
+        f.ldxs = x.lds;
+        f.W = w.q;
+        f.WS = w.s;
+        f.ldw = w.ldq;
+        f.ldws = w.lds;
+        f.M = (int)a->M;
+        f.N = (int)a->N;
+        f.K = (int)a->K;
+        f.act = (int)a->act;
+        f.bias = (const _Float16 *)a->bias;
+        f.R = (const _Float16 *)a->residual;
+        f.D = (_Float16 *)a->D;
+        f.Z = (_Float16 *)a->Z;
+        f.ldr = a->ldr;
+        f.ldd = a->ldd;
+        f.ldz = a->ldz;
+        return hip_status(fp8_launch_rows(bf, e5m2, f, s));
+    }
     stage_operand(pl.w, w, a->N, blocks_of(a->N), a->K, ws, st);
     GE_TRY(st.run(s));
     Fp8Params p = {};
     set_product8(p, pl.pl, a->M, a->N, a->K, x, w, 7);
-    const bool e5m2 = a->format == GE_FP8_E5M2;
     const int groups = (int)plan_groups(pl.pl);
     if (pl.pl.splits > 1) {
         SplitSumParams q = set_split8(p, pl.pl, (float *)(ws + pl.off_part));

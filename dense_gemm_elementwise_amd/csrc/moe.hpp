@@ -166,8 +166,6 @@ struct MoeScales {
 template <bool W8, int G, int NB>
 constexpr int moe_turn_bytes() { return G * RowBlocks<W8 ? 1 : 2>::BYTES + NB * RowBlocks<2>::BYTES; }
 
-constexpr int kShortRow = 16;  // elements; of shorter rows there is no piece of 16 bytes in 8 bits
-
 // One block of 128 columns: the weights of G times 16 rows and NB times 16 tokens, on their way.
 template <bool BF, bool W8, int G, int NB>
 struct MoeBlock {
@@ -249,10 +247,8 @@ struct MoeBlock {
     }
 };
 
-// acc[g][b] += rows g times the 16 tokens of block b, over every step-th block of
-// 128 columns from `first` on; K: the columns that exist.  DEPTH blocks' loads are
-// in flight together.  turned: moe_turn_bytes of LDS, the wave's own.  The blocks are taken
-// from block `turn` on, around the end, so that workgroups do not all walk their rows from the start.
+// acc[g][b] += rows g times the 16 tokens of block b, over the blocks of
+// stream_row_blocks.  turned: moe_turn_bytes of LDS, the wave's own.
 template <bool BF, bool W8, int G, int NB, int DEPTH>
 __device__ __forceinline__ void moe_product(f32x4 (&acc)[G][NB], const RowBlocks<W8 ? 1 : 2> (&w)[G],
                                             const MoeScales (&scales)[G], const RowBlocks<2> (&x)[NB], char *turned,
@@ -266,56 +262,12 @@ __device__ __forceinline__ void moe_product(f32x4 (&acc)[G][NB], const RowBlocks
         }
         return;
     }
-    // The steady loop has no branch around its loads, and the order of loads and uses
-    // is fixed, before it too: where paths join, the compiler waits for as many loads
-    // as either path would need.
-    const int whole = K >> 7;
-    const bool tail = (K & 127) && first <= whole && (whole - first) % step == 0;  // the last block this wave takes
-    int left = (whole > first ? (whole - first + step - 1) / step : 0) + tail;
-    int j = first + turn;  // the block, before it is wrapped around
-    j -= j >= whole ? whole : 0;
-    auto number = [&](int d) {  // of the d-th block from j on
-        const int i = j + d * step;
-        return tail && d == left - 1 ? whole : i >= whole ? i - whole : i;
-    };
-    if (left >= DEPTH) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; d++) {
-            ring[d].fetch(w, scales, x, number(d));
-            __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll 1
-        while (left >= 2 * DEPTH) {
-#pragma unroll
-            for (int d = 0; d < DEPTH; d++) {
-                ring[d].use(acc, turned, lane);
-                __builtin_amdgcn_sched_barrier(0);
-                ring[d].fetch(w, scales, x, number(d + DEPTH));
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            left -= DEPTH;
-            j += DEPTH * step;
-            j -= j >= whole ? whole : 0;
-        }
-#pragma unroll
-        for (int d = 0; d < DEPTH; d++) {
-            if (d == DEPTH - 1 && tail && left == DEPTH) ring[d].finish(w, x, whole);
+    stream_row_blocks<DEPTH>(
+        first, step, K, turn, [&](int d, int block) { ring[d].fetch(w, scales, x, block); },
+        [&](int d, int finish) {
+            if (finish >= 0) ring[d].finish(w, x, finish);
             ring[d].use(acc, turned, lane);
-        }
-        left -= DEPTH;
-        j += DEPTH * step;
-        j -= j >= whole ? whole : 0;
-    }
-    if (left > 0) {  // fewer than DEPTH: together, the last one again where there is none
-#pragma unroll
-        for (int d = 0; d < DEPTH; d++) ring[d].fetch(w, scales, x, number(min(d, left - 1)));
-#pragma unroll
-        for (int d = 0; d < DEPTH; d++) {
-            if (d >= left) continue;
-            if (tail && d == left - 1) ring[d].finish(w, x, whole);
-            ring[d].use(acc, turned, lane);
-        }
-    }
+        });
 }
 
 // h = act(Up x) of one expert and some tiles of 16 of its inner rows, for the

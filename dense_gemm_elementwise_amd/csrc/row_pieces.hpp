@@ -63,31 +63,96 @@ struct RowBlocks {
         for (int v = 0; v < NL; v++) off[v] = row(v * RPL + lane / LPR);
     }
     // (of rows of 16 bytes and more; where they end in the block, finish() follows)
-    __device__ __forceinline__ void load(i32x4 (&f)[NL], int block) const
+    // L: the loads that are made, of the first L RPL rows
+    template <int L>
+    __device__ __forceinline__ void load(i32x4 (&f)[L], int block) const
     {
         const uint32_t at = (uint32_t)min(col + block * (128 * ES), last);
 #pragma unroll
-        for (int v = 0; v < NL; v++) f[v] = load_piece<ES>(base + (off[v] + at));
+        for (int v = 0; v < L; v++) f[v] = load_piece<ES>(base + (off[v] + at));
     }
-    __device__ __forceinline__ void finish(i32x4 (&f)[NL], int block) const
+    template <int L>
+    __device__ __forceinline__ void finish(i32x4 (&f)[L], int block) const
     {
         const int miss = min(max(col + block * (128 * ES) - last, 0), 16);
 #pragma unroll
-        for (int v = 0; v < NL; v++) f[v] = move_down(f[v], miss);
+        for (int v = 0; v < L; v++) f[v] = move_down(f[v], miss);
     }
     // the only block of shorter rows
-    __device__ __forceinline__ void load_short(i32x4 (&f)[NL]) const
+    template <int L>
+    __device__ __forceinline__ void load_short(i32x4 (&f)[L]) const
     {
         const int K = (last + 16) / ES;
 #pragma unroll
-        for (int v = 0; v < NL; v++) f[v] = load_piece_short<ES>(base + (off[v] + (uint32_t)col), K - col / ES);
+        for (int v = 0; v < L; v++) f[v] = load_piece_short<ES>(base + (off[v] + (uint32_t)col), K - col / ES);
     }
     __device__ static __forceinline__ int at(int row, int piece) { return row * (128 * ES) + (piece ^ swz_a<LPR>(row)) * 16; }
-    __device__ static __forceinline__ void put(char *lds, const i32x4 (&f)[NL], int lane)
+    template <int L>
+    __device__ static __forceinline__ void put(char *lds, const i32x4 (&f)[L], int lane)
     {
 #pragma unroll
-        for (int v = 0; v < NL; v++) *(i32x4 *)(lds + at(v * RPL + lane / LPR, lane % LPR)) = f[v];
+        for (int v = 0; v < L; v++) *(i32x4 *)(lds + at(v * RPL + lane / LPR, lane % LPR)) = f[v];
     }
 };
+
+constexpr int kShortRow = 16;  // elements; of shorter rows there is no piece of 16 bytes in 8 bits
+
+// A wave takes every step-th block of 128 of K columns (kShortRow and more) from
+// block `first` on: fetch(d, block) issues the loads of slot d, use(d, finish) uses
+// them, with the block's number in finish where the rows end in it, otherwise -1.
+// DEPTH blocks' loads are in flight together.  The blocks are taken from block `turn` on,
+// around the end, so that workgroups do not all walk their rows from the start.
+template <int DEPTH, typename Fetch, typename Use>
+__device__ __forceinline__ void stream_row_blocks(int first, int step, int K, int turn, Fetch &&fetch, Use &&use)
+{
+    // The steady loop has no branch around its loads, and the order of loads and uses
+    // is fixed, before it too: where paths join, the compiler waits for as many loads
+    // as either path would need.
+    const int whole = K >> 7;
+    const bool tail = (K & 127) && first <= whole && (whole - first) % step == 0;  // the last block this wave takes
+    int left = (whole > first ? (whole - first + step - 1) / step : 0) + tail;
+    int j = first + turn;  // the block, before it is wrapped around
+    j -= j >= whole ? whole : 0;
+    auto number = [&](int d) {  // of the d-th block from j on
+        const int i = j + d * step;
+        return tail && d == left - 1 ? whole : i >= whole ? i - whole : i;
+    };
+    if (left >= DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) {
+            fetch(d, number(d));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll 1
+        while (left >= 2 * DEPTH) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; d++) {
+                use(d, -1);
+                __builtin_amdgcn_sched_barrier(0);
+                fetch(d, number(d + DEPTH));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            left -= DEPTH;
+            j += DEPTH * step;
+            j -= j >= whole ? whole : 0;
+        }
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) {
+            use(d, d == DEPTH - 1 && tail && left == DEPTH ? whole : -1);
+        }
+        left -= DEPTH;
+        j += DEPTH * step;
+        j -= j >= whole ? whole : 0;
+    }
+    if (left > 0) {  // fewer than DEPTH: together, the last one again where there is none
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) fetch(d, number(min(d, left - 1)));
+#pragma unroll
+        for (int d = 0; d < DEPTH; d++) {
+            if (d >= left) continue;
+            use(d, tail && d == left - 1 ? whole : -1);
+        }
+    }
+}
 
 }  // namespace gemm_epi

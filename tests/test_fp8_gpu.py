@@ -248,6 +248,49 @@ def test_linear_from_16_bits(M, N, K, dtype):
     check_product(d, z, value(x8, xs, "row"), value(w8, ws, "tile"), bias, residual, "silu", t)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("N, K", [(33, 15), (40, 17), (500, 100), (4200, 1037), (4096, 700), (4090, 2049), (8200, 515)])
+@pytest.mark.parametrize("M", [1, 3, 4, 5, 8, 9, 16])
+def test_linear_few_rows(M, N, K, dtype):
+    """Up to 16 rows: workgroups of 4 and of 16 waves, rows shorter than a load, x in 8 and in 16 bits."""
+    t = TYPES[dtype]
+    format = "e5m2" if (M + N) % 2 == 0 else "e4m3"
+    x8, xs, w8, ws = operands(M, N, K, M + N + K, format)
+    bias, residual = normal(N, seed=9, std=0.5, to=t), normal(M, N, seed=10, to=t)
+    d, z = ge.linear_fp8(x8, w8, ws, bias, residual, x_scale=xs, act="gelu", save_z=True, dtype=t)
+    check_product(d, z, value(x8, xs, "row"), value(w8, ws, "tile"), bias, residual, "gelu", t)
+    x = normal(M, K, seed=M, to=t)
+    x8, xs = ge.quantize_fp8(x)
+    d, z = ge.linear_fp8(x, w8, ws, bias, residual, act="relu", save_z=True)
+    check_product(d, z, value(x8, xs, "row"), value(w8, ws, "tile"), bias, residual, "relu", t)
+
+
+def test_linear_few_rows_in_place():
+    """Operands off every alignment are read where they lie: the bits of contiguous ones.  A row that is not finite
+    touches no other row, in a block's scale neither."""
+    t = torch.bfloat16
+    _, _, w8, ws = operands(1, 300, 515, 3)
+    x = normal(4, 515, seed=4, to=t)
+    want = ge.linear_fp8(x, w8, ws)
+    big = torch.full((301, 520), 0x7F, dtype=torch.uint8, device=DEV)
+    big[1:, 3:518] = w8.view(torch.uint8)
+    scales = torch.full((ws.shape[0], ws.shape[1] + 2), 0xFF, dtype=torch.uint8, device=DEV)
+    scales[:, 1:1 + ws.shape[1]] = ws.view(torch.uint8)
+    wide = torch.full((4, 522), float("nan"), dtype=t, device=DEV)
+    wide[:, 5:520] = x
+    args = big.view(E4)[1:, 3:518], scales.view(E8)[:, 1:1 + ws.shape[1]]
+    assert torch.equal(ge.linear_fp8(wide[:, 5:520], *args), want)
+    x8, xs = ge.quantize_fp8(x)
+    odd = torch.full((4, 517), 0x7F, dtype=torch.uint8, device=DEV)
+    odd[:, 1:516] = x8.view(torch.uint8)
+    assert torch.equal(ge.linear_fp8(odd.view(E4)[:, 1:516], *args, x_scale=xs, dtype=t),
+                       ge.linear_fp8(x8, w8, ws, x_scale=xs, dtype=t))
+    y = x.clone()
+    y[1, 514], y[2, 130] = float("nan"), float("inf")
+    got = ge.linear_fp8(y, w8, ws)
+    assert torch.equal(got[::3], want[::3]) and bool(torch.isnan(got[1]).all()) and not bool(torch.isfinite(got[2]).any())
+
+
 # each tile and a split contraction: (rows, columns, length) that the plan gives to 256 x 256, 128 x 256, two 128 x 128
 # on a compute unit, one with deep rings, and splits
 LARGE = [(4096, 4104, 650), (4000, 2500, 1037), (1100, 4096, 4096), (700, 8190, 900), (8200, 1000, 384),
