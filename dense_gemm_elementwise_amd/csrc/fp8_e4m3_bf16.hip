@@ -13,4 +13,9 @@ hipError_t fp8_launch_out_e4m3_bf16(int tile, const Fp8Params &p, int groups, hi
     return fp8_launch_out<true, 0>(tile, p, groups, s);
 }
 
+hipError_t fp8_launch_pair_e4m3_bf16(int tile, const Fp8Pair &p, hipStream_t s)
+{
+    return fp8_launch_pair<true, 0>(tile, p, s);
+}
+
 }  // namespace gemm_epi

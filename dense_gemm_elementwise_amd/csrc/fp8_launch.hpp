@@ -27,6 +27,12 @@ hipError_t fp8_launch_out_e4m3_bf16(int tile, const Fp8Params &p, int groups, hi
 hipError_t fp8_launch_out_e5m2_f16(int tile, const Fp8Params &p, int groups, hipStream_t s);
 hipError_t fp8_launch_out_e5m2_bf16(int tile, const Fp8Params &p, int groups, hipStream_t s);
 
+// Two products and the bias's gradient in one launch; tile: any but kFp8Small.
+hipError_t fp8_launch_pair_e4m3_f16(int tile, const Fp8Pair &p, hipStream_t s);
+hipError_t fp8_launch_pair_e4m3_bf16(int tile, const Fp8Pair &p, hipStream_t s);
+hipError_t fp8_launch_pair_e5m2_f16(int tile, const Fp8Pair &p, hipStream_t s);
+hipError_t fp8_launch_pair_e5m2_bf16(int tile, const Fp8Pair &p, hipStream_t s);
+
 // Up to 16 rows (fp8_rows.hpp).  Without scales p.X has 16 bits and up to 4 rows.
 struct FewRows8;
 hipError_t fp8_launch_rows(bool bf, bool e5m2, const FewRows8 &p, hipStream_t s);
@@ -71,6 +77,25 @@ hipError_t fp8_launch_out(int tile, const Fp8Params &p, int groups, hipStream_t 
     case 1: return fp8_launch_one<1, LE_OUT, 0, BF, FA>(p, groups, s);
     case 2: return fp8_launch_one<2, LE_OUT, 0, BF, FA>(p, groups, s);
     default: return fp8_launch_one<3, LE_OUT, 0, BF, FA>(p, groups, s);
+    }
+}
+
+template <int T, bool BF, int FA>
+hipError_t fp8_launch_pair_one(const Fp8Pair &p, hipStream_t s)
+{
+    constexpr Fp8Tile t = kFp8Tiles[T];
+    Fp8Pair arg = p;
+    void *args[] = {(void *)&arg};
+    const int groups = p.groups[0] + p.groups[1] + (p.bias.out ? (p.bias.cols + 255) / 256 : 0);
+    return hipLaunchKernel((const void *)&fp8_pair_kernel<t.bm, t.bn, t.depth, BF, FA>, dim3(groups), dim3(256), args, 0, s);
+}
+template <bool BF, int FA>
+hipError_t fp8_launch_pair(int tile, const Fp8Pair &p, hipStream_t s)
+{
+    switch (tile) {
+    case kFp8Big: return fp8_launch_pair_one<kFp8Big, BF, FA>(p, s);
+    case kFp8Wide: return fp8_launch_pair_one<kFp8Wide, BF, FA>(p, s);
+    default: return fp8_launch_pair_one<kFp8Deep, BF, FA>(p, s);
     }
 }
 

@@ -76,26 +76,24 @@ struct Operand8 {
 };
 struct Staging {
     PadBytes p = {};
-    int n = 0;
-    int64_t most = 0;
-    void add(const uint8_t *&src, int64_t &ld, int64_t rows, int64_t cols, int64_t ldo, uint8_t *dst)
+    int64_t pieces = 0;
+    void add(const uint8_t *&src, int64_t &ld, int64_t rows, int64_t cols, uint8_t *dst)
     {
+        const int n = p.n++;
         p.src[n] = src;
         p.lds[n] = ld;
-        p.rows[n] = rows;
-        p.cols[n] = cols;
-        p.ldo[n] = ldo;
+        p.rows[n] = (int)rows;
+        p.cols[n] = (int)cols;
+        p.ldo[n] = round_up(cols, 16);
         p.dst[n] = dst;
-        n++;
-        most = std::max(most, rows * ldo / 4);
+        pieces += rows * p.ldo[n] / 16;
         src = dst;
-        ld = ldo;
+        ld = p.ldo[n];
     }
+    int64_t groups(int threads) const { return std::min<int64_t>(ceil_div(pieces, threads), 8 * kCUs); }
     hipError_t run(hipStream_t s) const
     {
-        if (!n) return hipSuccess;
-        const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(most, 256), 4096);
-        return launch(pad_bytes_kernel, dim3(blocks, n), dim3(256), s, p);
+        return p.n ? launch(pad_bytes_kernel, dim3((unsigned)groups(256)), dim3(256), s, p) : hipSuccess;
     }
 };
 bool rows16(const void *p, int64_t ld) { return aligned(p, 16) && ld % 16 == 0; }
@@ -110,13 +108,13 @@ StageAt plan_operand(const void *q, int64_t ldq, const void *s, int64_t lds, int
 {
     StageAt at;
     if (!rows16(q, ldq)) at.q = lay.take(rows * round_up(cols, 16));
-    if (!rows4(s, lds)) at.s = lay.take(srows * round_up(blocks_of(cols), 4));
+    if (!rows4(s, lds)) at.s = lay.take(srows * round_up(blocks_of(cols), 16));
     return at;
 }
 void stage_operand(const StageAt &at, Operand8 &o, int64_t rows, int64_t srows, int64_t cols, char *ws, Staging &st)
 {
-    if (at.q >= 0) st.add(o.q, o.ldq, rows, cols, round_up(cols, 16), (uint8_t *)ws + at.q);
-    if (at.s >= 0) st.add(o.s, o.lds, srows, blocks_of(cols), round_up(blocks_of(cols), 4), (uint8_t *)ws + at.s);
+    if (at.q >= 0) st.add(o.q, o.ldq, rows, cols, (uint8_t *)ws + at.q);
+    if (at.s >= 0) st.add(o.s, o.lds, srows, blocks_of(cols), (uint8_t *)ws + at.s);
 }
 
 // ---- products -------------------------------------------------------------------
@@ -190,6 +188,16 @@ Plan8 plan_fp8(int64_t M, int64_t N, int64_t K)
     return best;
 }
 
+// The plan of another tile for the split of `like`: the sums along K keep their order.
+Plan8 plan_tile8(const Plan8 &like, int tile, int64_t M, int64_t N)
+{
+    Plan8 p = like;
+    p.tile = tile;
+    p.tiles_m = ceil_div(M, kFp8Tiles[tile].bm);
+    p.tiles_n = ceil_div(N, kFp8Tiles[tile].bn);
+    return p;
+}
+
 void set_product8(Fp8Params &p, const Plan8 &pl, int64_t M, int64_t N, int64_t K, const Operand8 &a, const Operand8 &b,
                   int shift_b)
 {
@@ -242,22 +250,41 @@ SplitSumParams set_split8(Fp8Params &p, const Plan8 &pl, float *part)
     return q;
 }
 
-// C = A B^T into D (16-bit)
-hipError_t run_product8(bool bf, bool e5m2, const Plan8 &pl, Fp8Params p, void *D, int64_t ldd, float *part, hipStream_t s)
+// C = A B^T into D (16-bit), in parts where it is split: p is set up for the
+// launch, sum for the one behind it that adds up the parts.
+struct Product8 {
+    Fp8Params p = {};
+    SplitSumParams sum = {};
+    int groups = 0;
+    bool split = false;
+};
+void set_out8(Product8 &o, const Plan8 &pl, void *D, int64_t ldd, float *part)
 {
-    const int groups = (int)plan_groups(pl);
-    if (pl.splits == 1) {
-        p.e.D = (_Float16 *)D;
-        p.e.ldd = ldd;
-        p.e.vec = dma_rows(D, ldd, p.e.N);
-        return launch_out8(bf, e5m2, pl.tile, p, groups, s);
+    o.groups = (int)plan_groups(pl);
+    o.split = pl.splits > 1;
+    if (o.split) {
+        o.sum = set_split8(o.p, pl, part);
+        o.sum.D = (_Float16 *)D;
+        o.sum.ldd = ldd;
+    } else {
+        o.p.e.D = (_Float16 *)D;
+        o.p.e.ldd = ldd;
+        o.p.e.vec = dma_rows(D, ldd, o.p.e.N);
     }
-    SplitSumParams q = set_split8(p, pl, part);
-    const hipError_t e = launch_out8(bf, e5m2, pl.tile, p, groups, s);
-    if (e != hipSuccess) return e;
-    q.D = (_Float16 *)D;
-    q.ldd = ldd;
-    return run_split_sum_out(bf, q, s);
+}
+hipError_t run_sum8(bool bf, const Product8 &o, hipStream_t s)
+{
+    return o.split ? run_split_sum_out(bf, o.sum, s) : hipSuccess;
+}
+hipError_t run_product8(bool bf, bool e5m2, const Plan8 &pl, const Product8 &o, hipStream_t s)
+{
+    const hipError_t e = launch_out8(bf, e5m2, pl.tile, o.p, o.groups, s);
+    return e == hipSuccess ? run_sum8(bf, o, s) : e;
+}
+hipError_t launch_pair8(bool bf, bool e5m2, int tile, const Fp8Pair &p, hipStream_t s)
+{
+    if (e5m2) return bf ? fp8_launch_pair_e5m2_bf16(tile, p, s) : fp8_launch_pair_e5m2_f16(tile, p, s);
+    return bf ? fp8_launch_pair_e4m3_bf16(tile, p, s) : fp8_launch_pair_e4m3_f16(tile, p, s);
 }
 
 // ---- linear ---------------------------------------------------------------------
@@ -398,10 +425,14 @@ int run_linear8(const ge_linear_fp8_args *a, const LinearPlan8 &pl)
     return hip_status(launch_fwd8(bf, e5m2, (int)a->act, pl.pl.tile, p, groups, s));
 }
 
+__global__ __launch_bounds__(256) void bias_sum_kernel(BiasSum p) { bias_sum(p, (int)blockIdx.x); }
+
 // ---- linear, backward -------------------------------------------------------------
 struct LinearGradPlan8 {
     StageAt x, w;
     Plan8 dx, dw;
+    bool pair = false;  // both in one launch, on dx's tile
+    int64_t off_dw = 0;
     int64_t off_q = 0, off_s = 0, off_qt = 0, off_st = 0, off_bias = 0, off_part = 0, bytes = 0;
 };
 
@@ -442,39 +473,57 @@ int plan_linear_grad8(const ge_linear_fp8_backward_args *a, LinearGradPlan8 &pl)
     pl.off_qt = lay.take(a->N * round_up(a->M, 16));
     pl.off_st = lay.take(a->N * round_up(blocks_of(a->M), 4));
     if (a->dbias && a->M > kBlock) pl.off_bias = lay.take(blocks_of(a->M) * a->N * 4);
-    int64_t part = 0;
     if (a->dX) {
         pl.w = plan_operand(a->WT, a->ldwt, a->WTS, a->ldwts, a->K, blocks_of(a->K), a->N, lay);
         pl.dx = plan_fp8(a->M, a->K, a->N);
         if (!plan_fits(pl.dx)) return GEMM_EPI_ERR_SHAPE;
-        part = std::max(part, pl.dx.part_bytes);
     }
     if (a->dW) {
         pl.x = plan_operand(a->XT, a->ldxt, a->XTS, a->ldxts, a->K, a->K, a->M, lay);
         pl.dw = plan_fp8(a->N, a->K, a->M);
         if (!plan_fits(pl.dw)) return GEMM_EPI_ERR_SHAPE;
-        part = std::max(part, pl.dw.part_bytes);
     }
-    pl.off_part = lay.take(part);
+    // Where both fit on the chip together, one launch on a tile that both share, if
+    // the longer one then takes less than both one after the other by a tenth (the
+    // estimates' error).  Apart and together, with dbias, us: 1001 x 1003 x 999 27.7 and 12.1,
+    // 1024^3 18.6 and 9.0, 2048 x 2048 x 1024 25.9 and 14.7, 1400^3 26.0 and 12.8,
+    // 700 x 300 x 5001 19.9 and 12.7, 2816^3 (256 x 256) 51.9 and 42.3.
+    if (a->dX && a->dW) {
+        double least = 0.9 * (cost8(a->M, a->K, a->N, pl.dx.tile, pl.dx.splits) +
+                              cost8(a->N, a->K, a->M, pl.dw.tile, pl.dw.splits));
+        const Plan8 x0 = pl.dx, w0 = pl.dw;
+        for (const int tile : {kFp8Deep, kFp8Wide, kFp8Big}) {
+            const Plan8 x = plan_tile8(x0, tile, a->M, a->K), w = plan_tile8(w0, tile, a->N, a->K);
+            const double c = std::max(cost8(a->M, a->K, a->N, tile, x.splits), cost8(a->N, a->K, a->M, tile, w.splits));
+            if (plan_groups(x) + plan_groups(w) > kCUs || c >= least) continue;
+            least = c;
+            pl.pair = true;
+            pl.dx = x;
+            pl.dw = w;
+        }
+    }
+    pl.off_dw = pl.pair ? round_up(pl.dx.part_bytes, 256) : 0;
+    pl.off_part = lay.take(std::max(a->dX ? pl.dx.part_bytes : 0, pl.off_dw + (a->dW ? pl.dw.part_bytes : 0)));
     pl.bytes = lay.bytes;
     return GEMM_EPI_OK;
 }
 
 template <int SRC, int ACT>
-hipError_t launch_dz3(int format, const QuantParams &q, hipStream_t s)
+hipError_t launch_dz3(int format, const QuantParams &q, int64_t pad_groups, hipStream_t s)
 {
-    const dim3 g((unsigned)blocks_of(q.C), (unsigned)blocks_of(q.R)), b(512);
+    const int64_t across = blocks_of(q.C);
+    const dim3 g((unsigned)across, (unsigned)(q.bands + ceil_div(pad_groups, across))), b(512);
     return format == GE_FP8_E4M3 ? launch(quant_kernel<SRC, false, true, 0, ACT>, g, b, s, q)
                                  : launch(quant_kernel<SRC, false, true, 1, ACT>, g, b, s, q);
 }
 template <int SRC>
-hipError_t launch_dz2(int act, int format, const QuantParams &q, hipStream_t s)
+hipError_t launch_dz2(int act, int format, const QuantParams &q, int64_t pad_groups, hipStream_t s)
 {
     switch (act) {
-    case ACT_RELU: return launch_dz3<SRC, ACT_RELU>(format, q, s);
-    case ACT_GELU: return launch_dz3<SRC, ACT_GELU>(format, q, s);
-    case ACT_SILU: return launch_dz3<SRC, ACT_SILU>(format, q, s);
-    default: return launch_dz3<SRC, ACT_IDENTITY>(format, q, s);
+    case ACT_RELU: return launch_dz3<SRC, ACT_RELU>(format, q, pad_groups, s);
+    case ACT_GELU: return launch_dz3<SRC, ACT_GELU>(format, q, pad_groups, s);
+    case ACT_SILU: return launch_dz3<SRC, ACT_SILU>(format, q, pad_groups, s);
+    default: return launch_dz3<SRC, ACT_IDENTITY>(format, q, pad_groups, s);
     }
 }
 
@@ -503,28 +552,45 @@ int run_linear_grad8(const ge_linear_fp8_backward_args *a, const LinearGradPlan8
     q.ldqt = round_up(a->M, 16);
     q.ST = (uint8_t *)ws + pl.off_st;
     q.ldst = round_up(blocks_of(a->M), 4);
-    const int bands = (int)blocks_of(a->M);
-    q.partial = !a->dbias ? nullptr : bands == 1 ? a->dbias : (float *)(ws + pl.off_bias);
-    GE_TRY(bf ? launch_dz2<QS_BF16>((int)a->act, (int)a->format, q, s)
-              : launch_dz2<QS_F16>((int)a->act, (int)a->format, q, s));
-    if (a->dbias && bands > 1) GE_TRY(run_colsum(q.partial, a->dbias, bands, (int)a->N, s));
+    q.bands = (int)blocks_of(a->M);
+    q.partial = !a->dbias ? nullptr : q.bands == 1 ? a->dbias : (float *)(ws + pl.off_bias);
     Staging st;
     Operand8 w = {(const uint8_t *)a->WT, (const uint8_t *)a->WTS, a->ldwt, a->ldwts};
     Operand8 x = {(const uint8_t *)a->XT, (const uint8_t *)a->XTS, a->ldxt, a->ldxts};
     if (a->dX) stage_operand(pl.w, w, a->K, blocks_of(a->K), a->N, ws, st);
     if (a->dW) stage_operand(pl.x, x, a->K, a->K, a->M, ws, st);
-    GE_TRY(st.run(s));
+    q.pad = st.p;
+    GE_TRY(bf ? launch_dz2<QS_BF16>((int)a->act, (int)a->format, q, st.groups(512), s)
+              : launch_dz2<QS_F16>((int)a->act, (int)a->format, q, st.groups(512), s));
     float *part = (float *)(ws + pl.off_part);
+    Product8 dx, dw;
     if (a->dX) {
-        Fp8Params p = {};
-        set_product8(p, pl.dx, a->M, a->K, a->N, {q.Q, q.S, q.ldq, q.lds}, w, 7);
-        GE_TRY(run_product8(bf, e5m2, pl.dx, p, a->dX, a->lddx, part, s));
+        set_product8(dx.p, pl.dx, a->M, a->K, a->N, {q.Q, q.S, q.ldq, q.lds}, w, 7);
+        set_out8(dx, pl.dx, a->dX, a->lddx, part);
     }
     if (a->dW) {
-        Fp8Params p = {};
-        set_product8(p, pl.dw, a->N, a->K, a->M, {q.QT, q.ST, q.ldqt, q.ldst}, x, 0);
-        GE_TRY(run_product8(bf, e5m2, pl.dw, p, a->dW, a->lddw, part, s));
+        set_product8(dw.p, pl.dw, a->N, a->K, a->M, {q.QT, q.ST, q.ldqt, q.ldst}, x, 0);
+        set_out8(dw, pl.dw, a->dW, a->lddw, part + pl.off_dw / 4);
     }
+    const bool sum_bias = a->dbias && q.bands > 1;
+    if (pl.pair) {
+        Fp8Pair pair = {{dx.p, dw.p}, {}, {dx.groups, dw.groups}};
+        const bool here = sum_bias && q.bands <= kBiasBands;
+        if (here) pair.bias = {q.partial, a->dbias, q.bands, (int)a->N};
+        GE_TRY(launch_pair8(bf, e5m2, pl.dx.tile, pair, s));
+        GE_TRY(run_sum8(bf, dx, s));
+        GE_TRY(run_sum8(bf, dw, s));
+        return sum_bias && !here ? hip_status(run_colsum(q.partial, a->dbias, q.bands, (int)a->N, s)) : GEMM_EPI_OK;
+    }
+    if (sum_bias) {
+        // (the same order of the sum as in a pair's launch: dbias has the same bits
+        // whichever other gradients are wanted)
+        GE_TRY(q.bands <= kBiasBands ? launch(bias_sum_kernel, dim3((unsigned)ceil_div(a->N, 256)), dim3(256), s,
+                                              BiasSum{q.partial, a->dbias, q.bands, (int)a->N})
+                                     : run_colsum(q.partial, a->dbias, q.bands, (int)a->N, s));
+    }
+    if (a->dX) GE_TRY(run_product8(bf, e5m2, pl.dx, dx, s));
+    if (a->dW) GE_TRY(run_product8(bf, e5m2, pl.dw, dw, s));
     return GEMM_EPI_OK;
 }
 

@@ -12,6 +12,42 @@
 
 namespace gemm_epi {
 
+// Operands and scales that the products cannot read in place (rows off the
+// 16-byte rule, scales off the 4-byte rule): copied to rows of ldo bytes, a
+// multiple of 16, of which those from cols on are zeros.  16 bytes a thread and turn.
+struct PadBytes {
+    const uint8_t *src[4];
+    uint8_t *dst[4];
+    int64_t lds[4], ldo[4];
+    int rows[4], cols[4];
+    int n;
+};
+// thread `at` of `threads`
+__device__ __forceinline__ void pad_bytes(const PadBytes &p, int64_t at, int64_t threads)
+{
+#pragma unroll 1
+    for (int v = 0; v < p.n; v++) {
+        const uint32_t pieces = (uint32_t)(p.ldo[v] / 16);
+        const int64_t total = (int64_t)p.rows[v] * pieces;
+        const int cols = p.cols[v];
+        for (int64_t i = at; i < total; i += threads) {
+            const int64_t r = i / pieces;
+            const int c = (int)(i - r * pieces) * 16;
+            const char *row = (const char *)p.src[v] + r * p.lds[v];
+            i32x4 x;
+            if (cols >= 16)
+                x = move_down(load_piece<1>(row + min(c, cols - 16)), min(max(c + 16 - cols, 0), 16));
+            else
+                x = load_piece_short<1>(row + c, cols - c);
+            *(i32x4 *)(p.dst[v] + r * p.ldo[v] + c) = x;
+        }
+    }
+}
+__global__ __launch_bounds__(256) void pad_bytes_kernel(PadBytes p)
+{
+    pad_bytes(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+
 struct QuantParams {
     const void *X;
     int64_t ldx;
@@ -22,6 +58,8 @@ struct QuantParams {
     const void *Z;
     int64_t ldz;
     float *partial;  // [bands][C], or NULL
+    int bands;       // of 128 rows; the grid's rows past them copy pad's operands
+    PadBytes pad;
 };
 
 enum QuantSrc : int { QS_F16 = 0, QS_BF16 = 1, QS_F32 = 2 };
@@ -64,6 +102,13 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
     const int r0 = (int)blockIdx.y * kBlock, c0 = (int)blockIdx.x * kBlock;
     const int rows = min(p.R - r0, kBlock), cols = min(p.C - c0, kBlock);
     const int n = cols - tx * 8;  // columns that exist from this thread's on
+
+    if constexpr (GRAD >= 0)
+        if ((int)blockIdx.y >= p.bands) {
+            const int64_t group = (int64_t)(blockIdx.y - p.bands) * gridDim.x + blockIdx.x;
+            pad_bytes(p.pad, group * 512 + tid, (int64_t)(gridDim.y - p.bands) * gridDim.x * 512);
+            return;
+        }
 
     float v[RT][8];
     if constexpr (SRC == QS_F32) {
@@ -262,29 +307,6 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
                 }
             }
         }
-    }
-}
-
-// Operands and scales that the products cannot read in place (rows off the
-// 16-byte rule, scales off the 4-byte rule): copied to rows of ldo bytes, byte
-// by byte.  One grid row per matrix.
-struct PadBytes {
-    const uint8_t *src[4];
-    uint8_t *dst[4];
-    int64_t lds[4], ldo[4], rows[4], cols[4];
-};
-__global__ __launch_bounds__(256) void pad_bytes_kernel(PadBytes p)
-{
-    const int v = blockIdx.y;
-    const int64_t groups = p.ldo[v] / 4, total = p.rows[v] * groups;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / groups, c = (i - r * groups) * 4;
-        const uint8_t *s = p.src[v] + r * p.lds[v] + c;
-        uint32_t w = 0;
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (c + e < p.cols[v]) w |= (uint32_t)s[e] << (8 * e);
-        *(uint32_t *)(p.dst[v] + r * p.ldo[v] + c) = w;
     }
 }
 

@@ -438,6 +438,14 @@ def test_backward_exact_dz(M, N, K, act, dtype, format):
     assert none is None and none2 is None and torch.equal(c, db)
 
 
+@pytest.mark.parametrize("M, N, K", [(1001, 1003, 999), (2048, 2050, 2040), (2816, 2800, 2811), (8400, 130, 129),
+                                     (700, 300, 5001)])
+def test_backward_of_both_together(M, N, K):
+    """Both products fit on the chip beside each other: on 128 x 128, 128 x 256 and 256 x 256 tiles, with more bands of
+    rows than the launch sums the bias's gradient of, and in splits."""
+    test_backward_exact_dz(M, N, K, "relu", "bf16", "e5m2")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("act", ["gelu", "silu"])
 @pytest.mark.parametrize("M, N, K", GRAD_SHAPES)
