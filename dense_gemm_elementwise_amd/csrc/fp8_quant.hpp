@@ -94,7 +94,9 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
     constexpr bool BF = SRC == QS_BF16;
     constexpr int PITCH = 132;  // bytes of a column in LDS, off the bank stride
     constexpr bool WITH_Z = GRAD > ACT_IDENTITY;
-    __shared__ float colmax[WAVES][kBlock];
+    constexpr bool PACKED = SRC != QS_F32 && GRAD <= ACT_RELU;  // elements stay in 16 bits, two to a dword
+    __shared__ __attribute__((aligned(16))) float colmax[WAVES][kBlock];  // (packed: dwords of two columns' magnitudes)
+    __shared__ __attribute__((aligned(16))) int colscale[kBlock];
     __shared__ float tilemax[WAVES];
     __shared__ __attribute__((aligned(16))) uint8_t turned[BOTH ? kBlock * PITCH : 8];
     __shared__ float colsum[GRAD >= 0 ? WAVES : 1][kBlock];
@@ -111,6 +113,7 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
         }
 
     float v[RT][8];
+    uint32_t d[RT][4];  // packed: columns 2 j and 2 j + 1
     if constexpr (SRC == QS_F32) {
         i32x4 x[RT][2];
 #pragma unroll
@@ -155,34 +158,51 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
         }
 #pragma unroll
         for (int i = 0; i < RT; i++) {
-            const half8 xv = __builtin_bit_cast(half8, x[i]);
+            if constexpr (PACKED) {
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                float d = ld16<BF>(xv[e]);
-                if constexpr (WITH_Z) {
-                    const float zv = ld16<BF>(__builtin_bit_cast(half8, z[i])[e]);
-                    if constexpr (GRAD == ACT_RELU)
-                        d = zv <= 0.0f ? 0.0f : d;  // a mask, as in linear_backward
-                    else
-                        d *= lin_act_grad<GRAD>(zv);  // (behind the row's end both are 0, and the slope of 0 is finite)
+                for (int j = 0; j < 4; j++) {
+                    d[i][j] = (uint32_t)x[i][j];
+                    if constexpr (GRAD == ACT_RELU) {  // a mask, as in linear_backward: 0 where z <= 0, a NaN of z passes
+                        const uint32_t zz = (uint32_t)z[i][j];
+                        const float lo = value_u16<BF>(zz & 0xFFFF), hi = value_u16<BF>(zz >> 16);
+                        d[i][j] = (lo <= 0.0f ? 0 : d[i][j] & 0xFFFF) | (hi <= 0.0f ? 0 : d[i][j] & 0xFFFF0000u);
+                    }
                 }
-                v[i][e] = d;
+            } else {
+                const half8 xv = __builtin_bit_cast(half8, x[i]);
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    v[i][e] = ld16<BF>(xv[e]);
+                    // (behind the row's end both are 0, and the slope of 0 is finite)
+                    if constexpr (WITH_Z) v[i][e] *= lin_act_grad<GRAD>(ld16<BF>(__builtin_bit_cast(half8, z[i])[e]));
+                }
             }
         }
     }
     if (rows < kBlock)  // (the last row stands for those that are not there)
 #pragma unroll
         for (int i = 0; i < RT; i++)
-            if (ty * RT + i >= rows)
+            if (ty * RT + i >= rows) {
 #pragma unroll
-                for (int e = 0; e < 8; e++) v[i][e] = 0.0f;
+                for (int e = 0; e < 8; e++) {
+                    if constexpr (PACKED)
+                        d[i][e / 2] = 0;
+                    else
+                        v[i][e] = 0.0f;
+                }
+            }
 
     if constexpr (GRAD >= 0) {
         if (p.partial) {
             float s[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                s[e] = (v[0][e] + v[1][e]) + (v[2][e] + v[3][e]);
+                if constexpr (PACKED) {
+                    auto f = [&](int i) { return value_u16<BF>(e & 1 ? d[i][e / 2] >> 16 : d[i][e / 2] & 0xFFFF); };
+                    s[e] = (f(0) + f(1)) + (f(2) + f(3));
+                } else {
+                    s[e] = (v[0][e] + v[1][e]) + (v[2][e] + v[3][e]);
+                }
                 s[e] += __shfl_xor(s[e], 16);
                 s[e] += __shfl_xor(s[e], 32);
             }
@@ -203,15 +223,28 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
     // the rows' maxima; where one is infinite, the finite elements' alone
     // (v_max drops a NaN by itself)
     float rm[RT];
+    uint32_t size[RT][4];  // packed: magnitudes, 0 for what is not finite
 #pragma unroll
     for (int i = 0; i < RT; i++) {
-        rm[i] = 0.0f;
+        if constexpr (PACKED) {
 #pragma unroll
-        for (int e = 0; e < 8; e++) rm[i] = __builtin_fmaxf(rm[i], __builtin_fabsf(v[i][e]));
-        if (!(rm[i] < __builtin_inff())) {
+            for (int j = 0; j < 4; j++) size[i][j] = d[i][j] & 0x7FFF7FFFu;
+            uint32_t m = max_u16x2(max_u16x2(size[i][0], size[i][1]), max_u16x2(size[i][2], size[i][3]));
+            if (has_not_finite<BF>(m)) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) size[i][j] = finite_u16x2<BF>(size[i][j]);
+                m = max_u16x2(max_u16x2(size[i][0], size[i][1]), max_u16x2(size[i][2], size[i][3]));
+            }
+            rm[i] = larger_of<BF>(m);
+        } else {
             rm[i] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; e++) rm[i] = __builtin_fmaxf(rm[i], finite_abs(v[i][e]));
+            for (int e = 0; e < 8; e++) rm[i] = __builtin_fmaxf(rm[i], __builtin_fabsf(v[i][e]));
+            if (!(rm[i] < __builtin_inff())) {
+                rm[i] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; e++) rm[i] = __builtin_fmaxf(rm[i], finite_abs(v[i][e]));
+            }
         }
     }
     int ex[RT];
@@ -245,9 +278,14 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
     if (!BOTH || p.Q) {
 #pragma unroll
         for (int i = 0; i < RT; i++) {
-            const float f = pow2f(-ex[i]);
-            const u32x2 q = {cvt4<FMT>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f),
-                             cvt4<FMT>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f)};
+            u32x2 q;
+            if constexpr (PACKED) {
+                q = u32x2{cvt4_16<FMT, BF>(d[i][0], d[i][1], ex[i]), cvt4_16<FMT, BF>(d[i][2], d[i][3], ex[i])};
+            } else {
+                const float f = pow2f(-ex[i]);
+                q = u32x2{cvt4<FMT>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f),
+                          cvt4<FMT>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f)};
+            }
             if (ty * RT + i < rows) store_bytes8(p.Q + (int64_t)(r0 + ty * RT + i) * p.ldq + c0 + tx * 8, q, n);
         }
     }
@@ -257,38 +295,63 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
 #pragma unroll
             for (int e = 0; e < 8; e++) ec[e] = ex[0];
         } else {
+            if constexpr (PACKED) {
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                float m = 0.0f;
-#pragma unroll
-                for (int i = 0; i < RT; i++) m = __builtin_fmaxf(m, __builtin_fabsf(v[i][e]));
-                if (!(m < __builtin_inff())) {
-                    m = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < RT; i++) m = __builtin_fmaxf(m, finite_abs(v[i][e]));
+                for (int j = 0; j < 4; j++) {
+                    uint32_t m = max_u16x2(max_u16x2(size[0][j], size[1][j]), max_u16x2(size[2][j], size[3][j]));
+                    m = max_u16x2(m, (uint32_t)__shfl_xor((int)m, 16));
+                    m = max_u16x2(m, (uint32_t)__shfl_xor((int)m, 32));
+                    if ((tid & 63) < 16) ((uint32_t *)colmax[wave])[tx * 4 + j] = m;
                 }
-                m = __builtin_fmaxf(m, __shfl_xor(m, 16));
-                m = __builtin_fmaxf(m, __shfl_xor(m, 32));
-                if ((tid & 63) < 16) colmax[wave][tx * 8 + e] = m;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    float m = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < RT; i++) m = __builtin_fmaxf(m, __builtin_fabsf(v[i][e]));
+                    if (!(m < __builtin_inff())) {
+                        m = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < RT; i++) m = __builtin_fmaxf(m, finite_abs(v[i][e]));
+                    }
+                    m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+                    m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+                    if ((tid & 63) < 16) colmax[wave][tx * 8 + e] = m;
+                }
             }
             __syncthreads();
             if (tid < kBlock) {  // the column's scale, for all that hold a part of it
-                float m = colmax[0][tid];
+                float m;
+                if constexpr (PACKED) {
+                    uint32_t u = 0;
 #pragma unroll
-                for (int w = 1; w < WAVES; w++) m = __builtin_fmaxf(m, colmax[w][tid]);
+                    for (int w = 0; w < WAVES; w++) u = max(u, (uint32_t)((const unsigned short *)colmax[w])[tid]);
+                    m = value_u16<BF>(u);
+                } else {
+                    m = colmax[0][tid];
+#pragma unroll
+                    for (int w = 1; w < WAVES; w++) m = __builtin_fmaxf(m, colmax[w][tid]);
+                }
                 const int e = block_exponent(m, TOP);
                 if (tid < cols) p.ST[(int64_t)(c0 + tid) * p.ldst + blockIdx.y] = (uint8_t)(e + 127);
-                colmax[0][tid] = __builtin_bit_cast(float, e);
+                colscale[tid] = e;
             }
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; e++) ec[e] = __builtin_bit_cast(int, colmax[0][tx * 8 + e]);
+            for (int e = 0; e < 8; e++) ec[e] = colscale[tx * 8 + e];
         }
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const float f = pow2f(-ec[e]);
-            *(uint32_t *)(turned + (tx * 8 + e) * PITCH + ty * RT) =
-                cvt4<FMT>(v[0][e] * f, v[1][e] * f, v[2][e] * f, v[3][e] * f);
+            uint32_t q;
+            if constexpr (PACKED) {
+                const uint32_t half = e & 1 ? 0x07060302u : 0x05040100u;  // the column's of two dwords
+                q = cvt4_16<FMT, BF>(__builtin_amdgcn_perm(d[1][e / 2], d[0][e / 2], half),
+                                     __builtin_amdgcn_perm(d[3][e / 2], d[2][e / 2], half), ec[e]);
+            } else {
+                const float f = pow2f(-ec[e]);
+                q = cvt4<FMT>(v[0][e] * f, v[1][e] * f, v[2][e] * f, v[3][e] * f);
+            }
+            *(uint32_t *)(turned + (tx * 8 + e) * PITCH + ty * RT) = q;
         }
         __syncthreads();
         // 8 threads a column, 16 bytes each
