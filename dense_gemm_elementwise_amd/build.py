@@ -5,10 +5,11 @@ fp16 kernels), csrc/gemm_epi_bf16.hip (the bfloat16 kernels) and
 csrc/gemm_epi_f32e.hip, csrc/gemm_epi_bf16_f32e.hip (fp16 / bfloat16 A and B
 with fp32 epilogue tensors) and csrc/gemm_epi_f16_bf16e.hip,
 csrc/gemm_epi_bf16_f16e.hip (the other 16-bit type for the epilogue tensors),
-and csrc/linear_*.hip (the training and serving operators of
+csrc/linear_*.hip (the training and serving operators of
 include/linear_ops.h: the C ABI with its small kernels, and the products by
-group and element type) in parallel for --offload-arch=gfx950 only, then
-links them into one shared library.
+group and element type) and csrc/fp8_*.hip, csrc/moe.hip (the 8-bit products and
+the mixture of experts of include/fp8_ops.h) in parallel for
+--offload-arch=gfx950 only, then links them into one shared library.
 Packed-fp32 VALU instructions are switched off (-packed-fp32-ops): the
 epilogue is plain scalar fp32 arithmetic.
 

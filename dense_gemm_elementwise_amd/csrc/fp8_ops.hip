@@ -25,10 +25,13 @@ int check_bytes(const void *p, int64_t ld, int64_t cols, int64_t limit, int null
 int check_format(int64_t f) { return f == GE_FP8_E4M3 || f == GE_FP8_E5M2 ? GEMM_EPI_OK : GEMM_EPI_ERR_DTYPE; }
 
 // ---- quantisation ---------------------------------------------------------------
+int64_t quant_groups(int64_t R, int64_t C) { return blocks_of(R) * blocks_of(C); }
+// 512 threads each, below 2^32 in all, with room for the staging of operands
+bool quant_fits(int64_t R, int64_t C) { return quant_groups(R, C) <= (1 << 23) - 16 * kCUs; }
 template <int SRC, bool TILE, bool BOTH>
 hipError_t launch_quant3(int format, const QuantParams &q, hipStream_t s)
 {
-    const dim3 g((unsigned)blocks_of(q.C), (unsigned)blocks_of(q.R)), b(512);
+    const dim3 g((unsigned)quant_groups(q.R, q.C)), b(512);
     return format == GE_FP8_E4M3 ? launch(quant_kernel<SRC, TILE, BOTH, 0, kNoGrad>, g, b, s, q)
                                  : launch(quant_kernel<SRC, TILE, BOTH, 1, kNoGrad>, g, b, s, q);
 }
@@ -55,6 +58,7 @@ int check_quantize(const ge_quantize_fp8_args *a)
     GE_CHECK(check_format(a->format));
     if (a->dtype < GEMM_EPI_F16 || a->dtype > GEMM_EPI_F32) return GEMM_EPI_ERR_DTYPE;
     if (a->R == 0) return GEMM_EPI_OK;
+    if (!quant_fits(a->R, a->C)) return GEMM_EPI_ERR_SHAPE;
     const bool tile = a->block == GE_BLOCK_TILE;
     const int64_t rb = blocks_of(a->R), cb = blocks_of(a->C);
     GE_CHECK(check_matrix(a->X, a->ldx, a->C, a->dtype == GEMM_EPI_F32 ? 4 : 2, GEMM_EPI_ERR_NULL_INPUT));
@@ -323,6 +327,7 @@ int plan_linear8(const ge_linear_fp8_args *a, LinearPlan8 &pl)
 {
     GE_CHECK(check_linear8(a));
     if (a->M == 0) return GEMM_EPI_OK;
+    if (!a->XS && !quant_fits(a->M, a->K)) return GEMM_EPI_ERR_SHAPE;
     Layout lay;
     pl.few = a->M <= kFewRows;
     if (pl.few) {
@@ -467,6 +472,7 @@ int plan_linear_grad8(const ge_linear_fp8_backward_args *a, LinearGradPlan8 &pl)
 {
     GE_CHECK(check_linear_grad8(a));
     if (a->M == 0) return GEMM_EPI_OK;
+    if (!quant_fits(a->M, a->N)) return GEMM_EPI_ERR_SHAPE;
     Layout lay;
     pl.off_q = lay.take(a->M * round_up(a->N, 16));
     pl.off_s = lay.take(a->M * round_up(blocks_of(a->N), 4));
@@ -511,8 +517,7 @@ int plan_linear_grad8(const ge_linear_fp8_backward_args *a, LinearGradPlan8 &pl)
 template <int SRC, int ACT>
 hipError_t launch_dz3(int format, const QuantParams &q, int64_t pad_groups, hipStream_t s)
 {
-    const int64_t across = blocks_of(q.C);
-    const dim3 g((unsigned)across, (unsigned)(q.bands + ceil_div(pad_groups, across))), b(512);
+    const dim3 g((unsigned)(quant_groups(q.R, q.C) + pad_groups)), b(512);
     return format == GE_FP8_E4M3 ? launch(quant_kernel<SRC, false, true, 0, ACT>, g, b, s, q)
                                  : launch(quant_kernel<SRC, false, true, 1, ACT>, g, b, s, q);
 }

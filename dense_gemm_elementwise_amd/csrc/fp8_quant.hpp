@@ -58,7 +58,7 @@ struct QuantParams {
     const void *Z;
     int64_t ldz;
     float *partial;  // [bands][C], or NULL
-    int bands;       // of 128 rows; the grid's rows past them copy pad's operands
+    int bands;       // of 128 rows; the workgroups past them copy pad's operands
     PadBytes pad;
 };
 
@@ -101,14 +101,16 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
     __shared__ __attribute__((aligned(16))) uint8_t turned[BOTH ? kBlock * PITCH : 8];
     __shared__ float colsum[GRAD >= 0 ? WAVES : 1][kBlock];
     const int tid = threadIdx.x, wave = tid >> 6, tx = tid & 15, ty = tid >> 4;
-    const int r0 = (int)blockIdx.y * kBlock, c0 = (int)blockIdx.x * kBlock;
+    // (one axis: an axis of its own for the rows' blocks would end at 65535)
+    const int across = (p.C + kBlock - 1) / kBlock, by = (int)blockIdx.x / across, bx = (int)blockIdx.x - by * across;
+    const int r0 = by * kBlock, c0 = bx * kBlock;
     const int rows = min(p.R - r0, kBlock), cols = min(p.C - c0, kBlock);
     const int n = cols - tx * 8;  // columns that exist from this thread's on
 
     if constexpr (GRAD >= 0)
-        if ((int)blockIdx.y >= p.bands) {
-            const int64_t group = (int64_t)(blockIdx.y - p.bands) * gridDim.x + blockIdx.x;
-            pad_bytes(p.pad, group * 512 + tid, (int64_t)(gridDim.y - p.bands) * gridDim.x * 512);
+        if ((int)blockIdx.x >= p.bands * across) {
+            pad_bytes(p.pad, ((int64_t)blockIdx.x - p.bands * across) * 512 + tid,
+                      ((int64_t)gridDim.x - p.bands * across) * 512);
             return;
         }
 
@@ -215,7 +217,7 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
                 float sum = 0.0f;
 #pragma unroll
                 for (int w = 0; w < WAVES; w += 2) sum += colsum[w][tid] + colsum[w + 1][tid];
-                p.partial[(int64_t)blockIdx.y * p.C + c0 + tid] = sum;
+                p.partial[(int64_t)by * p.C + c0 + tid] = sum;
             }
         }
     }
@@ -262,8 +264,8 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
 #pragma unroll
         for (int i = 0; i < RT; i++) ex[i] = e;
         if (tid == 0) {
-            if (p.S) p.S[(int64_t)blockIdx.y * p.lds + blockIdx.x] = (uint8_t)(e + 127);
-            if (BOTH) p.ST[(int64_t)blockIdx.x * p.ldst + blockIdx.y] = (uint8_t)(e + 127);
+            if (p.S) p.S[(int64_t)by * p.lds + bx] = (uint8_t)(e + 127);
+            if (BOTH) p.ST[(int64_t)bx * p.ldst + by] = (uint8_t)(e + 127);
         }
     } else {
 #pragma unroll
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
 #pragma unroll
             for (int i = 0; i < RT; i++)
                 if (ty * RT + i < rows)
-                    p.S[(int64_t)(r0 + ty * RT + i) * p.lds + blockIdx.x] = (uint8_t)(ex[i] + 127);
+                    p.S[(int64_t)(r0 + ty * RT + i) * p.lds + bx] = (uint8_t)(ex[i] + 127);
         }
     }
     if (!BOTH || p.Q) {
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
                     for (int w = 1; w < WAVES; w++) m = __builtin_fmaxf(m, colmax[w][tid]);
                 }
                 const int e = block_exponent(m, TOP);
-                if (tid < cols) p.ST[(int64_t)(c0 + tid) * p.ldst + blockIdx.y] = (uint8_t)(e + 127);
+                if (tid < cols) p.ST[(int64_t)(c0 + tid) * p.ldst + by] = (uint8_t)(e + 127);
                 colscale[tid] = e;
             }
             __syncthreads();

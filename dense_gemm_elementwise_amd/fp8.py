@@ -17,7 +17,8 @@ refused while gradients are recorded.
 stride along the rows and any row stride; their scales are float8_e8m0fnu
 (powers of two), by row blocks (R, ceil(C / 128)) or by tiles (ceil(R / 128),
 ceil(C / 128)).  Rows that start at multiples of 16 bytes (scales: of 4), as those of
-quantize_fp8 do, are read in place; others are copied first, on every call.
+quantize_fp8 do, are read in place; others are copied first, on every call, but
+for products of up to 16 rows and moe, which read all in place.
 """
 import ctypes
 import struct

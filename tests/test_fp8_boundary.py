@@ -196,6 +196,26 @@ def test_workspace_sizes():
     assert MOE.workspace(T=64)[1] == MOE.workspace(T=100000)[1]
 
 
+def test_few_rows_need_no_copies():
+    """Up to 16 rows read their operands in place at any alignment; x of 16 bits is quantised first past 4 rows."""
+    odd = dict(X=P + 1, ldx=203, XS=P + 1, ldxs=3, W=P + 3, ldw=201, WS=P + 1, ldws=2)
+    assert LINEAR.workspace(M=16, **odd) == (0, 0)
+    assert LINEAR.workspace(M=17, **odd)[1] > 0
+    half = dict(odd, XS=0, X=P + 2)
+    assert LINEAR.workspace(M=4, **half) == (0, 0)
+    rc, n = LINEAR.workspace(M=5, **half)
+    assert rc == 0 and n >= 5 * 200
+
+
+def test_quantised_matrices_have_fewer_than_2_23_blocks():
+    assert QUANT.run(R=2000000, C=2000000, ldx=2000000, ldq=2000000, lds=20000, ldqt=2000000, ldst=20000) == SHAPE
+    big = dict(K=1, ldx=1, ldw=16, N=1, XS=0)
+    assert LINEAR.workspace(M=2 ** 30, **big)[0] == SHAPE
+    assert LINEAR.workspace(M=9 * 10 ** 6, **big)[0] == 0
+    assert LINEAR_B.workspace(M=2000000, N=2000000, lddd=2000000, ldxt=2000000, ldxts=16000, ldwt=2000000, ldwts=16000,
+                              ldz=2000000, dW=0)[0] == SHAPE
+
+
 def test_python_refusals():
     h, e = torch.float16, torch.float8_e4m3fn
     x, w = torch.zeros(4, 8, dtype=h), torch.zeros(6, 8, dtype=e)
