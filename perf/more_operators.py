@@ -141,7 +141,8 @@ def _own(s):
             return ops.linear_fp8_backward(s["dd"], s["xt"], s["xt_scale"], s["wt"], s["wt_scale"], s["z"],
                                            act=s["act"])
         return ops.linear_fp8(s["x"], s["w"], s["w_scale"], s["bias"], s["residual"], x_scale=s["x_scale"],
-                              act=s["act"], save_z=s["M"] > 1)  # serving keeps no Z
+                              act=s["act"], save_z=s["M"] > 1,  # serving keeps no Z
+                              dtype=s["bias"].dtype)
     return ops.moe(s["x"], s["w_router"], s["up"], s["down"], top_k=s["k"], up_scale=s["up_scale"],
                    down_scale=s["down_scale"], act="silu")
 
