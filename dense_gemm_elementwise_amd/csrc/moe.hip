@@ -52,7 +52,7 @@ int check_moe(const ge_moe_args *a)
 }
 
 struct MoePlan {
-    int64_t logits = 0, chosen = 0, weight = 0, total = 0, hidden = 0, bytes = 0;
+    int64_t logits = 0, chosen = 0, weight = 0, total = 0, hidden = 0, low = 0, bytes = 0;
 };
 
 int plan_moe(const ge_moe_args *a, MoePlan &pl)
@@ -66,6 +66,7 @@ int plan_moe(const ge_moe_args *a, MoePlan &pl)
     pl.weight = lay.take(t * a->top_k * 4);
     pl.total = lay.take(t * 4);
     pl.hidden = lay.take(t * a->top_k * a->inner * 2);
+    pl.low = lay.take(t * a->top_k * a->inner);
     pl.bytes = lay.bytes;
     return GEMM_EPI_OK;
 }
@@ -155,6 +156,7 @@ int ge_moe(const ge_moe_args *a)
     q.weight = (float *)(ws + pl.weight);
     q.total = (float *)(ws + pl.total);
     q.hidden = (_Float16 *)(ws + pl.hidden);
+    q.low = (uint8_t *)ws + pl.low;
     const bool bf = a->dtype == GEMM_EPI_BF16;
     hipStream_t s = (hipStream_t)a->stream;
     for (int64_t t = 0; t < a->T; t += kMoeChunk) {

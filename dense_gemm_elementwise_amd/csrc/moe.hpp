@@ -38,7 +38,23 @@ struct MoeParams {
     float *weight;    // [T][k]: exp(logit - the token's largest)
     float *total;     // [T]: the sum of all experts' exp(logit - largest)
     _Float16 *hidden; // [T][k][I]
+    uint8_t *low;     // [T][k][I]: what hidden's rounding left, see low_byte
 };
+
+// h is an operand of 16-bit MFMAs.  Rounded to 16 bits alone it makes the layer's error
+// half as large again as the rounding of its result, so the remainder is kept
+// as well, times 2^9 (bf16) or 2^12 (fp16), in e5m2: 3 bits more for |h| from 2^-14 to
+// 57344.  The down product takes 14.6 us instead of 14.0 for one token in 16 bits, 12.0
+// for 10.4 in 8, 72 for 61 for 64 tokens.
+template <bool BF>
+constexpr float kLowScale = BF ? 0x1p9f : 0x1p12f;
+template <bool BF>
+__device__ __forceinline__ uint8_t low_byte(float h, _Float16 high)
+{
+    const float rest = (h - ld16<BF>(high)) * kLowScale<BF>;
+    const float r = __builtin_fabsf(rest) <= 57344.0f ? rest : 0.0f;  // (nor a NaN, nor an infinity)
+    return (uint8_t)__builtin_amdgcn_cvt_pk_bf8_f32(r, r, 0, false);
+}
 
 // Logits in an order that is total: a NaN below every number, -0 with +0.
 __device__ __forceinline__ uint32_t logit_key(float v)
@@ -52,20 +68,24 @@ __device__ __forceinline__ uint32_t logit_key(float v)
 struct Pair8 {
     half8 v[2];
 };
-template <bool BF>
+template <bool BF, bool E5M2 = false>
 __device__ __forceinline__ Pair8 widen(i32x4 q)
 {
-    // e4m3 has fewer digits and a smaller range than either 16-bit type: exact
+    // both formats have fewer digits than either 16-bit type, and no larger range: exact
     i32x4 r[2];
 #pragma unroll
     for (int u = 0; u < 4; u++) {
         int lo, hi;
         if constexpr (BF) {
-            lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[u], 1.0f, false));
-            hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[u], 1.0f, true));
+            lo = __builtin_bit_cast(int, (E5M2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q[u], 1.0f, false)
+                                                : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[u], 1.0f, false)));
+            hi = __builtin_bit_cast(int, (E5M2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(q[u], 1.0f, true)
+                                                : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[u], 1.0f, true)));
         } else {
-            lo = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[u], 1.0f, false));
-            hi = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[u], 1.0f, true));
+            lo = __builtin_bit_cast(int, (E5M2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(q[u], 1.0f, false)
+                                                : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[u], 1.0f, false)));
+            hi = __builtin_bit_cast(int, (E5M2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(q[u], 1.0f, true)
+                                                : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(q[u], 1.0f, true)));
         }
         r[u >> 1][(u & 1) * 2] = lo;
         r[u >> 1][(u & 1) * 2 + 1] = hi;
@@ -164,7 +184,10 @@ struct MoeScales {
 };
 
 template <bool W8, int G, int NB>
-constexpr int moe_turn_bytes() { return G * RowBlocks<W8 ? 1 : 2>::BYTES + NB * RowBlocks<2>::BYTES; }
+constexpr int moe_turn_bytes()
+{
+    return G * RowBlocks<W8 ? 1 : 2>::BYTES + NB * RowBlocks<2>::BYTES;
+}
 
 // One block of 128 columns: the weights of G times 16 rows and NB times 16 tokens, on their way.
 template <bool BF, bool W8, int G, int NB>
@@ -360,12 +383,15 @@ __global__ __launch_bounds__(256, 2) void moe_up_kernel(MoeParams p, int by_choi
         if constexpr (W8) ws[g].init(scales, p.ldus, r0, end, li);
     }
     const int turn = (i0 / 16 * 5 + expert * 3) % max(p.H >> 7, 1);
-    // 16 bits: an operand of the down product
+    // (an operand of the down product)
     auto store = [&](const float (&v)[G], int c, int r) {
         float h = lin_act<ACT>(v[0]);
         if constexpr (GATED) h *= v[1];
         const int t = list[c];
-        p.hidden[((int64_t)t * p.k + ranks[t]) * p.I + i0 + r] = st16<BF>(h);
+        const int64_t at = ((int64_t)t * p.k + ranks[t]) * p.I + i0 + r;
+        const _Float16 high = st16<BF>(h);
+        p.hidden[at] = high;
+        p.low[at] = low_byte<BF>(h, high);
     };
     // 16 NB tokens at a time (more read the weights again, from the caches)
     for (int n0 = 0; n0 < n; n0 += 16 * NB) {
@@ -416,12 +442,76 @@ __global__ __launch_bounds__(256, 2) void moe_up_kernel(MoeParams p, int by_choi
     }
 }
 
+// One block of 128 inner columns of 16 rows of Down and of h, high and low parts, on their way.
+template <bool BF, bool W8>
+struct DownBlock {
+    using W = RowBlocks<W8 ? 1 : 2>;
+    using High = RowBlocks<2>;
+    using Low = RowBlocks<1>;
+    static constexpr int BYTES = W::BYTES + High::BYTES + Low::BYTES;  // of LDS
+    struct Rows {
+        W w;
+        MoeScales ws;
+        High high;
+        Low low;
+    };
+    i32x4 w[W::NL], high[High::NL], low[Low::NL];
+    uint32_t s;
+
+    __device__ __forceinline__ void fetch(const Rows &r, int block)
+    {
+        r.w.load(w, block);
+        r.high.load(high, block);
+        r.low.load(low, block);
+        if constexpr (W8) s = r.ws.byte(block);
+    }
+    __device__ __forceinline__ void fetch_short(const Rows &r)
+    {
+        r.w.load_short(w);
+        r.high.load_short(high);
+        r.low.load_short(low);
+        if constexpr (W8) s = r.ws.byte(0);
+    }
+    __device__ __forceinline__ void finish(const Rows &r, int block)
+    {
+        r.w.finish(w, block);
+        r.high.finish(high, block);
+        r.low.finish(low, block);
+    }
+    // acc, acc_low += the products with the high and the low parts
+    __device__ __forceinline__ void use(f32x4 &acc, f32x4 &acc_low, char *turned, int lane) const
+    {
+        const int li = lane & 15, lg = lane >> 4;
+        char *th = turned + W::BYTES, *tl = th + High::BYTES;
+        W::put(turned, w, lane);
+        High::put(th, high, lane);
+        Low::put(tl, low, lane);
+        wave_lds_sync();
+        f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f}, part_low = part;  // 8-bit: the sums of the block, before its scales
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const Pair8 wv = get_pair<W8 ? 1 : 2, BF>(turned, u, li, lg), hv = get_pair<2, BF>(th, u, li, lg),
+                        lv = widen<BF, true>(*(const i32x4 *)(tl + Low::at(li, u * 4 + lg)));
+            f32x4 &to = W8 ? part : acc, &to_low = W8 ? part_low : acc_low;
+            to = mfma_pair<BF>(hv, wv, to);
+            to_low = mfma_pair<BF>(lv, wv, to_low);
+        }
+        if constexpr (W8) {
+            const float v = MoeScales::value(s);
+            acc += v * part;
+            acc_low += v * part_low;
+        }
+        wave_lds_sync();
+    }
+};
+
 // D = residual + sum of weight Down h for 16 of the layer's columns and all
 // tokens of the chunk.  The work is a list of units: a chosen expert, up to 16 of
 // its tokens and a part of its inner columns.  They are dealt out over the 8 waves,
 // each of which adds up its own sums of all tokens in LDS, in a fixed order.  What
 // bounds it is the bytes in flight: a wave streams over the ends of its units (64
-// experts of 4096 x 1024 in 8 bits 61 us, 4.4 TB/s; with units of 4 blocks that each
+// experts of 4096 x 1024 in 8 bits 61 us, 4.4 TB/s, before h had its low part, 72 with
+// it and two blocks a ring instead of three; with units of 4 blocks that each
 // drained before the next began 75 us).  Workgroups begin at different units.
 // Where all began at the first one and the same rows of h, that was 101 us.
 constexpr int kDownWaves = 8;
@@ -429,7 +519,7 @@ constexpr int kDownUnits = kMoeExperts + kMoeChunk * kMoeTop / 16;  // sum of ce
 template <bool BF, bool W8>
 __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
 {
-    constexpr int THREADS = 64 * kDownWaves, PAIRS = kMoeChunk * kMoeTop / THREADS, DEPTH = 3;
+    constexpr int THREADS = 64 * kDownWaves, PAIRS = kMoeChunk * kMoeTop / THREADS, DEPTH = 2;
     __shared__ unsigned long long users[kMoeExperts];  // tokens of each expert
     __shared__ uint16_t start[kMoeExperts];            // where its choices start in the list
     __shared__ uint16_t list[kMoeChunk * kMoeTop];     // the choices (t k + r), expert by expert, by token
@@ -438,7 +528,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
     __shared__ int count;
     __shared__ float share[kMoeChunk * kMoeTop];
     __shared__ float sums[kDownWaves][kMoeChunk][16];
-    __shared__ __attribute__((aligned(16))) char turned[kDownWaves][moe_turn_bytes<W8, 1, 1>()];
+    __shared__ __attribute__((aligned(16))) char turned[kDownWaves][DownBlock<BF, W8>::BYTES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), li = lane & 15,
               lg = lane >> 4;
     const int h0 = (int)blockIdx.x * 16, rows = (p.T + 15) / 16 * 16;
@@ -500,11 +590,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
     const int entries = __builtin_amdgcn_readfirstlane(count), blocks = (p.I + 127) >> 7;
     const int len = blocks / min(blocks, (kDownWaves + entries - 1) / entries);
     const int parts = (blocks + len - 1) / len, units = entries * parts, tail = p.I & 127 ? blocks - 1 : -1;
-    using Block = MoeBlock<BF, W8, 1, 1>;
+    using Block = DownBlock<BF, W8>;
     struct Unit {
-        typename Block::W w[1];
-        MoeScales ws[1];
-        RowBlocks<2> h[1];
+        typename Block::Rows rows;
         int first, n;    // blocks
         int at, tokens;  // in the list
     };
@@ -517,15 +605,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
         q.tokens = __builtin_amdgcn_readfirstlane(unit_tokens[i]);
         q.first = part * len;
         q.n = min(blocks - q.first, len);
-        q.w[0].init((const char *)p.Down + ((int64_t)e * p.down_stride + h0 * p.lddn) * (W8 ? 1 : 2), p.I, lane,
-                    [&](int r) { return (uint32_t)(min(r, p.H - 1 - h0) * (int)p.lddn) * (W8 ? 1 : 2); });
-        if constexpr (W8) q.ws[0].init(p.DS + (int64_t)e * p.ds_stride, p.ldds, h0, p.H, li);
-        // (rows past the last token repeat it; below 2^32 bytes: 2048 rows of 2^20)
-        q.h[0].init((const char *)p.hidden, p.I, lane,
-                    [&](int r) { return (uint32_t)list[q.at + min(r, q.tokens - 1)] * p.I * 2; });
+        q.rows.w.init((const char *)p.Down + ((int64_t)e * p.down_stride + h0 * p.lddn) * (W8 ? 1 : 2), p.I, lane,
+                      [&](int r) { return (uint32_t)(min(r, p.H - 1 - h0) * (int)p.lddn) * (W8 ? 1 : 2); });
+        if constexpr (W8) q.rows.ws.init(p.DS + (int64_t)e * p.ds_stride, p.ldds, h0, p.H, li);
+        // (rows past the last token repeat it; below 2^32 bytes: 2048 rows of 2^20 elements)
+        auto row = [&](int r) { return (uint32_t)list[q.at + min(r, q.tokens - 1)] * p.I; };
+        q.rows.high.init((const char *)p.hidden, p.I, lane, [&](int r) { return row(r) * 2; });
+        q.rows.low.init((const char *)p.low, p.I, lane, row);
         return q;
     };
-    f32x4 acc[1][1] = {{f32x4{0.0f, 0.0f, 0.0f, 0.0f}}};
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, acc_low = acc;
     auto close = [&](const Unit &q) {
         // the lane has tokens 4 lg .. of the 16, of column li
         float *at[4], old[4], by[4];
@@ -538,15 +627,15 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
         }
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            if (lg * 4 + j < q.tokens) *at[j] = old[j] + by[j] * acc[0][0][j];
-        acc[0][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (lg * 4 + j < q.tokens) *at[j] = old[j] + by[j] * (acc[j] + (1.0f / kLowScale<BF>) * acc_low[j]);
+        acc = acc_low = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     };
     if (p.I < kShortRow) {
         for (int u = wave; u < units; u += kDownWaves) {
             const Unit q = open(u);
             Block f;
-            f.fetch_short(q.w, q.ws, q.h);
-            f.use(acc, turned[wave], lane);
+            f.fetch_short(q.rows);
+            f.use(acc, acc_low, turned[wave], lane);
             close(q);
         }
     } else if (wave < units) {
@@ -557,15 +646,15 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
         Unit q = open(wave);
         int g = 0;  // the number in the unit of ring[0]'s block
         auto fetch = [&](int d, const Unit &of, int block) {
-            ring[d].fetch(of.w, of.ws, of.h, of.first + max(block, 0));
+            ring[d].fetch(of.rows, of.first + max(block, 0));
             __builtin_amdgcn_sched_barrier(0);
         };
         auto use = [&](int d) {
-            if (g + d >= 0) ring[d].use(acc, turned[wave], lane);
+            if (g + d >= 0) ring[d].use(acc, acc_low, turned[wave], lane);
             __builtin_amdgcn_sched_barrier(0);
         };
         auto end = [&]() {
-            if (q.first + q.n - 1 == tail) ring[DEPTH - 1].finish(q.w, q.h, tail);
+            if (q.first + q.n - 1 == tail) ring[DEPTH - 1].finish(q.rows, tail);
         };
         auto begin = [&](int n) { return n - (n + DEPTH - 1) / DEPTH * DEPTH; };
         g = begin(q.n);

@@ -620,6 +620,21 @@ def test_moe_many_tiles(T, H, E, I, k, w8):  # noqa: E741
     check_moe(T, H, E, I, k, "bf16", w8=w8, seed=42)
 
 
+@pytest.mark.parametrize("w8", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [1, 40])
+def test_moe_error_is_the_result_s_rounding(T, dtype, w8):
+    """h keeps what its rounding to 16 bits left in e5m2, rounded to 2^-3 of itself at most: h is off by 2^-3 of a
+    rounding to 16 bits.  Errors of independent signs, they add to the rounding of the result in squares: a factor of
+    sqrt(1 + 2^-6) = 1.008, 1.05 with the spread of 1024 values and more (1.41 with h in 16 bits alone)."""
+    t = TYPES[dtype]
+    x, wr, up, down, us, ds = moe_inputs(T, 1024, 8, 512, t, True, w8, 60)
+    got = ge.moe(x, wr, up, down, top_k=4, up_scale=us, down_scale=ds).double()
+    want, _ = ref_moe(x, wr, up, down, us, ds, 4, "silu", True, None, t)
+    rounded = want.to(t).double()
+    assert float((got - want).norm()) <= 1.05 * float((rounded - want).norm())
+
+
 @pytest.mark.parametrize("act", list(ACTS))
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("renormalize", [False, True])
