@@ -305,6 +305,7 @@ template <bool BF, bool W8, int ACT, bool GATED, int NB>
 __global__ __launch_bounds__(256, 2) void moe_up_kernel(MoeParams p, int by_choice, int shared)
 {
     constexpr int G = GATED ? 2 : 1;
+    constexpr int DEPTH = NB == 1 ? (W8 ? 3 : 2) : (W8 ? 2 : 1);  // what the registers hold
     __shared__ uint32_t keys[kMoeExperts];
     __shared__ int ranks[kMoeChunk];  // the expert's rank in each token's choice; k and more: not chosen
     __shared__ int list[kMoeChunk];   // the tokens that chose it
@@ -406,8 +407,8 @@ __global__ __launch_bounds__(256, 2) void moe_up_kernel(MoeParams p, int by_choi
 #pragma unroll
             for (int g = 0; g < G; g++) acc[g][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        moe_product<BF, W8, G, NB, NB == 1 ? (W8 ? 3 : 2) : (W8 ? 2 : 1)>(acc, w, ws, x, turned[wave], shared ? wave : 0, shared ? 4 : 1,
-                                                      p.H, turn, lane);
+        moe_product<BF, W8, G, NB, DEPTH>(acc, w, ws, x, turned[wave], shared ? wave : 0, shared ? 4 : 1, p.H, turn,
+                                          lane);
         if (!shared) {
             // lane: row li, tokens 4 lg .. + 3 of a block
 #pragma unroll
