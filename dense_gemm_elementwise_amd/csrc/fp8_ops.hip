@@ -142,7 +142,7 @@ bool plan_fits(const Plan8 &p) { return plan_groups(p) <= kMaxGroups; }
 // partial sums' round trip.  The pick was within 5% of the fastest on all 34 (for
 // instance 2400 x 3232 x 4096: 128 x 256 29.7, 128 x 128 32.5, 256 x 256 43.2;
 // 1536 x 1536 x 4096: deep 16.6, 24.1 without; 1024 x 1024 x 8192: 27.3, in
-// 4 splits 21.0).  256 x 128 was no faster than 128 x 256 by more than 3%.
+// 4 splits 21.0).
 double cost8(int64_t M, int64_t N, int64_t K, int tile, int splits)
 {
     const Fp8Tile t = kFp8Tiles[tile];

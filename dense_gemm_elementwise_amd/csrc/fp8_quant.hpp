@@ -85,7 +85,8 @@ __device__ __forceinline__ void store_bytes8(uint8_t *p, u32x2 v, int n)
 // LDS, 4 rows of a column (4 bytes) at a time.  Bound by the bytes: 2 in, 1 or 2 out.
 // All loads are issued together, at the edge too: a row's last 16 bytes where the
 // row ends inside them, moved down (with a branch a row and single elements at
-// the edge, 2400 x 3233 of fp16 into both orientations 13.8 us, 12.0 so).
+// the edge, 2400 x 3233 of fp16 into both orientations 13.8 us, 12.0 so, 10.0
+// with 16-bit elements kept packed; its bytes would take 6.4).
 // ---------------------------------------------------------------------------
 template <int SRC, bool TILE, bool BOTH, int FMT, int GRAD>
 __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
