@@ -291,6 +291,18 @@ def test_linear_few_rows_in_place():
     assert torch.equal(got[::3], want[::3]) and bool(torch.isnan(got[1]).all()) and not bool(torch.isfinite(got[2]).any())
 
 
+def test_linear_of_more_rows_than_a_grid_axis_holds_blocks_of():
+    """8.5 million rows of 16 bits are 66407 blocks of 128 (a second axis of a grid ends at 65535): any rows have the bits
+    that they have alone."""
+    M, N, K = 8500000, 16, 16
+    t = torch.bfloat16
+    x = normal(1000, K, seed=1, to=t).repeat(M // 1000, 1)
+    w8, ws = ge.quantize_fp8(normal(N, K, seed=2), block="tile")
+    d = ge.linear_fp8(x, w8, ws, act="relu")
+    want = ge.linear_fp8(x[:1000], w8, ws, act="relu")
+    assert d.shape == (M, N) and bool((d.view(-1, 1000, N) == want).all())
+
+
 # each tile and a split contraction: (rows, columns, length) that the plan gives to 256 x 256, 128 x 256, two 128 x 128
 # on a compute unit, one with deep rings, and splits
 LARGE = [(4096, 4104, 650), (4000, 2500, 1037), (1100, 4096, 4096), (700, 8190, 900), (8200, 1000, 384),
