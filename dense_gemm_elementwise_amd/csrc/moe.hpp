@@ -542,14 +542,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
         if (i >= p.T * p.k) continue;
         expert[j] = p.chosen[i];
         const int t = i / p.k;
+        const float all = p.total[t];
         float sum = 0.0f;
         if (p.renormalize) {
 #pragma unroll 8
             for (int r = 0; r < p.k; r++) sum += p.weight[t * p.k + r];
-        } else {
-            sum = p.total[t];
         }
-        share[i] = p.weight[i] / sum;
+        // (a NaN logit, chosen or not, is in `all` alone: the largest logit and the chosen ones' sum pass it by)
+        share[i] = p.weight[i] / (p.renormalize && all == all ? sum : all);
     }
     for (int i = lane; i < rows * 16; i += 64) sums[wave][i >> 4][i & 15] = 0.0f;
     __syncthreads();

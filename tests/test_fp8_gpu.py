@@ -731,6 +731,28 @@ def test_moe_empty():
     assert ge.moe(x[:0], wr, up, down, top_k=2).shape == (0, 64)
 
 
+@pytest.mark.parametrize("w8", [False, True])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("T, E, k", [(1, 8, 2), (1, 64, 8), (20, 8, 2), (70, 8, 3), (5, 4, 4)])
+def test_moe_nan_in_the_router(T, E, k, renormalize, w8):
+    """An expert with a NaN in its router row gives every token a NaN logit, so all of the softmax is NaN, though the
+    expert ranks last and is chosen by no token.  An infinity there, met by -1 in the other tokens, has a logit of -inf and
+    a weight of 0; met by 0 in one token it makes that token's weights NaN."""
+    x, wr, up, down, us, ds = moe_inputs(T, 128, E, 64, torch.bfloat16, w8=w8, seed=5)
+    kw = dict(top_k=k, up_scale=us, down_scale=ds, renormalize=renormalize)
+    assert bool(torch.isfinite(ge.moe(x, wr, up, down, **kw)).all())
+    bad = wr.clone()
+    bad[E - 1, 77] = float("nan")
+    assert bool(torch.isnan(ge.moe(x, bad, up, down, **kw)).all())
+    if k < E:
+        bad[E - 1, 77] = float("inf")
+        y = x.clone()
+        y[:, 77] = -1.0
+        y[T // 2, 77] = 0.0
+        got = torch.isnan(ge.moe(y, bad, up, down, **kw))
+        assert bool(got[T // 2].all()) and int(got.sum()) == got.shape[1]
+
+
 # ---- as they are used ---------------------------------------------------------------------
 
 def step(x, residual, w, w8, experts, dd):
