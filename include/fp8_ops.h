@@ -142,7 +142,8 @@ typedef struct {
  *   p = softmax of X Wr^T; each token takes the top_k experts of the largest
  *   logits (ties: the lowest index), weight p, or with renormalize p over the
  *   sum of the chosen ones;
- *   h = act(Up x), gated: act(gate) up, held in dtype and 3 bits more;
+ *   h = act(Up x), gated: act(gate) up, held in dtype and 3 bits more (bf16: of |h| from
+ *   2^-15 to 2^16, none to 3 outside; fp16: an infinity past 65504);
  *   D = residual + sum over the chosen experts of weight Down h.
  * D (T, hidden) may be the residual (or NULL: none), not X.  A NaN logit ranks below
  * every number and makes the token's weights NaN.  T may be 0, and any number: the

@@ -753,6 +753,34 @@ def test_moe_nan_in_the_router(T, E, k, renormalize, w8):
         assert bool(got[T // 2].all()) and int(got.sum()) == got.shape[1]
 
 
+@pytest.mark.parametrize("dtype, first, last", [("bf16", -14, 15), ("f16", -8, 15)])
+def test_moe_hidden_keeps_three_bits_beyond_16(dtype, first, last):
+    """h = big + rest with big in 16 bits, rest within half a step of it; Down is the identity and the residual -big, so
+    that the result is what the layer kept of rest.  e5m2 rounds it by at most 2^-3 of itself, and what is past its range is
+    off by less than a rounding of the largest remainder: at most 2^-3 of half a step of h.  (The sums add a rounding of
+    h to 32 bits at most twice, the result's one to 16.)"""
+    t = TYPES[dtype]
+    steps = 1 / torch.finfo(t).eps
+    g = torch.Generator().manual_seed(3)
+    e = torch.arange(first, last + 1).repeat_interleave(32).double()
+    n = len(e)
+    big = (torch.randint(1, int(steps), (n,), generator=g) / steps + 1) * torch.exp2(e)
+    half = torch.exp2(e) * half_step(t)
+    rest = (torch.empty(n).uniform_(-0.99, 0.99, generator=g).double() * half).to(t).double()
+    rest[15::32] = (0.98 * half[15::32]).to(t).double()
+    rest = torch.round(rest / torch.exp2(e - 22)) * torch.exp2(e - 22)  # (h is exact in 32 bits)
+    big = torch.where(torch.arange(n) % 2 == 0, big, -big)
+    up = torch.zeros(1, n, n, dtype=t)
+    up[0, :, 0], up[0, :, 1] = big.to(t), rest.to(t)
+    x, wr = torch.zeros(1, n, dtype=t), torch.zeros(1, n, dtype=t)
+    x[0, :2] = 1.0
+    got = ge.moe(x.to(DEV), wr.to(DEV), up.to(DEV), torch.eye(n, dtype=t)[None].to(DEV), top_k=1,
+                 residual=-big[None].to(t).to(DEV), act="identity")[0].double().cpu()
+    own = half * 2.0 ** -3 + 2 * 2.0 ** -24 * big.abs()
+    tol = own + half_step(t) * (rest.abs() + own) + (2.0 ** -25 if dtype == "f16" else 0.0)
+    assert bool(((got - rest).abs() <= tol).all()), float(((got - rest).abs() / tol).max())
+
+
 # ---- as they are used ---------------------------------------------------------------------
 
 def step(x, residual, w, w8, experts, dd):
