@@ -630,8 +630,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void moe_down_kernel(MoeParams p)
             old[j] = *at[j];
         }
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (lg * 4 + j < q.tokens) *at[j] = old[j] + by[j] * (acc[j] + (1.0f / kLowScale<BF>) * acc_low[j]);
+        for (int j = 0; j < 4; j++) {
+            // (what is not finite in Down is in the high part's sum; met by a remainder of 0 or of
+            // the other sign, the low part's is a NaN or the other infinity)
+            const float low = __builtin_fabsf(acc_low[j]) < __builtin_inff() ? (1.0f / kLowScale<BF>) * acc_low[j] : 0.0f;
+            if (lg * 4 + j < q.tokens) *at[j] = old[j] + by[j] * (acc[j] + low);
+        }
         acc = acc_low = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     };
     if (p.I < kShortRow) {

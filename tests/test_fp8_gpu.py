@@ -781,6 +781,26 @@ def test_moe_hidden_keeps_three_bits_beyond_16(dtype, first, last):
     assert bool(((got - rest).abs() <= tol).all()), float(((got - rest).abs() / tol).max())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [1, 20])
+def test_moe_infinite_down_weight(T, dtype):
+    """An infinite weight of Down times h (not zero) is an infinity of the product's sign."""
+    t = TYPES[dtype]
+    x, wr, up, down, _, _ = moe_inputs(T, 128, 1, 100, t, seed=9)
+    clean = ge.moe(x, wr, up, down, top_k=1)
+    g, u = (x.double() @ up[0].double().t()).split(100, 1)
+    h = torch.nn.functional.silu(g) * u
+    at = torch.nonzero(h.abs().amin(0) > 2e-3)[:, 0]  # (the sign of h is beyond doubt)
+    assert len(at) > 50
+    down[0, at, at] = float("inf")
+    down[0, at[::3], at[::3]] = -float("inf")
+    got = ge.moe(x, wr, up, down, top_k=1)
+    assert torch.equal(got[:, at].double(), torch.sign(h[:, at]) * down[0, at, at].double())
+    keep = torch.ones(128, dtype=torch.bool, device=DEV)
+    keep[at] = False
+    assert torch.equal(got[:, keep], clean[:, keep])
+
+
 # ---- as they are used ---------------------------------------------------------------------
 
 def step(x, residual, w, w8, experts, dd):
