@@ -21,6 +21,7 @@ quantize_fp8 do, are read in place; others are copied first, on every call, but
 for products of up to 16 rows and moe, which read all in place.
 """
 import ctypes
+import operator
 import struct
 
 import torch
@@ -277,7 +278,11 @@ def moe(x, w_router, w_up, w_down, *, top_k, up_scale=None, down_scale=None, res
     gated = w_up.shape[1] == 2 * I
     if not gated and w_up.shape[1] != I:
         raise ValueError(f"w_up has {w_up.shape[1]} rows for each expert, expected {2 * I} (gated) or {I}")
-    if not 1 <= int(top_k) <= min(E, 32):
+    try:
+        top_k = operator.index(top_k)
+    except TypeError:
+        raise TypeError(f"top_k must be an integer, got {top_k!r}") from None
+    if not 1 <= top_k <= min(E, 32):
         raise ValueError(f"top_k must lie in 1 .. {min(E, 32)}, got {top_k}")
     if (up_scale is None) != (down_scale is None):
         raise ValueError("up_scale and down_scale come together")

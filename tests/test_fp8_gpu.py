@@ -914,3 +914,12 @@ def test_python_checks():
         ge.moe(mx, wr, up, down, top_k=1, up_scale=ws)
     with pytest.raises(ValueError, match="requires grad"):
         ge.moe(mx, wr, up.clone().requires_grad_(), down, top_k=1)
+
+
+def test_moe_top_k_is_an_index():
+    import numpy
+    x, wr, up, down, _, _ = moe_inputs(2, 64, 4, 32, torch.float16)
+    for bad in (2.0, "2", None, 1.5):
+        with pytest.raises(TypeError, match="top_k must be an integer"):
+            ge.moe(x, wr, up, down, top_k=bad)
+    assert torch.equal(ge.moe(x, wr, up, down, top_k=numpy.int64(2)), ge.moe(x, wr, up, down, top_k=2))
