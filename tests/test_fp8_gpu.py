@@ -801,6 +801,94 @@ def test_moe_infinite_down_weight(T, dtype):
     assert torch.equal(got[:, keep], clean[:, keep])
 
 
+# ---- rows that end inside a block, and what lies behind them --------------------------------
+
+def behind(t, multiple):
+    """A copy of an 8-bit matrix that the products read in place, NaN bytes behind every row's end and below the last row."""
+    b = t.view(torch.uint8)
+    pitch = -(-b.shape[1] // multiple) * multiple + multiple
+    big = torch.full((b.shape[0] + 1, pitch), 0x7F if multiple == 16 else 0xFF, dtype=torch.uint8, device=DEV)
+    v = big[:b.shape[0], :b.shape[1]]
+    v.copy_(b)
+    return v.view(t.dtype)
+
+
+def integers(R, C, seed, tall, format="e4m3"):
+    """Integers -3 .. 3 under scales 1/2, 1 and 2: sums of up to 2^19 of their products are exact."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(-3, 4, (R, C), generator=g).float().to(FORMAT[format][3]).to(DEV)
+    s = torch.randint(126, 129, (-(-R // 128) if tall else R, -(-C // 128)), generator=g, dtype=torch.uint8)
+    return behind(q, 16), behind(s.to(DEV).view(E8), 4)
+
+
+def with_workspace_of_nans(name, head):
+    """One call through the C entry point with a workspace whose every byte is a NaN's (8 bits, scales and fp32 alike)."""
+    rc, need = fp8.workspace_bytes(name, head + fp8._NO_TAIL)
+    assert rc == 0
+    ws = torch.full((max(need, 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    assert fp8._functions()[name](head + fp8._TAIL.pack(ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)) == 0
+    torch.cuda.synchronize()
+
+
+# two 128 x 128 tiles on a compute unit, 256 x 256, 128 x 128 with deep rings, 128 x 256, and splits whose last part is
+# ragged: contractions of one, two, three and more blocks, of which the last one is short
+TAILS = ([(130, 200, k) for k in (5, 100, 250, 383, 500, 645)] +
+         [(1600, 5200, k) for k in (5, 100, 250, 383, 500, 645, 1037)] +
+         [(5200, 515, 300), (130, 8200, 389), (40, 8200, 645), (2050, 9, 1037)] +
+         [(1600, 2500, k) for k in (797, 863, 962, 1061)] +
+         [(130, 130, 4097), (130, 130, 4200), (130, 130, 4353), (300, 310, 4097), (300, 310, 4200), (300, 310, 4353),
+          (600, 600, 4500), (1100, 1100, 4353), (130, 130, 8197)])
+
+
+@pytest.mark.parametrize("format", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("M, N, K", TAILS)
+def test_linear_tails(M, N, K, format):
+    x8, xs = integers(M, K, M + K, False, format)
+    w8, ws = integers(N, K, N + K, True)
+    want = value(x8, xs, "row") @ value(w8, ws, "tile").t()
+    for t in (torch.bfloat16, torch.float16):
+        d, z = ge.linear_fp8(x8, w8, ws, x_scale=xs, act="relu", save_z=True, dtype=t)
+        same(z, want.float().to(t))
+        same(d, want.clamp(min=0).float().to(t))
+
+
+@pytest.mark.parametrize("M, N, K", [(5, 40, 300), (16, 70, 1283), (17, 70, 1283), (130, 200, 645), (1600, 5200, 383),
+                                     (1600, 2500, 797), (300, 310, 4353)])
+def test_linear_from_16_bits_over_an_old_workspace(M, N, K):
+    """x is quantised into the workspace: nothing that lay there before reaches the result."""
+    t = torch.bfloat16
+    x = normal(M, K, seed=M, to=t)
+    w8, ws = integers(N, K, N + K, True)
+    want = ge.linear_fp8(x, w8, ws)
+    d = torch.zeros_like(want)
+    with_workspace_of_nans("ge_linear_fp8", fp8._LINEAR8.pack(
+        M, N, K, x.data_ptr(), K, 0, 0, w8.data_ptr(), w8.stride(0), ws.data_ptr(), max(ws.stride(0), ws.shape[1]), 0,
+        0, 0, d.data_ptr(), N, 0, 0, 0, 1, 0))
+    assert torch.equal(d, want) and bool(torch.isfinite(d).all())
+
+
+# both products in one launch (on the tile with deep rings, 128 x 256, 256 x 256) and apart
+@pytest.mark.parametrize("M, N, K", [(5, 5, 1), (300, 5, 1), (100, 250, 130), (383, 100, 300), (389, 383, 515),
+                                     (645, 500, 130), (2811, 133, 100), (300, 5, 8200), (133, 133, 8200), (389, 5, 8200),
+                                     (645, 5, 6000), (1037, 300, 8200), (389, 389, 8200), (2050, 5201, 1601)])
+def test_backward_tails(M, N, K):
+    """Integers whose quantisation is exact; NaN bytes behind the operands' rows and in all of the workspace."""
+    dd = torch.randint(-3, 4, (M, N), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).to(DEV)
+    xt, xts = integers(K, M, K + M, False)
+    wt, wts = integers(K, N, K + N, True)
+    for format in (0, 1):
+        dx = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+        dw = torch.zeros(N, K, dtype=torch.bfloat16, device=DEV)
+        db = torch.zeros(N, device=DEV)
+        with_workspace_of_nans("ge_linear_fp8_backward", fp8._LINEAR8_GRAD.pack(
+            M, N, K, dd.data_ptr(), N, xt.data_ptr(), xt.stride(0), xts.data_ptr(), xts.stride(0), wt.data_ptr(),
+            wt.stride(0), wts.data_ptr(), wts.stride(0), 0, 0, dx.data_ptr(), K, dw.data_ptr(), K, db.data_ptr(), 0, 1,
+            format))
+        same(dx, (dd.double() @ value(wt, wts, "tile").t()).float().to(torch.bfloat16))
+        same(dw, (dd.double().t() @ value(xt, xts, "row").t()).float().to(torch.bfloat16))
+        same(db, dd.double().sum(0))
+
+
 # ---- as they are used ---------------------------------------------------------------------
 
 def step(x, residual, w, w8, experts, dd):
