@@ -100,8 +100,8 @@ struct Staging {
         return p.n ? launch(pad_bytes_kernel, dim3((unsigned)groups(256)), dim3(256), s, p) : hipSuccess;
     }
 };
-bool rows16(const void *p, int64_t ld) { return aligned(p, 16) && ld % 16 == 0; }
-bool rows4(const void *p, int64_t ld) { return aligned(p, 4) && ld % 4 == 0; }
+// rows that all begin at multiples of `unit` bytes (a single one has no pitch)
+bool rows_at(int64_t unit, const void *p, int64_t ld, int64_t rows) { return aligned(p, unit) && (rows == 1 || ld % unit == 0); }
 
 // Where an operand's copies lie; negative: read in place.
 struct StageAt {
@@ -111,14 +111,17 @@ StageAt plan_operand(const void *q, int64_t ldq, const void *s, int64_t lds, int
                      Layout &lay)
 {
     StageAt at;
-    if (!rows16(q, ldq)) at.q = lay.take(rows * round_up(cols, 16));
-    if (!rows4(s, lds)) at.s = lay.take(srows * round_up(blocks_of(cols), 16));
+    if (!rows_at(16, q, ldq, rows)) at.q = lay.take(rows * round_up(cols, 16));
+    if (!rows_at(4, s, lds, srows)) at.s = lay.take(srows * round_up(blocks_of(cols), 16));
     return at;
 }
 void stage_operand(const StageAt &at, Operand8 &o, int64_t rows, int64_t srows, int64_t cols, char *ws, Staging &st)
 {
     if (at.q >= 0) st.add(o.q, o.ldq, rows, cols, (uint8_t *)ws + at.q);
     if (at.s >= 0) st.add(o.s, o.lds, srows, blocks_of(cols), (uint8_t *)ws + at.s);
+    // (a single row's pitch is raised to the rule: rows that do not exist then lie behind the descriptors' ends)
+    o.ldq = round_up(o.ldq, 16);
+    o.lds = round_up(o.lds, 4);
 }
 
 // ---- products -------------------------------------------------------------------

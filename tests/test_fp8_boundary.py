@@ -207,6 +207,23 @@ def test_few_rows_need_no_copies():
     assert rc == 0 and n >= 5 * 200
 
 
+def test_a_single_row_has_no_pitch():
+    """Where it begins alone decides whether it is read in place."""
+    kw = dict(K=300, ldx=304, ldw=304, ldws=4, ldr=129, ldd=129, ldz=129)
+    for n in (1, 96, 128):
+        rc, least = LINEAR.workspace(N=n, **kw)
+        assert rc == 0
+        assert LINEAR.workspace(N=n, **{**kw, "ldws": 3}) == (0, least)
+        assert LINEAR.workspace(N=n, WS=P + 2, **{**kw, "ldws": 3})[1] > least
+    assert LINEAR.workspace(N=129, **{**kw, "ldws": 3})[1] > LINEAR.workspace(N=129, **kw)[1]  # two rows of scales
+    least = LINEAR.workspace(N=1, **kw)[1]
+    assert LINEAR.workspace(N=1, **{**kw, "ldw": 300}) == (0, least)
+    assert LINEAR.workspace(N=1, W=P + 8, **{**kw, "ldw": 300})[1] > least
+    kw = dict(K=1, lddx=1, lddw=1)
+    rc, least = LINEAR_B.workspace(**kw)
+    assert rc == 0 and LINEAR_B.workspace(**kw, ldxt=300, ldxts=3, ldwt=96, ldwts=1) == (0, least)
+
+
 def test_quantised_matrices_have_fewer_than_2_23_blocks():
     assert QUANT.run(R=2000000, C=2000000, ldx=2000000, ldq=2000000, lds=20000, ldqt=2000000, ldst=20000) == SHAPE
     big = dict(K=1, ldx=1, ldw=16, N=1, XS=0)

@@ -889,6 +889,25 @@ def test_backward_tails(M, N, K):
         same(db, dd.double().sum(0))
 
 
+@pytest.mark.parametrize("N, K", [(1, 300), (1, 4097), (96, 300), (128, 900), (100, 4097)])
+@pytest.mark.parametrize("M", [17, 300])
+def test_linear_with_one_row_of_scales(M, N, K):
+    """A single row has no pitch: read in place, also with fewer scales than a multiple of 4 and whatever lies behind."""
+    x8, xs = integers(M, K, M + K, False)
+    w8, ws = integers(N, K, N + K, True)
+    kb = ws.shape[1]
+    want = value(x8, xs, "row") @ value(w8, ws, "tile").t()
+    row = torch.full((kb + 8,), 0xFF, dtype=torch.uint8, device=DEV)
+    row[:kb] = ws.view(torch.uint8)[0]
+    one = row[:kb].view(E8)[None]
+    assert one.is_contiguous()
+    same(ge.linear_fp8(x8, w8, one, x_scale=xs, dtype=torch.float16), want.float().to(torch.float16))
+    if N == 1:
+        lone = torch.full((K + 32,), 0x7F, dtype=torch.uint8, device=DEV)
+        lone[:K] = w8.view(torch.uint8)[0]
+        same(ge.linear_fp8(x8, lone[:K].view(E4)[None], one, x_scale=xs, dtype=torch.float16), want.float().to(torch.float16))
+
+
 # ---- as they are used ---------------------------------------------------------------------
 
 def step(x, residual, w, w8, experts, dd):
