@@ -303,6 +303,57 @@ def test_linear_of_more_rows_than_a_grid_axis_holds_blocks_of():
     assert d.shape == (M, N) and bool((d.view(-1, 1000, N) == want).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M, N, K", [s for s in SHAPES if s[0] > 4] + [(5, 4200, 1037), (16, 500, 100), (1600, 5200, 645)])
+def test_linear_from_16_bits_has_the_bits_of_the_quantised_x(M, N, K, dtype):
+    x = (normal(M, K, seed=M) * torch.exp2(3 * normal(M, 1, seed=K)).clamp(2.0 ** -8, 2.0 ** 8)).to(TYPES[dtype])
+    _, _, w8, ws = operands(1, N, K, 2)
+    x8, xs = ge.quantize_fp8(x)
+    d, z = ge.linear_fp8(x, w8, ws, act="silu", save_z=True)
+    d8, z8 = ge.linear_fp8(x8, w8, ws, x_scale=xs, act="silu", save_z=True, dtype=x.dtype)
+    assert torch.equal(d, d8) and torch.equal(z, z8)
+
+
+@pytest.mark.parametrize("format", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M, N", [(1, 700), (2, 700), (3, 700), (4, 700), (1, 4200), (4, 4200), (5, 700), (17, 700)])
+def test_linear_from_16_bits_shows_what_x_became(M, N, dtype, format):
+    """Every row of W has a single 1, so D is elements of the quantised x, which have so few digits that D holds them:
+    borders of the scale, ties, subnormals, zeros, the type's largest and smallest values."""
+    t, top, K = TYPES[dtype], FORMAT[format][0], 700
+    x = torch.zeros(24, K, dtype=torch.float64)
+    x[:16] = normal(16, K, seed=3).double().cpu()
+    for i in range(16):
+        x[i, 5] = top * 2.0 ** (i - 12)
+        x[i, 130] = top * 2.0 ** (i - 20) * (1 + torch.finfo(t).eps)
+        x[i, 300:332] = torch.arange(1, 33) * 2.0 ** (i - 14)
+    x[17] = -0.0
+    x[18] = torch.finfo(t).max
+    x[19] = torch.finfo(t).tiny
+    x[20] = torch.finfo(t).smallest_normal * torch.finfo(t).eps
+    x[21, ::2] = torch.finfo(t).tiny
+    x[22, 699] = 1.0
+    x[23, 1::128] = -torch.finfo(t).max
+    x = x.to(t).to(DEV)
+    at = torch.arange(N) * 3 % K
+    w = torch.zeros(N, K)
+    w[torch.arange(N), at] = 1.0
+    w8 = w.to(E4).to(DEV)
+    ws = torch.full((-(-N // 128), -(-K // 128)), 127, dtype=torch.uint8, device=DEV)
+    q, scale = ref_quantize(x, "row", format)
+    # (the product in 64 bits: an element that is past fp16 is an infinity, and makes NaNs of its products with 0)
+    want = (value(q, scale, "row").cpu() @ w.double().t()).to(t).double()
+    for r in range(0, 24, M):
+        rows = x[r:r + M].contiguous()
+        d = torch.zeros(rows.shape[0], N, dtype=t, device=DEV)
+        head = fp8._LINEAR8.pack(rows.shape[0], N, K, rows.data_ptr(), K, 0, 0, w8.data_ptr(), K, ws.data_ptr(),
+                                 ws.shape[1], 0, 0, 0, d.data_ptr(), N, 0, 0, 0, fp8._DTYPES[t], fp8.FORMATS[format])
+        need = fp8.workspace_bytes("ge_linear_fp8", head + fp8._NO_TAIL)[1]
+        ws_ = torch.empty(max(need, 16), dtype=torch.uint8, device=DEV)
+        assert fp8._functions()["ge_linear_fp8"](
+            head + fp8._TAIL.pack(ws_.data_ptr(), need, torch.cuda.current_stream().cuda_stream)) == 0
+        same(d, want[r:r + M])
+
 # each tile and a split contraction: (rows, columns, length) that the plan gives to 256 x 256, 128 x 256, two 128 x 128
 # on a compute unit, one with deep rings, and splits
 LARGE = [(4096, 4104, 650), (4000, 2500, 1037), (1100, 4096, 4096), (700, 8190, 900), (8200, 1000, 384),
