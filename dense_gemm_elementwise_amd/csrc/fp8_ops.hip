@@ -59,7 +59,6 @@ int check_quantize(const ge_quantize_fp8_args *a)
     if (a->dtype < GEMM_EPI_F16 || a->dtype > GEMM_EPI_F32) return GEMM_EPI_ERR_DTYPE;
     if (a->R == 0) return GEMM_EPI_OK;
     if (!quant_fits(a->R, a->C)) return GEMM_EPI_ERR_SHAPE;
-    const bool tile = a->block == GE_BLOCK_TILE;
     const int64_t rb = blocks_of(a->R), cb = blocks_of(a->C);
     GE_CHECK(check_matrix(a->X, a->ldx, a->C, a->dtype == GEMM_EPI_F32 ? 4 : 2, GEMM_EPI_ERR_NULL_INPUT));
     GE_CHECK(check_bytes(a->Q, a->ldq, a->C, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_OUTPUT));
@@ -67,7 +66,7 @@ int check_quantize(const ge_quantize_fp8_args *a)
     if (!a->QT != !a->ST) return GEMM_EPI_ERR_NULL_OUTPUT;
     if (a->QT) {
         GE_CHECK(check_bytes(a->QT, a->ldqt, a->R, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_OUTPUT));
-        GE_CHECK(check_bytes(a->ST, a->ldst, tile ? rb : rb, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_OUTPUT));
+        GE_CHECK(check_bytes(a->ST, a->ldst, rb, GE_MAX_COLS + 128, GEMM_EPI_ERR_NULL_OUTPUT));
     }
     return GEMM_EPI_OK;
 }

@@ -265,32 +265,30 @@ __global__ __launch_bounds__(512) void quant_kernel(QuantParams p)
 #pragma unroll
         for (int i = 0; i < RT; i++) ex[i] = e;
         if (tid == 0) {
-            if (p.S) p.S[(int64_t)by * p.lds + bx] = (uint8_t)(e + 127);
+            p.S[(int64_t)by * p.lds + bx] = (uint8_t)(e + 127);
             if (BOTH) p.ST[(int64_t)bx * p.ldst + by] = (uint8_t)(e + 127);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < RT; i++) ex[i] = block_exponent(row16_max(rm[i]), TOP);
-        if (p.S && tx == 0) {
+        if (tx == 0) {
 #pragma unroll
             for (int i = 0; i < RT; i++)
                 if (ty * RT + i < rows)
                     p.S[(int64_t)(r0 + ty * RT + i) * p.lds + bx] = (uint8_t)(ex[i] + 127);
         }
     }
-    if (!BOTH || p.Q) {
 #pragma unroll
-        for (int i = 0; i < RT; i++) {
-            u32x2 q;
-            if constexpr (PACKED) {
-                q = u32x2{cvt4_16<FMT, BF>(d[i][0], d[i][1], ex[i]), cvt4_16<FMT, BF>(d[i][2], d[i][3], ex[i])};
-            } else {
-                const float f = pow2f(-ex[i]);
-                q = u32x2{cvt4<FMT>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f),
-                          cvt4<FMT>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f)};
-            }
-            if (ty * RT + i < rows) store_bytes8(p.Q + (int64_t)(r0 + ty * RT + i) * p.ldq + c0 + tx * 8, q, n);
+    for (int i = 0; i < RT; i++) {
+        u32x2 q;
+        if constexpr (PACKED) {
+            q = u32x2{cvt4_16<FMT, BF>(d[i][0], d[i][1], ex[i]), cvt4_16<FMT, BF>(d[i][2], d[i][3], ex[i])};
+        } else {
+            const float f = pow2f(-ex[i]);
+            q = u32x2{cvt4<FMT>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f),
+                      cvt4<FMT>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f)};
         }
+        if (ty * RT + i < rows) store_bytes8(p.Q + (int64_t)(r0 + ty * RT + i) * p.ldq + c0 + tx * 8, q, n);
     }
     if constexpr (BOTH) {
         int ec[8];
