@@ -396,6 +396,22 @@ def test_linear_error_is_about_the_result_s_rounding(M, N, K):
     d = ge.linear_fp8(x8, w8, ws, x_scale=xs, dtype=torch.float16).double()
     assert float((d - want).norm() / want.norm()) < 1.25 * half_step(torch.float16)
 
+
+@pytest.mark.parametrize("M", [1, 17])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_linear_cut_is_towards_zero(M, sign):
+    """Beside a product of 2^16 in its group a product of 2^3 is kept and less is cut, towards zero for either sign; the
+    bias takes the 2^16 away again."""
+    small = [2, 4, 8, 12, 14, -2, -4, -8, -12, -14]
+    x, w = torch.zeros(M, 128, device=DEV), torch.zeros(len(small), 128, device=DEV)
+    x[:, 0], x[:, 1] = 256.0, 2.0
+    w[:, 0], w[:, 1] = sign * 256.0, torch.tensor(small, device=DEV) / 2
+    one = torch.full((M, 1), 127, dtype=torch.uint8, device=DEV).view(E8)
+    bias = torch.full((len(small),), sign * -65536.0, dtype=torch.bfloat16, device=DEV)
+    d = ge.linear_fp8(x.to(E4), w.to(E4), one[:1], bias, x_scale=one)
+    want = torch.tensor([0, 0, 8, 8, 8, 0, 0, -8, -8, -8], device=DEV)
+    assert bool((d.double() == want).all())
+
 @pytest.mark.parametrize("M, N, K", [(1, 40, 300), (5, 40, 300), (40, 200, 640), (300, 260, 900), (129, 130, 2048)])
 def test_linear_is_exact_on_integers(M, N, K):
     """Small integers under scales that differ by row, block and tile: every sum is exact, so is the result's rounding.
