@@ -260,9 +260,10 @@ def moe(x, w_router, w_up, w_down, *, top_k, up_scale=None, down_scale=None, res
     gated layer (each expert's gate rows first) or (E, I, H) for a plain one, w_down
     (E, H, I).  Every token takes the top_k experts with the largest logits
     x w_router^T (ties: the lowest index), weighted by the softmax over all
-    experts, divided by the chosen ones' sum with renormalize.  An expert's
-    output is w_down h, h = act(gate) * up or act(up), h in x's type and 3 bits more
-    (bfloat16: where 2^-15 <= |h| < 2^16; float16: an infinity past 65504).
+    experts, divided by the chosen ones' sum with renormalize; logits are fp32
+    sums, and a NaN among a token's makes its weights NaN.  An expert's output is
+    w_down h, h = act(gate) * up or act(up), h in x's type and 3 bits more (bfloat16:
+    where 2^-15 <= |h| < 2^16; float16: an infinity past 65504).
     Returns residual (T, H; None: zero) + the weighted sum, (T, H).  w_up and w_down
     are of x's type, or float8_e4m3fn with up_scale and down_scale by tiles (E,
     ceil(rows / 128), ceil(columns / 128)).  Made for a few tokens: the chosen experts'
